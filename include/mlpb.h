@@ -34,6 +34,7 @@
  *       W2                  [t][H][Fs] bf16        b2 [H] bf16
  *       Z saved (GELU)      [T][F]  bf16, column i*Fs+j = shard i, feature j
  *       Z saved (SwiGLU)    [T][t][2][Fs] bf16 (G then U of each shard)
+ *                           (both 8-bit codes and scales under MLPB_FLAG_CHECKPOINT8)
  *       A saved             [T][F]  bf16
  *       Y, dX               [T][H] fp32 (bf16 under MLPB_FLAG_BF16_OUT)
  *       dW1, dW2            fp32 in the layouts of W1, W2;  db1 [F], db2 [H] fp32
@@ -132,6 +133,17 @@ typedef enum { MLPB_ACT_GELU_TANH = 0, MLPB_ACT_SWIGLU = 1 } mlpb_act;
  * "sp_gather_x", "sp_gather_dy", "sp_scatter_y", "sp_scatter_dx").  mlpb_forward then
  * needs the workspace; the workspace holds 8*T*H more bytes. */
 #define MLPB_FLAG_EMULATE_COPIES 0x20u
+/* 8-bit activation checkpoints ("Key math" of the concept note: activation memory is what
+ * recomputation saves).  With this flag the forward saves Z (G, U) for the backward as
+ * 8-bit codes with one power-of-two scale for each 32 features of a row (the format of
+ * mlpb_act8_save, of the bf16-rounded Z), written in fc1's epilogue and read in the dgrad
+ * GEMM's: Zsaved is T*F1 code bytes [T][F1] followed by T*F1/32 scale bytes [T][F1/32]
+ * (F1 = F for GELU, 2F for SwiGLU; mlpb_saved_size gives the sum), 0.52 times the bf16 Z.
+ * As under MLPB_FLAG_RECOMPUTE_ACT, which it implies, A is rewritten by the backward, here
+ * from the decoded Z, and only Zsaved must survive between the passes.  The forward's Y is bit
+ * for bit that of the block without the flag; the gradients are those of the decoded Z.
+ * Requires F/tp % 32 == 0; not combined with MLPB_FLAG_FP8. */
+#define MLPB_FLAG_CHECKPOINT8 0x100u
 
 typedef struct {
   int64_t tokens;          /* T: rows of X; multiple of 128 (0 allowed)           */
@@ -177,7 +189,8 @@ void mlpb_destroy(mlpb_handle *h);
 mlpb_status mlpb_workspace_size(const mlpb_handle *h, size_t *bytes);
 
 /* Bytes of the saved activations: z_bytes for Z (GELU, T*F*2) or G|U (SwiGLU,
- * T*2F*2); a_bytes for A (T*F*2). */
+ * T*2F*2), the codes and scales under MLPB_FLAG_CHECKPOINT8 (T*F1 + T*F1/32); a_bytes
+ * for A (T*F*2). */
 mlpb_status mlpb_saved_size(const mlpb_handle *h, size_t *z_bytes, size_t *a_bytes);
 
 /* Forward of the block ("The Tensor-Parallel Primitives" and "The Transformer
@@ -306,6 +319,35 @@ mlpb_status mlpb_bias_grad_noalloc(const void *in, int64_t rows, int64_t cols, f
 mlpb_status mlpb_quantize_e4m3(const void *in, int64_t batches, int64_t rows, int64_t cols,
                                void *q, void *qt, uint32_t *amax, int32_t *scale_exp,
                                mlpb_stream_t stream);
+
+/* 8-bit activation checkpoints: fc1's output saved as 8-bit codes, and the activation's
+ * backward from them -- the format and arithmetic of MLPB_FLAG_CHECKPOINT8 for callers whose
+ * GEMMs are their own.
+ *   act = MLPB_ACT_GELU_TANH: Z [T][F], A = gelu_tanh(Z); tp only has to divide F.
+ *   act = MLPB_ACT_SWIGLU: Z [T][tp][2][Fs] (G then U of each shard), A = silu(G) * U [T][F].
+ * Blocks of 32 consecutive features of a row's segment -- all F for GELU, each shard's Fs
+ * gate and Fs up features for SwiGLU; a segment's last block may be shorter -- share one
+ * scale byte.  With amax the block's largest magnitude and k the largest integer, at most
+ * 126, with amax 2^k <= 127 (k = 0 for zeros), each code is z 2^k rounded to the nearest
+ * integer, ties to even, and the scale byte is 127 - k: a code c stands for c 2^(byte - 127),
+ * exactly.  A block that holds an infinity or a NaN has the byte 255 and stands for NaN
+ * throughout (its codes mean nothing).
+ *
+ * mlpb_act8_scales: *per_row = scale bytes of a row (ceil(F / 32) for GELU,
+ * 2 tp ceil(Fs / 32) for SwiGLU).
+ * mlpb_act8_save: writes codes [T][F1] (layout of Z), scales [T][per_row] and, unless A is
+ * NULL, A = act(Z) in bf16, from the bf16 Z itself.
+ * mlpb_act8_grad: with z the values the codes stand for, writes dZ = dA act'(z) (layout of Z,
+ * bf16) and, unless A is NULL, A = act(z), for an upstream gradient dA [T][F] bf16.
+ * F % tp == 0 and (F/tp) % 8 == 0 (else MLPB_EUNSUPPORTED); tensors 16-byte aligned, scales
+ * of any alignment; outputs overlap no input.  tokens = 0 does nothing.  No handle, no
+ * workspace; allocate nothing. */
+mlpb_status mlpb_act8_scales(int32_t act, int64_t ffn, int32_t tp, int64_t *per_row);
+mlpb_status mlpb_act8_save(int32_t act, int64_t tokens, int64_t ffn, int32_t tp, const void *Z,
+                           void *A, void *codes, void *scales, mlpb_stream_t stream);
+mlpb_status mlpb_act8_grad(int32_t act, int64_t tokens, int64_t ffn, int32_t tp, const void *dA,
+                           const void *codes, const void *scales, void *dZ, void *A,
+                           mlpb_stream_t stream);
 
 /* Static English text of a status code. */
 const char *mlpb_status_str(mlpb_status s);

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/mlpb.h"
+#include "act8.cuh"
 #include "kernels.h"
 
 using namespace mlpb;
@@ -139,6 +140,7 @@ struct mlpb_handle {
   bool recompute;   // MLPB_FLAG_RECOMPUTE_ACT: the backward rewrites A from the saved Z
   bool fp8;         // MLPB_FLAG_FP8: E4M3 GEMMs, per-tensor power-of-two scales
   bool bf16_out;    // MLPB_FLAG_BF16_OUT: Y, dX (and the LN backward's dXn, dX) in bf16
+  bool ckpt8;       // MLPB_FLAG_CHECKPOINT8: Z (G, U) saved as 8-bit codes and scales
   bool emulate;     // MLPB_FLAG_EMULATE_COPIES: the SP gathers / scatters as device copies
   uint64_t wait_ns;
   int ln_blocks_per_shard;
@@ -249,8 +251,9 @@ mlpb_status run_gemm(mlpb_handle* h, GemmKind kind, bool fwd, const CUtensorMap&
   if (super_tiles == 0) return MLPB_OK;
   const int clusters = std::min(super_tiles, h->max_clusters);
   LaunchTimer lt(h, s, name, flops, bytes, p.split > 1 ? 2 : 1);
-  cudaError_t e = fwd ? launch_gemm_fwd(kind, a, b, p, clusters, s)
-                      : launch_gemm_bwd(kind, a, b, p, clusters, s);
+  cudaError_t e = p.codes != nullptr ? launch_gemm_ckpt8(kind, a, b, p, clusters, s)
+                  : fwd              ? launch_gemm_fwd(kind, a, b, p, clusters, s)
+                                     : launch_gemm_bwd(kind, a, b, p, clusters, s);
   if (e == cudaSuccess && p.split > 1) e = launch_split_fixup(p, s);
   lt.done();
   return from_cuda(e);
@@ -414,6 +417,10 @@ CopyLayout copy_layout(const mlpb_handle* h, void* workspace) {
   return CopyLayout{b, b + align256(2 * TH), b + 2 * align256(2 * TH)};
 }
 
+// Under MLPB_FLAG_CHECKPOINT8 Zsaved holds the codes [T][F1], then the scale bytes
+// [T][F1 / 32].
+size_t saved_codes_bytes(const mlpb_handle* h) { return static_cast<size_t>(h->T * h->F1); }
+
 size_t ws_total_bytes(const mlpb_handle* h) {
   return ws_base_bytes(h) + ws_f8_bytes(h) + ws_copy_bytes(h);
 }
@@ -444,7 +451,7 @@ mlpb_status mlpb_create(const mlpb_config* cfg, mlpb_handle** out) {
   if (c.seq_parallel_ln != 0 && c.seq_parallel_ln != 1) return MLPB_EINVAL;
   if ((c.flags & ~(MLPB_FLAG_FAULT_INJECT | MLPB_FLAG_ACCUMULATE_GRADS |
                    MLPB_FLAG_RECOMPUTE_ACT | MLPB_FLAG_FP8 | MLPB_FLAG_BF16_OUT |
-                   MLPB_FLAG_EMULATE_COPIES)) != 0)
+                   MLPB_FLAG_EMULATE_COPIES | MLPB_FLAG_CHECKPOINT8)) != 0)
     return MLPB_EINVAL;
   if (c.seq_parallel_ln && !(c.ln_eps > 0.f)) return MLPB_EINVAL;
   if ((c.flags & MLPB_FLAG_EMULATE_COPIES) && !c.seq_parallel_ln) return MLPB_EUNSUPPORTED;
@@ -454,6 +461,9 @@ mlpb_status mlpb_create(const mlpb_config* cfg, mlpb_handle** out) {
   if ((c.flags & MLPB_FLAG_FP8) &&
       ((c.ffn / c.tp) % 16 != 0 || (c.flags & MLPB_FLAG_RECOMPUTE_ACT)))
     return MLPB_EUNSUPPORTED;  // E4M3 rows must be 16-byte multiples for TMA
+  if ((c.flags & MLPB_FLAG_CHECKPOINT8) &&
+      ((c.ffn / c.tp) % 32 != 0 || (c.flags & MLPB_FLAG_FP8)))
+    return MLPB_EUNSUPPORTED;  // an epilogue's 32-column chunk is one block of codes
   if (c.seq_parallel_ln && (c.tokens % c.tp != 0 || c.hidden > 16384)) return MLPB_EUNSUPPORTED;
   const int64_t f1 = c.act == MLPB_ACT_SWIGLU ? 2 * c.ffn : c.ffn;
   // int32 tile/coordinate arithmetic inside the kernels
@@ -473,7 +483,8 @@ mlpb_status mlpb_create(const mlpb_config* cfg, mlpb_handle** out) {
   h->F1 = f1;
   h->fault_pending = (c.flags & MLPB_FLAG_FAULT_INJECT) != 0;
   h->accumulate = (c.flags & MLPB_FLAG_ACCUMULATE_GRADS) != 0;
-  h->recompute = (c.flags & MLPB_FLAG_RECOMPUTE_ACT) != 0;
+  h->ckpt8 = (c.flags & MLPB_FLAG_CHECKPOINT8) != 0;
+  h->recompute = h->ckpt8 || (c.flags & MLPB_FLAG_RECOMPUTE_ACT) != 0;
   h->fp8 = (c.flags & MLPB_FLAG_FP8) != 0;
   h->bf16_out = (c.flags & MLPB_FLAG_BF16_OUT) != 0;
   h->emulate = (c.flags & MLPB_FLAG_EMULATE_COPIES) != 0;
@@ -497,6 +508,7 @@ mlpb_status mlpb_create(const mlpb_config* cfg, mlpb_handle** out) {
   if (load_encoder() != MLPB_OK || gemm_fwd_set_smem_attrs() != cudaSuccess ||
       gemm_bwd_set_smem_attrs() != cudaSuccess ||
       (h->fp8 && gemm_f8_set_smem_attrs() != cudaSuccess) ||
+      (h->ckpt8 && gemm_ckpt8_set_smem_attrs() != cudaSuccess) ||
       cudaMalloc(reinterpret_cast<void**>(&h->d_err), sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_err, 0, sizeof(uint32_t)) != cudaSuccess) {
     if (h->d_err) cudaFree(h->d_err);
@@ -548,7 +560,8 @@ mlpb_status mlpb_workspace_size(const mlpb_handle* h, size_t* bytes) {
 
 mlpb_status mlpb_saved_size(const mlpb_handle* h, size_t* z_bytes, size_t* a_bytes) {
   if (h == nullptr || z_bytes == nullptr || a_bytes == nullptr) return MLPB_EINVAL;
-  *z_bytes = static_cast<size_t>(h->T * h->F1 * 2);
+  *z_bytes = h->ckpt8 ? saved_codes_bytes(h) + saved_codes_bytes(h) / kActBlock
+                      : static_cast<size_t>(h->T * h->F1 * 2);
   *a_bytes = static_cast<size_t>(h->T * h->F * 2);
   return MLPB_OK;
 }
@@ -697,6 +710,11 @@ static mlpb_status forward_core(mlpb_handle* h, const void* X, const void* W1, c
   p.num_kb = static_cast<int>(cdiv(H, kBK));
   p.out0 = Zsaved;
   p.out1 = Asaved;
+  if (h->ckpt8) {
+    p.codes = static_cast<uint8_t*>(Zsaved);
+    p.scales = p.codes + saved_codes_bytes(h);
+  }
+  const double zb = h->ckpt8 ? 1.0 + 1.0 / kActBlock : 2.0;  // bytes of a saved value
   p.fault_inject = h->fault_pending ? 1 : 0;
   h->fault_pending = false;
   p.raster_group = short_k_raster_group(h);
@@ -705,12 +723,12 @@ static mlpb_status forward_core(mlpb_handle* h, const void* X, const void* W1, c
     p.num_n_tiles = static_cast<int>(cdiv(F, kBN));
     p.bias = static_cast<const __nv_bfloat16*>(b1);
     st = run_gemm(h, GemmKind::FC1_GELU, true, ta1, tb1, p, s, "fc1_gelu", 2.0 * T * F * H,
-                  2.0 * (T * H + F * H + 2 * T * F) + (bias ? 2.0 * F : 0.0));
+                  2.0 * (T * H + F * H + T * F) + zb * T * F + (bias ? 2.0 * F : 0.0));
   } else {
     p.tiles_per_shard = static_cast<int>(cdiv(Fs, 128));
     p.num_n_tiles = static_cast<int>(t * p.tiles_per_shard);
     st = run_gemm(h, GemmKind::FC1_SWIGLU, true, ta1, tb1, p, s, "fc1_swiglu", 4.0 * T * F * H,
-                  2.0 * (T * H + 2 * F * H + 3 * T * F));
+                  2.0 * (T * H + 2 * F * H + T * F) + 2.0 * zb * T * F);
   }
   if (st != MLPB_OK) return st;
 
@@ -880,9 +898,14 @@ static mlpb_status backward_core(mlpb_handle* h, const void* X, const void* W1, 
     p.out0 = dZ;
     p.out1 = recompute ? Asaved : nullptr;
     p.colsum = bias ? part1 : nullptr;
+    if (h->ckpt8) {  // the epilogue only reads them
+      p.codes = static_cast<uint8_t*>(const_cast<void*>(Zsaved));
+      p.scales = p.codes + saved_codes_bytes(h);
+    }
+    const double zb = h->ckpt8 ? 1.0 + 1.0 / kActBlock : 2.0;
     st = run_gemm(h, h->swiglu ? GemmKind::DGRAD_SWIGLU : GemmKind::DGRAD_GELU, false, tdgA,
                   tdgB, p, s, h->swiglu ? "dgrad_swiglu" : "dgrad_gelu", 2.0 * T * F * H,
-                  2.0 * (T * H + F * H + 2 * T * F1) + (recompute ? 2.0 * T * F : 0.0) +
+                  2.0 * (T * H + F * H + T * F1) + zb * T * F1 + (recompute ? 2.0 * T * F : 0.0) +
                       (bias ? 4.0 * ws_db1_parts(h) * F : 0.0));
   }
   if (st == MLPB_OK && (cudaEventRecord(h->ev_dz, s) != cudaSuccess ||

@@ -28,6 +28,8 @@
 // a call, 128-byte = 128-element K-major rows, every operand K-major from its own or its
 // transposed E4M3 copy) and rescales each accumulator by 2^-(k_a + k_b) in the epilogue;
 // FC1 and DGRAD also record the amax of the bf16 A / dZ they write.
+// The Q8 instantiations of FC1 and DGRAD write and read the saved activations as 8-bit
+// checkpoints (act8.cuh): a thread's 32-column chunk of its row is one block of codes.
 //
 // The contractions (T tokens, H hidden, F ffn, t shards, Fs = F/t, F1 = F or 2F):
 //   FC1_GELU      Z = X W1^T + b1, A = gelu(Z)       M=T  N=F      K=H   A,B K-major
@@ -48,9 +50,11 @@
 //                 measured 11-20 % faster than this shape with MN-major operands)
 #pragma once
 
+#include "act8.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
 #include "gemm_params.h"
+#include "pointwise.cuh"
 
 namespace mlpb {
 
@@ -96,81 +100,6 @@ __device__ __forceinline__ void unit_range(int u, int split, int split_start, in
   part = j - (j / split) * split;
   kb0 = num_kb * part / split;
   kb1 = num_kb * (part + 1) / split;
-}
-
-// ------------------------------------------------------------------ pointwise math
-// tanh-form GELU written with s = sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3): since
-// 1 + tanh(u) = 2 sigmoid(2u), gelu(z) = z s, the same function without cancellation for
-// z << 0, and gelu'(z) = s + z s (1 - s) 2 sqrt(2/pi) (1 + 3 * 0.044715 z^2).  The
-// constants are folded so that e^{-2u} = 2^{z (a + b z^2)} is one base-2 exponential:
-//   a = -2k log2(e), b = -2k c log2(e),  k = sqrt(2/pi), c = 0.044715.
-// For |z| past ~10 the exponential overflows to +inf (s = 0) or underflows to 0 (s = 1),
-// and both forms then return their limits (0 and z; 0 and 1) with no inf * 0.
-constexpr float kSqrt2OverPi = 0.7978845608028654f;
-constexpr float kGeluCubic = 0.044715f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGeluA = -2.0f * kSqrt2OverPi * kLog2e;               // -2k log2(e)
-constexpr float kGeluB = -2.0f * kSqrt2OverPi * kGeluCubic * kLog2e;  // -2kc log2(e)
-constexpr float kGeluD0 = 2.0f * kSqrt2OverPi;                        // 2k
-constexpr float kGeluD2 = 6.0f * kSqrt2OverPi * kGeluCubic;           // 6kc
-
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
-
-// 2^x (the MUFU base-2 exponential; subnormal results flush to zero).
-__device__ __forceinline__ float ex2_f(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Two fp32 values in one 64-bit register (lo in the low half) and the f32x2 arithmetic
-// of the sm_100 family: one instruction for both lanes, each rounded as its fp32 form.
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
-// e^{-2u} + 1 for two values of z (one MUFU exponential each), and its reciprocal s.
-__device__ __forceinline__ uint64_t gelu_s_x2(uint64_t z, uint64_t z2) {
-  float u0, u1, d0, d1;
-  f2_unpack(f2_mul(z, f2_fma(z2, f2_pack(kGeluB, kGeluB), f2_pack(kGeluA, kGeluA))), u0, u1);
-  f2_unpack(f2_add(f2_pack(ex2_f(u0), ex2_f(u1)), f2_pack(1.0f, 1.0f)), d0, d1);
-  return f2_pack(__fdividef(1.0f, d0), __fdividef(1.0f, d1));
-}
-
-// gelu(z) = z s for two values.
-__device__ __forceinline__ uint64_t gelu_x2(uint64_t z) { return f2_mul(z, gelu_s_x2(z, f2_mul(z, z))); }
-
-// gelu'(z) = s + d s (1 - s), d = 2k z (1 + 3c z^2), for two values.
-__device__ __forceinline__ uint64_t gelu_grad_x2(uint64_t z) {
-  const uint64_t z2 = f2_mul(z, z);
-  const uint64_t s = gelu_s_x2(z, z2);
-  const uint64_t d = f2_mul(z, f2_fma(z2, f2_pack(kGeluD2, kGeluD2), f2_pack(kGeluD0, kGeluD0)));
-  return f2_fma(d, f2_sub(s, f2_mul(s, s)), s);
 }
 
 // v[e] = gelu(v[e]) over 32 values, two at a time.
@@ -230,6 +159,40 @@ __device__ __forceinline__ void store_f32x32(float* p, int nvalid, const float (
                            __float_as_uint(v[q * 4 + 2]), __float_as_uint(v[q * 4 + 3]));
       st_global_v4(p + q * 4, u);
     }
+  }
+}
+
+// 8-bit checkpoint of a chunk: the bf16 roundings of v as one block of 32 codes at `codes`
+// and its scale byte.  A thread's chunk is exactly one block, so no lane talks to another.
+__device__ __forceinline__ void store_act8x32(uint8_t* codes, uint8_t* scale,
+                                              const float (&v)[32]) {
+  uint32_t w[16], m = 0u, q[8];
+  pack_bf16x32(v, w);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = absmax_bf16x2(m, w[e]);
+  const uint32_t sb = act8_scale_byte(max(m & 0xffffu, m >> 16));
+  const float f = act8_to_codes(sb);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 a = unpack_bf16x2(w[2 * e]), b = unpack_bf16x2(w[2 * e + 1]);
+    q[e] = act8_pack4(a.x, a.y, b.x, b.y, f);
+  }
+  st_global_v4(codes, make_uint4(q[0], q[1], q[2], q[3]));
+  st_global_v4(codes + 16, make_uint4(q[4], q[5], q[6], q[7]));
+  *scale = static_cast<uint8_t>(sb);
+}
+
+__device__ __forceinline__ void load_act8x32(const uint8_t* codes, const uint8_t* scale,
+                                             float (&v)[32]) {
+  const uint4 a = ld_global_nc_v4(codes), b = ld_global_nc_v4(codes + 16);
+  const float s = act8_step(__ldg(scale));
+  const uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float t[4];
+    act8_unpack4(q[e], s, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * e + i] = t[i];
   }
 }
 
@@ -293,8 +256,9 @@ __device__ __forceinline__ void track_amax(const float (&v)[32], int nv, float& 
 
 // Epilogue of one 128 x 256 tile for the calling thread's row.  `tacc` is the TMEM
 // address of the accumulator at this warp's lane quarter.  All branches that skip
-// tcgen05.ld are uniform across the warp.
-template <GemmKind K, bool F8 = false>
+// tcgen05.ld are uniform across the warp.  Q8: the saved Z (or G, U) is an 8-bit checkpoint
+// (p.codes, p.scales) instead of bf16; every chunk is then a whole block (Fs % 32 == 0).
+template <GemmKind K, bool F8 = false, bool Q8 = false>
 __device__ __forceinline__ void epilogue_tile(uint32_t tacc, int row, int mt, int nt,
                                               const GemmParams& p, float sc, float& am) {
   const int m = mt * kBM + row;
@@ -317,7 +281,13 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tacc, int row, int mt, in
         for (int e = 0; e < 32; e += 2)
           f2_unpack(f2_add(f2_pack(v[e], v[e + 1]), f2_pack(b[e], b[e + 1])), v[e], v[e + 1]);
       }
-      if (row_ok) store_bf16x32(Z + col, nv, v);
+      if constexpr (Q8) {
+        if (row_ok)
+          store_act8x32(p.codes + static_cast<size_t>(m) * p.F + col,
+                        p.scales + (static_cast<size_t>(m) * p.F + col) / kActBlock, v);
+      } else {
+        if (row_ok) store_bf16x32(Z + col, nv, v);
+      }
       gelu_x32(v);
       if (row_ok) {
         store_bf16x32(A + col, nv, v);
@@ -339,7 +309,13 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tacc, int row, int mt, in
       load_acc<F8>(tacc + c * 32, g, sc);
       load_acc<F8>(tacc + 128 + c * 32, u, sc);
       const int nv = min(32, p.Fs - jc);
-      if (row_ok) {
+      if constexpr (Q8) {
+        if (row_ok) {
+          const size_t o = (static_cast<size_t>(m) * p.F + static_cast<size_t>(i) * p.Fs) * 2 + jc;
+          store_act8x32(p.codes + o, p.scales + o / kActBlock, g);
+          store_act8x32(p.codes + o + p.Fs, p.scales + (o + p.Fs) / kActBlock, u);
+        }
+      } else if (row_ok) {
         store_bf16x32(GU + jc, nv, g);
         store_bf16x32(GU + p.Fs + jc, nv, u);
       }
@@ -404,7 +380,10 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tacc, int row, int mt, in
         uint32_t w[16];  // the stored bf16 dZ, two to a word
         if (row_ok) {
           float z[32];
-          load_bf16x32(p.aux + o, nv, z);
+          if constexpr (Q8)
+            load_act8x32(p.codes + o, p.scales + o / kActBlock, z);
+          else
+            load_bf16x32(p.aux + o, nv, z);
           if (A != nullptr) {
             float a[32];
 #pragma unroll
@@ -439,8 +418,13 @@ __device__ __forceinline__ void epilogue_tile(uint32_t tacc, int row, int mt, in
         const int i = f / p.Fs;
         const size_t o = static_cast<size_t>(m) * 2 * p.F + f + static_cast<size_t>(i) * p.Fs;
         float g[32], u[32];
-        load_bf16x32(p.aux + o, nv, g);
-        load_bf16x32(p.aux + o + p.Fs, nv, u);
+        if constexpr (Q8) {
+          load_act8x32(p.codes + o, p.scales + o / kActBlock, g);
+          load_act8x32(p.codes + o + p.Fs, p.scales + (o + p.Fs) / kActBlock, u);
+        } else {
+          load_bf16x32(p.aux + o, nv, g);
+          load_bf16x32(p.aux + o + p.Fs, nv, u);
+        }
         if (A != nullptr) {
           float a[32];
 #pragma unroll
@@ -664,7 +648,7 @@ __device__ __forceinline__ void issue_stage_pair(const CUtensorMap* tA, const CU
   }
 }
 
-template <GemmKind K, bool F8 = false>
+template <GemmKind K, bool F8 = false, bool Q8 = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB, const GemmParams p) {
@@ -897,7 +881,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           store_f32x32(P + c * 32, 32, v);
         }
       } else {
-        epilogue_tile<K, F8>(tacc, row, mp * 2 + rank, nt, p, sc, am);
+        epilogue_tile<K, F8, Q8>(tacc, row, mp * 2 + rank, nt, p, sc, am);
       }
       if constexpr (F8) {
         if (p.amax_out != nullptr) {  // non-negative floats order like their bit patterns

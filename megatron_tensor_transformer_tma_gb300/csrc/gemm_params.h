@@ -76,6 +76,9 @@ struct GemmParams {
   // MN-major operands loaded through a 3-D map, one box of both 64-wide chunks a stage:
   // bit 0 A, bit 1 B (else two 2-D boxes).
   int mn3d;
+  // 8-bit checkpoints (FC1_*, DGRAD_*): codes [T][F1] and their scale bytes [T][F1 / 32]
+  uint8_t* codes;
+  uint8_t* scales;
 };
 
 // FP8 stage: the same 16 KB A and B-half tiles, 128 one-byte elements deep.

@@ -22,6 +22,10 @@ cudaError_t launch_split_fixup(const GemmParams& p, cudaStream_t s);
 cudaError_t gemm_f8_set_smem_attrs();
 cudaError_t launch_gemm_f8(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
                            const GemmParams& p, int clusters, cudaStream_t s);
+// gemm_ckpt8.cu: FC1 and DGRAD with the saved activations as 8-bit checkpoints.
+cudaError_t gemm_ckpt8_set_smem_attrs();
+cudaError_t launch_gemm_ckpt8(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
+                              const GemmParams& p, int clusters, cudaStream_t s);
 cudaError_t launch_gemm_fwd(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
                             const GemmParams& p, int clusters, cudaStream_t s);
 cudaError_t launch_gemm_bwd(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,

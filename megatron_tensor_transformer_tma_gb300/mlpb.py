@@ -31,6 +31,9 @@ MLPB_FLAG_RECOMPUTE_ACT = 0x4
 MLPB_FLAG_FP8 = 0x8
 MLPB_FLAG_BF16_OUT = 0x10
 MLPB_FLAG_EMULATE_COPIES = 0x20
+MLPB_FLAG_CHECKPOINT8 = 0x100
+
+ACT8_BLOCK = 32  # features that share a scale byte of an 8-bit activation checkpoint
 
 # Every symbol include/mlpb.h declares.
 EXPORTED = (
@@ -38,6 +41,7 @@ EXPORTED = (
     "mlpb_backward", "mlpb_layernorm_sp_fwd", "mlpb_layernorm_sp_bwd", "mlpb_last_device_error",
     "mlpb_enable_timing", "mlpb_read_timings", "mlpb_status_str", "mlpb_bias_grad_noalloc",
     "mlpb_branch_forward", "mlpb_branch_backward", "mlpb_quantize_e4m3",
+    "mlpb_act8_scales", "mlpb_act8_save", "mlpb_act8_grad",
 )
 
 
@@ -73,6 +77,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "(the MLP block has no non-CUDA implementation)")
     lib = ctypes.CDLL(path)
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    I32, I64 = ctypes.c_int32, ctypes.c_int64
     H = ctypes.c_void_p
     sig = {
         "mlpb_create": (I, [ctypes.POINTER(mlpb_config), ctypes.POINTER(H)]),
@@ -92,6 +97,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mlpb_branch_backward": (I, [H] + [P] * 19),
         "mlpb_quantize_e4m3": (I, [P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P, P, P,
                                    P]),
+        "mlpb_act8_scales": (I, [I32, I64, I32, ctypes.POINTER(I64)]),
+        "mlpb_act8_save": (I, [I32, I64, I64, I32] + [P] * 5),
+        "mlpb_act8_grad": (I, [I32, I64, I64, I32] + [P] * 6),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -124,6 +132,48 @@ def _ptr(t, dtype=None, shape=None, name="tensor"):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _arg(t, dtype, shape, name, dev):
+    """The data pointer of a contiguous CUDA tensor of this dtype and shape on CUDA device
+    number `dev` (None passes)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, other tensors on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _cuda_index(t, name):
+    """The CUDA device number that a call's tensors live on, taken from its first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call_on(dev, name, args, stream):
+    """Calls a library function with `args` and a stream (None: the current one of device
+    `dev`), with that device current: the library launches on the current device."""
+    fn = getattr(load_library(), name)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    s = s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, s), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s), name)
 
 
 def _stream(stream):
@@ -185,15 +235,23 @@ def _w1_shape(c):
     return (c.tp, 2, fs, c.hidden) if c.act == MLPB_ACT_SWIGLU else (c.tp, fs, c.hidden)
 
 
+def _saved_z(h: Handle):
+    """(dtype, shape) of Zsaved: bf16 [T][F1], or the bytes of an 8-bit checkpoint."""
+    c = h.cfg
+    f1 = 2 * c.ffn if c.act == MLPB_ACT_SWIGLU else c.ffn
+    if c.flags & MLPB_FLAG_CHECKPOINT8:
+        return torch.uint8, (c.tokens * f1 + c.tokens * f1 // ACT8_BLOCK,)
+    return torch.bfloat16, (c.tokens, f1)
+
+
 def mlpb_forward(h: Handle, X, W1, b1, W2, b2, Y, Zsaved, Asaved, workspace=None, stream=None):
     c = h.cfg
     T, Hd, F, t = c.tokens, c.hidden, c.ffn, c.tp
     bf = torch.bfloat16
-    f1 = 2 * F if c.act == MLPB_ACT_SWIGLU else F
     args = [
         _ptr(X, bf, (T, Hd), "X"), _ptr(W1, bf, _w1_shape(c), "W1"), _ptr(b1, bf, (F,), "b1"),
         _ptr(W2, bf, (t, Hd, F // t), "W2"), _ptr(b2, bf, (Hd,), "b2"),
-        _ptr(Y, out_dtype(c), (T, Hd), "Y"), _ptr(Zsaved, bf, (T, f1), "Zsaved"),
+        _ptr(Y, out_dtype(c), (T, Hd), "Y"), _ptr(Zsaved, *_saved_z(h), "Zsaved"),
         _ptr(Asaved, bf, (T, F), "Asaved"), _ptr(workspace, None, None, "workspace"),
     ]
     _check(load_library().mlpb_forward(h.ptr, *args, _stream(stream)), "mlpb_forward")
@@ -204,10 +262,9 @@ def mlpb_backward(h: Handle, X, W1, W2, Zsaved, Asaved, dY, dX, dW1, dW2, db1, d
     c = h.cfg
     T, Hd, F, t = c.tokens, c.hidden, c.ffn, c.tp
     bf, f32 = torch.bfloat16, torch.float32
-    f1 = 2 * F if c.act == MLPB_ACT_SWIGLU else F
     args = [
         _ptr(X, bf, (T, Hd), "X"), _ptr(W1, bf, _w1_shape(c), "W1"),
-        _ptr(W2, bf, (t, Hd, F // t), "W2"), _ptr(Zsaved, bf, (T, f1), "Zsaved"),
+        _ptr(W2, bf, (t, Hd, F // t), "W2"), _ptr(Zsaved, *_saved_z(h), "Zsaved"),
         _ptr(Asaved, bf, (T, F), "Asaved"), _ptr(dY, bf, (T, Hd), "dY"),
         _ptr(dX, out_dtype(c), (T, Hd), "dX"), _ptr(dW1, f32, _w1_shape(c), "dW1"),
         _ptr(dW2, f32, (t, Hd, F // t), "dW2"), _ptr(db1, f32, (F,), "db1"),
@@ -246,14 +303,13 @@ def mlpb_branch_forward(h: Handle, X, gamma, beta, W1, b1, W2, b2, Y, Xn, mean, 
     c = h.cfg
     T, Hd, F, t = c.tokens, c.hidden, c.ffn, c.tp
     bf, f32 = torch.bfloat16, torch.float32
-    f1 = 2 * F if c.act == MLPB_ACT_SWIGLU else F
     args = [
         _ptr(X, bf, (T, Hd), "X"), _ptr(gamma, bf, (Hd,), "gamma"), _ptr(beta, bf, (Hd,), "beta"),
         _ptr(W1, bf, _w1_shape(c), "W1"), _ptr(b1, bf, (F,), "b1"),
         _ptr(W2, bf, (t, Hd, F // t), "W2"), _ptr(b2, bf, (Hd,), "b2"),
         _ptr(Y, out_dtype(c), (T, Hd), "Y"), _ptr(Xn, bf, (T, Hd), "Xn"),
         _ptr(mean, f32, (T,), "mean"),
-        _ptr(rstd, f32, (T,), "rstd"), _ptr(Zsaved, bf, (T, f1), "Zsaved"),
+        _ptr(rstd, f32, (T,), "rstd"), _ptr(Zsaved, *_saved_z(h), "Zsaved"),
         _ptr(Asaved, bf, (T, F), "Asaved"), _ptr(workspace, None, None, "workspace"),
     ]
     _check(load_library().mlpb_branch_forward(h.ptr, *args, _stream(stream)),
@@ -265,12 +321,11 @@ def mlpb_branch_backward(h: Handle, X, gamma, W1, W2, Xn, mean, rstd, Zsaved, As
     c = h.cfg
     T, Hd, F, t = c.tokens, c.hidden, c.ffn, c.tp
     bf, f32 = torch.bfloat16, torch.float32
-    f1 = 2 * F if c.act == MLPB_ACT_SWIGLU else F
     args = [
         _ptr(X, bf, (T, Hd), "X"), _ptr(gamma, bf, (Hd,), "gamma"),
         _ptr(W1, bf, _w1_shape(c), "W1"), _ptr(W2, bf, (t, Hd, F // t), "W2"),
         _ptr(Xn, bf, (T, Hd), "Xn"), _ptr(mean, f32, (T,), "mean"), _ptr(rstd, f32, (T,), "rstd"),
-        _ptr(Zsaved, bf, (T, f1), "Zsaved"), _ptr(Asaved, bf, (T, F), "Asaved"),
+        _ptr(Zsaved, *_saved_z(h), "Zsaved"), _ptr(Asaved, bf, (T, F), "Asaved"),
         _ptr(dY, bf, (T, Hd), "dY"), _ptr(dX, out_dtype(c), (T, Hd), "dX"),
         _ptr(dW1, f32, _w1_shape(c), "dW1"), _ptr(dW2, f32, (t, Hd, F // t), "dW2"),
         _ptr(db1, f32, (F,), "db1"), _ptr(db2, f32, (Hd,), "db2"),
@@ -298,6 +353,52 @@ def mlpb_quantize_e4m3(inp, q=None, qt=None, amax=None, scale_exp=None, stream=N
             _ptr(amax, torch.int32, (1,), "amax"), _ptr(scale_exp, torch.int32, (1,), "scale_exp")]
     _check(load_library().mlpb_quantize_e4m3(*args, _stream(stream)), "mlpb_quantize_e4m3")
     return amax, scale_exp
+
+
+_ACTS = {"gelu": MLPB_ACT_GELU_TANH, "swiglu": MLPB_ACT_SWIGLU}
+
+
+def mlpb_act8_scales(act, ffn, tp=1) -> int:
+    """Scale bytes of a row of an 8-bit activation checkpoint (act: "gelu" or "swiglu")."""
+    n = ctypes.c_int64()
+    _check(load_library().mlpb_act8_scales(_ACTS[act], ffn, tp, ctypes.byref(n)),
+           "mlpb_act8_scales")
+    return n.value
+
+
+def mlpb_act8_save(act, Z, A, codes, scales, tp=1, stream=None):
+    """Saves fc1's bf16 output Z ([T][F], or [T][2F] as [T][tp][2][Fs] for "swiglu") as int8
+    codes (Z's shape) and uint8 scales [T][mlpb_act8_scales()], and writes A = act(Z) [T][F]
+    bf16 unless A is None."""
+    dev = _cuda_index(Z, "Z")
+    if Z.dim() != 2:
+        raise ValueError(f"Z: expected [tokens][features], got {tuple(Z.shape)}")
+    T, f1 = Z.shape
+    F = f1 // 2 if act == "swiglu" else f1
+    f1 = 2 * F if act == "swiglu" else F  # an odd width fails Z's shape check
+    nb = mlpb_act8_scales(act, F, tp)
+    args = [_ACTS[act], T, F, tp, _arg(Z, torch.bfloat16, (T, f1), "Z", dev),
+            _arg(A, torch.bfloat16, (T, F), "A", dev),
+            _arg(codes, torch.int8, (T, f1), "codes", dev),
+            _arg(scales, torch.uint8, (T, nb), "scales", dev)]
+    _call_on(dev, "mlpb_act8_save", args, stream)
+
+
+def mlpb_act8_grad(act, dA, codes, scales, dZ, A=None, tp=1, stream=None):
+    """dZ = dA act'(z) (bf16, codes' shape) for the values z that an 8-bit checkpoint stands
+    for, and A = act(z) [T][F] bf16 unless A is None; dA [T][F] bf16."""
+    dev = _cuda_index(dA, "dA")
+    if dA.dim() != 2:
+        raise ValueError(f"dA: expected [tokens][features], got {tuple(dA.shape)}")
+    T, F = dA.shape
+    f1 = 2 * F if act == "swiglu" else F
+    nb = mlpb_act8_scales(act, F, tp)
+    args = [_ACTS[act], T, F, tp, _arg(dA, torch.bfloat16, (T, F), "dA", dev),
+            _arg(codes, torch.int8, (T, f1), "codes", dev),
+            _arg(scales, torch.uint8, (T, nb), "scales", dev),
+            _arg(dZ, torch.bfloat16, (T, f1), "dZ", dev),
+            _arg(A, torch.bfloat16, (T, F), "A", dev)]
+    _call_on(dev, "mlpb_act8_grad", args, stream)
 
 
 def mlpb_last_device_error(h: Handle, stream=None) -> int:
@@ -346,9 +447,9 @@ class MLPBlock:
                                flags)
         self.handle = mlpb_create(self.cfg)
         self.device = torch.device(device)
-        f1 = 2 * ffn if act == "swiglu" else ffn
         self.act = act
-        self.Z = torch.empty((tokens, f1), dtype=torch.bfloat16, device=self.device)
+        z_dtype, z_shape = _saved_z(self.handle)
+        self.Z = torch.empty(z_shape, dtype=z_dtype, device=self.device)
         self.A = torch.empty((tokens, ffn), dtype=torch.bfloat16, device=self.device)
         self.workspace = torch.empty(mlpb_workspace_size(self.handle), dtype=torch.uint8,
                                      device=self.device)
@@ -423,3 +524,34 @@ class MLPBranch(MLPBlock):
                              self.A, dY, g["dX"], g["dW1"], g["dW2"], g["db1"], g["db2"],
                              g["dgamma"], g["dbeta"], self.workspace, stream)
         return g
+
+
+class ActCheckpoint8:
+    """An activation whose input is kept for the backward as 8-bit codes: save() in the
+    forward returns A = act(Z), grad() in the backward returns dZ and A again.  Owns the codes
+    and scales of one [tokens][ffn] activation (tp shards), the only memory that has to live
+    between the two."""
+
+    def __init__(self, tokens, ffn, tp=1, act="gelu", device="cuda"):
+        self.tokens, self.ffn, self.tp, self.act = tokens, ffn, tp, act
+        self.device = torch.device(device)
+        self.width = 2 * ffn if act == "swiglu" else ffn
+        self.codes = torch.empty((tokens, self.width), dtype=torch.int8, device=self.device)
+        self.scales = torch.empty((tokens, mlpb_act8_scales(act, ffn, tp)), dtype=torch.uint8,
+                                  device=self.device)
+
+    def _new(self, width):
+        return torch.empty((self.tokens, width), dtype=torch.bfloat16, device=self.device)
+
+    def save(self, Z, A=None, stream=None):
+        A = self._new(self.ffn) if A is None else A
+        mlpb_act8_save(self.act, Z, A, self.codes, self.scales, self.tp, stream)
+        return A
+
+    def grad(self, dA, dZ=None, A=None, codes=None, scales=None, stream=None):
+        """(dZ, A); codes and scales other than the ones this object holds may be given."""
+        dZ = self._new(self.width) if dZ is None else dZ
+        A = self._new(self.ffn) if A is None else A
+        mlpb_act8_grad(self.act, dA, self.codes if codes is None else codes,
+                       self.scales if scales is None else scales, dZ, A, self.tp, stream)
+        return dZ, A
