@@ -349,6 +349,70 @@ mlpb_status mlpb_act8_grad(int32_t act, int64_t tokens, int64_t ffn, int32_t tp,
                            const void *codes, const void *scales, void *dZ, void *A,
                            mlpb_stream_t stream);
 
+/* The join between two blocks of a transformer's residual stream, in one pass each way: the
+ * norm after a block, its gate, the residual scale, the sum, and the norm before the next
+ * block ("The Transformer Stack": norms, residual connections around each branch).
+ *     P    = norm_post(Y)                          (P = Y with MLPB_NORM_NONE)
+ *     Xout = res_scale * X + gate[group] * P       (gate, res_scale: 1 where absent)
+ *     Xn   = norm_pre(Xout)                        (not written with MLPB_NORM_NONE)
+ * LAYER: (x - mean) / sqrt(var + eps) * gamma + beta, biased variance;  RMS: x / sqrt(mean x^2
+ * + eps) * gamma, no beta.  norm_pre is that of Xout as stored.  A gate is one [hidden] row
+ * for each of gate_groups contiguous row blocks of tokens / gate_groups rows (1: one gate for
+ * all; the number of sequences: one for each; tokens: one for each token).
+ * Without a block (has_block 0) the call is norm_pre alone, Xn = norm_pre(X): the norm in front
+ * of a first block. */
+typedef enum { MLPB_NORM_NONE = 0, MLPB_NORM_LAYER = 1, MLPB_NORM_RMS = 2 } mlpb_norm;
+
+/* mlpb_join_config.flags */
+#define MLPB_JOIN_STREAM_F32 0x1u       /* X, Xout, dXout, dX are fp32 (else bf16)           */
+#define MLPB_JOIN_BLOCK_F32 0x2u        /* Y, dXn are fp32 (else bf16)                       */
+#define MLPB_JOIN_ACCUMULATE_GRADS 0x4u /* parameter gradients are added into, as under      \
+                                           MLPB_FLAG_ACCUMULATE_GRADS                        */
+
+typedef struct {
+  int64_t tokens;      /* rows (0 allowed), below 2^31                                       */
+  int64_t hidden;      /* a multiple of 8, at most 16384                                     */
+  int64_t gate_groups; /* 0: no gate; else a divisor of tokens                               */
+  int32_t has_block;   /* 0: norm_pre alone (no post norm, gate or residual scale then)      */
+  int32_t post_norm;   /* mlpb_norm                                                          */
+  int32_t pre_norm;    /* mlpb_norm                                                          */
+  float eps;           /* of both norms, inside the root                                     */
+  uint32_t flags;      /* MLPB_JOIN_*                                                        */
+} mlpb_join_config;
+
+/* Bytes of the workspace of mlpb_join_bwd on the current device (the parameter gradients'
+ * partial sums). */
+mlpb_status mlpb_join_workspace_size(const mlpb_join_config *cfg, size_t *bytes);
+
+/* Forward.  X, Y [tokens][hidden]; res_scale one fp32 on the device, or NULL; gate
+ * [gate_groups][hidden], gamma_* and beta_* [hidden] bf16, given exactly where the
+ * configuration has them; Xout like X; Xn bf16; stats [tokens][4] fp32: mean and 1/sqrt(...)
+ * of Y's row, then of Xout's (zeros where there is no norm; the mean of an RMS norm is 0), for
+ * the backward.  Xout may be X's buffer; no other output may overlap an input.  Without a
+ * block Y, Xout and res_scale are NULL.  No workspace; 16-byte aligned tensors. */
+mlpb_status mlpb_join_fwd(const mlpb_join_config *cfg, const void *X, const void *Y,
+                          const float *res_scale, const void *gate, const void *gamma_post,
+                          const void *beta_post, const void *gamma_pre, const void *beta_pre,
+                          void *Xout, void *Xn, float *stats, mlpb_stream_t stream);
+
+/* Backward, for the gradients dXout of Xout (NULL: zero, with a pre norm) and dXn of Xn (NULL
+ * without a pre norm):
+ *     dh = dXout + norm_pre'(dXn),  dX = res_scale dh,  dY = norm_post'(gate dh)  (dY bf16)
+ * and, in fp32, dres_scale (one value), dgate [gate_groups][hidden], dgamma_*, dbeta_*
+ * [hidden], each given exactly where its parameter is.  Sums run in a fixed order: the same
+ * bits every run.  Xout and stats are the forward's (without a block Xout is X itself, and X,
+ * Y, dY are NULL).  Y is read with a post norm or a gate, X with a res_scale; either may be
+ * NULL otherwise.  dX may be dXout's buffer; no other output may overlap an input.  tokens =
+ * 0 writes zero parameter gradients.  `workspace`: mlpb_join_workspace_size() bytes, not
+ * shared by calls that overlap. */
+mlpb_status mlpb_join_bwd(const mlpb_join_config *cfg, const void *X, const void *Y,
+                          const void *Xout, const float *stats, const float *res_scale,
+                          const void *gate, const void *gamma_post, const void *beta_post,
+                          const void *gamma_pre, const void *dXout, const void *dXn, void *dX,
+                          void *dY, float *dres_scale, float *dgate, float *dgamma_post,
+                          float *dbeta_post, float *dgamma_pre, float *dbeta_pre,
+                          void *workspace, mlpb_stream_t stream);
+
 /* Static English text of a status code. */
 const char *mlpb_status_str(mlpb_status s);
 

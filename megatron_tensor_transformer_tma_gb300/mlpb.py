@@ -33,6 +33,12 @@ MLPB_FLAG_BF16_OUT = 0x10
 MLPB_FLAG_EMULATE_COPIES = 0x20
 MLPB_FLAG_CHECKPOINT8 = 0x100
 
+MLPB_NORM_NONE = 0
+MLPB_NORM_LAYER = 1
+MLPB_NORM_RMS = 2
+MLPB_JOIN_STREAM_F32 = 0x1
+MLPB_JOIN_BLOCK_F32 = 0x2
+MLPB_JOIN_ACCUMULATE_GRADS = 0x4
 ACT8_BLOCK = 32  # features that share a scale byte of an 8-bit activation checkpoint
 
 # Every symbol include/mlpb.h declares.
@@ -42,6 +48,7 @@ EXPORTED = (
     "mlpb_enable_timing", "mlpb_read_timings", "mlpb_status_str", "mlpb_bias_grad_noalloc",
     "mlpb_branch_forward", "mlpb_branch_backward", "mlpb_quantize_e4m3",
     "mlpb_act8_scales", "mlpb_act8_save", "mlpb_act8_grad",
+    "mlpb_join_workspace_size", "mlpb_join_fwd", "mlpb_join_bwd",
 )
 
 
@@ -50,6 +57,14 @@ class mlpb_config(ctypes.Structure):
         ("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("ffn", ctypes.c_int64),
         ("tp", ctypes.c_int32), ("act", ctypes.c_int32), ("has_bias", ctypes.c_int32),
         ("seq_parallel_ln", ctypes.c_int32), ("ln_eps", ctypes.c_float), ("flags", ctypes.c_uint32),
+    ]
+
+
+class mlpb_join_config(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("gate_groups", ctypes.c_int64),
+        ("has_block", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+        ("pre_norm", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32),
     ]
 
 
@@ -100,6 +115,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mlpb_act8_scales": (I, [I32, I64, I32, ctypes.POINTER(I64)]),
         "mlpb_act8_save": (I, [I32, I64, I64, I32] + [P] * 5),
         "mlpb_act8_grad": (I, [I32, I64, I64, I32] + [P] * 6),
+        "mlpb_join_workspace_size": (I, [ctypes.POINTER(mlpb_join_config), ctypes.POINTER(Z)]),
+        "mlpb_join_fwd": (I, [ctypes.POINTER(mlpb_join_config)] + [P] * 12),
+        "mlpb_join_bwd": (I, [ctypes.POINTER(mlpb_join_config)] + [P] * 21),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -401,6 +419,92 @@ def mlpb_act8_grad(act, dA, codes, scales, dZ, A=None, tp=1, stream=None):
     _call_on(dev, "mlpb_act8_grad", args, stream)
 
 
+_NORMS = {"none": MLPB_NORM_NONE, "layer": MLPB_NORM_LAYER, "rms": MLPB_NORM_RMS}
+
+
+def make_join_config(tokens, hidden, post_norm="none", pre_norm="none", gate_groups=0, eps=1e-5,
+                     stream_dtype=torch.bfloat16, block_dtype=torch.bfloat16, accumulate=False,
+                     has_block=True) -> mlpb_join_config:
+    """Norms by name ("none", "layer", "rms"); dtypes torch.bfloat16 or torch.float32."""
+    for t in (stream_dtype, block_dtype):
+        if t not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"join: tensors are bfloat16 or float32, not {t}")
+    flags = ((MLPB_JOIN_STREAM_F32 if stream_dtype == torch.float32 else 0)
+             | (MLPB_JOIN_BLOCK_F32 if block_dtype == torch.float32 else 0)
+             | (MLPB_JOIN_ACCUMULATE_GRADS if accumulate else 0))
+    return mlpb_join_config(tokens, hidden, gate_groups, 1 if has_block else 0,
+                            _NORMS[post_norm], _NORMS[pre_norm], eps, flags)
+
+
+def _join_types(c):
+    return (torch.float32 if c.flags & MLPB_JOIN_STREAM_F32 else torch.bfloat16,
+            torch.float32 if c.flags & MLPB_JOIN_BLOCK_F32 else torch.bfloat16)
+
+
+def mlpb_join_workspace_size(cfg: mlpb_join_config) -> int:
+    """Bytes of mlpb_join_bwd's workspace on the current CUDA device."""
+    n = ctypes.c_size_t()
+    _check(load_library().mlpb_join_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "mlpb_join_workspace_size")
+    return n.value
+
+
+def mlpb_join_fwd(cfg, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre, Xout, Xn,
+                  stats, stream=None):
+    """The join between two blocks (include/mlpb.h): Xout = res_scale X + gate norm_post(Y),
+    Xn = norm_pre(Xout), and the rows' statistics for the backward."""
+    dev = _cuda_index(X, "X")
+    T, H = cfg.tokens, cfg.hidden
+    bf, f32 = torch.bfloat16, torch.float32
+    xt, yt = _join_types(cfg)
+    row, vec = (T, H), (H,)
+    args = [ctypes.byref(cfg), _arg(X, xt, row, "X", dev), _arg(Y, yt, row, "Y", dev),
+            _arg(res_scale, f32, (1,), "res_scale", dev),
+            _arg(gate, bf, (cfg.gate_groups, H), "gate", dev),
+            _arg(gamma_post, bf, vec, "gamma_post", dev),
+            _arg(beta_post, bf, vec, "beta_post", dev),
+            _arg(gamma_pre, bf, vec, "gamma_pre", dev), _arg(beta_pre, bf, vec, "beta_pre", dev),
+            _arg(Xout, xt, row, "Xout", dev), _arg(Xn, bf, row, "Xn", dev),
+            _arg(stats, f32, (T, 4), "stats", dev)]
+    _call_on(dev, "mlpb_join_fwd", args, stream)
+
+
+def mlpb_join_bwd(cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post, gamma_pre, dXout,
+                  dXn, dX, dY, dres_scale, dgate, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre,
+                  workspace, stream=None):
+    """Backward of mlpb_join_fwd for the gradients dXout and dXn of its outputs."""
+    dev = _cuda_index(dX, "dX")
+    T, H = cfg.tokens, cfg.hidden
+    bf, f32 = torch.bfloat16, torch.float32
+    xt, yt = _join_types(cfg)
+    row, vec, gates = (T, H), (H,), (cfg.gate_groups, H)
+    if workspace is not None and workspace.numel() * workspace.element_size() < _join_ws(cfg, dev):
+        raise ValueError("workspace: smaller than mlpb_join_workspace_size()")
+    args = [ctypes.byref(cfg), _arg(X, xt, row, "X", dev), _arg(Y, yt, row, "Y", dev),
+            _arg(Xout, xt, row, "Xout", dev), _arg(stats, f32, (T, 4), "stats", dev),
+            _arg(res_scale, f32, (1,), "res_scale", dev), _arg(gate, bf, gates, "gate", dev),
+            _arg(gamma_post, bf, vec, "gamma_post", dev),
+            _arg(beta_post, bf, vec, "beta_post", dev),
+            _arg(gamma_pre, bf, vec, "gamma_pre", dev), _arg(dXout, xt, row, "dXout", dev),
+            _arg(dXn, yt, row, "dXn", dev), _arg(dX, xt, row, "dX", dev),
+            _arg(dY, bf, row, "dY", dev), _arg(dres_scale, f32, (1,), "dres_scale", dev),
+            _arg(dgate, f32, gates, "dgate", dev),
+            _arg(dgamma_post, f32, vec, "dgamma_post", dev),
+            _arg(dbeta_post, f32, vec, "dbeta_post", dev),
+            _arg(dgamma_pre, f32, vec, "dgamma_pre", dev),
+            _arg(dbeta_pre, f32, vec, "dbeta_pre", dev),
+            _arg(workspace, torch.uint8, None if workspace is None else workspace.shape,
+                 "workspace", dev)]
+    _call_on(dev, "mlpb_join_bwd", args, stream)
+
+
+def _join_ws(cfg, dev):
+    if dev == torch.cuda.current_device():
+        return mlpb_join_workspace_size(cfg)
+    with torch.cuda.device(dev):
+        return mlpb_join_workspace_size(cfg)
+
+
 def mlpb_last_device_error(h: Handle, stream=None) -> int:
     """Returns the status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
     return load_library().mlpb_last_device_error(h.ptr, _stream(stream))
@@ -555,3 +659,64 @@ class ActCheckpoint8:
         mlpb_act8_grad(self.act, dA, self.codes if codes is None else codes,
                        self.scales if scales is None else scales, dZ, A, self.tp, stream)
         return dZ, A
+
+
+class Join:
+    """The join between two blocks of one shape: forward() returns (Xout, Xn, stats),
+    backward() the gradient dict.  Owns the backward's workspace."""
+
+    def __init__(self, tokens, hidden, post_norm="none", pre_norm="none", gate_groups=0, eps=1e-5,
+                 stream_dtype=torch.bfloat16, block_dtype=torch.bfloat16, accumulate=False,
+                 has_block=True, device="cuda"):
+        self.cfg = make_join_config(tokens, hidden, post_norm, pre_norm, gate_groups, eps,
+                                    stream_dtype, block_dtype, accumulate, has_block)
+        self.device = torch.device(device)
+        self.workspace = torch.empty(_join_ws(self.cfg, self.device), dtype=torch.uint8,
+                                     device=self.device)
+
+    def _rows(self, dtype):
+        return torch.empty((self.cfg.tokens, self.cfg.hidden), dtype=dtype, device=self.device)
+
+    def forward(self, X, Y=None, res_scale=None, gate=None, gamma_post=None, beta_post=None,
+                gamma_pre=None, beta_pre=None, Xout=None, Xn=None, stats=None, stream=None):
+        """(Xout, Xn, stats); Xout is None without a block, Xn without a pre norm.  Pass the
+        stream X itself as Xout to update it in place."""
+        c = self.cfg
+        if Xout is None and c.has_block:
+            Xout = self._rows(_join_types(c)[0])
+        if Xn is None and c.pre_norm != MLPB_NORM_NONE:
+            Xn = self._rows(torch.bfloat16)
+        if stats is None:
+            stats = torch.empty((c.tokens, 4), dtype=torch.float32, device=self.device)
+        mlpb_join_fwd(c, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre, Xout,
+                      Xn, stats, stream)
+        return Xout, Xn, stats
+
+    def alloc_grads(self, res_scale=False):
+        """Gradient buffers: dX, dY and the parameters' (zeroed when they accumulate)."""
+        c = self.cfg
+        new = torch.zeros if c.flags & MLPB_JOIN_ACCUMULATE_GRADS else torch.empty
+
+        def par(on, *shape):
+            return new(shape, dtype=torch.float32, device=self.device) if on else None
+        H, layer = c.hidden, MLPB_NORM_LAYER
+        return dict(
+            dX=self._rows(_join_types(c)[0]),
+            dY=self._rows(torch.bfloat16) if c.has_block else None,
+            dres_scale=par(res_scale, 1), dgate=par(c.gate_groups > 0, c.gate_groups, H),
+            dgamma_post=par(c.post_norm != MLPB_NORM_NONE, H),
+            dbeta_post=par(c.post_norm == layer, H),
+            dgamma_pre=par(c.pre_norm != MLPB_NORM_NONE, H),
+            dbeta_pre=par(c.pre_norm == layer, H))
+
+    def backward(self, X, Y, Xout, stats, dXout, dXn=None, res_scale=None, gate=None,
+                 gamma_post=None, beta_post=None, gamma_pre=None, beta_pre=None, grads=None,
+                 stream=None):
+        """The gradients for dXout (None: zero) and dXn of forward()'s outputs; X and Y may be
+        None where the backward does not read them (include/mlpb.h)."""
+        g = self.alloc_grads(res_scale is not None) if grads is None else grads
+        mlpb_join_bwd(self.cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post,
+                      gamma_pre, dXout, dXn, g["dX"], g["dY"], g["dres_scale"], g["dgate"],
+                      g["dgamma_post"], g["dbeta_post"], g["dgamma_pre"], g["dbeta_pre"],
+                      self.workspace, stream)
+        return g
