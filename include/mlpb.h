@@ -413,6 +413,50 @@ mlpb_status mlpb_join_bwd(const mlpb_join_config *cfg, const void *X, const void
                           float *dbeta_post, float *dgamma_pre, float *dbeta_pre,
                           void *workspace, mlpb_stream_t stream);
 
+/* A mixture-of-experts MLP for a few tokens (decoding), in one launch: the block's MLP with
+ * `experts` experts in the place of its shards, of which every token takes `topk`.
+ *     l   = X Wr^T                                  (router logits, fp32)
+ *     ids = the topk experts of largest l, descending, equal ones by index (NaN last)
+ *     w   = softmax(l) at ids, over all experts; divided by its sum over ids with `normalize`
+ *     Y   = sum over a token's experts of w W2_e act(W1_e x)       (no biases)
+ * Every routed expert's weights are read once for all of its tokens.  w act(W1_e x) is rounded
+ * to bf16 (the second product's operand); every sum is fp32. */
+typedef struct {
+  int32_t max_tokens; /* most tokens of a call, 1..64                                         */
+  int32_t hidden;     /* a multiple of 8                                                      */
+  int32_t ffn;        /* features of one expert, a multiple of 8                              */
+  int32_t experts;    /* 1..256                                                               */
+  int32_t topk;       /* 1..16, at most experts                                               */
+  int32_t act;        /* mlpb_act                                                             */
+  int32_t normalize;  /* 1: the weights of a token sum to 1                                   */
+  uint32_t flags;     /* 0                                                                    */
+} mlpb_moe_config;
+
+typedef struct mlpb_moe mlpb_moe; /* opaque; owns three device words and no tensors */
+
+/* Validates *cfg and allocates the handle on the current device; EINVAL for null arguments or
+ * values out of range, EUNSUPPORTED for sizes outside those above (or hidden, ffn > 2^20). */
+mlpb_status mlpb_moe_create(const mlpb_moe_config *cfg, mlpb_moe **out);
+void mlpb_moe_destroy(mlpb_moe *h);
+
+/* Bytes of the workspace of mlpb_moe_forward (logits and activations of max_tokens). */
+mlpb_status mlpb_moe_workspace_size(const mlpb_moe *h, size_t *bytes);
+
+/* Forward of `tokens` <= max_tokens rows (0 does nothing).  X [tokens][hidden]; Wr
+ * [experts][hidden]; W1 [experts][2][ffn][hidden] (gate, up) for SwiGLU, [experts][ffn][hidden]
+ * for GELU; W2 [experts][hidden][ffn]; Y [tokens][hidden]: all bf16, 16-byte aligned.  ids
+ * [tokens][topk] int32 and weights [tokens][topk] fp32 receive the routing.  The launch is
+ * cooperative (one CTA on every SM, which synchronise).  The current device must be the
+ * handle's.  Calls of one handle, or with one workspace, must not overlap on the GPU (use one
+ * stream, or a handle and a workspace for each; a captured graph counts as its call). */
+mlpb_status mlpb_moe_forward(mlpb_moe *h, int64_t tokens, const void *X, const void *Wr,
+                             const void *W1, const void *W2, void *Y, int32_t *ids,
+                             float *weights, void *workspace, mlpb_stream_t stream);
+
+/* As mlpb_last_device_error, for a mixture-of-experts handle: MLPB_ETIMEOUT if a bounded wait
+ * of its launches expired since the last call. */
+mlpb_status mlpb_moe_last_device_error(mlpb_moe *h, mlpb_stream_t stream);
+
 /* Static English text of a status code. */
 const char *mlpb_status_str(mlpb_status s);
 

@@ -49,6 +49,8 @@ EXPORTED = (
     "mlpb_branch_forward", "mlpb_branch_backward", "mlpb_quantize_e4m3",
     "mlpb_act8_scales", "mlpb_act8_save", "mlpb_act8_grad",
     "mlpb_join_workspace_size", "mlpb_join_fwd", "mlpb_join_bwd",
+    "mlpb_moe_create", "mlpb_moe_destroy", "mlpb_moe_workspace_size", "mlpb_moe_forward",
+    "mlpb_moe_last_device_error",
 )
 
 
@@ -66,6 +68,11 @@ class mlpb_join_config(ctypes.Structure):
         ("has_block", ctypes.c_int32), ("post_norm", ctypes.c_int32),
         ("pre_norm", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32),
     ]
+
+
+class mlpb_moe_config(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("max_tokens", "hidden", "ffn", "experts", "topk",
+                                              "act", "normalize")] + [("flags", ctypes.c_uint32)]
 
 
 class mlpb_kernel_time(ctypes.Structure):
@@ -118,6 +125,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mlpb_join_workspace_size": (I, [ctypes.POINTER(mlpb_join_config), ctypes.POINTER(Z)]),
         "mlpb_join_fwd": (I, [ctypes.POINTER(mlpb_join_config)] + [P] * 12),
         "mlpb_join_bwd": (I, [ctypes.POINTER(mlpb_join_config)] + [P] * 21),
+        "mlpb_moe_create": (I, [ctypes.POINTER(mlpb_moe_config), ctypes.POINTER(H)]),
+        "mlpb_moe_destroy": (None, [H]),
+        "mlpb_moe_workspace_size": (I, [H, ctypes.POINTER(Z)]),
+        "mlpb_moe_forward": (I, [H, I64] + [P] * 9),
+        "mlpb_moe_last_device_error": (I, [H, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -505,6 +517,68 @@ def _join_ws(cfg, dev):
         return mlpb_join_workspace_size(cfg)
 
 
+@dataclasses.dataclass
+class MoEHandle:
+    ptr: int
+    cfg: mlpb_moe_config
+    device: int  # CUDA device number it was created on
+
+
+def make_moe_config(max_tokens, hidden, ffn, experts, topk, act="swiglu", normalize=True,
+                    flags=0) -> mlpb_moe_config:
+    return mlpb_moe_config(max_tokens, hidden, ffn, experts, topk, _ACTS[act],
+                           1 if normalize else 0, flags)
+
+
+def mlpb_moe_create(cfg: mlpb_moe_config) -> MoEHandle:
+    """A mixture-of-experts handle on the current CUDA device."""
+    h = ctypes.c_void_p()
+    _check(load_library().mlpb_moe_create(ctypes.byref(cfg), ctypes.byref(h)), "mlpb_moe_create")
+    return MoEHandle(h.value, cfg, torch.cuda.current_device())
+
+
+def mlpb_moe_destroy(h: MoEHandle):
+    if h is not None and h.ptr:
+        load_library().mlpb_moe_destroy(h.ptr)
+        h.ptr = 0
+
+
+def mlpb_moe_workspace_size(h: MoEHandle) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().mlpb_moe_workspace_size(h.ptr, ctypes.byref(n)),
+           "mlpb_moe_workspace_size")
+    return n.value
+
+
+def mlpb_moe_forward(h: MoEHandle, X, Wr, W1, W2, Y, ids, weights, workspace, stream=None):
+    """Router, experts and combination of the mixture-of-experts MLP for the rows of X
+    (include/mlpb.h); ids int32 and weights fp32 [tokens][topk] receive the routing."""
+    dev = _cuda_index(X, "X")
+    if dev != h.device:
+        raise ValueError(f"X: on cuda:{dev}, the handle on cuda:{h.device}")
+    c = h.cfg
+    if X.dim() != 2:
+        raise ValueError(f"X: expected [tokens][hidden], got {tuple(X.shape)}")
+    T, H, F, E = X.shape[0], c.hidden, c.ffn, c.experts
+    bf = torch.bfloat16
+    w1 = (E, 2, F, H) if c.act == MLPB_ACT_SWIGLU else (E, F, H)
+    if workspace is not None and workspace.numel() * workspace.element_size() \
+            < mlpb_moe_workspace_size(h):
+        raise ValueError("workspace: smaller than mlpb_moe_workspace_size()")
+    args = [h.ptr, T, _arg(X, bf, (T, H), "X", dev), _arg(Wr, bf, (E, H), "Wr", dev),
+            _arg(W1, bf, w1, "W1", dev), _arg(W2, bf, (E, H, F), "W2", dev),
+            _arg(Y, bf, (T, H), "Y", dev), _arg(ids, torch.int32, (T, c.topk), "ids", dev),
+            _arg(weights, torch.float32, (T, c.topk), "weights", dev),
+            _arg(workspace, torch.uint8, None if workspace is None else workspace.shape,
+                 "workspace", dev)]
+    _call_on(dev, "mlpb_moe_forward", args, stream)
+
+
+def mlpb_moe_last_device_error(h: MoEHandle, stream=None) -> int:
+    """The status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
+    return load_library().mlpb_moe_last_device_error(h.ptr, _stream(stream))
+
+
 def mlpb_last_device_error(h: Handle, stream=None) -> int:
     """Returns the status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
     return load_library().mlpb_last_device_error(h.ptr, _stream(stream))
@@ -720,3 +794,37 @@ class Join:
                       g["dgamma_post"], g["dbeta_post"], g["dgamma_pre"], g["dbeta_pre"],
                       self.workspace, stream)
         return g
+
+
+class MoEDecode:
+    """A mixture-of-experts MLP for up to max_tokens (64) tokens: forward() returns (Y, ids,
+    weights).  Owns a handle and its workspace."""
+
+    def __init__(self, max_tokens, hidden, ffn, experts, topk, act="swiglu", normalize=True,
+                 device="cuda"):
+        self.cfg = make_moe_config(max_tokens, hidden, ffn, experts, topk, act, normalize)
+        self.device = torch.device(device)
+        with torch.cuda.device(self.device):
+            self.handle = mlpb_moe_create(self.cfg)
+        self.workspace = torch.empty(mlpb_moe_workspace_size(self.handle), dtype=torch.uint8,
+                                     device=self.device)
+
+    def close(self):
+        mlpb_moe_destroy(self.handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def forward(self, X, Wr, W1, W2, Y=None, ids=None, weights=None, stream=None):
+        T, c = X.shape[0], self.cfg
+        if Y is None:
+            Y = torch.empty((T, c.hidden), dtype=torch.bfloat16, device=self.device)
+        if ids is None:
+            ids = torch.empty((T, c.topk), dtype=torch.int32, device=self.device)
+        if weights is None:
+            weights = torch.empty((T, c.topk), dtype=torch.float32, device=self.device)
+        mlpb_moe_forward(self.handle, X, Wr, W1, W2, Y, ids, weights, self.workspace, stream)
+        return Y, ids, weights
