@@ -419,8 +419,8 @@ mlpb_status mlpb_join_bwd(const mlpb_join_config *cfg, const void *X, const void
  *     ids = the topk experts of largest l, descending, equal ones by index (NaN last)
  *     w   = softmax(l) at ids, over all experts; divided by its sum over ids with `normalize`
  *     Y   = sum over a token's experts of w W2_e act(W1_e x)       (no biases)
- * Every routed expert's weights are read once for all of its tokens.  w act(W1_e x) is rounded
- * to bf16 (the second product's operand); every sum is fp32. */
+ * Every routed expert's weights are read once for all of its tokens.  act(W1_e x) is rounded to
+ * bf16 (the second product's operand); every sum is fp32. */
 typedef struct {
   int32_t max_tokens; /* most tokens of a call, 1..64                                         */
   int32_t hidden;     /* a multiple of 8                                                      */
@@ -432,14 +432,15 @@ typedef struct {
   uint32_t flags;     /* 0                                                                    */
 } mlpb_moe_config;
 
-typedef struct mlpb_moe mlpb_moe; /* opaque; owns three device words and no tensors */
+typedef struct mlpb_moe mlpb_moe; /* opaque; owns a few device words and no tensors */
 
 /* Validates *cfg and allocates the handle on the current device; EINVAL for null arguments or
  * values out of range, EUNSUPPORTED for sizes outside those above (or hidden, ffn > 2^20). */
 mlpb_status mlpb_moe_create(const mlpb_moe_config *cfg, mlpb_moe **out);
 void mlpb_moe_destroy(mlpb_moe *h);
 
-/* Bytes of the workspace of mlpb_moe_forward (logits and activations of max_tokens). */
+/* Bytes of the workspace of mlpb_moe_forward (logits, activations and unweighted outputs of
+ * max_tokens). */
 mlpb_status mlpb_moe_workspace_size(const mlpb_moe *h, size_t *bytes);
 
 /* Forward of `tokens` <= max_tokens rows (0 does nothing).  X [tokens][hidden]; Wr

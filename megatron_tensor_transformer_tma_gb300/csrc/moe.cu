@@ -1,31 +1,43 @@
 // A whole mixture-of-experts MLP for a few tokens (decoding), in one cooperative launch.
 //
 //   l = X Wr^T, the top k experts of each token by l, w = softmax(l) at them (or w / sum w)
-//   a_s = w_s act(W1_e x_t)        for every pair s = (t, e)         bf16 [pairs][Fe]
-//   Y_t = sum over t's pairs of W2_e a_s
+//   a_s = act(W1_e x_t),  y_s = W2_e a_s        for every pair s = (t, e)
+//   Y_t = sum over t's pairs of w_s y_s
 //
 // Bound by memory: up to 64 tokens share each expert's weights, which move once (a few flops a
-// byte).  One CTA an SM runs three phases with a barrier over the grid between them:
-//   router  a CTA takes an expert's row of Wr and eight tokens at a time;
-//   fc1     units of 16 weight rows (8 gate and the same 8 up features, or 16 for GELU) of one
-//           expert times that expert's tokens;
-//   fc2     units of 16 output columns over all routed experts, so that a column's sum over
-//           experts stays in one CTA (no atomics, a fixed order).
-// The 16 warps of a CTA split a unit's K in steps of 32, warp w taking steps w, w + 16, ...,
-// so that the CTA reads a kilobyte of each row at once; their partial sums meet in shared
-// memory at the unit's end.
+// byte).  One CTA an SM runs four phases with a barrier over the grid between them:
+//   router   a CTA takes one or four pairs of expert and token at a time;
+//   fc1      units of 16 weight rows (8 gate and the same 8 up features, or 16 for GELU) of one
+//            expert times that expert's tokens;
+//   fc2      the same with 16 output columns a unit, into fp32 rows y_s;
+//   combine  the pairs of a token, weighted, in order: no atomics, the same bits every run.
+// (fc2 by units that run over all experts needs no y_s and no fourth phase, but has a unit for
+// only every 16 output columns: 1.7 for each SM at H 4096, the second round on two thirds of
+// them; and its columns are all T tokens, mostly not the expert's.)
+//
+// A CTA is four groups, each with units and a ring of shared-memory stages (16 rows by 256) of
+// its own: a warp that fills the stages with tiled bulk copies (cp.async.bulk.tensor, 8 rows by
+// 256 each), and four that multiply, each 64 of a stage's K; their partial sums meet in shared
+// memory at the unit's end, while the other groups go on.  (With all sixteen multiplying warps
+// at every stage, a stage took 0.4 us whatever it held: one warp's wait, loads, products and
+// release after the other.)  Weights depend on the routing only, so the copies run on over the
+// ends of units and over the barrier between fc1 and fc2: fc2's first weights arrive while the
+// last CTAs finish fc1.  Tokens' fragments (from L2) each lane copies for itself, into a slot of
+// its own in the same stage, as far ahead.
+// Two other ways to move the weights measured slower: cp.async of each lane's own fragments was
+// bound by instructions, about 200 a kilobyte (T 1: 4.1 TB/s over all); and bulk copies of
+// single rows, one a lane, by their issue, about 70 ns each (2.1 TB/s).
 //
 // The products run on mma.sync m16n8k16 with the weights as the 16-row operand and tokens as
-// its 8 columns.  tcgen05 has no shape for this: its M is 64 or 128 rows of one operand and it
-// would want both operands staged whole in shared memory, while the tensor work here is under a
-// tenth of the time even at 64 tokens.  K is permuted the same way in both operands so that a
-// lane's fragments are 16 consecutive bytes of a row: what a lane multiplies it copies itself
-// (cp.async into slots of its own, as in join.cuh), and the ring of the next steps needs no
-// barriers and runs on over the units' ends -- and over the barrier between fc1 and fc2: fc2's
-// first weights are on their way while the last CTAs finish fc1.
+// its 8 columns.  tcgen05 has no shape for this: its M is 64 or 128 rows, and the tensor work
+// here is under a tenth of the time even at 64 tokens.  K is permuted the same way in both
+// operands so that a lane's fragments are 16 consecutive bytes of a row.
 //
 // a is rounded to bf16, as every activation that a GEMM of this library reads; logits, softmax
-// and all sums are fp32.
+// and all sums are fp32.  Every wait is bounded (common.cuh).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <new>
 
@@ -35,17 +47,22 @@
 
 namespace mlpb {
 
-constexpr int kMoeThreads = 512;
+constexpr int kMoeThreads = 512;  // the multiplying warps
 constexpr int kMoeWarps = kMoeThreads / 32;
+constexpr int kMoeGroups = 4;                          // of four of them
+constexpr int kMoeBlock = kMoeThreads + 32 * kMoeGroups;  // and a copying warp for each group
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 256;
 constexpr int kMoeMaxTopk = 16;
-constexpr int kMoeUnits = 24;  // 16-byte ring units a thread
-constexpr int kMoeRing = kMoeUnits * kMoeThreads * 16;
-constexpr int kMoeTile = 130;  // floats a warp's 16 x 8 partial tile takes (see moe_reduce)
+constexpr int kMoeKc = 256;     // K of a stage, and of a tiled copy
+constexpr int kMoeBoxRows = 8;  // rows of a tiled copy
+constexpr uint32_t kMoeBox = kMoeKc * kMoeBoxRows * 2;
+constexpr uint32_t kMoeStageW = 2 * kMoeBox;  // a stage's weights; its tokens take 512 bytes each
+constexpr uint32_t kMoeRing = 48u << 10;      // of one group
+constexpr int kMoeMaxStages = 5;
 constexpr int kMoePairs = kMoeMaxTokens * kMoeMaxTopk;
 
-enum MoeSite : uint32_t { kSiteMoeBarrier = 16 };
+enum MoeSite : uint32_t { kSiteMoeGrid = 16, kSiteMoeEmpty = 17, kSiteMoeFull = 18 };
 
 struct MoeSync {  // device words of a handle, zero between launches
   uint32_t arrived, done, err;
@@ -54,10 +71,11 @@ struct MoeSync {  // device words of a handle, zero between launches
 struct MoeParams {
   const __nv_bfloat16 *X, *Wr, *W1, *W2;
   __nv_bfloat16* Y;
-  int32_t* ids;    // [T][K]
-  float* weights;  // [T][K]
-  float* logits;   // [T][E] scratch
-  __nv_bfloat16* act;  // [T * K][Fe] scratch
+  int32_t* ids;        // [T][K]
+  float* weights;      // [T][K]
+  float* logits;       // [T][E] scratch
+  __nv_bfloat16* act;  // [T * K][Fe] scratch: a_s, pairs ordered by expert, then token
+  float* pair_y;       // [T * K][H] scratch: y_s
   int T, H, Fe, E, K;
   int gated, normalize;
   MoeSync* sync;
@@ -65,33 +83,22 @@ struct MoeParams {
 };
 
 struct MoeShared {
-  float part[2][kMoeWarps * kMoeTile];
-  uint64_t mask[kMoeMaxExperts];      // tokens of an expert
-  uint16_t off[kMoeMaxExperts];       // its first pair
-  uint16_t active[kMoeMaxExperts];    // routed experts, ascending
-  uint16_t ids[kMoePairs];            // [T][K]
-  float w[kMoePairs];                 // [T][K]
-  uint8_t tok[kMoePairs];             // token of pair s (pairs ordered by expert, then token)
-  float wpair[kMoePairs];             // its weight
-  int n_active, most;                 // routed experts, most tokens of one
-  int abort;
+  float part[kMoeGroups][2][4 * 128];  // partial tiles of a group's four warps, twice
+  uint64_t full[kMoeGroups][kMoeMaxStages], empty[kMoeGroups][kMoeMaxStages];
+  uint64_t mask[kMoeMaxExperts];    // tokens of an expert
+  uint16_t off[kMoeMaxExperts];     // its first pair
+  uint16_t active[kMoeMaxExperts];  // routed experts, ascending
+  uint16_t ids[kMoePairs];          // [T][K]
+  float w[kMoePairs];               // [T][K]
+  uint16_t slot[kMoePairs];         // [T][K]: the pair
+  uint8_t tok[kMoePairs];           // token of a pair
+  int n_active, most;               // routed experts, most tokens of one
+  uint32_t abort;
 };
 
-constexpr size_t kMoeSmem = kMoeRing + sizeof(MoeShared);
-
-// 16 bytes, or zeros where !ok (src is then any valid address).
-__device__ __forceinline__ void moe_copy(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void moe_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void moe_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+constexpr size_t kMoeSmem = kMoeGroups * kMoeRing + sizeof(MoeShared);
+static_assert(kMoeSmem <= 227 * 1024, "shared memory of a CTA");
+static_assert(kMoeRing >= kMoeStageW + kMoeMaxTokens * kMoeKc * 2, "a stage at the most tokens");
 
 // c += A B: A 16 x 16 (lane: rows lane/4 and lane/4 + 8), B 16 x 8 (lane: column lane/4).
 __device__ __forceinline__ void moe_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -103,55 +110,59 @@ __device__ __forceinline__ void moe_mma(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A barrier over the grid, number k (1, 2, ...) of the launch.  Bounded: false when it expired
-// in any thread 0 (the launch then ends without its results and the handle reports it).
-__device__ __forceinline__ bool moe_grid_barrier(const MoeParams& p, MoeShared& sh, uint32_t k) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(&p.sync->arrived, 1u);
-    const uint32_t want = k * gridDim.x;
-    const uint64_t t0 = globaltimer_ns();
-    uint32_t seen;
-    for (uint32_t i = 1;; ++i) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
-                   : "=r"(seen)
-                   : "l"(&p.sync->arrived)
-                   : "memory");
-      if (seen >= want) break;
-      if ((i & 63u) == 0u && globaltimer_ns() - t0 > p.wait_ns) {
-        atomicCAS(&p.sync->err, 0u, kDevErrTimeout | kSiteMoeBarrier);
-        sh.abort = 1;
-        break;
-      }
-    }
-    __threadfence();
-  }
-  __syncthreads();
-  return sh.abort == 0;
+// Barriers over the grid, number k (1, 2) of the launch: every CTA arrives once, and waits until
+// all have.  The wait is bounded: false when it expired here or elsewhere in the CTA (the launch
+// then ends without its results and the handle reports it).
+__device__ __forceinline__ void moe_grid_arrive(const MoeParams& p) {
+  __threadfence();
+  atomicAdd(&p.sync->arrived, 1u);
 }
 
-// Sum of the 16 warps' partial tiles (16 rows x 8 columns, c as moe_mma leaves it) for the
-// value that this thread reads: column n = tid / 64, row r = (tid / 8) % 8 + 8 ((tid / 4) % 2);
-// its four neighbours tid % 4 add four warps each and all four return the sum.  The layout --
-// row bits 0-1, bit 3, bit 2, then the column, and 130 floats a warp -- keeps a warp's reads
-// on 32 different banks.  `buf` alternates between calls: one barrier a call.
+__device__ __forceinline__ bool moe_grid_wait(const MoeParams& p, MoeShared& sh, uint32_t k) {
+  const uint32_t want = k * gridDim.x;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t seen;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
+                 : "=r"(seen)
+                 : "l"(&p.sync->arrived)
+                 : "memory");
+    if (seen >= want) break;
+    if ((i & 63u) == 0u) {
+      if (*const_cast<volatile uint32_t*>(&sh.abort)) return false;
+      if (globaltimer_ns() - t0 > p.wait_ns) {
+        atomicCAS(&p.sync->err, 0u, kDevErrTimeout | kSiteMoeGrid);
+        *const_cast<volatile uint32_t*>(&sh.abort) = 1u;
+        return false;
+      }
+    }
+  }
+  __threadfence();
+  return true;
+}
+
+// A barrier of the multiplying warps.
+__device__ __forceinline__ void moe_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kMoeThreads) : "memory");
+}
+
+// The group, and the thread's and the warp's number in it.
+__device__ __forceinline__ int moe_group() { return threadIdx.x >> 7; }
+__device__ __forceinline__ int moe_thread() { return threadIdx.x & 127; }
+__device__ __forceinline__ int moe_warp() { return (threadIdx.x >> 5) & 3; }
+
+// Sum of a group's four partial tiles (16 rows x 8 columns, c as moe_mma leaves it), of which
+// each thread returns one value: column thread / 16, row (thread / 2) % 8 + 8 (thread % 2) -- a
+// gate and its up are neighbours.  `buf` alternates between calls: one barrier a call.
 __device__ __forceinline__ float moe_reduce(MoeShared& sh, int buf, const float (&c)[4]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, n0 = (lane & 3) * 2;
-  float* t = sh.part[buf] + warp * kMoeTile + (g >> 2) * 8 + (g & 3);
-  t[n0 * 16] = c[0];
-  t[(n0 + 1) * 16] = c[1];
-  t[n0 * 16 + 4] = c[2];
-  t[(n0 + 1) * 16 + 4] = c[3];
-  __syncthreads();
-  const int part = threadIdx.x & 3, up = (threadIdx.x >> 2) & 1, f = (threadIdx.x >> 3) & 7;
-  const int n = threadIdx.x >> 6;
-  const float* s = sh.part[buf] + part * 4 * kMoeTile + n * 16 + (f >> 2) * 8 + up * 4 + (f & 3);
-  float v = (s[0] + s[kMoeTile]) + (s[2 * kMoeTile] + s[3 * kMoeTile]);
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  v += __shfl_xor_sync(0xffffffffu, v, 2);
-  return v;
+  const int lane = threadIdx.x & 31;
+  float* part = sh.part[moe_group()][buf];
+  float2* t = reinterpret_cast<float2*>(part + moe_warp() * 128 + (lane & 3) * 32 + (lane >> 2) * 2);
+  t[0] = make_float2(c[0], c[2]);
+  t[8] = make_float2(c[1], c[3]);
+  asm volatile("bar.sync %0, 128;" ::"r"(moe_group() + 2) : "memory");
+  const float* s = part + moe_thread();
+  return (s[0] + s[128]) + (s[256] + s[384]);
 }
 
 // ------------------------------------------------------------------ router
@@ -166,36 +177,37 @@ __device__ __forceinline__ float moe_dot8(const uint4& a, const uint4& b, float 
   return s;
 }
 
-__device__ void moe_logits(const MoeParams& p, MoeShared& sh) {
+// A pair of expert and token at a time, K over all sixteen warps, or with more pairs than CTAs
+// four pairs, K over four warps each.  The code is kept short: it runs once, and fetching it
+// takes longer than running it.
+__device__ __forceinline__ void moe_logits(const MoeParams& p, MoeShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tgs = (p.T + 7) / 8;
+  const int pairs = p.E * p.T;
+  const int w = pairs <= static_cast<int>(gridDim.x) ? kMoeWarps : 4;  // warps of a pair
+  const int at_once = kMoeWarps / w, sub = warp & (w - 1);
   int buf = 0;
-  for (int u = blockIdx.x; u < p.E * tgs; u += gridDim.x, buf ^= 1) {
-    const int tg = u / p.E, e = u - tg * p.E, t0 = tg * 8, nt = min(8, p.T - t0);
-    const __nv_bfloat16* w = p.Wr + static_cast<size_t>(e) * p.H;
-    const __nv_bfloat16* x = p.X + static_cast<size_t>(t0) * p.H;
-    float acc[8];
+#pragma unroll 1
+  for (int first = blockIdx.x * at_once; first < pairs; first += gridDim.x * at_once, buf ^= 1) {
+    const int pair = first + warp / w;
+    float acc = 0.f;
+    if (pair < pairs) {
+      const int t = pair / p.E, e = pair - t * p.E;
+      const __nv_bfloat16* a = p.Wr + static_cast<size_t>(e) * p.H;
+      const __nv_bfloat16* x = p.X + static_cast<size_t>(t) * p.H;
+#pragma unroll 2
+      for (int c = (sub * 32 + lane) * 8; c < p.H; c += w * 256)
+        acc = moe_dot8(ld_global_nc_v4(a + c), ld_global_nc_v4(x + c), acc);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) acc[t] = 0.f;
-    for (int c = threadIdx.x * 8; c < p.H; c += kMoeThreads * 8) {
-      const uint4 a = ld_global_nc_v4(w + c);
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-        if (t < nt) acc[t] = moe_dot8(a, ld_global_nc_v4(x + static_cast<size_t>(t) * p.H + c), acc[t]);
+      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     }
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t >= nt) break;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-      if (lane == 0) sh.part[buf][warp * 8 + t] = acc[t];
-    }
-    __syncthreads();
-    if (threadIdx.x < nt) {
+    if (lane == 0) sh.part[0][buf][warp] = acc;
+    moe_sync();
+    if (pair < pairs && sub == 0 && lane == 0) {
       float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < kMoeWarps; ++k) s += sh.part[buf][k * 8 + threadIdx.x];
-      __stcg(p.logits + static_cast<size_t>(t0 + threadIdx.x) * p.E + e, s);
+#pragma unroll 1
+      for (int k = 0; k < w; ++k) s += sh.part[0][buf][warp + k];
+      const int t = pair / p.E;
+      __stcg(p.logits + static_cast<size_t>(t) * p.E + (pair - t * p.E), s);
     }
   }
 }
@@ -207,11 +219,11 @@ __device__ __forceinline__ uint32_t moe_key(float l) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// Every CTA routes all tokens itself (a warp a token) from the logits, then lists the pairs by
-// expert; CTA 0 writes ids and weights out.
-__device__ void moe_route(const MoeParams& p, MoeShared& sh) {
+// A token's choices from its logits, by one warp; kPer experts a lane.  CTA 0 writes ids and
+// weights out.
+template <int kPer>
+__device__ __forceinline__ void moe_choose(const MoeParams& p, MoeShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kPer = kMoeMaxExperts / 32;
   for (int t = warp; t < p.T; t += kMoeWarps) {
     float l[kPer];
     uint32_t key[kPer];
@@ -271,13 +283,25 @@ __device__ void moe_route(const MoeParams& p, MoeShared& sh) {
       }
     }
   }
-  __syncthreads();
+}
+
+// Every CTA routes all tokens itself, then lists the pairs by expert.
+__device__ void moe_route(const MoeParams& p, MoeShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (p.E <= 32)
+    moe_choose<1>(p, sh);
+  else if (p.E <= 64)
+    moe_choose<2>(p, sh);
+  else if (p.E <= 128)
+    moe_choose<4>(p, sh);
+  else
+    moe_choose<8>(p, sh);
   // tokens of each expert, as a bit mask
   for (int e = threadIdx.x; e < p.E; e += kMoeThreads) sh.mask[e] = 0ull;
-  __syncthreads();
+  moe_sync();
   for (int i = threadIdx.x; i < p.T * p.K; i += kMoeThreads)
     atomicOr(reinterpret_cast<unsigned long long*>(&sh.mask[sh.ids[i]]), 1ull << (i / p.K));
-  __syncthreads();
+  moe_sync();
   if (warp == 0) {  // offsets of the experts' pairs, and the routed experts in order
     int pairs = 0, routed = 0, most = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -301,329 +325,369 @@ __device__ void moe_route(const MoeParams& p, MoeShared& sh) {
       sh.most = most;
     }
   }
-  __syncthreads();
+  moe_sync();
   for (int i = threadIdx.x; i < p.T * p.K; i += kMoeThreads) {
     const int e = sh.ids[i], t = i / p.K;
     const int s = sh.off[e] + __popcll(sh.mask[e] & ((1ull << t) - 1ull));
     sh.tok[s] = static_cast<uint8_t>(t);
-    sh.wpair[s] = sh.w[i];
+    sh.slot[i] = static_cast<uint16_t>(s);
   }
-  __syncthreads();
 }
 
-// ------------------------------------------------------------------ fc1
-// Tiles of eight of an expert's tokens, at most NT; a step's slot is 2 + NT units a thread.
-template <int NT>
-__device__ void moe_fc1(const MoeParams& p, MoeShared& sh, uint32_t ring, const uint8_t* ring_p,
-                        int& buf) {
-  constexpr int kDepth = kMoeUnits / (2 + NT);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int rows = p.gated ? 8 : 16;  // features of a unit
-  const int fgs = (p.Fe + rows - 1) / rows;
-  const int items = sh.n_active * fgs;
-  const int ks = (p.H + 31) / 32;
-  const int steps = warp < ks ? (ks - warp + kMoeWarps - 1) / kMoeWarps : 0;
-  const uint32_t mine = ring + threadIdx.x * 16;
-  const uint8_t* mine_p = ring_p + threadIdx.x * 16;
-  constexpr uint32_t kUnit = kMoeThreads * 16;
+// ------------------------------------------------------------------ the rings
+// A group's ring.  A stage: the weights (8 rows by 256, twice), then for each multiplying warp
+// 128 bytes (its 64 of K) of up to `most` tokens.
+struct MoeRing {
+  uint32_t base;       // shared-memory address of stage 0
+  const uint8_t* ptr;  // the same as a pointer
+  uint32_t full, empty;  // its barriers
+  uint32_t stage_bytes, most;
+  int stages;
+  __device__ __forceinline__ MoeRing(uint8_t* smem, MoeShared& sh, int group)
+      : base(smem_u32(smem + group * kMoeRing)),
+        ptr(smem + group * kMoeRing),
+        full(smem_u32(sh.full[group])),
+        empty(smem_u32(sh.empty[group])),
+        most(sh.most) {
+    stage_bytes = kMoeStageW + most * (kMoeKc * 2);
+    stages = min(kMoeMaxStages, static_cast<int>(kMoeRing / stage_bytes));
+  }
+};
 
-  // the copies' place: unit pi, step pk; its rows and tokens
-  int pi = blockIdx.x, pk = warp, pn = 0;
-  const __nv_bfloat16 *lo = nullptr, *hi = nullptr;
-  bool lo_ok = false, hi_ok = false;
-  int tok[NT];
-  auto open = [&]() {
-    if (pi >= items) return;
-    const int a = pi / fgs, f = (pi - a * fgs) * rows + g;
-    const int e = sh.active[a];
-    if (p.gated) {
-      lo = p.W1 + (static_cast<size_t>(e) * 2 * p.Fe + f) * p.H;
-      hi = lo + static_cast<size_t>(p.Fe) * p.H;
-      lo_ok = hi_ok = f < p.Fe;
-    } else {
-      lo = p.W1 + (static_cast<size_t>(e) * p.Fe + f) * p.H;
-      hi = lo + static_cast<size_t>(8) * p.H;
-      lo_ok = f < p.Fe;
-      hi_ok = f + 8 < p.Fe;
+// Where one side of a ring is.
+struct MoePlace {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(const MoeRing& r) {
+    if (++stage == r.stages) {
+      stage = 0;
+      phase ^= 1u;
     }
-    pn = __popcll(sh.mask[e]);
+  }
+};
+
+// The units of fc1 and fc2: expert by expert, `rows` features or 16 output columns each.  Unit u
+// belongs to CTA u mod grid, and there to the groups in turn.
+template <bool kFc1>
+struct MoeUnits {
+  int rows, per, count, kcs, len;  // rows of a unit, units of an expert, of all; stages; K
+  __device__ __forceinline__ MoeUnits(const MoeParams& p, const MoeShared& sh) {
+    rows = kFc1 && p.gated ? 8 : 16;
+    per = ((kFc1 ? p.Fe : p.H) + rows - 1) / rows;
+    count = sh.n_active * per;
+    len = kFc1 ? p.H : p.Fe;
+    kcs = (len + kMoeKc - 1) / kMoeKc;
+  }
+  static __device__ __forceinline__ int first(int group) { return blockIdx.x + group * gridDim.x; }
+  static __device__ __forceinline__ int step() { return kMoeGroups * gridDim.x; }
+};
+
+// A wait of many threads: without the clock as long as it is short.
+__device__ __forceinline__ bool moe_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc,
+                                         uint32_t site) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_bounded(bar, parity, wc, site);
+}
+
+// ------------------------------------------------------------------ the copying threads
+// Rows and columns past the matrix read as zeros; rows that belong to another expert, where a
+// unit reaches past its own, give outputs that are dropped.
+template <bool kFc1>
+__device__ __forceinline__ bool moe_fill(const MoeParams& p, const MoeShared& sh,
+                                         const MoeRing& ring, const WaitCtx& wc,
+                                         const CUtensorMap* m, int group, MoePlace& at,
+                                         uint32_t& armed, uint32_t& armed_phase) {
+  const MoeUnits<kFc1> d(p, sh);
+  for (int u = d.first(group); u < d.count; u += d.step()) {
+    const int a = u / d.per, r = (u - a * d.per) * d.rows;
+    const int e = sh.active[a];
+    const int r0 = (kFc1 ? (p.gated ? 2 * e : e) * p.Fe : e * p.H) + r;
+    const int r1 = r0 + (kFc1 && p.gated ? p.Fe : 8);
+    for (int kc = 0; kc < d.kcs; ++kc) {
+      if (!moe_wait(ring.empty + 8 * at.stage, at.phase ^ 1u, wc, kSiteMoeEmpty)) return false;
+      const uint32_t bar = ring.full + 8 * at.stage;
+      const uint32_t dst = ring.base + at.stage * ring.stage_bytes;
+      mbar_arrive_expect_tx(bar, kMoeStageW);
+      tma_load_2d(dst, m, bar, kc * kMoeKc, r0);
+      tma_load_2d(dst + kMoeBox, m, bar, kc * kMoeKc, r1);
+      armed |= 1u << at.stage;
+      armed_phase = (armed_phase & ~(1u << at.stage)) | (at.phase << at.stage);
+      at.next(ring);
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void moe_copy_thread(const MoeParams& p, MoeShared& sh,
+                                                const MoeRing& ring, const WaitCtx& wc,
+                                                const CUtensorMap* m1, const CUtensorMap* m2,
+                                                int group) {
+  MoePlace at;
+  uint32_t armed = 0, armed_phase = 0;
+  if (moe_fill<true>(p, sh, ring, wc, m1, group, at, armed, armed_phase))
+    moe_fill<false>(p, sh, ring, wc, m2, group, at, armed, armed_phase);
+  // every copy that was issued has landed (also after an expired wait)
+  for (int s = 0; s < ring.stages; ++s)
+    if (armed & (1u << s)) wait_drain(ring.full + 8 * s, (armed_phase >> s) & 1u, wc);
+}
+
+// ------------------------------------------------------------------ the multiplying warps
+__device__ __forceinline__ void moe_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void moe_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits for this thread's oldest group of copies when `ahead` (1 to 5) groups are in flight.
+__device__ __forceinline__ void moe_wait_oldest(int ahead) {
+  if (ahead >= 5)
+    asm volatile("cp.async.wait_group 4;" ::: "memory");
+  else if (ahead == 4)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (ahead == 3)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (ahead == 2)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// A lane's place in step i (0, 1) of a stage: rows lane / 4 and lane / 4 + 8, and 8 of K from
+// moe_col() + 32 i.
+__device__ __forceinline__ int moe_col() { return moe_warp() * 64 + (threadIdx.x & 3) * 8; }
+
+// Offset in a stage of this lane's slot for the expert's token number t and step i.
+__device__ __forceinline__ uint32_t moe_slot(const MoeRing& ring, int i, int t) {
+  return kMoeStageW + ((moe_warp() * 2 + i) * ring.most + t) * 64 + (threadIdx.x & 3) * 16;
+}
+
+// A lane's copies of its tokens' fragments -- column lane / 4 of tile j is the expert's token
+// number j * 8 + lane / 4 -- one stage after the other, ahead of the products.
+template <int NT, bool kFc1>
+struct MoeTokens {
+  const MoeParams& p;
+  const MoeShared& sh;
+  const MoeRing& ring;
+  const MoeUnits<kFc1>& d;
+  int u, kc, stage, n;
+  const __nv_bfloat16* src;
+  int row[NT];  // offsets of the tokens' rows (elements)
+
+  __device__ __forceinline__ MoeTokens(const MoeParams& p_, const MoeShared& sh_,
+                                       const MoeRing& ring_, const MoeUnits<kFc1>& d_, int stage_)
+      : p(p_), sh(sh_), ring(ring_), d(d_), u(d_.first(moe_group())), kc(0), stage(stage_), n(0) {
+    src = (kFc1 ? p.X : p.act) + moe_col();
+    open();
+  }
+  __device__ __forceinline__ void open() {
+    if (u >= d.count) return;
+    const int e = sh.active[u / d.per], off = sh.off[e], g = (threadIdx.x & 31) >> 2;
+    n = __popcll(sh.mask[e]);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      tok[j] = j * 8 + g < pn ? sh.tok[sh.off[e] + j * 8 + g] : -1;
-  };
-  auto produce = [&](int slot) {
-    if (pi < items) {
-      const int c = pk * 32 + q * 8;
-      const bool in = c < p.H;
-      const uint32_t d = mine + slot * (2 + NT) * kUnit;
-      moe_copy(d, lo_ok && in ? lo + c : p.X, lo_ok && in);
-      moe_copy(d + kUnit, hi_ok && in ? hi + c : p.X, hi_ok && in);
+    for (int j = 0; j < NT; ++j) {
+      const int s = off + min(j * 8 + g, n - 1);
+      row[j] = kFc1 ? sh.tok[s] * p.H : s * p.Fe;
+    }
+  }
+  __device__ __forceinline__ void issue() {
+    if (u < d.count) {
+      const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j * 8 < pn) {
-          const bool ok = in && tok[j] >= 0;
-          moe_copy(d + (2 + j) * kUnit, ok ? p.X + static_cast<size_t>(tok[j]) * p.H + c : p.X, ok);
+      for (int i = 0; i < 2; ++i)
+        if (kc * kMoeKc + moe_col() + i * 32 < d.len) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            if (j * 8 + g < n)
+              moe_copy16(ring.base + stage * ring.stage_bytes + moe_slot(ring, i, j * 8 + g),
+                         src + row[j] + kc * kMoeKc + i * 32);
         }
-      pk += kMoeWarps;
-      if (pk >= ks) {
-        pk = warp;
-        pi += gridDim.x;
+      if (++stage == ring.stages) stage = 0;
+      if (++kc == d.kcs) {
+        kc = 0;
+        u += d.step();
         open();
       }
     }
     moe_commit();
-  };
-  if (steps == 0) pi = items;  // fewer steps than warps: nothing to copy
-  open();
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) produce(s);
+  }
+};
 
-  int slot = 0;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const int a = it / fgs, e = sh.active[a], f0 = (it - a * fgs) * rows;
+// fc1 or fc2 with up to NT tiles of eight of an expert's tokens.  After a wait that expired
+// (`dead`), a lane waits no more and works on with what the stages hold: the launch is lost and
+// reported, but every barrier that the warps share still meets all of them.
+template <int NT, bool kFc1>
+__device__ void moe_multiply(const MoeParams& p, MoeShared& sh, const MoeRing& ring,
+                             const WaitCtx& wc, MoePlace& at, int& buf, bool& dead) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  const MoeUnits<kFc1> d(p, sh);
+  MoeTokens<NT, kFc1> tokens(p, sh, ring, d, at.stage);
+#pragma unroll 1
+  for (int s = 0; s < ring.stages; ++s) tokens.issue();
+#pragma unroll 1
+  for (int u = d.first(moe_group()); u < d.count; u += d.step()) {
+    const int a = u / d.per, e = sh.active[a], r0 = (u - a * d.per) * d.rows;
     const int n = __popcll(sh.mask[e]);
     float c[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
-    for (int st = 0; st < steps; ++st) {
-      moe_wait<kDepth - 1>();
-      const uint8_t* s = mine_p + slot * (2 + NT) * kUnit;
-      const uint4 l = *reinterpret_cast<const uint4*>(s);
-      const uint4 h = *reinterpret_cast<const uint4*>(s + kUnit);
-      uint4 x[NT];
+#pragma unroll 1
+    for (int kc = 0; kc < d.kcs; ++kc) {
+      if (!dead) dead = !moe_wait(ring.full + 8 * at.stage, at.phase, wc, kSiteMoeFull);
+      moe_wait_oldest(ring.stages);
+      const uint8_t* st = ring.ptr + at.stage * ring.stage_bytes;
+      const int left = d.len - kc * kMoeKc - moe_col();
+      constexpr int kHeld = NT <= 2 ? 2 : 1;  // steps whose tokens are in registers at once
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j * 8 < n) x[j] = *reinterpret_cast<const uint4*>(s + (2 + j) * kUnit);
+      for (int i0 = 0; i0 < 2; i0 += kHeld) {
+        uint4 l[kHeld], h[kHeld], x[kHeld][NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j * 8 < n) {
-          moe_mma(c[j], l.x, h.x, l.y, h.y, x[j].x, x[j].y);
-          moe_mma(c[j], l.z, h.z, l.w, h.w, x[j].z, x[j].w);
+        for (int i = 0; i < kHeld; ++i) {
+          const uint8_t* w = st + g * (kMoeKc * 2) + (moe_col() + (i0 + i) * 32) * 2;
+          l[i] = *reinterpret_cast<const uint4*>(w);
+          h[i] = *reinterpret_cast<const uint4*>(w + kMoeBox);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            x[i][j] = make_uint4(0, 0, 0, 0);  // past K's end, and past the expert's tokens
+            if (j * 8 + g < n && (i0 + i) * 32 < left)
+              x[i][j] = *reinterpret_cast<const uint4*>(st + moe_slot(ring, i0 + i, j * 8 + g));
+          }
         }
-      produce(slot);  // the slot has been read
-      if (++slot == kDepth) slot = 0;
+        if (i0 + kHeld == 2) {  // every lane has read what it wants of the stage
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ring.empty + 8 * at.stage);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            if (j * 8 < n) {
+              moe_mma(c[j], l[i].x, h[i].x, l[i].y, h[i].y, x[i][j].x, x[i][j].y);
+              moe_mma(c[j], l[i].z, h[i].z, l[i].w, h[i].w, x[i][j].z, x[i][j].w);
+            }
+      }
+      at.next(ring);
+      tokens.issue();  // into the slots just read
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j * 8 >= n) break;
       float v = moe_reduce(sh, buf, c[j]);
       buf ^= 1;
-      const int up = (threadIdx.x >> 2) & 1, f = (threadIdx.x >> 3) & 7;
-      const int col = j * 8 + (threadIdx.x >> 6);
-      bool write;
-      int feat;
-      if (p.gated) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, 4);  // gate's thread has up
-        v = v * sigmoid_f(v) * o;
-        feat = f0 + f;
-        write = (threadIdx.x & 7) == 0;
-      } else {
-        float z;
-        f2_unpack(gelu_x2(f2_pack(v, v)), v, z);
-        feat = f0 + f + 8 * up;
-        write = (threadIdx.x & 3) == 0;
-      }
-      if (write && col < n && feat < p.Fe) {
-        const int pair = sh.off[e] + col;
-        p.act[static_cast<size_t>(pair) * p.Fe + feat] = __float2bfloat16_rn(v * sh.wpair[pair]);
-      }
-    }
-  }
-}
-
-// ------------------------------------------------------------------ fc2
-// Columns of the products are all T tokens (NT tiles of 8); an expert's step copies and
-// multiplies the tiles in which it has tokens.
-template <int NT>
-struct MoeFc2 {
-  static constexpr int kDepth = kMoeUnits / (2 + NT);
-  static constexpr uint32_t kUnit = kMoeThreads * 16;
-
-  const MoeParams& p;
-  const MoeShared& sh;
-  int g, q, warp, ks, items, steps_total;
-  uint32_t mine;
-  // place of the copies
-  int pi, pa, pk;
-  const __nv_bfloat16 *lo, *hi;
-  bool lo_ok, hi_ok;
-  uint64_t mask;
-  int off;
-
-  __device__ MoeFc2(const MoeParams& p_, const MoeShared& sh_, uint32_t ring) : p(p_), sh(sh_) {
-    const int lane = threadIdx.x & 31;
-    warp = threadIdx.x >> 5;
-    g = lane >> 2;
-    q = lane & 3;
-    ks = (p.Fe + 31) / 32;
-    items = (p.H + 15) / 16;
-    steps_total = sh.n_active * ks;  // of a unit, over all its warps
-    mine = ring + threadIdx.x * 16;
-  }
-  // the first step of this warp: experts in order, steps of K within each
-  __device__ void first(int item) {
-    pi = item;
-    pk = warp;
-    pa = 0;
-    settle();
-  }
-  __device__ void settle() {
-    while (pk >= ks) {
-      pk -= ks;
-      ++pa;
-    }
-    if (pa >= sh.n_active) {  // the unit's steps are done: on to the next one
-      pi += gridDim.x;
-      pk = warp;
-      pa = 0;
-      if (warp >= steps_total) pi = items;  // this warp has no steps at all
-      while (pk >= ks && pi < items) {
-        pk -= ks;
-        ++pa;
-      }
-    }
-    if (pi < items) {
-      const int e = sh.active[pa], r = pi * 16 + g;
-      lo = p.W2 + (static_cast<size_t>(e) * p.H + r) * p.Fe;
-      hi = lo + static_cast<size_t>(8) * p.Fe;
-      lo_ok = r < p.H;
-      hi_ok = r + 8 < p.H;
-      mask = sh.mask[e];
-      off = sh.off[e];
-    }
-  }
-  __device__ __forceinline__ void weights(int slot) const {
-    const int c = pk * 32 + q * 8;
-    const bool in = c < p.Fe;
-    const uint32_t d = mine + slot * (2 + NT) * kUnit;
-    moe_copy(d, lo_ok && in ? lo + c : p.X, lo_ok && in);
-    moe_copy(d + kUnit, hi_ok && in ? hi + c : p.X, hi_ok && in);
-  }
-  __device__ __forceinline__ void tokens(int slot) const {
-    const int c = pk * 32 + q * 8;
-    const bool in = c < p.Fe;
-    const uint32_t d = mine + slot * (2 + NT) * kUnit;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (((mask >> (8 * j)) & 0xffull) == 0ull) continue;
-      const int t = j * 8 + g;
-      const bool ok = in && ((mask >> t) & 1ull) != 0ull;
-      const int s = off + __popcll(mask & ((1ull << t) - 1ull));
-      moe_copy(d + (2 + j) * kUnit, ok ? p.act + static_cast<size_t>(s) * p.Fe + c : p.X, ok);
-    }
-  }
-  __device__ __forceinline__ bool more() const { return pi < items; }
-  __device__ __forceinline__ void next() {
-    pk += kMoeWarps;
-    settle();
-  }
-};
-
-template <int NT>
-__device__ bool moe_fc2(const MoeParams& p, MoeShared& sh, uint32_t ring, const uint8_t* ring_p,
-                        int& buf) {
-  using F = MoeFc2<NT>;
-  constexpr int kDepth = F::kDepth;
-  F f(p, sh, ring);
-  // the first steps' weights do not wait for fc1
-  f.first(blockIdx.x);
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) {
-    if (f.more()) {
-      f.weights(s);
-      f.next();
-    }
-  }
-  moe_commit();
-  if (!moe_grid_barrier(p, sh, 2)) return false;
-  f.first(blockIdx.x);
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) {
-    if (f.more()) {
-      f.tokens(s);
-      f.next();
-    }
-  }
-  moe_commit();
-  moe_wait<0>();
-  const uint8_t* mine_p = ring_p + threadIdx.x * 16;
-  const int steps =
-      f.warp < f.steps_total ? (f.steps_total - f.warp + kMoeWarps - 1) / kMoeWarps : 0;
-  int slot = 0;
-  for (int it = blockIdx.x; it < f.items; it += gridDim.x) {
-    float c[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
-    int a = 0, k = f.warp;
-    for (int st = 0; st < steps; ++st, k += kMoeWarps) {
-      while (k >= f.ks) {
-        k -= f.ks;
-        ++a;
-      }
-      const uint64_t mask = sh.mask[sh.active[a]];
-      moe_wait<kDepth - 1>();
-      const uint8_t* s = mine_p + slot * (2 + NT) * F::kUnit;
-      const uint4 l = *reinterpret_cast<const uint4*>(s);
-      const uint4 h = *reinterpret_cast<const uint4*>(s + F::kUnit);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (((mask >> (8 * j)) & 0xffull) != 0ull) {
-          const uint4 x = *reinterpret_cast<const uint4*>(s + (2 + j) * F::kUnit);
-          moe_mma(c[j], l.x, h.x, l.y, h.y, x.x, x.y);
-          moe_mma(c[j], l.z, h.z, l.w, h.w, x.z, x.w);
+      const int up = moe_thread() & 1, f = (moe_thread() >> 1) & 7;
+      const int t = j * 8 + (moe_thread() >> 4);
+      const size_t s = sh.off[e] + t;
+      if constexpr (kFc1) {
+        int feat = r0 + f;
+        if (p.gated) {
+          const float o = __shfl_xor_sync(0xffffffffu, v, 1);  // the gate's thread gets its up
+          v = v * sigmoid_f(v) * o;
+        } else {
+          float z;
+          f2_unpack(gelu_x2(f2_pack(v, v)), v, z);
+          feat += 8 * up;
         }
-      if (f.more()) {
-        f.weights(slot);
-        f.tokens(slot);
-        f.next();
+        if (t < n && feat < p.Fe && !(p.gated && up))
+          p.act[s * p.Fe + feat] = __float2bfloat16_rn(v);
+      } else {
+        const int r = r0 + f + 8 * up;
+        if (t < n && r < p.H) __stcg(p.pair_y + s * p.H + r, v);
       }
-      moe_commit();
-      if (++slot == kDepth) slot = 0;
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (j * 8 >= p.T) break;
-      const float v = moe_reduce(sh, buf, c[j]);
-      buf ^= 1;
-      const int r = it * 16 + ((threadIdx.x >> 3) & 7) + 8 * ((threadIdx.x >> 2) & 1);
-      const int t = j * 8 + (threadIdx.x >> 6);
-      if ((threadIdx.x & 3) == 0 && t < p.T && r < p.H)
-        p.Y[static_cast<size_t>(t) * p.H + r] = __float2bfloat16_rn(v);
     }
   }
-  return true;
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const MoeParams p) {
-  extern __shared__ __align__(16) uint8_t moe_smem[];
-  MoeShared& sh = *reinterpret_cast<MoeShared*>(moe_smem + kMoeRing);
-  const uint32_t ring = smem_u32(moe_smem);
-  if (threadIdx.x == 0) sh.abort = 0;
-  moe_logits(p, sh);
-  if (moe_grid_barrier(p, sh, 1)) {
-    moe_route(p, sh);
-    int buf = 0;
-    if (sh.most <= 8)
-      moe_fc1<1>(p, sh, ring, moe_smem, buf);
-    else if (sh.most <= 16)
-      moe_fc1<2>(p, sh, ring, moe_smem, buf);
-    else if (sh.most <= 32)
-      moe_fc1<4>(p, sh, ring, moe_smem, buf);
-    else
-      moe_fc1<8>(p, sh, ring, moe_smem, buf);
-    moe_wait<0>();
-    if (p.T <= 8)
-      moe_fc2<1>(p, sh, ring, moe_smem, buf);
-    else if (p.T <= 16)
-      moe_fc2<2>(p, sh, ring, moe_smem, buf);
-    else if (p.T <= 32)
-      moe_fc2<4>(p, sh, ring, moe_smem, buf);
-    else
-      moe_fc2<8>(p, sh, ring, moe_smem, buf);
+template <bool kFc1>
+__device__ __forceinline__ void moe_phase(const MoeParams& p, MoeShared& sh, const MoeRing& ring,
+                                          const WaitCtx& wc, MoePlace& at, int& buf, bool& dead,
+                                          uint32_t barrier) {
+  if (sh.most <= 8)
+    moe_multiply<1, kFc1>(p, sh, ring, wc, at, buf, dead);
+  else if (sh.most <= 16)
+    moe_multiply<2, kFc1>(p, sh, ring, wc, at, buf, dead);
+  else if (sh.most <= 32)
+    moe_multiply<4, kFc1>(p, sh, ring, wc, at, buf, dead);
+  else
+    moe_multiply<8, kFc1>(p, sh, ring, wc, at, buf, dead);
+  moe_sync();  // the CTA's results are written
+  if (threadIdx.x == 0) {
+    moe_grid_arrive(p);
+    moe_grid_wait(p, sh, barrier);
   }
-  moe_wait<0>();
-  // the last CTA out leaves the barrier's words as it found them, after an expired wait too
+  moe_sync();
+}
+
+// Y_t = sum over t's pairs, in the order of its choices, of w y.
+__device__ __forceinline__ void moe_combine(const MoeParams& p, const MoeShared& sh) {
+  const int per = p.H / 8;
+  for (int i = blockIdx.x * kMoeThreads + threadIdx.x; i < p.T * per; i += gridDim.x * kMoeThreads) {
+    const int t = i / per, c = (i - t * per) * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < p.K; ++k) {
+      const float w = sh.w[t * p.K + k];
+      const float4* y = reinterpret_cast<const float4*>(
+          p.pair_y + static_cast<size_t>(sh.slot[t * p.K + k]) * p.H + c);
+      const float4 a = __ldcg(y), b = __ldcg(y + 1);
+      v[0] = fmaf(w, a.x, v[0]); v[1] = fmaf(w, a.y, v[1]);
+      v[2] = fmaf(w, a.z, v[2]); v[3] = fmaf(w, a.w, v[3]);
+      v[4] = fmaf(w, b.x, v[4]); v[5] = fmaf(w, b.y, v[5]);
+      v[6] = fmaf(w, b.z, v[6]); v[7] = fmaf(w, b.w, v[7]);
+    }
+    st_global_v4(p.Y + static_cast<size_t>(t) * p.H + c,
+                 make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  }
+}
+
+__global__ void __launch_bounds__(kMoeBlock, 1)
+    moe_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w2,
+               const MoeParams p) {
+  extern __shared__ __align__(128) uint8_t moe_smem[];
+  MoeShared& sh = *reinterpret_cast<MoeShared*>(moe_smem + kMoeGroups * kMoeRing);
+  const bool multiplies = threadIdx.x < kMoeThreads;
+  if (threadIdx.x == 0) sh.abort = 0u;
+  if (multiplies) moe_logits(p, sh);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    moe_grid_arrive(p);
+    if (!moe_grid_wait(p, sh, 1)) {  // it will not come to the other barriers
+      moe_grid_arrive(p);
+      moe_grid_arrive(p);
+    }
+  }
+  __syncthreads();
+  if (sh.abort == 0u) {
+    if (multiplies) moe_route(p, sh);
+    __syncthreads();
+    const int group = multiplies ? moe_group() : (threadIdx.x - kMoeThreads) >> 5;
+    const MoeRing ring(moe_smem, sh, group);
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kMoeGroups; ++i)
+        for (int s = 0; s < ring.stages; ++s) {
+          mbar_init(smem_u32(&sh.full[i][s]), 1);
+          mbar_init(smem_u32(&sh.empty[i][s]), 4);
+        }
+      mbar_fence_init();
+    }
+    __syncthreads();
+    const WaitCtx wc{&sh.abort, &p.sync->err, p.wait_ns};
+    if (multiplies) {
+      MoePlace at;
+      int buf = 0;
+      bool dead = false;
+      moe_phase<true>(p, sh, ring, wc, at, buf, dead, 2);
+      moe_phase<false>(p, sh, ring, wc, at, buf, dead, 3);
+      moe_combine(p, sh);
+    } else if ((threadIdx.x & 31) == 0) {
+      moe_copy_thread(p, sh, ring, wc, &map_w1, &map_w2, group);
+    }
+  }
+  // the last CTA out leaves the barriers' word as it found it, after an expired wait too
   __syncthreads();
   if (threadIdx.x == 0 && atomicAdd(&p.sync->done, 1u) == gridDim.x - 1) {
     p.sync->arrived = 0u;
@@ -642,10 +706,26 @@ struct mlpb_moe {
   mlpb_moe_config cfg;
   int device, grid;
   MoeSync* sync;
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
 };
+
+// A row-major bf16 matrix in boxes of 8 rows by 256 columns; what is past its edges reads zero.
+static bool moe_map(const mlpb_moe* h, CUtensorMap* m, const void* base, uint64_t rows,
+                    uint64_t cols) {
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {kMoeKc, kMoeBoxRows}, steps[2] = {1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                   box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 static size_t moe_logits_bytes(const mlpb_moe_config& c) {
   return moe_align(static_cast<size_t>(c.max_tokens) * c.experts * 4);
+}
+
+static size_t moe_act_bytes(const mlpb_moe_config& c) {
+  return moe_align(static_cast<size_t>(c.max_tokens) * c.topk * c.ffn * 2);
 }
 
 extern "C" mlpb_status mlpb_moe_create(const mlpb_moe_config* cfg, mlpb_moe** out) {
@@ -676,9 +756,18 @@ extern "C" mlpb_status mlpb_moe_create(const mlpb_moe_config* cfg, mlpb_moe** ou
     delete h;
     return MLPB_EUNSUPPORTED;
   }
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found{};
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess || fn == nullptr) {
+    delete h;
+    return MLPB_ECUDA;
+  }
+  h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   if (cudaFuncSetAttribute(moe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kMoeSmem)) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moe_kernel, kMoeThreads, kMoeSmem) !=
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moe_kernel, kMoeBlock, kMoeSmem) !=
           cudaSuccess ||
       per_sm < 1 || cudaMalloc(reinterpret_cast<void**>(&h->sync), sizeof(MoeSync)) != cudaSuccess ||
       cudaMemset(h->sync, 0, sizeof(MoeSync)) != cudaSuccess) {
@@ -700,7 +789,8 @@ extern "C" void mlpb_moe_destroy(mlpb_moe* h) {
 extern "C" mlpb_status mlpb_moe_workspace_size(const mlpb_moe* h, size_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MLPB_EINVAL;
   const mlpb_moe_config& c = h->cfg;
-  *bytes = moe_logits_bytes(c) + moe_align(static_cast<size_t>(c.max_tokens) * c.topk * c.ffn * 2);
+  *bytes = moe_logits_bytes(c) + moe_act_bytes(c) +
+           moe_align(static_cast<size_t>(c.max_tokens) * c.topk * c.hidden * 4);
   return MLPB_OK;
 }
 
@@ -729,7 +819,9 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
   p.ids = ids;
   p.weights = weights;
   p.logits = static_cast<float*>(workspace);
-  p.act = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + moe_logits_bytes(c));
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + moe_logits_bytes(c);
+  p.act = reinterpret_cast<__nv_bfloat16*>(ws);
+  p.pair_y = reinterpret_cast<float*>(ws + moe_act_bytes(c));
   p.T = static_cast<int>(tokens);
   p.H = static_cast<int>(c.hidden);
   p.Fe = static_cast<int>(c.ffn);
@@ -739,9 +831,14 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
   p.normalize = c.normalize;
   p.sync = h->sync;
   p.wait_ns = kDefaultWaitNs;
+  CUtensorMap m1, m2;
+  const uint64_t f1 = static_cast<uint64_t>(c.ffn) * (p.gated ? 2 : 1);
+  if (!moe_map(h, &m1, W1, c.experts * f1, c.hidden) ||
+      !moe_map(h, &m2, W2, static_cast<uint64_t>(c.experts) * c.hidden, c.ffn))
+    return MLPB_EINVAL;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(h->grid));
-  cfg.blockDim = dim3(kMoeThreads);
+  cfg.blockDim = dim3(kMoeBlock);
   cfg.dynamicSmemBytes = kMoeSmem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -749,7 +846,7 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_kernel, p) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
+  return cudaLaunchKernelEx(&cfg, moe_kernel, m1, m2, p) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
 }
 
 extern "C" mlpb_status mlpb_moe_last_device_error(mlpb_moe* h, mlpb_stream_t stream) {
