@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libmlpb.so")
 SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_bwd.cu", "reduce.cu", "layernorm.cu",
            "reduce_noalloc.cu", "fp8.cu", "gemm_fp8.cu", "gemm_ckpt8.cu", "act8.cu",
-           "join.cu", "join_fwd.cu", "join_bwd.cu", "join_bwd_split.cu",
+           "join.cu", "join_bf16.cu", "join_y32.cu", "join_x32.cu", "join_f32.cu",
            "moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -73,12 +73,12 @@ struct JoinPlan {
 
 static size_t join_align(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// The backward's CTAs (as many as its registers let run at once, 512 threads an SM) and its
-// partial rows in the workspace.
+// The backward's CTAs (as many as run at once, 512 threads an SM) and its partial rows in the
+// workspace.
 static JoinPlan join_plan(const mlpb_join_config& c, int num_sms) {
   JoinPlan q{};
-  const int threads = join_threads(join_tpr(c.hidden)), rows = threads / join_tpr(c.hidden);
-  const int target = num_sms * (threads <= 256 ? 2 : 1);
+  const int wpr = join_bwd_wpr(c.hidden), rows = join_rows(wpr);
+  const int target = num_sms * (512 / join_threads(wpr));
   const int64_t groups = std::max<int64_t>(1, c.gate_groups);
   const int64_t per = groups > 0 ? c.tokens / groups : 0;  // rows of a group
   const int64_t want = std::max<int64_t>(1, (per + rows - 1) / rows);
@@ -204,9 +204,13 @@ extern "C" mlpb_status mlpb_join_fwd(const mlpb_join_config* cfg, const void* X,
   p.Xout = Xout;
   p.Xn = static_cast<bf*>(Xn);
   p.stats = stats;
-  const cudaError_t e = launch_join_fwd(p, (c.flags & MLPB_JOIN_STREAM_F32) != 0,
-                                        (c.flags & MLPB_JOIN_BLOCK_F32) != 0, sms,
-                                        reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool y32 = (c.flags & MLPB_JOIN_BLOCK_F32) != 0;
+  const cudaError_t e = (c.flags & MLPB_JOIN_STREAM_F32) != 0
+                            ? (y32 ? join_fwd_run<float, float>(p, sms, s)
+                                   : join_fwd_run<float, bf>(p, sms, s))
+                            : (y32 ? join_fwd_run<bf, float>(p, sms, s)
+                                   : join_fwd_run<bf, bf>(p, sms, s));
   return e == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
 }
 
@@ -284,10 +288,12 @@ extern "C" mlpb_status mlpb_join_bwd(const mlpb_join_config* cfg, const void* X,
   p.part_gpre = part(pre, q.o_gpre);
   p.part_bpre = part(pre_ln, q.o_bpre);
   p.part_alpha = part(res_scale != nullptr, q.o_alpha);
-  const bool x32 = (c.flags & MLPB_JOIN_STREAM_F32) != 0;
   const bool y32 = (c.flags & MLPB_JOIN_BLOCK_F32) != 0;
-  cudaError_t e = x32 || y32 ? launch_join_bwd_split(p, x32, y32, q.grid, s)
-                             : launch_join_bwd_bf16(p, q.grid, s);
+  cudaError_t e = (c.flags & MLPB_JOIN_STREAM_F32) != 0
+                      ? (y32 ? join_bwd_run<float, float>(p, q.grid, s)
+                             : join_bwd_run<float, bf>(p, q.grid, s))
+                      : (y32 ? join_bwd_run<bf, float>(p, q.grid, s)
+                             : join_bwd_run<bf, bf>(p, q.grid, s));
   if (e != cudaSuccess) return MLPB_ECUDA;
   JoinSums r{};
   auto want = [&](const float* from, float* to) {

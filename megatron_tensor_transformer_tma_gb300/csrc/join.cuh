@@ -13,10 +13,14 @@
 // layernorm.cu, needs one more barrier a row, and waits that can expire, for which these calls
 // have no handle to report to.)
 //
-// A row belongs to kTpr threads (32 to 1024, 16 of its elements each); a CTA of 256 or more
-// threads holds kRows of them.  The norms' parameters are read again for every row: the data
-// bypasses L1 (cp.async.cg, or the streaming reads of one line by one warp), so they stay
-// there, and the registers stay free.
+// Per element the arithmetic is 15 (forward) to 25 (backward) instructions in f32x2 pairs, so
+// what else a thread does for a row -- addresses, shuffles, barriers -- is spread over as many
+// elements as its registers hold: 32 of a row in the forward, 16 in the backward, which keeps
+// column sums too.  (8 a thread, with twice to four times the threads: the backward of T 8192
+// H 8192 took 95 instructions an element and 290 us.)  And the usual call -- both norms, every
+// warp's columns all inside the row -- has an instantiation of its own (kPlain) without the
+// masks and the checks of what there is, which are half of the general one's instructions.  A
+// CTA of up to 256 threads holds several rows where a row needs fewer.
 #pragma once
 
 #include <algorithm>
@@ -24,10 +28,10 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pointwise.cuh"
 
 namespace mlpb {
 
-constexpr int kJoinVpt = 2;  // vectors of 8 elements a thread
 constexpr int kJoinMaxBuf = 3;
 
 struct JoinParams {
@@ -59,14 +63,18 @@ struct JoinParams {
   bool direct_late;      // X and dXout are not in the ring (it would not fit)
 };
 
-// Threads of a row: 16 elements each, at least a warp (H <= 16384).
-inline int join_tpr(int64_t H) {
-  int t = 32;
-  while (t < 1024 && static_cast<int64_t>(t) * kJoinVpt * 8 < H) t *= 2;
-  return t;
-}
+// Rows and threads of a CTA with `wpr` warps a row.
+constexpr int join_rows(int wpr) { return wpr >= 8 ? 1 : 8 / wpr; }
+constexpr int join_threads(int wpr) { return 32 * wpr * join_rows(wpr); }
 
-constexpr int join_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+// Warps of a row, of those that there are kernels for: 256 elements each up to H 256, else 1024
+// in the forward and 512 (above 8192 1024) in the backward; 5 and 10 for H 5120.
+inline int join_fwd_wpr(int64_t H) {
+  return H <= 1024 ? 1 : H <= 2048 ? 2 : H <= 4096 ? 4 : H == 5120 ? 5 : H <= 8192 ? 8 : 16;
+}
+inline int join_bwd_wpr(int64_t H) {
+  return H <= 256 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 4096 ? 8 : H == 5120 ? 10 : 16;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -87,186 +95,171 @@ __device__ __forceinline__ void cp_async_wait_ring(int nbuf) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Which elements of a row a thread holds.  All bf16: 8 consecutive ones a vector (16 bytes).
-// Where a tensor is fp32 (kSplit), 4 + 4 of them 128 apart, so that a warp's 16-byte accesses
-// to it are consecutive too: a 32-byte sector read in two halves by two instructions would
-// cross L2 twice.
-template <bool kSplit, int kTpr>
+// Which elements of a row a thread holds: kVpt vectors of 8, as halves of 4.  All bf16: a
+// vector is 8 consecutive elements (16 bytes).  Where a tensor is fp32 (kSplit), its halves are
+// 128 apart, so that a warp's 16-byte accesses to it are consecutive too: a 32-byte sector read
+// in two halves by two instructions would cross L2 twice.  Half h starts at c[h], and is all
+// inside the row or not at all; with kFull, all are.
+template <bool kSplit, int kVpt, bool kFull>
 struct JoinCols {
-  int c[kJoinVpt][2];
-  bool ok[kJoinVpt][2];
-  __device__ __forceinline__ JoinCols(int tr, int H) {
+  int c[2 * kVpt], H;
+  __device__ __forceinline__ JoinCols(int wpr, int H_) : H(H_) {
+    const int warp = (threadIdx.x / 32) % wpr, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < kJoinVpt; ++k) {
-      if constexpr (kSplit) {
-        c[k][0] = (k * kTpr + (tr & ~31)) * 8 + (tr & 31) * 4;
-        c[k][1] = c[k][0] + 128;
-      } else {
-        c[k][0] = (k * kTpr + tr) * 8;
-        c[k][1] = c[k][0] + 4;
-      }
-      ok[k][0] = c[k][0] < H;
-      ok[k][1] = c[k][1] < H;
+    for (int k = 0; k < kVpt; ++k) {
+      const int v = (k * wpr + warp) * 256;
+      c[2 * k] = v + (kSplit ? lane * 4 : lane * 8);
+      c[2 * k + 1] = c[2 * k] + (kSplit ? 128 : 4);
     }
   }
+  __device__ __forceinline__ bool ok(int h) const { return kFull || c[h] < H; }
 };
 
-// Bytes of a thread's slots for one row of a tensor of type E.
-template <class E>
-constexpr int join_slot() {
-  return kJoinVpt * 8 * static_cast<int>(sizeof(E));
+// Eight values as four f32x2 pairs (elements 0 and 1, 2 and 3, ...): two to a half.
+using JoinVec = uint64_t[4];
+
+__device__ __forceinline__ uint64_t join_pair(uint32_t w) {  // two bf16
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t join_twice(float f) { return f2_pack(f, f); }
+__device__ __forceinline__ float join_add_pair(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ void join_unpack(const uint4& u, JoinVec& v) {
+  v[0] = join_pair(u.x);
+  v[1] = join_pair(u.y);
+  v[2] = join_pair(u.z);
+  v[3] = join_pair(u.w);
+}
+__device__ __forceinline__ void join_unpack_half(uint2 u, uint64_t* v) {
+  v[0] = join_pair(u.x);
+  v[1] = join_pair(u.y);
+}
+__device__ __forceinline__ void join_unpack_half(float4 u, uint64_t* v) {
+  v[0] = f2_pack(u.x, u.y);
+  v[1] = f2_pack(u.z, u.w);
 }
 
-// Starts the copy of this thread's elements of a row into its slots at `dst` (the address of
-// thread 0's; `nt` threads side by side).
-template <class E, bool kSplit, int kTpr>
-__device__ __forceinline__ void join_copy(uint32_t dst, int nt, const E* row,
-                                          const JoinCols<kSplit, kTpr>& jc) {
-  constexpr int kHalf = 4 * static_cast<int>(sizeof(E));  // bytes of four elements
+// Bytes of a warp's slots for one row of a tensor of type E: vector by vector, half by half
+// where it is split, the lanes side by side.
+template <class E, int kVpt>
+constexpr uint32_t join_slots() {
+  return 32 * kVpt * 8 * static_cast<uint32_t>(sizeof(E));
+}
+
+// Starts the copy of this thread's elements of a row into its slots of the warp's at `dst`.
+template <class E, bool kSplit, int kVpt, bool kFull>
+__device__ __forceinline__ void join_copy(uint32_t dst, const E* row,
+                                          const JoinCols<kSplit, kVpt, kFull>& jc) {
+  constexpr int kHalf = 4 * static_cast<int>(sizeof(E));  // bytes of a half
+  const uint32_t lane = threadIdx.x & 31;
+  if constexpr (!kSplit) {
+    static_assert(kHalf == 8, "8 consecutive elements are bf16");
 #pragma unroll
-  for (int k = 0; k < kJoinVpt; ++k) {
-    if constexpr (!kSplit) {
-      static_assert(kHalf == 8, "8 consecutive elements are bf16");
-      if (jc.ok[k][0]) cp_async16(dst + (k * nt + threadIdx.x) * 16, row + jc.c[k][0]);
-    } else {
+    for (int k = 0; k < kVpt; ++k)
+      if (jc.ok(2 * k)) cp_async16(dst + (k * 32 + lane) * 16, row + jc.c[2 * k]);
+  } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t d = dst + ((k * 2 + h) * nt + threadIdx.x) * kHalf;
-        if (jc.ok[k][h]) {
-          if constexpr (kHalf == 16)
-            cp_async16(d, row + jc.c[k][h]);
-          else
-            cp_async8(d, row + jc.c[k][h]);
-        }
+    for (int h = 0; h < 2 * kVpt; ++h)
+      if (jc.ok(h)) {
+        if constexpr (kHalf == 16)
+          cp_async16(dst + (h * 32 + lane) * 16, row + jc.c[h]);
+        else
+          cp_async8(dst + (h * 32 + lane) * 8, row + jc.c[h]);
       }
-    }
   }
-}
-
-__device__ __forceinline__ void join_unpack4(uint2 u, float* v) {
-  const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = b.x;
-  v[3] = b.y;
-}
-
-__device__ __forceinline__ void join_unpack4(float4 u, float* v) {
-  v[0] = u.x;
-  v[1] = u.y;
-  v[2] = u.z;
-  v[3] = u.w;
 }
 
 // Vector k of the thread's elements from its slots (zeros past the row's end).
-template <class E, bool kSplit, int kTpr>
-__device__ __forceinline__ void join_read(const uint8_t* src, int nt, int k,
-                                          const JoinCols<kSplit, kTpr>& jc, float (&v)[8]) {
+template <class E, bool kSplit, int kVpt, bool kFull>
+__device__ __forceinline__ void join_read(const uint8_t* src, int k,
+                                          const JoinCols<kSplit, kVpt, kFull>& jc, JoinVec& v) {
+  const uint32_t lane = threadIdx.x & 31;
   if constexpr (!kSplit) {
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (jc.ok[k][0])
-      u = *reinterpret_cast<const uint4*>(src + (k * nt + threadIdx.x) * 16);
-    join_unpack4(make_uint2(u.x, u.y), v);
-    join_unpack4(make_uint2(u.z, u.w), v + 4);
+    if (jc.ok(2 * k)) u = *reinterpret_cast<const uint4*>(src + (k * 32 + lane) * 16);
+    join_unpack(u, v);
   } else {
     using U = typename std::conditional<sizeof(E) == 4, float4, uint2>::type;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       U u{};
-      if (jc.ok[k][h])
-        u = *reinterpret_cast<const U*>(src + ((k * 2 + h) * nt + threadIdx.x) * sizeof(U));
-      join_unpack4(u, v + 4 * h);
+      if (jc.ok(2 * k + h))
+        u = *reinterpret_cast<const U*>(src + ((2 * k + h) * 32 + lane) * sizeof(U));
+      join_unpack_half(u, v + 2 * h);
     }
   }
 }
 
-// Vector k of a row in global memory.  kParam: a read-only parameter; otherwise a tensor that
-// this thread may overwrite afterwards.
-template <class E, bool kSplit, int kTpr, bool kParam>
-__device__ __forceinline__ void join_load(const E* row, int k, const JoinCols<kSplit, kTpr>& jc,
-                                          float (&v)[8]) {
-  if constexpr (!kSplit) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (jc.ok[k][0]) {
-      const uint4* q = reinterpret_cast<const uint4*>(row + jc.c[k][0]);
-      u = kParam ? __ldg(q) : *q;
-    }
-    join_unpack4(make_uint2(u.x, u.y), v);
-    join_unpack4(make_uint2(u.z, u.w), v + 4);
-  } else {
-    using U = typename std::conditional<sizeof(E) == 4, float4, uint2>::type;
+// Vector k of a row of a tensor that this thread may overwrite afterwards.
+template <class E, bool kSplit, int kVpt, bool kFull>
+__device__ __forceinline__ void join_load(const E* row, int k,
+                                          const JoinCols<kSplit, kVpt, kFull>& jc, JoinVec& v) {
+  using U = typename std::conditional<sizeof(E) == 4, float4, uint2>::type;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      U u{};
-      if (jc.ok[k][h]) {
-        const U* q = reinterpret_cast<const U*>(row + jc.c[k][h]);
-        u = kParam ? __ldg(q) : *q;
-      }
-      join_unpack4(u, v + 4 * h);
-    }
+  for (int h = 0; h < 2; ++h) {
+    U u{};
+    if (jc.ok(2 * k + h)) u = *reinterpret_cast<const U*>(row + jc.c[2 * k + h]);
+    join_unpack_half(u, v + 2 * h);
   }
 }
 
-// Writes vector k of a row; for bf16 `v` becomes what was stored.
-template <class E, bool kSplit, int kTpr>
-__device__ __forceinline__ void join_store(E* row, int k, const JoinCols<kSplit, kTpr>& jc,
-                                           float (&v)[8]) {
+// Vector k of a parameter, packed (zeros past its end, and where there is none).
+template <bool kSplit, int kVpt, bool kFull>
+__device__ __forceinline__ uint4 join_param(const __nv_bfloat16* p, int k,
+                                            const JoinCols<kSplit, kVpt, kFull>& jc) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (p == nullptr) return u;
+  if constexpr (!kSplit) {
+    if (jc.ok(2 * k)) u = ld_global_nc_v4(p + jc.c[2 * k]);
+  } else {
+    if (jc.ok(2 * k)) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + jc.c[2 * k]));
+      u.x = a.x;
+      u.y = a.y;
+    }
+    if (jc.ok(2 * k + 1)) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + jc.c[2 * k + 1]));
+      u.z = a.x;
+      u.w = a.y;
+    }
+  }
+  return u;
+}
+
+// Writes vector k of a row; with kBack, `v` becomes what was stored.
+template <class E, bool kBack, bool kSplit, int kVpt, bool kFull>
+__device__ __forceinline__ void join_store(E* row, int k, const JoinCols<kSplit, kVpt, kFull>& jc,
+                                           JoinVec& v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(v[i], f[2 * i], f[2 * i + 1]);
   if constexpr (sizeof(E) == 4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (jc.ok[k][h])
-        *reinterpret_cast<float4*>(row + jc.c[k][h]) =
-            make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      if (jc.ok(2 * k + h))
+        *reinterpret_cast<float4*>(row + jc.c[2 * k + h]) =
+            make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
   } else {
-    uint2 u[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u[h] = make_uint2(pack_bf16x2(v[4 * h], v[4 * h + 1]), pack_bf16x2(v[4 * h + 2], v[4 * h + 3]));
-      join_unpack4(u[h], v + 4 * h);
-    }
+    const uint4 u = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
     if constexpr (!kSplit) {
-      if (jc.ok[k][0])
-        st_global_v4(row + jc.c[k][0], make_uint4(u[0].x, u[0].y, u[1].x, u[1].y));
+      if (jc.ok(2 * k)) st_global_v4(row + jc.c[2 * k], u);
     } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (jc.ok[k][h]) *reinterpret_cast<uint2*>(row + jc.c[k][h]) = u[h];
+      if (jc.ok(2 * k)) *reinterpret_cast<uint2*>(row + jc.c[2 * k]) = make_uint2(u.x, u.y);
+      if (jc.ok(2 * k + 1)) *reinterpret_cast<uint2*>(row + jc.c[2 * k + 1]) = make_uint2(u.z, u.w);
     }
+    if constexpr (kBack) join_unpack(u, v);
   }
 }
 
-// Adds NV (1 or 2) values over the kTpr threads of a row, in a fixed order.  `sh` holds two
-// float2 for every warp of the CTA; consecutive calls use them in turn (`par`), so one barrier
-// a call is enough: who writes a place again has passed a barrier that every reader of it
-// reached after reading.
-template <int kTpr, int NV>
-__device__ __forceinline__ void join_sum(float (&v)[NV], float2* sh, int& par) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if constexpr (kTpr > 32) {
-    constexpr int kWarps = kTpr / 32;
-    const int group = threadIdx.x / kTpr;
-    float2* slot = sh + par * (join_threads(kTpr) / 32) + group * kWarps;
-    par ^= 1;
-    if ((threadIdx.x & 31) == 0)
-      slot[(threadIdx.x / 32) % kWarps] = make_float2(v[0], NV > 1 ? v[NV - 1] : 0.f);
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kTpr) : "memory");
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 s = slot[w];
-      v[0] += s.x;
-      if (NV > 1) v[NV - 1] += s.y;
-    }
-  }
-}
+constexpr int kJoinMaxWarps = 16;
 
-cudaError_t launch_join_fwd(const JoinParams& p, bool x32, bool y32, int num_sms, cudaStream_t s);
-cudaError_t launch_join_bwd_bf16(const JoinParams& p, int grid, cudaStream_t s);
-cudaError_t launch_join_bwd_split(const JoinParams& p, bool x32, bool y32, int grid,
-                                  cudaStream_t s);
+template <class XT, class YT>
+cudaError_t join_fwd_run(const JoinParams& p, int num_sms, cudaStream_t s);
+template <class XT, class YT>
+cudaError_t join_bwd_run(const JoinParams& p, int grid, cudaStream_t s);
 
 }  // namespace mlpb

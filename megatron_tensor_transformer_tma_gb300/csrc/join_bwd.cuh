@@ -1,9 +1,15 @@
-// Backward of the join between two blocks (join.cuh): the kernel and its launcher; the
-// translation units instantiate it for their types.
+// Backward of the join between two blocks (join.cuh): the kernel and its launcher; join_*.cu
+// instantiate them for their types.
 //
-// Two reductions a row: g = dXn gamma_pre gives mean(g), mean(g xh) and with them
-// dh = dXout + rstd_h (g - mean g - xh mean(g xh)); then u = gate dh gamma_post gives
-// mean(u), mean(u yh) and dY.
+// With g = dXn gamma_pre, t = dXout + rstd_h g and w = gate gamma_post,
+//   dh = t - rstd_h (mean g + xh mean(g xh)),  u = w dh,  dY = rstd_y (u - mean u - yh mean(u yh))
+// (the plain means with LayerNorm only).  mean(u yh) looks as if it had to wait for dh and so for
+// the first means, but it is linear in them:
+//   sum u yh = sum w yh t - rstd_h (mean g sum w yh + mean(g xh) sum w yh xh),
+// and sum u alike.  So a row takes one pass for all its sums (3, or 7 with LayerNorm), one
+// reduction, and one pass for what it writes.  (Two reductions, one after the other, cost a
+// row of H 8192 about 0.9 us of 3.5.)  xh and t stay in registers between the passes (kKeep);
+// with LayerNorm's twice as many column sums, or 32 columns a thread, they are computed again.
 //
 // The parameters' gradients need only four sums over rows for each column: sum dXn xh and
 // sum dXn (the pre-norm's), and, within one gate group, S1 = sum dh yh and S0 = sum dh:
@@ -21,99 +27,144 @@
 
 namespace mlpb {
 
-// Adds the kRows rows' accumulators of a column up, over the CTA's groups of threads, in row
-// order (the ring's shared memory is free by then: every copy has been waited for, since each
-// thread's last wait left only groups of rows past the end, which copied nothing).
-template <int kTpr>
-__device__ __forceinline__ void join_combine(float (&v)[kJoinVpt][8]) {
-  constexpr int NT = join_threads(kTpr), kRows = NT / kTpr;
-  if constexpr (kRows > 1) {
-    extern __shared__ __align__(16) uint8_t join_smem[];
-    float* acc = reinterpret_cast<float*>(join_smem);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+// Adds a CTA's rows' accumulators of a column up, in row order, for the first row's warps (the
+// ring's shared memory is free by then: every copy has been waited for, since each thread's last
+// wait left only groups of rows past the end, which copied nothing).
+template <int rows, int kVpt>
+__device__ __forceinline__ void join_combine(JoinVec (&v)[kVpt]) {
+  if constexpr (rows == 1) return;
+  extern __shared__ __align__(16) uint8_t join_smem[];
+  uint64_t* acc = reinterpret_cast<uint64_t*>(join_smem) + threadIdx.x;
+  const int nt = blockDim.x, tpr = nt / rows;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kJoinVpt * 8; ++i) acc[i * NT + threadIdx.x] = v[i / 8][i % 8];
-    __syncthreads();
-    const int tr = threadIdx.x % kTpr;
+  for (int i = 0; i < kVpt * 4; ++i) acc[i * nt] = v[i / 4][i % 4];
+  __syncthreads();
+  if (threadIdx.x < tpr)
+    for (int r = 1; r < rows; ++r)
 #pragma unroll
-    for (int i = 0; i < kJoinVpt * 8; ++i) {
-      float t = 0.f;
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) t += acc[i * NT + r * kTpr + tr];
-      v[i / 8][i % 8] = t;
-    }
-    __syncthreads();
-  }
+      for (int i = 0; i < kVpt * 4; ++i)
+        v[i / 4][i % 4] = f2_add(v[i / 4][i % 4], acc[i * nt + r * tpr]);
+  __syncthreads();
 }
 
 // A row's vector k of fp32 values at `row` (+= with add).
-template <bool kSplit, int kTpr>
-__device__ __forceinline__ void join_put(float* row, int k, const JoinCols<kSplit, kTpr>& jc,
-                                         const float (&v)[8], bool add) {
+template <bool kSplit, int kVpt, bool kFull>
+__device__ __forceinline__ void join_put(float* row, int k, const JoinCols<kSplit, kVpt, kFull>& jc,
+                                         const JoinVec& v, bool add) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (!jc.ok[k][h]) continue;
-    float4* q = reinterpret_cast<float4*>(row + jc.c[k][h]);
-    float4 o = add ? *q : make_float4(0.f, 0.f, 0.f, 0.f);
-    o.x += v[4 * h];
-    o.y += v[4 * h + 1];
-    o.z += v[4 * h + 2];
-    o.w += v[4 * h + 3];
+    if (!jc.ok(2 * k + h)) continue;
+    float4* q = reinterpret_cast<float4*>(row + jc.c[2 * k + h]);
+    float4 o = add ? *q : make_float4(0.f, 0.f, 0.f, 0.f), t;
+    f2_unpack(v[2 * h], t.x, t.y);
+    f2_unpack(v[2 * h + 1], t.z, t.w);
+    o.x += t.x;
+    o.y += t.y;
+    o.z += t.z;
+    o.w += t.w;
     *q = o;
   }
 }
 
-template <class XT, class YT, int kTpr, bool kBeta>
-__global__ void __launch_bounds__(join_threads(kTpr), kTpr <= 512 ? 512 / join_threads(kTpr) : 1)
+// Adds NV values over the wpr warps of a row, in a fixed order; one barrier, as join_sum.  The
+// shuffles of a warp's sums give away half of the values a lane still has, so that 8 values take
+// 9 of them, not 40; a lane then owns one value, and after the barrier adds up every eighth (or
+// fourth) warp's.
+template <int wpr, int NV>
+__device__ __forceinline__ void join_sums(float (&v)[NV], float (*sh)[kJoinMaxWarps][8], int& par) {
+  constexpr int P = NV <= 4 ? 4 : 8, kLanes = 32 / P;  // lanes of a value
+  const int lane = threadIdx.x & 31, own = lane / kLanes;
+  float t[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) t[i] = i < NV ? v[i] : 0.f;
+#pragma unroll
+  for (int w = P / 2, o = 16; w >= 1; w >>= 1, o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? t[i] : t[i + w], keep = up ? t[i + w] : t[i];
+      t[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
+  if constexpr (wpr > 1) {
+    const int warp = threadIdx.x / 32, row = warp / wpr;
+    if (lane % kLanes == 0) sh[par][warp][own] = t[0];
+    asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "n"(wpr * 32) : "memory");
+    t[0] = 0.f;
+#pragma unroll
+    for (int w0 = 0; w0 < wpr; w0 += kLanes) {
+      const int w = w0 + lane % kLanes;
+      if (w < wpr) t[0] += sh[par][row * wpr + w][own];
+    }
+    par ^= 1;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, t[0], i * kLanes);
+}
+
+template <class XT, class YT, int kVpt, int kWpr, bool kBeta, bool kPlain>
+__global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
     join_bwd_kernel(const JoinParams p) {
-  constexpr int NT = join_threads(kTpr);
-  constexpr int kRows = NT / kTpr;
   constexpr bool kSplit = sizeof(XT) == 4 || sizeof(YT) == 4;
+  constexpr bool kKeep = !kBeta && kVpt <= 2;
   using bf = __nv_bfloat16;
   extern __shared__ __align__(16) uint8_t join_smem[];
-  __shared__ float2 sh[2 * NT / 32];
-  const int tr = threadIdx.x % kTpr;
-  const int sub = threadIdx.x / kTpr;
-  const JoinCols<kSplit, kTpr> jc(tr, p.H);
-  const bool has_pre = p.pre != MLPB_NORM_NONE, has_post = p.post != MLPB_NORM_NONE;
+  constexpr int kSums = kBeta ? 7 : 3;
+  __shared__ float sh[2][kJoinMaxWarps][8];
+  constexpr int rows = join_rows(kWpr);
+  const int warp = threadIdx.x / 32, sub = warp / kWpr;
+  const JoinCols<kSplit, kVpt, kPlain> jc(kWpr, p.H);
+  const bool has_block = kPlain || p.has_block;
+  const bool has_pre = kPlain || p.pre != MLPB_NORM_NONE;
+  const bool has_post = kPlain || p.post != MLPB_NORM_NONE;
   const bool need_y = has_post || p.gate != nullptr;
+  const bool has_dxout = kPlain || p.dXout != nullptr;
   const bool need_x = p.part_alpha != nullptr;
-  const bool late_ring = !p.direct_late;
+  const bool late_ring = kPlain || !p.direct_late;
 
-  // the slots of a stage: Xout, dXn, Y, dXout, X (those that are read)
+  // a warp's slots of a stage: Xout, dXn, Y, dXout, X (those that are read)
+  constexpr uint32_t kXs = join_slots<XT, kVpt>(), kYs = join_slots<YT, kVpt>();
   uint32_t off = 0;
-  const uint32_t o_xout = off;
-  off += has_pre ? NT * join_slot<XT>() : 0;
-  const uint32_t o_dxn = off;
-  off += has_pre ? NT * join_slot<YT>() : 0;
+  const uint32_t o_xout = off, o_dxn = off + kXs;
+  off += has_pre ? kXs + kYs : 0;
   const uint32_t o_y = off;
-  off += need_y ? NT * join_slot<YT>() : 0;
+  off += need_y ? kYs : 0;
   const uint32_t o_dxout = off;
-  off += late_ring && p.dXout ? NT * join_slot<XT>() : 0;
+  off += late_ring && has_dxout ? kXs : 0;
   const uint32_t o_x = off;
-  off += late_ring && need_x ? NT * join_slot<XT>() : 0;
-  const uint32_t stage = off;
-  const uint32_t base = smem_u32(join_smem);
+  off += late_ring && need_x ? kXs : 0;
+  const uint32_t slots = off;
+  const uint32_t mine = warp * p.nbuf * slots;
+  const uint32_t base = smem_u32(join_smem) + mine;
 
   const float inv_h = 1.0f / static_cast<float>(p.H);
-  const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
+  const uint64_t alpha = join_twice(p.alpha != nullptr ? *p.alpha : 1.0f);
   const XT* Xout = static_cast<const XT*>(p.Xout);
   const XT* X = static_cast<const XT*>(p.X);
   const XT* dXout = static_cast<const XT*>(p.dXout);
   const YT* Y = static_cast<const YT*>(p.Y);
   const YT* dXn = static_cast<const YT*>(p.dXn);
 
-  float a1[kJoinVpt][8], a0[kJoinVpt][8];  // sum dXn xh, sum dXn
-  float s1[kJoinVpt][8], s0[kJoinVpt][8];  // sum dh yh, sum dh of the group
-  float d_alpha = 0.f;
+  JoinVec a1[kVpt], a0[kVpt];  // sum dXn xh, sum dXn
+  JoinVec s1[kVpt], s0[kVpt];  // sum dh yh, sum dh of the group
+  uint64_t d_alpha = 0ull;
+  uint4 gpre[kVpt];
+  JoinVec gw[kVpt];  // gate gamma_post of the group
 #pragma unroll
-  for (int k = 0; k < kJoinVpt; ++k)
+  for (int k = 0; k < kVpt; ++k) {
+    gpre[k] = join_param(p.gamma_pre, k, jc);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a1[k][e] = s1[k][e] = 0.f;
-      if (kBeta) a0[k][e] = s0[k][e] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      a1[k][i] = s1[k][i] = 0ull;
+      if (kBeta) a0[k][i] = s0[k][i] = 0ull;
     }
+  }
 
   const int bpg = p.blocks_per_group;
   const int groups = p.G > 0 ? p.G : 1;
@@ -123,253 +174,332 @@ __global__ void __launch_bounds__(join_threads(kTpr), kTpr <= 512 ? 512 / join_t
 
   for (int g = blockIdx.x / bpg; g < groups; g += walkers) {
     const int64_t r_end = (g + int64_t(1)) * p.rows_per_group;
-    const int64_t row0 = g * p.rows_per_group + (blockIdx.x % bpg) * kRows + sub;
-    const int64_t step = static_cast<int64_t>(bpg) * kRows;
+    const int64_t row0 = g * p.rows_per_group + (blockIdx.x % bpg) * rows + sub;
+    const int64_t step = static_cast<int64_t>(bpg) * rows;
     const bf* gate = p.gate != nullptr ? p.gate + static_cast<int64_t>(g) * p.H : nullptr;
 
     auto issue = [&](int b, int64_t row) {
       if (row < r_end) {
-        const uint32_t d = base + b * stage;
+        const uint32_t d = base + b * slots;
+        const int64_t o = row * p.H;
         if (has_pre) {
-          join_copy<XT>(d + o_xout, NT, Xout + row * p.H, jc);
-          join_copy<YT>(d + o_dxn, NT, dXn + row * p.H, jc);
+          join_copy<XT>(d + o_xout, Xout + o, jc);
+          join_copy<YT>(d + o_dxn, dXn + o, jc);
         }
-        if (need_y) join_copy<YT>(d + o_y, NT, Y + row * p.H, jc);
-        if (late_ring && p.dXout) join_copy<XT>(d + o_dxout, NT, dXout + row * p.H, jc);
-        if (late_ring && need_x) join_copy<XT>(d + o_x, NT, X + row * p.H, jc);
+        if (need_y) join_copy<YT>(d + o_y, Y + o, jc);
+        if (late_ring && has_dxout) join_copy<XT>(d + o_dxout, dXout + o, jc);
+        if (late_ring && need_x) join_copy<XT>(d + o_x, X + o, jc);
       }
       cp_async_commit();
     };
     for (int b = 0; b < p.nbuf; ++b) issue(b, row0 + b * step);
+#pragma unroll
+    for (int k = 0; k < kVpt; ++k) {
+      JoinVec w;
+      join_unpack(join_param(gate, k, jc), gw[k]);
+      join_unpack(join_param(p.gamma_post, k, jc), w);
+      if (has_post) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gw[k][i] = gate != nullptr ? f2_mul(gw[k][i], w[i]) : w[i];
+      }
+    }
+
+    float w_sum = 0.f;  // sum of w over the row
+    if (kBeta && p.post == MLPB_NORM_LAYER) {
+      uint64_t t = 0ull;
+#pragma unroll
+      for (int k = 0; k < kVpt; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = f2_add(t, gw[k][i]);
+      float v[kSums] = {join_add_pair(t)};
+      join_sums<kWpr>(v, sh, par);
+      w_sum = v[0];
+    }
 
     int b = 0;
+    float4 next = make_float4(0.f, 0.f, 0.f, 0.f);  // the next row's statistics, a row ahead
+    if (row0 < r_end) next = __ldg(reinterpret_cast<const float4*>(p.stats + row0 * 4));
     for (int64_t row = row0; row < r_end; row += step) {
+      const float4 stat = next;
+      if (row + step < r_end)
+        next = __ldg(reinterpret_cast<const float4*>(p.stats + (row + step) * 4));
       cp_async_wait_ring(p.nbuf);
-      const uint8_t* st = join_smem + b * stage;
-      const float4 stat = __ldg(reinterpret_cast<const float4*>(p.stats + row * 4));
-      float m[2] = {0.f, 0.f};
-      if (has_pre) {
+      uint8_t* st = join_smem + mine + b * slots;
+      const uint64_t mu_h = join_twice(stat.z), rs_h = join_twice(stat.w);
+      const uint64_t mu_y = join_twice(stat.x), rs_y = join_twice(stat.y);
+      // xh and t of vector k, and dXn
+      auto start = [&](int k, JoinVec& xh, JoinVec& t, JoinVec& d, uint64_t* g_sum,
+                       uint64_t* gx_sum) {
+        if (!has_dxout) {
 #pragma unroll
-        for (int k = 0; k < kJoinVpt; ++k) {
-          float x[8], d[8], w[8];
-          join_read<XT>(st + o_xout, NT, k, jc, x);
-          join_read<YT>(st + o_dxn, NT, k, jc, d);
-          join_load<bf, kSplit, kTpr, true>(p.gamma_pre, k, jc, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xh = (x[e] - stat.z) * stat.w;
-            const float q = d[e] * w[e];
-            m[0] += q;
-            m[1] = fmaf(q, xh, m[1]);
-            a1[k][e] = fmaf(d[e], xh, a1[k][e]);
-            if (kBeta) a0[k][e] += d[e];
-          }
-        }
-        join_sum<kTpr, 2>(m, sh, par);
-        m[0] = p.pre == MLPB_NORM_LAYER ? m[0] * inv_h : 0.f;
-        m[1] *= inv_h;
-      }
-      float dh[kJoinVpt][8], yh[kJoinVpt][8];
-      float n[2] = {0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kJoinVpt; ++k) {
-        if (p.dXout == nullptr) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dh[k][e] = 0.f;
+          for (int i = 0; i < 4; ++i) t[i] = 0ull;
         } else if (late_ring) {
-          join_read<XT>(st + o_dxout, NT, k, jc, dh[k]);
+          join_read<XT>(st + o_dxout, k, jc, t);
         } else {
-          join_load<XT, kSplit, kTpr, false>(dXout + row * p.H, k, jc, dh[k]);
+          join_load<XT>(dXout + row * p.H, k, jc, t);
         }
         if (has_pre) {
-          float x[8], d[8], w[8];
-          join_read<XT>(st + o_xout, NT, k, jc, x);
-          join_read<YT>(st + o_dxn, NT, k, jc, d);
-          join_load<bf, kSplit, kTpr, true>(p.gamma_pre, k, jc, w);
+          JoinVec w;
+          join_read<XT>(st + o_xout, k, jc, xh);
+          join_read<YT>(st + o_dxn, k, jc, d);
+          join_unpack(gpre[k], w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xh = (x[e] - stat.z) * stat.w;
-            dh[k][e] += stat.w * (d[e] * w[e] - m[0] - xh * m[1]);
+          for (int i = 0; i < 4; ++i) {
+            xh[i] = f2_mul(kBeta ? f2_sub(xh[i], mu_h) : xh[i], rs_h);
+            const uint64_t q = f2_mul(d[i], w[i]);
+            t[i] = f2_fma(rs_h, q, t[i]);
+            if (gx_sum != nullptr) {
+              *gx_sum = f2_fma(q, xh[i], *gx_sum);
+              if (kBeta) *g_sum = f2_add(*g_sum, q);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xh[i] = d[i] = 0ull;
+        }
+      };
+      auto normed_y = [&](int k, JoinVec& yh) {
+        join_read<YT>(st + o_y, k, jc, yh);
+        if (has_post) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            yh[i] = f2_mul(kBeta ? f2_sub(yh[i], mu_y) : yh[i], rs_y);
+        }
+      };
+      JoinVec kx[kVpt], kt[kVpt];  // kKeep: xh and t
+      // sums of g xh, w yh t, w yh xh; g, w t, w xh, w yh
+      uint64_t q[7] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int k = 0; k < kVpt; ++k) {
+        JoinVec xh, t, d;
+        start(k, xh, t, d, &q[3], &q[0]);
+        if (has_pre) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a1[k][i] = f2_fma(d[i], xh[i], a1[k][i]);
+            if (kBeta) a0[k][i] = f2_add(a0[k][i], d[i]);
+          }
+        }
+        if (has_post) {
+          JoinVec yh;
+          normed_y(k, yh);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // w is zero past the row's end
+            const uint64_t wy = f2_mul(gw[k][i], yh[i]);
+            q[1] = f2_fma(wy, t[i], q[1]);
+            q[2] = f2_fma(wy, xh[i], q[2]);
+            if (kBeta) {
+              q[4] = f2_fma(gw[k][i], t[i], q[4]);
+              q[5] = f2_fma(gw[k][i], xh[i], q[5]);
+              q[6] = f2_add(q[6], wy);
+            }
+          }
+        }
+        if (kKeep) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            kx[k][i] = xh[i];
+            kt[k][i] = t[i];
+          }
+        }
+      }
+      float sum[kSums];
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) sum[i] = join_add_pair(q[i]);
+      if (has_pre || has_post) join_sums<kWpr>(sum, sh, par);
+      // dh = t + xh cx - cg
+      const float cx = -stat.w * sum[0] * inv_h;
+      float cg = 0.f, u0 = 0.f, u1 = fmaf(cx, sum[2], sum[1]);  // sums of u, u yh
+      if constexpr (kBeta) {
+        cg = p.pre == MLPB_NORM_LAYER ? stat.w * sum[3] * inv_h : 0.f;
+        u1 = fmaf(-cg, sum[6], u1);
+        if (p.post == MLPB_NORM_LAYER) u0 = fmaf(-cg, w_sum, fmaf(cx, sum[5], sum[4]));
+      }
+      const uint64_t cx2 = join_twice(cx);
+      [[maybe_unused]] const uint64_t cg2 = join_twice(cg), c0 = join_twice(u0 * inv_h);
+      const uint64_t c1 = join_twice(-u1 * inv_h);
+#pragma unroll
+      for (int k = 0; k < kVpt; ++k) {
+        JoinVec dh;
+        if constexpr (kKeep) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dh[i] = f2_fma(kx[k][i], cx2, kt[k][i]);
+        } else {
+          JoinVec xh, d;
+          start(k, xh, dh, d, nullptr, nullptr);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dh[i] = f2_fma(xh[i], cx2, dh[i]);
+            if (kBeta) dh[i] = f2_sub(dh[i], cg2);
           }
         }
         if (need_x) {
-          float x[8];
+          JoinVec x;
           if (late_ring)
-            join_read<XT>(st + o_x, NT, k, jc, x);
+            join_read<XT>(st + o_x, k, jc, x);
           else
-            join_load<XT, kSplit, kTpr, true>(X + row * p.H, k, jc, x);
+            join_load<XT>(X + row * p.H, k, jc, x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (jc.ok[k][e / 4]) d_alpha = fmaf(dh[k][e], x[e], d_alpha);
+          for (int i = 0; i < 4; ++i) d_alpha = f2_fma(dh[i], x[i], d_alpha);  // x is 0 past the end
+        }
+        if (p.alpha != nullptr) {
+          JoinVec dx;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dx[i] = f2_mul(alpha, dh[i]);
+          join_store<XT, false>(static_cast<XT*>(p.dX) + row * p.H, k, jc, dx);
+        } else {
+          join_store<XT, false>(static_cast<XT*>(p.dX) + row * p.H, k, jc, dh);
         }
         if (need_y) {
-          join_read<YT>(st + o_y, NT, k, jc, yh[k]);
+          JoinVec yh;
+          normed_y(k, yh);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (has_post) yh[k][e] = (yh[k][e] - stat.x) * stat.y;
-            s1[k][e] = fmaf(dh[k][e], yh[k][e], s1[k][e]);
-            if (kBeta) s0[k][e] += dh[k][e];
+          for (int i = 0; i < 4; ++i) {
+            s1[k][i] = f2_fma(dh[i], yh[i], s1[k][i]);
+            if (kBeta) s0[k][i] = f2_add(s0[k][i], dh[i]);
+            dh[i] = f2_mul(dh[i], gw[k][i]);  // u
+          }
+          if (has_post) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dh[i] = f2_mul(rs_y, f2_fma(yh[i], c1, kBeta ? f2_sub(dh[i], c0) : dh[i]));
           }
         }
+        if (has_block) join_store<bf, false>(p.dY + row * p.H, k, jc, dh);
       }
       issue(b, row + p.nbuf * step);  // this row's slots have been read
       if (++b == p.nbuf) b = 0;
-#pragma unroll
-      for (int k = 0; k < kJoinVpt; ++k) {
-        float dx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] = alpha * dh[k][e];
-        join_store<XT>(static_cast<XT*>(p.dX) + row * p.H, k, jc, dx);
-        if (p.has_block && gate != nullptr) {
-          float w[8];
-          join_load<bf, kSplit, kTpr, true>(gate, k, jc, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dh[k][e] *= w[e];
-        }
-        if (has_post) {
-          float w[8];
-          join_load<bf, kSplit, kTpr, true>(p.gamma_post, k, jc, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dh[k][e] *= w[e];  // u, zero past the row's end as gamma is
-            n[0] += dh[k][e];
-            n[1] = fmaf(dh[k][e], yh[k][e], n[1]);
-          }
-        }
-      }
-      if (has_post) {
-        join_sum<kTpr, 2>(n, sh, par);
-        n[0] = p.post == MLPB_NORM_LAYER ? n[0] * inv_h : 0.f;
-        n[1] *= inv_h;
-#pragma unroll
-        for (int k = 0; k < kJoinVpt; ++k)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dh[k][e] = stat.y * (dh[k][e] - n[0] - yh[k][e] * n[1]);
-      }
-      if (p.has_block) {
-#pragma unroll
-        for (int k = 0; k < kJoinVpt; ++k) join_store<bf>(p.dY + row * p.H, k, jc, dh[k]);
-      }
     }
 
     // The end of this CTA's rows of the group: S1 and S0 over the CTA, and what they give.
     if (need_y) {
-      join_combine<kTpr>(s1);
-      if (kBeta) join_combine<kTpr>(s0);
+      join_combine<rows>(s1);
+      if (kBeta) join_combine<rows>(s0);
       if (sub == 0) {
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * p.H;
 #pragma unroll
-        for (int k = 0; k < kJoinVpt; ++k) {
-          float w[8], t[8];
+        for (int k = 0; k < kVpt; ++k) {
+          JoinVec w, t;
           if (gate != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = s1[k][e];
+            for (int i = 0; i < 4; ++i) t[i] = s1[k][i];
             if (has_post) {
-              join_load<bf, kSplit, kTpr, true>(p.gamma_post, k, jc, w);
+              join_unpack(join_param(p.gamma_post, k, jc), w);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) t[e] *= w[e];
+              for (int i = 0; i < 4; ++i) t[i] = f2_mul(t[i], w[i]);
             }
             if (kBeta && p.beta_post != nullptr) {
-              join_load<bf, kSplit, kTpr, true>(p.beta_post, k, jc, w);
+              join_unpack(join_param(p.beta_post, k, jc), w);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) t[e] = fmaf(w[e], s0[k][e], t[e]);
+              for (int i = 0; i < 4; ++i) t[i] = f2_fma(w[i], s0[k][i], t[i]);
             }
             if (bpg > 1)
               join_put(p.part_gate + slot, k, jc, t, false);
             else
               join_put(p.dgate + static_cast<int64_t>(g) * p.H, k, jc, t, p.accumulate != 0);
-            join_load<bf, kSplit, kTpr, true>(gate, k, jc, w);
+            join_unpack(join_param(gate, k, jc), w);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+            for (int i = 0; i < 4; ++i) w[i] = join_twice(1.0f);
           }
           if (p.part_gpost != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = w[e] * s1[k][e];
+            for (int i = 0; i < 4; ++i) t[i] = f2_mul(w[i], s1[k][i]);
             join_put(p.part_gpost + slot, k, jc, t, !first);
           }
           if (kBeta && p.part_bpost != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = w[e] * s0[k][e];
+            for (int i = 0; i < 4; ++i) t[i] = f2_mul(w[i], s0[k][i]);
             join_put(p.part_bpost + slot, k, jc, t, !first);
           }
         }
       }
       first = false;
 #pragma unroll
-      for (int k = 0; k < kJoinVpt; ++k)
+      for (int k = 0; k < kVpt; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s1[k][e] = 0.f;
-          if (kBeta) s0[k][e] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          s1[k][i] = 0ull;
+          if (kBeta) s0[k][i] = 0ull;
         }
     }
   }
 
   if (has_pre) {
-    join_combine<kTpr>(a1);
-    if (kBeta) join_combine<kTpr>(a0);
+    join_combine<rows>(a1);
+    if (kBeta) join_combine<rows>(a0);
     if (sub == 0) {
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * p.H;
 #pragma unroll
-      for (int k = 0; k < kJoinVpt; ++k) {
+      for (int k = 0; k < kVpt; ++k) {
         join_put(p.part_gpre + slot, k, jc, a1[k], false);
-        if (kBeta && p.part_bpre != nullptr)
-          join_put(p.part_bpre + slot, k, jc, a0[k], false);
+        if (kBeta && p.part_bpre != nullptr) join_put(p.part_bpre + slot, k, jc, a0[k], false);
       }
     }
   }
   if (need_x) {  // the CTA's part of dalpha, added in warp order
+    float d = join_add_pair(d_alpha);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d_alpha += __shfl_xor_sync(0xffffffffu, d_alpha, o);
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x / 32].x = d_alpha;
+    if ((threadIdx.x & 31) == 0) sh[0][threadIdx.x / 32][0] = d;
     __syncthreads();
     if (threadIdx.x == 0) {
       float t = 0.f;
-      for (int w = 0; w < NT / 32; ++w) t += sh[w].x;
+      for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) t += sh[0][w][0];
       p.part_alpha[blockIdx.x] = t;
     }
   }
 }
 
-// CTAs of the launch: with few groups, each gets an equal number of CTAs of its own; with
-// more groups than CTAs, a CTA walks groups.
-template <class XT, class YT, int kTpr, bool kBeta>
-static cudaError_t join_bwd_launch(JoinParams p, int grid, cudaStream_t s) {
-  constexpr int NT = join_threads(kTpr);
-  const bool has_pre = p.pre != MLPB_NORM_NONE;
-  const bool need_y = p.post != MLPB_NORM_NONE || p.gate != nullptr;
-  const size_t early = NT * ((has_pre ? join_slot<XT>() + join_slot<YT>() : 0) +
-                             (need_y ? join_slot<YT>() : 0));
-  const size_t late = NT * ((p.dXout != nullptr ? join_slot<XT>() : 0) +
-                            (p.part_alpha != nullptr ? join_slot<XT>() : 0));
-  const size_t room = (208u << 10) / (NT <= 256 ? 2 : 1);
+template <class XT, class YT, int kVpt, int kWpr, bool kBeta>
+static cudaError_t join_bwd_launch(JoinParams p, bool plain, int grid, cudaStream_t s) {
+  constexpr int threads = join_threads(kWpr), warps = threads / 32;
+  const bool has_pre = p.pre != MLPB_NORM_NONE, has_post = p.post != MLPB_NORM_NONE;
+  const bool need_y = has_post || p.gate != nullptr;
+  constexpr size_t xs = warps * join_slots<XT, kVpt>(), ys = warps * join_slots<YT, kVpt>();
+  const size_t early = (has_pre ? xs + ys : 0) + (need_y ? ys : 0);
+  const size_t late = (p.dXout != nullptr ? xs : 0) + (p.part_alpha != nullptr ? xs : 0);
+  const size_t room = (208u << 10) / (512 / threads);
   p.direct_late = early + late > room;
   const size_t stage = p.direct_late ? early : early + late;
   p.nbuf = static_cast<int>(std::max<size_t>(
       1, std::min<size_t>(kJoinMaxBuf, room / std::max<size_t>(stage, 1))));
   size_t smem = p.nbuf * stage;
-  if (NT > kTpr) smem = std::max(smem, static_cast<size_t>(NT) * kJoinVpt * 8 * 4);
-  auto* kernel = join_bwd_kernel<XT, YT, kTpr, kBeta>;
+  if (join_rows(kWpr) > 1)
+    smem = std::max(smem, static_cast<size_t>(threads) * kVpt * 32);  // join_combine
+  auto* kernel = join_bwd_kernel<XT, YT, kVpt, kWpr, kBeta, false>;
+  if constexpr (kVpt == 2) {
+    if (plain && p.H == 256 * kVpt * kWpr && !p.direct_late)
+      kernel = join_bwd_kernel<XT, YT, kVpt, kWpr, kBeta, true>;
+  }
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kernel<<<grid, NT, smem, s>>>(p);
+  kernel<<<grid, threads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <class XT, class YT, bool kBeta>
 static cudaError_t join_bwd_pick(const JoinParams& p, int grid, cudaStream_t s) {
-  switch (join_tpr(p.H)) {
-    case 32: return join_bwd_launch<XT, YT, 32, kBeta>(p, grid, s);
-    case 64: return join_bwd_launch<XT, YT, 64, kBeta>(p, grid, s);
-    case 128: return join_bwd_launch<XT, YT, 128, kBeta>(p, grid, s);
-    case 256: return join_bwd_launch<XT, YT, 256, kBeta>(p, grid, s);
-    case 512: return join_bwd_launch<XT, YT, 512, kBeta>(p, grid, s);
-    default: return join_bwd_launch<XT, YT, 1024, kBeta>(p, grid, s);
+  const bool plain =
+      p.pre != MLPB_NORM_NONE && p.post != MLPB_NORM_NONE && p.has_block && p.dXout != nullptr;
+  switch (join_bwd_wpr(p.H)) {
+    case 1: return join_bwd_launch<XT, YT, 1, 1, kBeta>(p, plain, grid, s);
+    case 2: return join_bwd_launch<XT, YT, 2, 2, kBeta>(p, plain, grid, s);
+    case 4: return join_bwd_launch<XT, YT, 2, 4, kBeta>(p, plain, grid, s);
+    case 8: return join_bwd_launch<XT, YT, 2, 8, kBeta>(p, plain, grid, s);
+    case 10: return join_bwd_launch<XT, YT, 2, 10, kBeta>(p, plain, grid, s);
   }
+  return p.H <= 8192 ? join_bwd_launch<XT, YT, 2, 16, kBeta>(p, plain, grid, s)
+                     : join_bwd_launch<XT, YT, 4, 16, kBeta>(p, plain, grid, s);
+}
+
+template <class XT, class YT>
+cudaError_t join_bwd_run(const JoinParams& p, int grid, cudaStream_t s) {
+  return p.post == MLPB_NORM_LAYER || p.pre == MLPB_NORM_LAYER
+             ? join_bwd_pick<XT, YT, true>(p, grid, s)
+             : join_bwd_pick<XT, YT, false>(p, grid, s);
 }
 
 }  // namespace mlpb
