@@ -80,4 +80,13 @@ __device__ __forceinline__ uint64_t gelu_grad_x2(uint64_t z) {
   return f2_fma(d, f2_sub(s, f2_mul(s, s)), s);
 }
 
+// gelu'(z), and gelu(z) in `gelu`, for two values: one exponential and reciprocal each for both.
+__device__ __forceinline__ uint64_t gelu_both_x2(uint64_t z, uint64_t& gelu) {
+  const uint64_t z2 = f2_mul(z, z);
+  const uint64_t s = gelu_s_x2(z, z2);
+  const uint64_t d = f2_mul(z, f2_fma(z2, f2_pack(kGeluD2, kGeluD2), f2_pack(kGeluD0, kGeluD0)));
+  gelu = f2_mul(z, s);
+  return f2_fma(d, f2_sub(s, f2_mul(s, s)), s);
+}
+
 }  // namespace mlpb
