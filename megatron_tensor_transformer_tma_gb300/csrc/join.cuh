@@ -257,6 +257,19 @@ __device__ __forceinline__ void join_store(E* row, int k, const JoinCols<kSplit,
 
 constexpr int kJoinMaxWarps = 16;
 
+// Lets a kernel have `smem` bytes of dynamic shared memory. 48 KB, the kernel's static arrays
+// among them (4 KB at most), need no leave. The leave is always for the same size: one for
+// each launch's own would be undone by a second host thread before the first one's launch.
+constexpr size_t kJoinMaxSmem = 212u << 10;
+
+template <class K>
+cudaError_t join_smem_attr(K* kernel, size_t smem) {
+  return smem <= (44u << 10)
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kJoinMaxSmem));
+}
+
 template <class XT, class YT>
 cudaError_t join_fwd_run(const JoinParams& p, int num_sms, cudaStream_t s);
 template <class XT, class YT>

@@ -473,8 +473,7 @@ static cudaError_t join_bwd_launch(JoinParams p, bool plain, int grid, cudaStrea
     if (plain && p.H == 256 * kVpt * kWpr && !p.direct_late)
       kernel = join_bwd_kernel<XT, YT, kVpt, kWpr, kBeta, true>;
   }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  const cudaError_t e = join_smem_attr(kernel, smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, threads, smem, s>>>(p);
   return cudaGetLastError();

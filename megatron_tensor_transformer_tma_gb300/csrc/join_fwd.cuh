@@ -214,9 +214,13 @@ static cudaError_t join_fwd_launch(JoinParams p, int num_sms, cudaStream_t s) {
   constexpr int threads = join_threads(kWpr);
   const size_t stage =
       threads / 32 * (join_slots<XT, kVpt>() + (p.has_block ? join_slots<YT, kVpt>() : 0));
-  // rows in flight: what lets the CTAs that the registers admit (512 threads) share an SM
-  const size_t room = (208u << 10) / (512 / threads);
+  constexpr int ctas = 512 / threads;  // an SM's, by the registers
+  const int64_t tiles = (p.T + join_rows(kWpr) - 1) / join_rows(kWpr);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(ctas) * num_sms));
+  // stages in flight: what lets those CTAs share an SM, and no more than a CTA has turns
+  const size_t room = (208u << 10) / ctas;
   p.nbuf = static_cast<int>(std::max<size_t>(1, std::min<size_t>(kJoinMaxBuf, room / stage)));
+  p.nbuf = static_cast<int>(std::min<int64_t>(p.nbuf, (tiles + grid - 1) / grid));
   const size_t smem = p.nbuf * stage;
   auto* kernel = join_fwd_kernel<XT, YT, kVpt, kWpr, kBeta, false>;
   if constexpr (kVpt == 4) {
@@ -224,15 +228,8 @@ static cudaError_t join_fwd_launch(JoinParams p, int num_sms, cudaStream_t s) {
         p.H == 256 * kVpt * kWpr)
       kernel = join_fwd_kernel<XT, YT, kVpt, kWpr, kBeta, true>;
   }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  int per_sm = 1;
-  if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+  const cudaError_t e = join_smem_attr(kernel, smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (p.T + join_rows(kWpr) - 1) / join_rows(kWpr);
-  const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(std::max(1, per_sm)) * num_sms));
   kernel<<<grid, threads, smem, s>>>(p);
   return cudaGetLastError();
 }

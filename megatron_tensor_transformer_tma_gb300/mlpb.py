@@ -171,6 +171,8 @@ def _arg(t, dtype, shape, name, dev):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     if t.dtype != dtype:
@@ -179,9 +181,7 @@ def _arg(t, dtype, shape, name, dev):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on cuda:{t.get_device()}, other tensors on cuda:{dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on cuda:{t.get_device()}, other tensors on cuda:{dev}")
 
 
 def _cuda_index(t, name):
@@ -193,12 +193,19 @@ def _cuda_index(t, name):
     return t.get_device()
 
 
+# The current stream's handle without a Stream object around it, where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call_on(dev, name, args, stream):
     """Calls a library function with `args` and a stream (None: the current one of device
     `dev`), with that device current: the library launches on the current device."""
     fn = getattr(load_library(), name)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    s = s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+    if stream is None:
+        s = _raw_stream(dev)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if dev == torch.cuda.current_device():
         _check(fn(*args, s), name)
     else:
