@@ -25,10 +25,13 @@ struct JoinSums {
 };
 
 // The second pass: block (x, y) sums 32 columns of sum y (then of the groups' dgate rows): warp
-// w takes partial rows w, w + 8, ..., and the eight warps' sums are added in warp order.  The
-// last block in x of row 0 adds dalpha up, in 64 bits.
-__global__ void __launch_bounds__(256) join_sums_kernel(const JoinSums p) {
-  __shared__ float red[8][33];
+// w takes partial rows w, w + 16, ..., and the warps' sums are added in warp order.  The last
+// block in x of row 0 adds dalpha up, in 64 bits.  Bound by latency: 15 MB from L2 in 7 us at
+// T 8192 H 8192, eight loads in flight a thread (with eight warps and four loads 9).  Launched
+// while the first pass ends, it gains 1 us of 150: not kept.
+constexpr int kJoinSumWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinSumWarps) join_sums_kernel(const JoinSums p) {
+  __shared__ float red[kJoinSumWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0 && p.dalpha != nullptr && warp == 0) {
@@ -53,20 +56,31 @@ __global__ void __launch_bounds__(256) join_sums_kernel(const JoinSums p) {
   const int c = blockIdx.x * 32 + lane;
   float t = 0.f;
   if (c < p.H) {
-#pragma unroll 4
-    for (int k = warp; k < q.np; k += 8) t += q.part[k * H + c];
+    const float* from = q.part + c;
+#pragma unroll 1
+    for (int k = warp; k < q.np; k += 8 * kJoinSumWarps) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = k + i * kJoinSumWarps;
+        v[i] = r < q.np ? from[r * H] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += v[i];
+    }
   }
   red[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && c < p.H) {
     t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += red[w][lane];
+    for (int w = 0; w < kJoinSumWarps; ++w) t += red[w][lane];
     q.out[c] = p.accumulate ? q.out[c] + t : t;
   }
 }
 
 struct JoinPlan {
+  JoinShape shape;
   int grid, blocks_per_group;
   size_t o_gate, o_gpost, o_bpost, o_gpre, o_bpre, o_alpha, bytes;
 };
@@ -75,12 +89,13 @@ static size_t join_align(size_t x) { return (x + 255) & ~static_cast<size_t>(255
 
 // The backward's CTAs (as many as run at once, 512 threads an SM) and its partial rows in the
 // workspace.
-static JoinPlan join_plan(const mlpb_join_config& c, int num_sms) {
+static JoinPlan join_plan(const mlpb_join_config& c, bool plain, int num_sms) {
   JoinPlan q{};
-  const int wpr = join_bwd_wpr(c.hidden), rows = join_rows(wpr);
-  const int target = num_sms * (512 / join_threads(wpr));
   const int64_t groups = std::max<int64_t>(1, c.gate_groups);
-  const int64_t per = groups > 0 ? c.tokens / groups : 0;  // rows of a group
+  const int64_t per = c.tokens / groups;  // rows of a group
+  q.shape = join_bwd_shape(c.hidden, plain,
+                           std::min<int64_t>(per, (c.tokens + num_sms - 1) / num_sms));
+  const int rows = q.shape.rows, target = plain ? num_sms * (512 / q.shape.threads) : num_sms / q.shape.cluster;
   const int64_t want = std::max<int64_t>(1, (per + rows - 1) / rows);
   q.blocks_per_group = static_cast<int>(
       std::max<int64_t>(1, std::min<int64_t>(want, target / groups)));
@@ -98,7 +113,7 @@ static JoinPlan join_plan(const mlpb_join_config& c, int num_sms) {
   q.o_bpost = take(c.post_norm == MLPB_NORM_LAYER ? row : 0);
   q.o_gpre = take(c.pre_norm != MLPB_NORM_NONE ? row : 0);
   q.o_bpre = take(c.pre_norm == MLPB_NORM_LAYER ? row : 0);
-  q.o_alpha = take(static_cast<size_t>(q.grid) * 4);
+  q.o_alpha = take(static_cast<size_t>(q.grid * q.shape.cluster) * 4);
   q.bytes = std::max<size_t>(o, 256);
   return q;
 }
@@ -164,7 +179,8 @@ extern "C" mlpb_status mlpb_join_workspace_size(const mlpb_join_config* cfg, siz
   if (bytes == nullptr) return MLPB_EINVAL;
   int sms = 0;
   if (!join_sms(&sms)) return MLPB_ECUDA;
-  *bytes = join_plan(*cfg, sms).bytes;
+  *bytes = join_plan(*cfg, false, sms).bytes;
+  if (join_bwd_has_plain(cfg->hidden)) *bytes = std::max(*bytes, join_plan(*cfg, true, sms).bytes);
   return MLPB_OK;
 }
 
@@ -262,7 +278,8 @@ extern "C" mlpb_status mlpb_join_bwd(const mlpb_join_config* cfg, const void* X,
   int sms = 0;
   if (!join_sms(&sms)) return MLPB_ECUDA;
   using bf = __nv_bfloat16;
-  const JoinPlan q = join_plan(c, sms);
+  const bool plain = pre && post && dXout != nullptr && join_bwd_has_plain(c.hidden);
+  const JoinPlan q = join_plan(c, plain, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   auto part = [&](bool on, size_t o) { return on ? reinterpret_cast<float*>(ws + o) : nullptr; };
   JoinParams p = join_base(c);
@@ -290,10 +307,10 @@ extern "C" mlpb_status mlpb_join_bwd(const mlpb_join_config* cfg, const void* X,
   p.part_alpha = part(res_scale != nullptr, q.o_alpha);
   const bool y32 = (c.flags & MLPB_JOIN_BLOCK_F32) != 0;
   cudaError_t e = (c.flags & MLPB_JOIN_STREAM_F32) != 0
-                      ? (y32 ? join_bwd_run<float, float>(p, q.grid, s)
-                             : join_bwd_run<float, bf>(p, q.grid, s))
-                      : (y32 ? join_bwd_run<bf, float>(p, q.grid, s)
-                             : join_bwd_run<bf, bf>(p, q.grid, s));
+                      ? (y32 ? join_bwd_run<float, float>(p, q.shape, plain, q.grid, s)
+                             : join_bwd_run<float, bf>(p, q.shape, plain, q.grid, s))
+                      : (y32 ? join_bwd_run<bf, float>(p, q.shape, plain, q.grid, s)
+                             : join_bwd_run<bf, bf>(p, q.shape, plain, q.grid, s));
   if (e != cudaSuccess) return MLPB_ECUDA;
   JoinSums r{};
   auto want = [&](const float* from, float* to) {
@@ -309,16 +326,14 @@ extern "C" mlpb_status mlpb_join_bwd(const mlpb_join_config* cfg, const void* X,
   r.per_group = q.blocks_per_group;
   r.part_alpha = p.part_alpha;
   r.dalpha = dres_scale;
-  r.np_alpha = q.grid;
+  r.np_alpha = q.grid * q.shape.cluster;
   r.H = p.H;
   r.accumulate = p.accumulate;
   if (r.n + r.groups == 0 && r.dalpha == nullptr) return MLPB_OK;
-  const dim3 grid(static_cast<unsigned>((p.H + 31) / 32 + 1),
-                  static_cast<unsigned>(std::max(1, r.n + r.groups)));
-  if (r.n + r.groups == 0) {  // dalpha alone: only the last block of the row
-    join_sums_kernel<<<1, 256, 0, s>>>(r);
-  } else {
-    join_sums_kernel<<<grid, 256, 0, s>>>(r);
-  }
+  const dim3 grid = r.n + r.groups == 0  // dalpha alone: only the last block of the row
+                        ? dim3(1)
+                        : dim3(static_cast<unsigned>((p.H + 31) / 32 + 1),
+                               static_cast<unsigned>(r.n + r.groups));
+  join_sums_kernel<<<grid, 32 * kJoinSumWarps, 0, s>>>(r);
   return cudaGetLastError() == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
 }

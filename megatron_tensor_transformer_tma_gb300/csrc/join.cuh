@@ -20,7 +20,15 @@
 // H 8192 took 95 instructions an element and 290 us.)  And the usual call -- both norms, every
 // warp's columns all inside the row -- has an instantiation of its own (kPlain) without the
 // masks and the checks of what there is, which are half of the general one's instructions.  A
-// CTA of up to 256 threads holds several rows where a row needs fewer.
+// CTA holds several rows where a row needs few warps.
+//
+// Measured (bandwidth over the bytes that a call cannot do without; the copy that the card
+// reaches is 6.8 TB/s): forward T 8192 H 8192 bf16, RMSNorms and a gate, 92 us, 5.8 TB/s;
+// backward 156 us, 5.2 TB/s, of which 143 the first pass; backward T 16384 H 4096 fp32,
+// LayerNorms, 265 us, 6.6 TB/s.  What keeps the bf16 backward from the last fifth is the chain
+// of a row (its reduction among it) with one row an SM in registers.  Ragged widths: RMS
+// T 3000 H 7000 30 us forward (83 %), 62 backward (60 %); LayerNorms T 11061 H 2184 81 and 98
+// (35 and 44 %), bound by instructions and the chain of their four reductions.
 #pragma once
 
 #include <algorithm>
@@ -43,6 +51,10 @@ struct JoinParams {
   bool has_block;
   float eps;
   int nbuf;
+  // the general backward's
+  int wpr, rows;   // warps of a row, rows of a CTA
+  int ring_bytes;  // of the ring
+  bool ragged;     // some of the threads' columns are past the row's end
   // forward (inputs of both)
   const void *X, *Y;
   const float* alpha;
@@ -56,24 +68,56 @@ struct JoinParams {
   __nv_bfloat16* dY;
   float* dgate;          // [G][H], written here when a group has one CTA (blocks_per_group 1)
   float* part_gate;      // [G * blocks_per_group][H] otherwise
-  float *part_gpost, *part_bpost, *part_gpre, *part_bpre;  // [gridDim.x][H], NULL: not wanted
+  float *part_gpost, *part_bpost, *part_gpre, *part_bpre;  // [walkers][H], NULL: not wanted
   float* part_alpha;     // [gridDim.x]
   int blocks_per_group;  // CTAs of a gate group; 1 when a CTA walks several groups
   int accumulate;        // dgate is added into (blocks_per_group 1)
-  bool direct_late;      // X and dXout are not in the ring (it would not fit)
 };
 
-// Rows and threads of a CTA with `wpr` warps a row.
+// The warps of a row are a compile-time number (kWpr), but in the backward's general
+// instantiations, where they are a runtime one (kWpr -12 or -16: one CTA of up to 12 or 16 warps
+// an SM).
+constexpr int kJoinMaxWarps = 16;
 constexpr int join_rows(int wpr) { return wpr >= 8 ? 1 : 8 / wpr; }
-constexpr int join_threads(int wpr) { return 32 * wpr * join_rows(wpr); }
+constexpr int join_threads(int wpr) { return wpr < 0 ? -32 * wpr : 32 * wpr * join_rows(wpr); }
+constexpr int join_ctas(int wpr) { return wpr < 0 ? 1 : 512 / join_threads(wpr); }  // of an SM
 
-// Warps of a row, of those that there are kernels for: 256 elements each up to H 256, else 1024
-// in the forward and 512 (above 8192 1024) in the backward; 5 and 10 for H 5120.
+// Warps of a row in the forward, of those that there are kernels for: 256 elements each up to H
+// 256, else 1024.
 inline int join_fwd_wpr(int64_t H) {
   return H <= 1024 ? 1 : H <= 2048 ? 2 : H <= 4096 ? 4 : H == 5120 ? 5 : H <= 8192 ? 8 : 16;
 }
-inline int join_bwd_wpr(int64_t H) {
-  return H <= 256 ? 1 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 4096 ? 8 : H == 5120 ? 10 : 16;
+
+// How a backward is laid out: vectors of a thread, warps of a row in one CTA, rows and threads of a
+// CTA, CTAs that share a row (a cluster, in the backward above H 8192).
+struct JoinShape {
+  int vpt, wpr, rows, threads, cluster;
+};
+inline JoinShape join_shape_plain(int vpt, int wpr) {
+  return JoinShape{vpt, wpr, join_rows(wpr), join_threads(wpr), 1};
+}
+// `max` warps of a CTA, more where one row needs more; at most `most` rows: few rows are spread
+// over the SMs.
+inline JoinShape join_shape_general(int vpt, int64_t H, int max, int64_t most, int cluster = 1) {
+  const int columns = 256 * vpt * cluster;
+  const int wpr = static_cast<int>((H + columns - 1) / columns);
+  const int rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(max / wpr, most)));
+  return JoinShape{vpt, wpr, rows, 32 * wpr * rows, cluster};
+}
+
+// The backward's: plain instantiations for 16 elements a thread at these widths; the general ones
+// hold as many (8 up to H 256), on 12 warps of 168 registers where a row fits them (with
+// LayerNorm 16 of 128 registers spill: T 11061 H 2184, 119 us against 104; RMS T 7122 H 2936, 64
+// against 60), and above H 8192 with two CTAs a row (32 elements a thread in one CTA: T 610
+// H 9856 44 us against 30, T 1024 H 16384 with LayerNorm over 90 against 88; three CTAs of 12
+// warps there 128).
+inline bool join_bwd_has_plain(int64_t H) {
+  return H == 1024 || H == 2048 || H == 4096 || H == 5120 || H == 8192;
+}
+inline JoinShape join_bwd_shape(int64_t H, bool plain, int64_t most) {
+  if (plain) return join_shape_plain(2, static_cast<int>(H / 512));
+  return H <= 256 ? join_shape_general(1, H, 16, most)
+                  : join_shape_general(2, H, 12, most, H <= 8192 ? 1 : 2);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -100,11 +144,16 @@ __device__ __forceinline__ void cp_async_wait_ring(int nbuf) {
 // 128 apart, so that a warp's 16-byte accesses to it are consecutive too: a 32-byte sector read
 // in two halves by two instructions would cross L2 twice.  Half h starts at c[h], and is all
 // inside the row or not at all; with kFull, all are.
+//
+// What is past the row's end is not copied or stored, and its parameters are zeros.  The forward
+// reads zeros in its place, and skips the vectors that a warp has none of (reading them all: T
+// 3712 H 4392 41 us against 30).  The backward, whose instructions the masks doubled, reads all,
+// from slots that are cleared before the first copy.
 template <bool kSplit, int kVpt, bool kFull>
 struct JoinCols {
   int c[2 * kVpt], H;
-  __device__ __forceinline__ JoinCols(int wpr, int H_) : H(H_) {
-    const int warp = (threadIdx.x / 32) % wpr, lane = threadIdx.x & 31;
+  __device__ __forceinline__ JoinCols(int wpr, int warp, int H_) : H(H_) {  // warp of a row's
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 0; k < kVpt; ++k) {
       const int v = (k * wpr + warp) * 256;
@@ -114,6 +163,13 @@ struct JoinCols {
   }
   __device__ __forceinline__ bool ok(int h) const { return kFull || c[h] < H; }
 };
+
+// Zeros in a CTA's ring, before its first copy.
+__device__ __forceinline__ void join_clear(uint8_t* ring, int bytes) {
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+    *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
 
 // Eight values as four f32x2 pairs (elements 0 and 1, 2 and 3, ...): two to a half.
 using JoinVec = uint64_t[4];
@@ -172,39 +228,93 @@ __device__ __forceinline__ void join_copy(uint32_t dst, const E* row,
   }
 }
 
-// Vector k of the thread's elements from its slots (zeros past the row's end).
-template <class E, bool kSplit, int kVpt, bool kFull>
+// Vector k of the thread's elements from its slots (zeros past the row's end, with `all` what the
+// slots hold).
+template <class E, bool all, bool kSplit, int kVpt, bool kFull>
 __device__ __forceinline__ void join_read(const uint8_t* src, int k,
                                           const JoinCols<kSplit, kVpt, kFull>& jc, JoinVec& v) {
   const uint32_t lane = threadIdx.x & 31;
   if constexpr (!kSplit) {
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (jc.ok(2 * k)) u = *reinterpret_cast<const uint4*>(src + (k * 32 + lane) * 16);
+    if (all || jc.ok(2 * k)) u = *reinterpret_cast<const uint4*>(src + (k * 32 + lane) * 16);
     join_unpack(u, v);
   } else {
     using U = typename std::conditional<sizeof(E) == 4, float4, uint2>::type;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       U u{};
-      if (jc.ok(2 * k + h))
+      if (all || jc.ok(2 * k + h))
         u = *reinterpret_cast<const U*>(src + ((2 * k + h) * 32 + lane) * sizeof(U));
       join_unpack_half(u, v + 2 * h);
     }
   }
 }
 
-// Vector k of a row of a tensor that this thread may overwrite afterwards.
-template <class E, bool kSplit, int kVpt, bool kFull>
-__device__ __forceinline__ void join_load(const E* row, int k,
-                                          const JoinCols<kSplit, kVpt, kFull>& jc, JoinVec& v) {
-  using U = typename std::conditional<sizeof(E) == 4, float4, uint2>::type;
+// A vector as it was copied: unpacked pair by pair, where the arithmetic wants it, it takes half
+// the registers.
+template <class E>
+struct JoinRaw {
+  static constexpr int kWords = 2 * static_cast<int>(sizeof(E));
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    U u{};
-    if (jc.ok(2 * k + h)) u = *reinterpret_cast<const U*>(row + jc.c[2 * k + h]);
-    join_unpack_half(u, v + 2 * h);
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-}
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (sizeof(E) == 4)
+      return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else
+      return join_pair(w[i]);
+  }
+  __device__ __forceinline__ void set(int i, uint64_t v) {  // rounds to E
+    float a, b;
+    f2_unpack(v, a, b);
+    if constexpr (sizeof(E) == 4) {
+      w[2 * i] = __float_as_uint(a);
+      w[2 * i + 1] = __float_as_uint(b);
+    } else {
+      w[i] = pack_bf16x2(a, b);
+    }
+  }
+  // vector k from the thread's slots
+  template <bool kSplit>
+  __device__ __forceinline__ void read(const uint8_t* src, int k) {
+    const uint32_t lane = threadIdx.x & 31;
+    if constexpr (!kSplit) {
+      const uint4 u = *reinterpret_cast<const uint4*>(src + (k * 32 + lane) * 16);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* q = src + ((2 * k + h) * 32 + lane) * (4 * sizeof(E));
+        if constexpr (sizeof(E) == 4) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q);
+          w[4 * h] = u.x, w[4 * h + 1] = u.y, w[4 * h + 2] = u.z, w[4 * h + 3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(q);
+          w[2 * h] = u.x, w[2 * h + 1] = u.y;
+        }
+      }
+    }
+  }
+  // vector k into a row
+  template <bool kSplit, int kVpt, bool kFull>
+  __device__ __forceinline__ void store(E* row, int k, const JoinCols<kSplit, kVpt, kFull>& jc) const {
+    if constexpr (!kSplit) {
+      if (jc.ok(2 * k)) st_global_v4(row + jc.c[2 * k], make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!jc.ok(2 * k + h)) continue;
+        if constexpr (sizeof(E) == 4)
+          *reinterpret_cast<uint4*>(row + jc.c[2 * k + h]) =
+              make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+        else
+          *reinterpret_cast<uint2*>(row + jc.c[2 * k + h]) = make_uint2(w[2 * h], w[2 * h + 1]);
+      }
+    }
+  }
+};
 
 // Vector k of a parameter, packed (zeros past its end, and where there is none).
 template <bool kSplit, int kVpt, bool kFull>
@@ -255,8 +365,6 @@ __device__ __forceinline__ void join_store(E* row, int k, const JoinCols<kSplit,
   }
 }
 
-constexpr int kJoinMaxWarps = 16;
-
 // Lets a kernel have `smem` bytes of dynamic shared memory. 48 KB, the kernel's static arrays
 // among them (4 KB at most), need no leave. The leave is always for the same size: one for
 // each launch's own would be undone by a second host thread before the first one's launch.
@@ -273,6 +381,7 @@ cudaError_t join_smem_attr(K* kernel, size_t smem) {
 template <class XT, class YT>
 cudaError_t join_fwd_run(const JoinParams& p, int num_sms, cudaStream_t s);
 template <class XT, class YT>
-cudaError_t join_bwd_run(const JoinParams& p, int grid, cudaStream_t s);
+cudaError_t join_bwd_run(const JoinParams& p, const JoinShape& sh, bool plain, int grid,
+                         cudaStream_t s);
 
 }  // namespace mlpb

@@ -27,14 +27,14 @@
 
 namespace mlpb {
 
-// Adds a CTA's rows' accumulators of a column up, in row order, for the first row's warps (the
-// ring's shared memory is free by then: every copy has been waited for, since each thread's last
-// wait left only groups of rows past the end, which copied nothing).
-template <int rows, int kVpt>
-__device__ __forceinline__ void join_combine(JoinVec (&v)[kVpt]) {
-  if constexpr (rows == 1) return;
-  extern __shared__ __align__(16) uint8_t join_smem[];
-  uint64_t* acc = reinterpret_cast<uint64_t*>(join_smem) + threadIdx.x;
+// Adds a CTA's rows' accumulators of a column up, in row order, for the first row's warps, by way
+// of `smem`: the plain instantiations' ring (which is free by then: every copy has been waited
+// for, since each thread's last wait left only groups of rows past the end, which copied
+// nothing), or memory behind the general ones', whose ring keeps its zeros.
+template <int kVpt>
+__device__ __forceinline__ void join_combine(JoinVec (&v)[kVpt], int rows, uint8_t* smem) {
+  if (rows == 1) return;
+  uint64_t* acc = reinterpret_cast<uint64_t*>(smem) + threadIdx.x;
   const int nt = blockDim.x, tpr = nt / rows;
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
@@ -42,6 +42,7 @@ __device__ __forceinline__ void join_combine(JoinVec (&v)[kVpt]) {
   for (int i = 0; i < kVpt * 4; ++i) acc[i * nt] = v[i / 4][i % 4];
   __syncthreads();
   if (threadIdx.x < tpr)
+#pragma unroll 1
     for (int r = 1; r < rows; ++r)
 #pragma unroll
       for (int i = 0; i < kVpt * 4; ++i)
@@ -68,12 +69,19 @@ __device__ __forceinline__ void join_put(float* row, int k, const JoinCols<kSpli
   }
 }
 
-// Adds NV values over the wpr warps of a row, in a fixed order; one barrier, as join_sum.  The
-// shuffles of a warp's sums give away half of the values a lane still has, so that 8 values take
-// 9 of them, not 40; a lane then owns one value, and after the barrier adds up every eighth (or
-// fourth) warp's.
-template <int wpr, int NV>
-__device__ __forceinline__ void join_sums(float (&v)[NV], float (*sh)[kJoinMaxWarps][8], int& par) {
+// This CTA's number in a cluster of kCl.
+template <int kCl>
+__device__ __forceinline__ int join_rank() {
+  return kCl == 1 ? 0 : static_cast<int>(cluster_ctarank());
+}
+
+// Adds NV values over the warps of a row (wpr in each CTA), in a fixed order; one barrier, as
+// join_sum.  The shuffles of a warp's sums give away half of the values a lane still has, so that
+// 8 values take 9 of them, not 40; a lane then owns one value, and after the barrier adds up every
+// eighth (or fourth) warp's.  Two CTAs of a row (kCl) write their warps' sums into both.
+template <int kWpr, int kCl, int NV>
+__device__ __forceinline__ void join_sums(float (&v)[NV], int wpr,
+                                          float (*sh)[kCl * kJoinMaxWarps][8], int& par) {
   constexpr int P = NV <= 4 ? 4 : 8, kLanes = 32 / P;  // lanes of a value
   const int lane = threadIdx.x & 31, own = lane / kLanes;
   float t[P];
@@ -90,15 +98,25 @@ __device__ __forceinline__ void join_sums(float (&v)[NV], float (*sh)[kJoinMaxWa
   }
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
-  if constexpr (wpr > 1) {
+  if (kCl > 1 || (kWpr != 1 && wpr > 1)) {
     const int warp = threadIdx.x / 32, row = warp / wpr;
-    if (lane % kLanes == 0) sh[par][warp][own] = t[0];
-    asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "n"(wpr * 32) : "memory");
+    if constexpr (kCl > 1) {
+      if (lane % kLanes < kCl) {  // a lane for each CTA
+        const uint32_t to = smem_u32(&sh[par][join_rank<kCl>() * wpr + warp][own]);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(to, lane % kLanes)),
+                     "f"(t[0])
+                     : "memory");
+      }
+      cluster_sync();
+    } else {
+      if (lane % kLanes == 0) sh[par][warp][own] = t[0];
+      asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "r"(wpr * 32) : "memory");
+    }
     t[0] = 0.f;
 #pragma unroll
-    for (int w0 = 0; w0 < wpr; w0 += kLanes) {
+    for (int w0 = 0; w0 < kCl * (kWpr > 0 ? kWpr : -kWpr); w0 += kLanes) {
       const int w = w0 + lane % kLanes;
-      if (w < wpr) t[0] += sh[par][row * wpr + w][own];
+      if (w < kCl * wpr) t[0] += sh[par][row * wpr + w][own];
     }
     par ^= 1;
 #pragma unroll
@@ -108,25 +126,76 @@ __device__ __forceinline__ void join_sums(float (&v)[NV], float (*sh)[kJoinMaxWa
   for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, t[0], i * kLanes);
 }
 
-template <class XT, class YT, int kVpt, int kWpr, bool kBeta, bool kPlain>
-__global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
+// What a thread needs of the parameters for every row: gamma_pre (packed) and w = gate gamma_post
+// of its columns, in registers, or (kSmem) in shared memory that is the thread's own: where they
+// would not fit, the compiler's spills miss what the ring leaves of L1.
+template <int kVpt, bool kSmem>
+struct JoinFactors {
+  uint4 g[kSmem ? 1 : kVpt];
+  JoinVec w[kSmem ? 1 : kVpt];
+  uint4* own;
+  static constexpr size_t kBytes = kSmem ? 48 * kVpt : 0;  // of a thread
+  __device__ __forceinline__ JoinFactors(void* smem) : own(static_cast<uint4*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ void set_pre(int k, const uint4& v) {
+    if constexpr (kSmem)
+      own[3 * k * blockDim.x] = v;
+    else
+      g[k] = v;
+  }
+  __device__ __forceinline__ void set_w(int k, const JoinVec& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kSmem)
+        reinterpret_cast<uint64_t*>(own + (3 * k + 1 + i / 2) * blockDim.x)[i % 2] = v[i];
+      else
+        w[k][i] = v[i];
+    }
+  }
+  __device__ __forceinline__ void pre(int k, JoinVec& v) const {
+    if constexpr (kSmem)
+      join_unpack(own[3 * k * blockDim.x], v);
+    else
+      join_unpack(g[k], v);
+  }
+  __device__ __forceinline__ void get_w(int k, JoinVec& v) const {
+    if constexpr (kSmem) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(own + (3 * k + 1 + h) * blockDim.x);
+        v[2 * h] = t.x;
+        v[2 * h + 1] = t.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = w[k][i];
+    }
+  }
+};
+
+// Whether they are in shared memory.
+template <int kWpr, bool kBeta>
+constexpr bool join_bwd_smem() {
+  return kWpr < 0 || kBeta;
+}
+
+template <class XT, class YT, int kVpt, int kWpr, bool kBeta, int kCl>
+__global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
     join_bwd_kernel(const JoinParams p) {
-  constexpr bool kSplit = sizeof(XT) == 4 || sizeof(YT) == 4;
-  constexpr bool kKeep = !kBeta && kVpt <= 2;
+  constexpr bool kSplit = sizeof(XT) == 4 || sizeof(YT) == 4, kPlain = kWpr > 0;
+  constexpr bool kKeep = !kBeta;
   using bf = __nv_bfloat16;
   extern __shared__ __align__(16) uint8_t join_smem[];
   constexpr int kSums = kBeta ? 7 : 3;
-  __shared__ float sh[2][kJoinMaxWarps][8];
-  constexpr int rows = join_rows(kWpr);
-  const int warp = threadIdx.x / 32, sub = warp / kWpr;
-  const JoinCols<kSplit, kVpt, kPlain> jc(kWpr, p.H);
+  __shared__ float sh[2][kCl * kJoinMaxWarps][8];
+  const int wpr = kPlain ? kWpr : p.wpr, rows = kPlain ? join_rows(kWpr) : p.rows;
+  const int warp = threadIdx.x / 32, sub = warp / wpr;
+  const JoinCols<kSplit, kVpt, kPlain> jc(kCl * wpr, join_rank<kCl>() * wpr + warp % wpr, p.H);
   const bool has_block = kPlain || p.has_block;
   const bool has_pre = kPlain || p.pre != MLPB_NORM_NONE;
   const bool has_post = kPlain || p.post != MLPB_NORM_NONE;
   const bool need_y = has_post || p.gate != nullptr;
   const bool has_dxout = kPlain || p.dXout != nullptr;
   const bool need_x = p.part_alpha != nullptr;
-  const bool late_ring = kPlain || !p.direct_late;
 
   // a warp's slots of a stage: Xout, dXn, Y, dXout, X (those that are read)
   constexpr uint32_t kXs = join_slots<XT, kVpt>(), kYs = join_slots<YT, kVpt>();
@@ -136,9 +205,9 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
   const uint32_t o_y = off;
   off += need_y ? kYs : 0;
   const uint32_t o_dxout = off;
-  off += late_ring && has_dxout ? kXs : 0;
+  off += has_dxout ? kXs : 0;
   const uint32_t o_x = off;
-  off += late_ring && need_x ? kXs : 0;
+  off += need_x ? kXs : 0;
   const uint32_t slots = off;
   const uint32_t mine = warp * p.nbuf * slots;
   const uint32_t base = smem_u32(join_smem) + mine;
@@ -154,11 +223,14 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
   JoinVec a1[kVpt], a0[kVpt];  // sum dXn xh, sum dXn
   JoinVec s1[kVpt], s0[kVpt];  // sum dh yh, sum dh of the group
   uint64_t d_alpha = 0ull;
-  uint4 gpre[kVpt];
-  JoinVec gw[kVpt];  // gate gamma_post of the group
+  // behind the ring
+  using Factors = JoinFactors<kVpt, join_bwd_smem<kWpr, kBeta>()>;
+  Factors fac(join_smem + p.ring_bytes);
+  uint8_t* comb = kPlain ? join_smem : join_smem + p.ring_bytes + Factors::kBytes * blockDim.x;
+  if (!kPlain && p.ragged) join_clear(join_smem, p.ring_bytes);
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
-    gpre[k] = join_param(p.gamma_pre, k, jc);
+    fac.set_pre(k, join_param(p.gamma_pre, k, jc));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       a1[k][i] = s1[k][i] = 0ull;
@@ -168,61 +240,65 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
 
   const int bpg = p.blocks_per_group;
   const int groups = p.G > 0 ? p.G : 1;
-  const int walkers = gridDim.x / bpg;  // CTAs apart: groups a CTA steps over
+  const int walker = blockIdx.x / kCl;        // this CTA, or cluster
+  const int walkers = gridDim.x / kCl / bpg;  // of a turn: groups that a walker steps over
   int par = 0;
   bool first = true;
+  if constexpr (kCl > 1) cluster_sync();  // the other CTA's shared memory is there
 
-  for (int g = blockIdx.x / bpg; g < groups; g += walkers) {
-    const int64_t r_end = (g + int64_t(1)) * p.rows_per_group;
-    const int64_t row0 = g * p.rows_per_group + (blockIdx.x % bpg) * rows + sub;
-    const int64_t step = static_cast<int64_t>(bpg) * rows;
+  for (int g = walker / bpg; g < groups; g += walkers) {
+    // (below 2^31, and what is added beyond the end below 2^14)
+    const uint32_t r_end = (g + 1u) * static_cast<uint32_t>(p.rows_per_group);
+    const uint32_t row0 = r_end - static_cast<uint32_t>(p.rows_per_group) + (walker % bpg) * rows + sub;
+    const uint32_t step = bpg * rows;
     const bf* gate = p.gate != nullptr ? p.gate + static_cast<int64_t>(g) * p.H : nullptr;
 
-    auto issue = [&](int b, int64_t row) {
+    auto issue = [&](int b, uint32_t row) {
       if (row < r_end) {
         const uint32_t d = base + b * slots;
-        const int64_t o = row * p.H;
+        const int64_t o = static_cast<int64_t>(row) * p.H;
         if (has_pre) {
           join_copy<XT>(d + o_xout, Xout + o, jc);
           join_copy<YT>(d + o_dxn, dXn + o, jc);
         }
         if (need_y) join_copy<YT>(d + o_y, Y + o, jc);
-        if (late_ring && has_dxout) join_copy<XT>(d + o_dxout, dXout + o, jc);
-        if (late_ring && need_x) join_copy<XT>(d + o_x, X + o, jc);
+        if (has_dxout) join_copy<XT>(d + o_dxout, dXout + o, jc);
+        if (need_x) join_copy<XT>(d + o_x, X + o, jc);
       }
       cp_async_commit();
     };
     for (int b = 0; b < p.nbuf; ++b) issue(b, row0 + b * step);
+    uint64_t ws = 0ull;
 #pragma unroll
     for (int k = 0; k < kVpt; ++k) {
-      JoinVec w;
-      join_unpack(join_param(gate, k, jc), gw[k]);
-      join_unpack(join_param(p.gamma_post, k, jc), w);
+      JoinVec w, t;
+      join_unpack(join_param(gate, k, jc), w);
       if (has_post) {
+        join_unpack(join_param(p.gamma_post, k, jc), t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) gw[k][i] = gate != nullptr ? f2_mul(gw[k][i], w[i]) : w[i];
+        for (int i = 0; i < 4; ++i) w[i] = gate != nullptr ? f2_mul(w[i], t[i]) : t[i];
       }
+      fac.set_w(k, w);
+      if (kBeta)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws = f2_add(ws, w[i]);
     }
 
     float w_sum = 0.f;  // sum of w over the row
     if (kBeta && p.post == MLPB_NORM_LAYER) {
-      uint64_t t = 0ull;
-#pragma unroll
-      for (int k = 0; k < kVpt; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t = f2_add(t, gw[k][i]);
-      float v[kSums] = {join_add_pair(t)};
-      join_sums<kWpr>(v, sh, par);
+      float v[kSums] = {join_add_pair(ws)};
+      join_sums<kWpr, kCl>(v, wpr, sh, par);
       w_sum = v[0];
     }
 
     int b = 0;
     float4 next = make_float4(0.f, 0.f, 0.f, 0.f);  // the next row's statistics, a row ahead
-    if (row0 < r_end) next = __ldg(reinterpret_cast<const float4*>(p.stats + row0 * 4));
-    for (int64_t row = row0; row < r_end; row += step) {
+    if (row0 < r_end) next = __ldg(reinterpret_cast<const float4*>(p.stats + static_cast<int64_t>(row0) * 4));
+    for (uint32_t row = row0; row < r_end; row += step) {
+      const int64_t at = static_cast<int64_t>(row) * p.H;
       const float4 stat = next;
       if (row + step < r_end)
-        next = __ldg(reinterpret_cast<const float4*>(p.stats + (row + step) * 4));
+        next = __ldg(reinterpret_cast<const float4*>(p.stats + static_cast<int64_t>(row + step) * 4));
       cp_async_wait_ring(p.nbuf);
       uint8_t* st = join_smem + mine + b * slots;
       const uint64_t mu_h = join_twice(stat.z), rs_h = join_twice(stat.w);
@@ -233,16 +309,14 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
         if (!has_dxout) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) t[i] = 0ull;
-        } else if (late_ring) {
-          join_read<XT>(st + o_dxout, k, jc, t);
         } else {
-          join_load<XT>(dXout + row * p.H, k, jc, t);
+          join_read<XT, true>(st + o_dxout, k, jc, t);
         }
         if (has_pre) {
           JoinVec w;
-          join_read<XT>(st + o_xout, k, jc, xh);
-          join_read<YT>(st + o_dxn, k, jc, d);
-          join_unpack(gpre[k], w);
+          join_read<XT, true>(st + o_xout, k, jc, xh);
+          join_read<YT, true>(st + o_dxn, k, jc, d);
+          fac.pre(k, w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             xh[i] = f2_mul(kBeta ? f2_sub(xh[i], mu_h) : xh[i], rs_h);
@@ -259,7 +333,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
         }
       };
       auto normed_y = [&](int k, JoinVec& yh) {
-        join_read<YT>(st + o_y, k, jc, yh);
+        join_read<YT, true>(st + o_y, k, jc, yh);
         if (has_post) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -281,16 +355,17 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
           }
         }
         if (has_post) {
-          JoinVec yh;
+          JoinVec yh, gw;
           normed_y(k, yh);
+          fac.get_w(k, gw);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // w is zero past the row's end
-            const uint64_t wy = f2_mul(gw[k][i], yh[i]);
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t wy = f2_mul(gw[i], yh[i]);
             q[1] = f2_fma(wy, t[i], q[1]);
             q[2] = f2_fma(wy, xh[i], q[2]);
             if (kBeta) {
-              q[4] = f2_fma(gw[k][i], t[i], q[4]);
-              q[5] = f2_fma(gw[k][i], xh[i], q[5]);
+              q[4] = f2_fma(gw[i], t[i], q[4]);
+              q[5] = f2_fma(gw[i], xh[i], q[5]);
               q[6] = f2_add(q[6], wy);
             }
           }
@@ -306,7 +381,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
       float sum[kSums];
 #pragma unroll
       for (int i = 0; i < kSums; ++i) sum[i] = join_add_pair(q[i]);
-      if (has_pre || has_post) join_sums<kWpr>(sum, sh, par);
+      if (has_pre || has_post) join_sums<kWpr, kCl>(sum, wpr, sh, par);
       // dh = t + xh cx - cg
       const float cx = -stat.w * sum[0] * inv_h;
       float cg = 0.f, u0 = 0.f, u1 = fmaf(cx, sum[2], sum[1]);  // sums of u, u yh
@@ -335,29 +410,27 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
         }
         if (need_x) {
           JoinVec x;
-          if (late_ring)
-            join_read<XT>(st + o_x, k, jc, x);
-          else
-            join_load<XT>(X + row * p.H, k, jc, x);
+          join_read<XT, true>(st + o_x, k, jc, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d_alpha = f2_fma(dh[i], x[i], d_alpha);  // x is 0 past the end
+          for (int i = 0; i < 4; ++i) d_alpha = f2_fma(dh[i], x[i], d_alpha);
         }
         if (p.alpha != nullptr) {
           JoinVec dx;
 #pragma unroll
           for (int i = 0; i < 4; ++i) dx[i] = f2_mul(alpha, dh[i]);
-          join_store<XT, false>(static_cast<XT*>(p.dX) + row * p.H, k, jc, dx);
+          join_store<XT, false>(static_cast<XT*>(p.dX) + at, k, jc, dx);
         } else {
-          join_store<XT, false>(static_cast<XT*>(p.dX) + row * p.H, k, jc, dh);
+          join_store<XT, false>(static_cast<XT*>(p.dX) + at, k, jc, dh);
         }
         if (need_y) {
-          JoinVec yh;
+          JoinVec yh, gw;
           normed_y(k, yh);
+          fac.get_w(k, gw);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             s1[k][i] = f2_fma(dh[i], yh[i], s1[k][i]);
             if (kBeta) s0[k][i] = f2_add(s0[k][i], dh[i]);
-            dh[i] = f2_mul(dh[i], gw[k][i]);  // u
+            dh[i] = f2_mul(dh[i], gw[i]);  // u
           }
           if (has_post) {
 #pragma unroll
@@ -365,7 +438,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
               dh[i] = f2_mul(rs_y, f2_fma(yh[i], c1, kBeta ? f2_sub(dh[i], c0) : dh[i]));
           }
         }
-        if (has_block) join_store<bf, false>(p.dY + row * p.H, k, jc, dh);
+        if (has_block) join_store<bf, false>(p.dY + at, k, jc, dh);
       }
       issue(b, row + p.nbuf * step);  // this row's slots have been read
       if (++b == p.nbuf) b = 0;
@@ -373,10 +446,10 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
 
     // The end of this CTA's rows of the group: S1 and S0 over the CTA, and what they give.
     if (need_y) {
-      join_combine<rows>(s1);
-      if (kBeta) join_combine<rows>(s0);
+      join_combine(s1, rows, comb);
+      if (kBeta) join_combine(s0, rows, comb);
       if (sub == 0) {
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) * p.H;
+        const int64_t slot = static_cast<int64_t>(walker) * p.H;
 #pragma unroll
         for (int k = 0; k < kVpt; ++k) {
           JoinVec w, t;
@@ -426,10 +499,10 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
   }
 
   if (has_pre) {
-    join_combine<rows>(a1);
-    if (kBeta) join_combine<rows>(a0);
+    join_combine(a1, rows, comb);
+    if (kBeta) join_combine(a0, rows, comb);
     if (sub == 0) {
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * p.H;
+      const int64_t slot = static_cast<int64_t>(walker) * p.H;
 #pragma unroll
       for (int k = 0; k < kVpt; ++k) {
         join_put(p.part_gpre + slot, k, jc, a1[k], false);
@@ -452,53 +525,72 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
   }
 }
 
-template <class XT, class YT, int kVpt, int kWpr, bool kBeta>
-static cudaError_t join_bwd_launch(JoinParams p, bool plain, int grid, cudaStream_t s) {
-  constexpr int threads = join_threads(kWpr), warps = threads / 32;
+template <class XT, class YT, int kVpt, int kWpr, bool kBeta, int kCl = 1>
+static cudaError_t join_bwd_launch(JoinParams p, const JoinShape& sh, int grid, cudaStream_t s) {
   const bool has_pre = p.pre != MLPB_NORM_NONE, has_post = p.post != MLPB_NORM_NONE;
   const bool need_y = has_post || p.gate != nullptr;
-  constexpr size_t xs = warps * join_slots<XT, kVpt>(), ys = warps * join_slots<YT, kVpt>();
+  const int warps = sh.threads / 32;
+  const size_t xs = warps * join_slots<XT, kVpt>(), ys = warps * join_slots<YT, kVpt>();
   const size_t early = (has_pre ? xs + ys : 0) + (need_y ? ys : 0);
   const size_t late = (p.dXout != nullptr ? xs : 0) + (p.part_alpha != nullptr ? xs : 0);
-  const size_t room = (208u << 10) / (512 / threads);
-  p.direct_late = early + late > room;
-  const size_t stage = p.direct_late ? early : early + late;
+  constexpr size_t kFactors = JoinFactors<kVpt, join_bwd_smem<kWpr, kBeta>()>::kBytes;
+  // (the general ones' rows meet in memory of their own)
+  const size_t comb = sh.rows > 1 ? static_cast<size_t>(sh.threads) * kVpt * 32 : 0;
+  const size_t room = (208u << 10) / join_ctas(kWpr) - kFactors * sh.threads -
+                      (kWpr < 0 ? comb : 0);
+  const size_t stage = early + late;  // 160 KB an SM at most: one fits
   p.nbuf = static_cast<int>(std::max<size_t>(
       1, std::min<size_t>(kJoinMaxBuf, room / std::max<size_t>(stage, 1))));
   size_t smem = p.nbuf * stage;
-  if (join_rows(kWpr) > 1)
-    smem = std::max(smem, static_cast<size_t>(threads) * kVpt * 32);  // join_combine
-  auto* kernel = join_bwd_kernel<XT, YT, kVpt, kWpr, kBeta, false>;
-  if constexpr (kVpt == 2) {
-    if (plain && p.H == 256 * kVpt * kWpr && !p.direct_late)
-      kernel = join_bwd_kernel<XT, YT, kVpt, kWpr, kBeta, true>;
-  }
+  if (kWpr > 0) smem = std::max(smem, comb);
+  p.ring_bytes = static_cast<int>(smem);
+  smem += kFactors * sh.threads + (kWpr < 0 ? comb : 0);
+  p.ragged = p.H % (256 * kVpt * kCl * sh.wpr) != 0;
+  p.wpr = sh.wpr;
+  p.rows = sh.rows;
+  auto* kernel = join_bwd_kernel<XT, YT, kVpt, kWpr, kBeta, kCl>;
   const cudaError_t e = join_smem_attr(kernel, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, threads, smem, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * kCl));
+  cfg.blockDim = dim3(static_cast<unsigned>(sh.threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {kCl, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = kCl > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// `sh` is join_bwd_shape's for this call.
 template <class XT, class YT, bool kBeta>
-static cudaError_t join_bwd_pick(const JoinParams& p, int grid, cudaStream_t s) {
-  const bool plain =
-      p.pre != MLPB_NORM_NONE && p.post != MLPB_NORM_NONE && p.has_block && p.dXout != nullptr;
-  switch (join_bwd_wpr(p.H)) {
-    case 1: return join_bwd_launch<XT, YT, 1, 1, kBeta>(p, plain, grid, s);
-    case 2: return join_bwd_launch<XT, YT, 2, 2, kBeta>(p, plain, grid, s);
-    case 4: return join_bwd_launch<XT, YT, 2, 4, kBeta>(p, plain, grid, s);
-    case 8: return join_bwd_launch<XT, YT, 2, 8, kBeta>(p, plain, grid, s);
-    case 10: return join_bwd_launch<XT, YT, 2, 10, kBeta>(p, plain, grid, s);
+static cudaError_t join_bwd_pick(const JoinParams& p, const JoinShape& sh, bool plain, int grid,
+                                 cudaStream_t s) {
+  if (plain) {
+    switch (sh.wpr) {
+      case 2: return join_bwd_launch<XT, YT, 2, 2, kBeta>(p, sh, grid, s);
+      case 4: return join_bwd_launch<XT, YT, 2, 4, kBeta>(p, sh, grid, s);
+      case 8: return join_bwd_launch<XT, YT, 2, 8, kBeta>(p, sh, grid, s);
+      case 10: return join_bwd_launch<XT, YT, 2, 10, kBeta>(p, sh, grid, s);
+      default: return join_bwd_launch<XT, YT, 2, 16, kBeta>(p, sh, grid, s);
+    }
   }
-  return p.H <= 8192 ? join_bwd_launch<XT, YT, 2, 16, kBeta>(p, plain, grid, s)
-                     : join_bwd_launch<XT, YT, 4, 16, kBeta>(p, plain, grid, s);
+  if (sh.vpt == 1) return join_bwd_launch<XT, YT, 1, -16, kBeta>(p, sh, grid, s);
+  if (sh.cluster == 1)
+    return sh.wpr <= 12 ? join_bwd_launch<XT, YT, 2, -12, kBeta>(p, sh, grid, s)
+                        : join_bwd_launch<XT, YT, 2, -16, kBeta>(p, sh, grid, s);
+  return sh.wpr <= 12 ? join_bwd_launch<XT, YT, 2, -12, kBeta, 2>(p, sh, grid, s)
+                      : join_bwd_launch<XT, YT, 2, -16, kBeta, 2>(p, sh, grid, s);
 }
 
 template <class XT, class YT>
-cudaError_t join_bwd_run(const JoinParams& p, int grid, cudaStream_t s) {
+cudaError_t join_bwd_run(const JoinParams& p, const JoinShape& sh, bool plain, int grid,
+                         cudaStream_t s) {
   return p.post == MLPB_NORM_LAYER || p.pre == MLPB_NORM_LAYER
-             ? join_bwd_pick<XT, YT, true>(p, grid, s)
-             : join_bwd_pick<XT, YT, false>(p, grid, s);
+             ? join_bwd_pick<XT, YT, true>(p, sh, plain, grid, s)
+             : join_bwd_pick<XT, YT, false>(p, sh, plain, grid, s);
 }
 
 }  // namespace mlpb

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
   const bool has_block = kPlain || p.has_block;
   const bool has_post = kPlain || p.post != MLPB_NORM_NONE;
   const bool has_pre = kPlain || p.pre != MLPB_NORM_NONE;
-  const JoinCols<kSplit, kVpt, kPlain> jc(kWpr, p.H);
+  const JoinCols<kSplit, kVpt, kPlain> jc(kWpr, warp % kWpr, p.H);
   constexpr uint32_t kXs = join_slots<XT, kVpt>();
   const uint32_t slots = kXs + (has_block ? join_slots<YT, kVpt>() : 0);  // a warp's, of a stage
   const uint32_t mine = warp * p.nbuf * slots;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
     float mu_y = 0.f, rs_y = 0.f, mu_h = 0.f, rs_h = 0.f;
     if (has_block) {
 #pragma unroll
-      for (int k = 0; k < kVpt; ++k) join_read<YT>(st + kXs, k, jc, v[k]);
+      for (int k = 0; k < kVpt; ++k) join_read<YT, false>(st + kXs, k, jc, v[k]);
       if (has_post) join_stats<kBeta, kWpr>(v, jc, p.post, inv_h, p.eps, sh, par, mu_y, rs_y);
 #pragma unroll
       for (int k = 0; k < kVpt; ++k) {
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[k][i] = f2_mul(v[k][i], gw[k][i]);
         }
-        join_read<XT>(st, k, jc, t);
+        join_read<XT, false>(st, k, jc, t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[k][i] = f2_fma(alpha, t[i], v[k][i]);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < kVpt; ++k) join_read<XT>(st, k, jc, v[k]);
+      for (int k = 0; k < kVpt; ++k) join_read<XT, false>(st, k, jc, v[k]);
     }
     issue(b, row + p.nbuf * step);  // the slots of this row have been read
     if (++b == p.nbuf) b = 0;

@@ -5,6 +5,7 @@
 namespace mlpb {
 
 template cudaError_t join_fwd_run<float, __nv_bfloat16>(const JoinParams&, int, cudaStream_t);
-template cudaError_t join_bwd_run<float, __nv_bfloat16>(const JoinParams&, int, cudaStream_t);
+template cudaError_t join_bwd_run<float, __nv_bfloat16>(
+    const JoinParams&, const JoinShape&, bool, int, cudaStream_t);
 
 }  // namespace mlpb

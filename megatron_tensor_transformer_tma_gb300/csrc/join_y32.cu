@@ -5,6 +5,7 @@
 namespace mlpb {
 
 template cudaError_t join_fwd_run<__nv_bfloat16, float>(const JoinParams&, int, cudaStream_t);
-template cudaError_t join_bwd_run<__nv_bfloat16, float>(const JoinParams&, int, cudaStream_t);
+template cudaError_t join_bwd_run<__nv_bfloat16, float>(
+    const JoinParams&, const JoinShape&, bool, int, cudaStream_t);
 
 }  // namespace mlpb
