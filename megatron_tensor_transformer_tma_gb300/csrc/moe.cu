@@ -770,7 +770,8 @@ extern "C" mlpb_status mlpb_moe_create(const mlpb_moe_config* cfg, mlpb_moe** ou
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moe_kernel, kMoeBlock, kMoeSmem) !=
           cudaSuccess ||
       per_sm < 1 || cudaMalloc(reinterpret_cast<void**>(&h->sync), sizeof(MoeSync)) != cudaSuccess ||
-      cudaMemset(h->sync, 0, sizeof(MoeSync)) != cudaSuccess) {
+      cudaMemset(h->sync, 0, sizeof(MoeSync)) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come
     if (h->sync) cudaFree(h->sync);
     delete h;
     return MLPB_ECUDA;
@@ -851,12 +852,14 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
 
 extern "C" mlpb_status mlpb_moe_last_device_error(mlpb_moe* h, mlpb_stream_t stream) {
   if (h == nullptr) return MLPB_EINVAL;
-  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MLPB_ECUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaStreamSynchronize(s) != cudaSuccess) return MLPB_ECUDA;
   uint32_t v = 0;
   if (cudaMemcpy(&v, &h->sync->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess)
     return MLPB_ECUDA;
   if (v == 0) return MLPB_OK;
-  if (cudaMemset(&h->sync->err, 0, sizeof(uint32_t)) != cudaSuccess) return MLPB_ECUDA;
+  if (cudaMemsetAsync(&h->sync->err, 0, sizeof(uint32_t), s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MLPB_ECUDA;
   return MLPB_ETIMEOUT;
 }

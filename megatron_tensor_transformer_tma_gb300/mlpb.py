@@ -7,8 +7,10 @@ Loading fails loudly when libmlpb.so has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
+import functools
 import os
 
 import torch
@@ -213,6 +215,15 @@ def _call_on(dev, name, args, stream):
             _check(fn(*args, s), name)
 
 
+def _on(stream):
+    """A context in which new tensors belong to the stream that the call will run on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -395,6 +406,7 @@ def mlpb_quantize_e4m3(inp, q=None, qt=None, amax=None, scale_exp=None, stream=N
 _ACTS = {"gelu": MLPB_ACT_GELU_TANH, "swiglu": MLPB_ACT_SWIGLU}
 
 
+@functools.lru_cache(maxsize=None)
 def mlpb_act8_scales(act, ffn, tp=1) -> int:
     """Scale bytes of a row of an 8-bit activation checkpoint (act: "gelu" or "swiglu")."""
     n = ctypes.c_int64()
@@ -729,14 +741,17 @@ class ActCheckpoint8:
         return torch.empty((self.tokens, width), dtype=torch.bfloat16, device=self.device)
 
     def save(self, Z, A=None, stream=None):
-        A = self._new(self.ffn) if A is None else A
+        if A is None:
+            with _on(stream):
+                A = self._new(self.ffn)
         mlpb_act8_save(self.act, Z, A, self.codes, self.scales, self.tp, stream)
         return A
 
     def grad(self, dA, dZ=None, A=None, codes=None, scales=None, stream=None):
         """(dZ, A); codes and scales other than the ones this object holds may be given."""
-        dZ = self._new(self.width) if dZ is None else dZ
-        A = self._new(self.ffn) if A is None else A
+        with _on(stream):
+            dZ = self._new(self.width) if dZ is None else dZ
+            A = self._new(self.ffn) if A is None else A
         mlpb_act8_grad(self.act, dA, self.codes if codes is None else codes,
                        self.scales if scales is None else scales, dZ, A, self.tp, stream)
         return dZ, A
@@ -763,12 +778,13 @@ class Join:
         """(Xout, Xn, stats); Xout is None without a block, Xn without a pre norm.  Pass the
         stream X itself as Xout to update it in place."""
         c = self.cfg
-        if Xout is None and c.has_block:
-            Xout = self._rows(_join_types(c)[0])
-        if Xn is None and c.pre_norm != MLPB_NORM_NONE:
-            Xn = self._rows(torch.bfloat16)
-        if stats is None:
-            stats = torch.empty((c.tokens, 4), dtype=torch.float32, device=self.device)
+        with _on(stream):
+            if Xout is None and c.has_block:
+                Xout = self._rows(_join_types(c)[0])
+            if Xn is None and c.pre_norm != MLPB_NORM_NONE:
+                Xn = self._rows(torch.bfloat16)
+            if stats is None:
+                stats = torch.empty((c.tokens, 4), dtype=torch.float32, device=self.device)
         mlpb_join_fwd(c, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre, Xout,
                       Xn, stats, stream)
         return Xout, Xn, stats
@@ -795,7 +811,10 @@ class Join:
                  stream=None):
         """The gradients for dXout (None: zero) and dXn of forward()'s outputs; X and Y may be
         None where the backward does not read them (include/mlpb.h)."""
-        g = self.alloc_grads(res_scale is not None) if grads is None else grads
+        g = grads
+        if g is None:
+            with _on(stream):
+                g = self.alloc_grads(res_scale is not None)
         mlpb_join_bwd(self.cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post,
                       gamma_pre, dXout, dXn, g["dX"], g["dY"], g["dres_scale"], g["dgate"],
                       g["dgamma_post"], g["dbeta_post"], g["dgamma_pre"], g["dbeta_pre"],
@@ -827,11 +846,12 @@ class MoEDecode:
 
     def forward(self, X, Wr, W1, W2, Y=None, ids=None, weights=None, stream=None):
         T, c = X.shape[0], self.cfg
-        if Y is None:
-            Y = torch.empty((T, c.hidden), dtype=torch.bfloat16, device=self.device)
-        if ids is None:
-            ids = torch.empty((T, c.topk), dtype=torch.int32, device=self.device)
-        if weights is None:
-            weights = torch.empty((T, c.topk), dtype=torch.float32, device=self.device)
+        with _on(stream):
+            if Y is None:
+                Y = torch.empty((T, c.hidden), dtype=torch.bfloat16, device=self.device)
+            if ids is None:
+                ids = torch.empty((T, c.topk), dtype=torch.int32, device=self.device)
+            if weights is None:
+                weights = torch.empty((T, c.topk), dtype=torch.float32, device=self.device)
         mlpb_moe_forward(self.handle, X, Wr, W1, W2, Y, ids, weights, self.workspace, stream)
         return Y, ids, weights

@@ -156,6 +156,26 @@ def test_no_tokens_other_stream_and_graph():
     assert torch.equal(out, dZ) and torch.equal(ck2.codes, ck.codes)
 
 
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_offsets_past_32_bits(act):
+    """The last rows of 2^32 values and more."""
+    F = 32768
+    f1 = 2 * F if act == "swiglu" else F
+    T, n = 2 ** 32 // f1 + 24, 5
+    z, dA = _inputs(n, F, act, 7, special=False)
+    Z = torch.zeros(T, f1, dtype=torch.bfloat16, device="cuda")
+    D = torch.zeros(T, F, dtype=torch.bfloat16, device="cuda")
+    Z[-n:], D[-n:] = z.cuda(), dA.cuda()
+    big, small = mlpb.ActCheckpoint8(T, F, 1, act), mlpb.ActCheckpoint8(n, F, 1, act)
+    A, a = big.save(Z), small.save(z.cuda())
+    assert torch.equal(A[-n:], a) and (A[:-n] == 0).all()
+    assert torch.equal(big.codes[-n:], small.codes) and torch.equal(big.scales[-n:], small.scales)
+    del Z
+    dZ, A2 = big.grad(D)
+    dz, a2 = small.grad(dA.cuda())
+    assert torch.equal(dZ[-n:], dz) and torch.equal(A2[-n:], a2)
+
+
 def test_refusals():
     z = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
     ck = mlpb.ActCheckpoint8(4, 64, 1, "gelu")

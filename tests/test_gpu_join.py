@@ -177,6 +177,36 @@ def test_shapes_and_types(T, H):
     _run(T, H, "layer", "rms", 0, True, *types[(i + 2) % 4])
 
 
+# widths that leave warps, or CTAs of a row, with few columns or none; rows that share a CTA
+@pytest.mark.parametrize("H", [256, 264, 512, 776, 1536, 2184, 2936, 4392, 6024, 6152, 7000, 8208,
+                               12288, 12296, 13000, 16376])
+def test_widths(H):
+    for i, T in enumerate((5, 460)):
+        types = [(BF, BF), (F32, F32), (BF, F32), (F32, BF)][(H // 8 + i) % 4]
+        _run(T, H, "layer", "layer", 5, True, *types)
+        _run(T, H, "rms", "rms", 0, False, *types)
+        _run(T, H, "none", "layer", T, True, *types)
+
+
+def test_rows_of_two_ctas():
+    """Above 8192 columns: in place, accumulated, captured, groups more and fewer than walkers."""
+    for G in (2, 380):
+        T, H = 380, 9000
+        d, par, plan, out, got = _run(T, H, "layer", "rms", G, True, BF, BF)
+        acc = mlpb.Join(T, H, "layer", "rms", G, EPS, accumulate=True)
+        grads = acc.alloc_grads(True)
+        grads["dX"] = d["dXout"].clone()
+        stat = (out[0], out[2])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            acc.backward(d["X"], d["Y"], *stat, grads["dX"], d["dXn"], grads=grads, **par)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in got.items():
+            assert (v is None and grads[k] is None) or torch.equal(v, grads[k]), k
+        del graph
+
+
 @pytest.mark.parametrize("T,H,G", [(1000, 320, 8), (2048, 64, 1024), (1500, 136, 500),
                                    (400, 8192, 400), (640, 1024, 2)])
 def test_groups(T, H, G):

@@ -1,6 +1,6 @@
-"""The operators around and in place of the block, as a layer uses them, one after the other: a training step of two MLP
-sub-blocks (join, block with 8-bit checkpoints, join, ...) forward and backward, and a
-serving step of two mixture-of-experts sub-blocks (join, experts, join, ...).
+"""The operators around and in place of the block, one after the other as a layer uses them: a
+training step of two MLP sub-blocks (join, block with 8-bit checkpoints, join, ...) forward and
+backward, and a serving step of two mixture-of-experts sub-blocks (join, experts, join, ...).
 
 Every stage is checked against its fp64 oracle on the inputs that the stage before it stored,
 with that operator's own tolerances.  The whole chain's gradients are checked against
@@ -258,3 +258,32 @@ def test_serving_step_captured():
         torch.cuda.synchronize()
         assert torch.equal(x, want[s])
     del graph
+
+
+def test_calls_on_a_given_stream():
+    """stream= as an object and as a handle: what a call allocates belongs to that stream, and a
+    new handle serves a stream that does not wait for the default one."""
+    d, X = _serve_params()
+    d["g"].append(torch.ones(MH, dtype=BF, device="cuda"))
+    torch.cuda.synchronize()
+    z = torch.randn(64, 512, device="cuda").to(BF)
+    plan = mlpb.Join(MT, MH, "rms", "rms")
+    ck = mlpb.ActCheckpoint8(64, 512)
+    par = dict(gamma_post=d["g"][0], gamma_pre=d["g"][1])
+
+    def run(**kw):
+        moe = mlpb.MoEDecode(MT, MH, MF, ME, MK)
+        out = moe.forward(X, *d["w"][0], **kw)
+        o = plan.forward(X, out[0], **par, **kw)
+        g = plan.backward(None, out[0], o[0], o[2], X, X, **par, **kw)
+        a = ck.save(z, **kw)
+        return [*out, *o, g["dX"], g["dY"], g["dgamma_pre"], a, *ck.grad(a, **kw)], moe
+    want, keep = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for kw in (dict(stream=side), dict(stream=side.cuda_stream)):
+        got, m = run(**kw)
+        side.synchronize()
+        assert mlpb.mlpb_moe_last_device_error(m.handle, side) == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -177,6 +177,39 @@ def test_same_bits_stream_and_two_graphs():
         assert mlpb.mlpb_moe_last_device_error(p2.handle) == 0
 
 
+def test_offsets_past_32_bits():
+    """Weights of more than 2^32 elements: the last experts are those of a small layer with the
+    same rows (the first ones, of zeros, have logits of zero and are not taken)."""
+    T, H, F, E, n = 3, 4096, 8200, 66, 3
+    d = [t.cuda() for t in _make(T, H, F, n, "swiglu")]
+    d[1] = (d[0][:1].float().sign() * d[1].float().abs() + 0.0).to(BF)  # token 0 takes them
+    d[0] = d[0][:1].expand(T, -1).contiguous()
+    Wr = torch.zeros(E, H, dtype=BF, device="cuda")
+    W1 = torch.zeros(E, 2, F, H, dtype=BF, device="cuda")
+    W2 = torch.zeros(E, H, F, dtype=BF, device="cuda")
+    Wr[-n:], W1[-n:], W2[-n:] = d[1], d[2], d[3]
+    big, small = mlpb.MoEDecode(T, H, F, E, n), mlpb.MoEDecode(T, H, F, n, n)
+    Y, ids, w = big.forward(d[0], Wr, W1, W2)
+    y, ids2, w2 = small.forward(*d)
+    assert torch.equal(ids, ids2 + (E - n))
+    # The two sum their logits in different orders (the first form of this test held them equal
+    # to 2^-20, which forgets that): each is within D of the exact ones, its normalised weights
+    # within 2 (2 D + 16 u), the two within twice that of each other.
+    x = d[0][0].double()
+    D = (8 * -(-H // 4096) + 24) * U * (d[1].double().abs() @ x.abs()).max().item()
+    rel = 2 * 2 * (2 * D + 16 * U)
+    assert ((w - w2).abs() <= rel * w2).all()
+    # the outputs differ by that of the experts' weighted parts (with 1 % for their rounded
+    # activations), and by a step of bf16, 2^-7 of the value
+    part = torch.zeros(H, dtype=torch.float64, device="cuda")
+    for k, e in enumerate(ids2[0].tolist()):
+        g, u = d[2][e].double() @ x
+        part += w2[0, k] * (d[3][e].double() @ (g * torch.sigmoid(g) * u)).abs()
+    bound = 1.01 * rel * part + 2.0 ** -7 * y.double().abs()
+    assert ((Y.double() - y.double()).abs() <= bound).all()
+    assert mlpb.mlpb_moe_last_device_error(big.handle) == 0
+
+
 def test_refusals():
     d = [t.cuda() for t in _make(4, 64, 32, 8, "swiglu")]
     plan = mlpb.MoEDecode(4, 64, 32, 8, 2)
