@@ -10,7 +10,12 @@
 // halves of a block; 8 where rows are not 32-byte aligned throughout), neighbouring threads a
 // block, whose largest magnitude takes a shuffle or two.  A CTA is ux column units by 256 / ux
 // rows, ux the power of two that covers a row's units (at most 256), so narrow rows do not idle
-// threads; every thread walks kAct8Rows rows of its columns, whose loads are issued together.
+// threads; every thread walks act8_rows() rows of its columns, whose loads are issued together.
+//
+// Measured, with the rate of the bytes above (a copy reaches 6.8 TB/s): GELU T8192 F20480 save
+// 124 us, 6.8 TB/s, grad 181 us, 6.5 TB/s; SwiGLU T16384 F11008 save 214 us, 6.8 TB/s, grad
+// 301 us, 6.0 TB/s (its mix has the most streams, three in and three out, and 80 registers a
+// thread: instructions issue in 55 % of its cycles, stalled on loads otherwise).
 #include <algorithm>
 
 #include "../../include/mlpb.h"

@@ -769,23 +769,25 @@ class Join:
         self.device = torch.device(device)
         self.workspace = torch.empty(_join_ws(self.cfg, self.device), dtype=torch.uint8,
                                      device=self.device)
+        self._stream_dtype, self._has_block = stream_dtype, bool(has_block)
+        self._has_pre = self.cfg.pre_norm != MLPB_NORM_NONE
+        self._shape, self._stats = (tokens, hidden), (tokens, 4)
 
     def _rows(self, dtype):
-        return torch.empty((self.cfg.tokens, self.cfg.hidden), dtype=dtype, device=self.device)
+        return torch.empty(self._shape, dtype=dtype, device=self.device)
 
     def forward(self, X, Y=None, res_scale=None, gate=None, gamma_post=None, beta_post=None,
                 gamma_pre=None, beta_pre=None, Xout=None, Xn=None, stats=None, stream=None):
         """(Xout, Xn, stats); Xout is None without a block, Xn without a pre norm.  Pass the
         stream X itself as Xout to update it in place."""
-        c = self.cfg
         with _on(stream):
-            if Xout is None and c.has_block:
-                Xout = self._rows(_join_types(c)[0])
-            if Xn is None and c.pre_norm != MLPB_NORM_NONE:
+            if Xout is None and self._has_block:
+                Xout = self._rows(self._stream_dtype)
+            if Xn is None and self._has_pre:
                 Xn = self._rows(torch.bfloat16)
             if stats is None:
-                stats = torch.empty((c.tokens, 4), dtype=torch.float32, device=self.device)
-        mlpb_join_fwd(c, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre, Xout,
+                stats = torch.empty(self._stats, dtype=torch.float32, device=self.device)
+        mlpb_join_fwd(self.cfg, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre, Xout,
                       Xn, stats, stream)
         return Xout, Xn, stats
 
