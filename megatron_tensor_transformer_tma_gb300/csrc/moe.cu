@@ -24,23 +24,28 @@
 // ends of units and over the barrier between fc1 and fc2: fc2's first weights arrive while the
 // last CTAs finish fc1.  Tokens' fragments (from L2) each lane copies for itself, into a slot of
 // its own in the same stage, as far ahead.
+// Where an expert has more than 16 tokens, those copies, 512 bytes a token for every 8 KB of
+// weights, would leave one stage in a group's ring.  Then the CTA has one ring and works on
+// units of 64 rows, 16 for each group, and a stage holds its tokens once for all four: T 64
+// H 4096 Fe 1792 4 experts top 2 73 us (with rings of the groups 125; two groups with units of
+// 32 rows 154), 16 experts top 4 153 us (170); from 9 tokens on it loses (T 24 57 us against
+// 51).
 // Two other ways to move the weights measured slower: cp.async of each lane's own fragments was
 // bound by instructions, about 200 a kilobyte (T 1: 4.1 TB/s over all); and bulk copies of
 // single rows, one a lane, by their issue, about 70 ns each (2.1 TB/s).
 //
 // The products run on mma.sync m16n8k16 with the weights as the 16-row operand and tokens as
-// its 8 columns.  tcgen05 has no shape for this: its M is 64 or 128 rows, and the tensor work
-// here is under a tenth of the time even at 64 tokens.  K is permuted the same way in both
-// operands so that a lane's fragments are 16 consecutive bytes of a row.
+// its 8 columns.  (tcgen05 takes 64 or 128 rows: units four times as large would leave 2 for an
+// SM at T 1, and the tensor pipe is busy 5 % of the time there, 12 % at T 16, a quarter with 38
+// tokens an expert.)  K is permuted the same way in both operands so that a lane's fragments are
+// 16 consecutive bytes of a row.
 //
 // Measured, over the bytes of the routed experts' weights (a copy reaches 6.8 TB/s): SwiGLU T 1
-// H 4096 Fe 1376 top 8: 271 MB in 68 us, 4.0 TB/s; T 16 H 4096 Fe 688 128 experts top 8: 1.39 GB
-// in 235 us, 5.9 TB/s; T 64 H 5120 Fe 2560 32 experts top 4: 2.52 GB in 415 us, 6.1 TB/s.  At T 1
+// H 4096 Fe 1376 top 8: 271 MB in 65 us, 4.2 TB/s; T 16 H 4096 Fe 688 128 experts top 8: 1.39 GB
+// in 228 us, 6.1 TB/s; T 64 H 5120 Fe 2560 32 experts top 4: 2.52 GB in 415 us, 6.1 TB/s.  At T 1
 // the launch, router, choice and three barriers take 13 us of that, and fc1 ends between 35 and
 // 48 us by the part of the chip an SM is in (units claimed one by one instead measured 74 us in
-// all).  Above 16 tokens an expert the tokens' copies, 512 bytes each for 8 KB of weights, leave
-// one stage in a ring: T 64 H 4096 Fe 1792 4 experts top 2 takes 125 us against 26 for its bytes
-// (units of 32 rows, with half the copies, 154).
+// all).
 //
 // a is rounded to bf16, as every activation that a GEMM of this library reads; logits, softmax
 // and all sums are fp32.  Every wait is bounded (common.cuh).
@@ -49,6 +54,7 @@
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "../../include/mlpb.h"
 #include "common.cuh"
@@ -69,6 +75,7 @@ constexpr uint32_t kMoeBox = kMoeKc * kMoeBoxRows * 2;
 constexpr uint32_t kMoeStageW = 2 * kMoeBox;  // a stage's weights; its tokens take 512 bytes each
 constexpr uint32_t kMoeRing = 48u << 10;      // of one group
 constexpr int kMoeMaxStages = 5;
+constexpr int kMoeSharedFrom = 17;  // tokens of an expert from which a CTA works on one unit
 constexpr int kMoePairs = kMoeMaxTokens * kMoeMaxTopk;
 
 enum MoeSite : uint32_t { kSiteMoeGrid = 16, kSiteMoeEmpty = 17, kSiteMoeFull = 18 };
@@ -344,9 +351,12 @@ __device__ void moe_route(const MoeParams& p, MoeShared& sh) {
 }
 
 // ------------------------------------------------------------------ the rings
-// A group's ring.  A stage: the weights (8 rows by 256, twice), then for each multiplying warp
-// 128 bytes (its 64 of K) of up to `most` tokens.
+// A group's ring (kTiles 1), or the CTA's (kTiles 4).  A stage: for each tile of 16 rows the
+// weights (8 rows by 256, twice), then for each warp of a group 128 bytes (its 64 of K) of up to
+// `most` tokens.
+template <int kTiles>
 struct MoeRing {
+  static constexpr uint32_t kWeights = kTiles * kMoeStageW;
   uint32_t base;       // shared-memory address of stage 0
   const uint8_t* ptr;  // the same as a pointer
   uint32_t full, empty;  // its barriers
@@ -358,8 +368,12 @@ struct MoeRing {
         full(smem_u32(sh.full[group])),
         empty(smem_u32(sh.empty[group])),
         most(sh.most) {
-    stage_bytes = kMoeStageW + most * (kMoeKc * 2);
-    stages = min(kMoeMaxStages, static_cast<int>(kMoeRing / stage_bytes));
+    stage_bytes = kWeights + most * (kMoeKc * 2);
+    stages = min(kMoeMaxStages, static_cast<int>(kTiles * kMoeRing / stage_bytes));
+  }
+  // Offset in a stage of a lane's slot for the expert's token number t and step i.
+  __device__ __forceinline__ uint32_t slot(int i, int t) const {
+    return kWeights + ((moe_warp() * 2 + i) * most + t) * 64 + (threadIdx.x & 3) * 16;
   }
 };
 
@@ -367,28 +381,31 @@ struct MoeRing {
 struct MoePlace {
   int stage = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ void next(const MoeRing& r) {
-    if (++stage == r.stages) {
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
     }
   }
 };
 
-// The units of fc1 and fc2: expert by expert, `rows` features or 16 output columns each.  Unit u
-// belongs to CTA u mod grid, and there to the groups in turn.
-template <bool kFc1>
+// The units of fc1 and fc2: expert by expert, `rows` features or output columns each, kTiles
+// tiles of weight rows.  Unit u belongs to CTA u mod grid, and there to the groups in turn, or to
+// all of them (kTiles 4).
+template <int kTiles, bool kFc1>
 struct MoeUnits {
   int rows, per, count, kcs, len;  // rows of a unit, units of an expert, of all; stages; K
   __device__ __forceinline__ MoeUnits(const MoeParams& p, const MoeShared& sh) {
-    rows = kFc1 && p.gated ? 8 : 16;
+    rows = kTiles * (kFc1 && p.gated ? 8 : 16);
     per = ((kFc1 ? p.Fe : p.H) + rows - 1) / rows;
     count = sh.n_active * per;
     len = kFc1 ? p.H : p.Fe;
     kcs = (len + kMoeKc - 1) / kMoeKc;
   }
-  static __device__ __forceinline__ int first(int group) { return blockIdx.x + group * gridDim.x; }
-  static __device__ __forceinline__ int step() { return kMoeGroups * gridDim.x; }
+  static __device__ __forceinline__ int first(int group) {
+    return kTiles == 1 ? blockIdx.x + group * gridDim.x : blockIdx.x;
+  }
+  static __device__ __forceinline__ int step() { return kMoeGroups / kTiles * gridDim.x; }
 };
 
 // A wait of many threads: without the clock as long as it is short.
@@ -403,40 +420,45 @@ __device__ __forceinline__ bool moe_wait(uint32_t bar, uint32_t parity, const Wa
 // ------------------------------------------------------------------ the copying threads
 // Rows and columns past the matrix read as zeros; rows that belong to another expert, where a
 // unit reaches past its own, give outputs that are dropped.
-template <bool kFc1>
+template <int kTiles, bool kFc1>
 __device__ __forceinline__ bool moe_fill(const MoeParams& p, const MoeShared& sh,
-                                         const MoeRing& ring, const WaitCtx& wc,
+                                         const MoeRing<kTiles>& ring, const WaitCtx& wc,
                                          const CUtensorMap* m, int group, MoePlace& at,
                                          uint32_t& armed, uint32_t& armed_phase) {
-  const MoeUnits<kFc1> d(p, sh);
+  const MoeUnits<kTiles, kFc1> d(p, sh);
+  const bool gated = kFc1 && p.gated;
   for (int u = d.first(group); u < d.count; u += d.step()) {
     const int a = u / d.per, r = (u - a * d.per) * d.rows;
     const int e = sh.active[a];
-    const int r0 = (kFc1 ? (p.gated ? 2 * e : e) * p.Fe : e * p.H) + r;
-    const int r1 = r0 + (kFc1 && p.gated ? p.Fe : 8);
+    const int r0 = (kFc1 ? (gated ? 2 * e : e) * p.Fe : e * p.H) + r;
+    const int r1 = r0 + (gated ? p.Fe : 8), tile = gated ? 8 : 16;
     for (int kc = 0; kc < d.kcs; ++kc) {
       if (!moe_wait(ring.empty + 8 * at.stage, at.phase ^ 1u, wc, kSiteMoeEmpty)) return false;
       const uint32_t bar = ring.full + 8 * at.stage;
       const uint32_t dst = ring.base + at.stage * ring.stage_bytes;
-      mbar_arrive_expect_tx(bar, kMoeStageW);
-      tma_load_2d(dst, m, bar, kc * kMoeKc, r0);
-      tma_load_2d(dst + kMoeBox, m, bar, kc * kMoeKc, r1);
+      mbar_arrive_expect_tx(bar, ring.kWeights);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        tma_load_2d(dst + 2 * t * kMoeBox, m, bar, kc * kMoeKc, r0 + t * tile);
+        tma_load_2d(dst + (2 * t + 1) * kMoeBox, m, bar, kc * kMoeKc, r1 + t * tile);
+      }
       armed |= 1u << at.stage;
       armed_phase = (armed_phase & ~(1u << at.stage)) | (at.phase << at.stage);
-      at.next(ring);
+      at.next(ring.stages);
     }
   }
   return true;
 }
 
+template <int kTiles>
 __device__ __forceinline__ void moe_copy_thread(const MoeParams& p, MoeShared& sh,
-                                                const MoeRing& ring, const WaitCtx& wc,
+                                                const MoeRing<kTiles>& ring, const WaitCtx& wc,
                                                 const CUtensorMap* m1, const CUtensorMap* m2,
                                                 int group) {
   MoePlace at;
   uint32_t armed = 0, armed_phase = 0;
-  if (moe_fill<true>(p, sh, ring, wc, m1, group, at, armed, armed_phase))
-    moe_fill<false>(p, sh, ring, wc, m2, group, at, armed, armed_phase);
+  if (moe_fill<kTiles, true>(p, sh, ring, wc, m1, group, at, armed, armed_phase))
+    moe_fill<kTiles, false>(p, sh, ring, wc, m2, group, at, armed, armed_phase);
   // every copy that was issued has landed (also after an expired wait)
   for (int s = 0; s < ring.stages; ++s)
     if (armed & (1u << s)) wait_drain(ring.full + 8 * s, (armed_phase >> s) & 1u, wc);
@@ -448,6 +470,12 @@ __device__ __forceinline__ void moe_copy16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void moe_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Of 16 bytes, or zeros (src is not read then).
+__device__ __forceinline__ void moe_copy16_or_0(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
 }
 // Waits for this thread's oldest group of copies when `ahead` (1 to 5) groups are in flight.
 __device__ __forceinline__ void moe_wait_oldest(int ahead) {
@@ -467,25 +495,21 @@ __device__ __forceinline__ void moe_wait_oldest(int ahead) {
 // moe_col() + 32 i.
 __device__ __forceinline__ int moe_col() { return moe_warp() * 64 + (threadIdx.x & 3) * 8; }
 
-// Offset in a stage of this lane's slot for the expert's token number t and step i.
-__device__ __forceinline__ uint32_t moe_slot(const MoeRing& ring, int i, int t) {
-  return kMoeStageW + ((moe_warp() * 2 + i) * ring.most + t) * 64 + (threadIdx.x & 3) * 16;
-}
-
 // A lane's copies of its tokens' fragments -- column lane / 4 of tile j is the expert's token
 // number j * 8 + lane / 4 -- one stage after the other, ahead of the products.
 template <int NT, bool kFc1>
 struct MoeTokens {
   const MoeParams& p;
   const MoeShared& sh;
-  const MoeRing& ring;
-  const MoeUnits<kFc1>& d;
+  const MoeRing<1>& ring;
+  const MoeUnits<1, kFc1>& d;
   int u, kc, stage, n;
   const __nv_bfloat16* src;
   int row[NT];  // offsets of the tokens' rows (elements)
 
   __device__ __forceinline__ MoeTokens(const MoeParams& p_, const MoeShared& sh_,
-                                       const MoeRing& ring_, const MoeUnits<kFc1>& d_, int stage_)
+                                       const MoeRing<1>& ring_, const MoeUnits<1, kFc1>& d_,
+                                       int stage_)
       : p(p_), sh(sh_), ring(ring_), d(d_), u(d_.first(moe_group())), kc(0), stage(stage_), n(0) {
     src = (kFc1 ? p.X : p.act) + moe_col();
     open();
@@ -509,7 +533,7 @@ struct MoeTokens {
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             if (j * 8 + g < n)
-              moe_copy16(ring.base + stage * ring.stage_bytes + moe_slot(ring, i, j * 8 + g),
+              moe_copy16(ring.base + stage * ring.stage_bytes + ring.slot(i, j * 8 + g),
                          src + row[j] + kc * kMoeKc + i * 32);
         }
       if (++stage == ring.stages) stage = 0;
@@ -523,14 +547,40 @@ struct MoeTokens {
   }
 };
 
+// Writes a thread's value of a tile (moe_reduce): 16 weight rows from feature or column r0 on,
+// the expert's tokens j * 8 to j * 8 + 7.
+template <bool kFc1>
+__device__ __forceinline__ void moe_result(const MoeParams& p, const MoeShared& sh, int e, int n,
+                                           int r0, int j, float v) {
+  const int up = moe_thread() & 1, f = (moe_thread() >> 1) & 7;
+  const int t = j * 8 + (moe_thread() >> 4);
+  const size_t s = sh.off[e] + t;
+  if constexpr (kFc1) {
+    int feat = r0 + f;
+    if (p.gated) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, 1);  // the gate's thread gets its up
+      v = v * sigmoid_f(v) * o;
+    } else {
+      float z;
+      f2_unpack(gelu_x2(f2_pack(v, v)), v, z);
+      feat += 8 * up;
+    }
+    if (t < n && feat < p.Fe && !(p.gated && up))
+      p.act[s * p.Fe + feat] = __float2bfloat16_rn(v);
+  } else {
+    const int r = r0 + f + 8 * up;
+    if (t < n && r < p.H) __stcg(p.pair_y + s * p.H + r, v);
+  }
+}
+
 // fc1 or fc2 with up to NT tiles of eight of an expert's tokens.  After a wait that expired
 // (`dead`), a lane waits no more and works on with what the stages hold: the launch is lost and
 // reported, but every barrier that the warps share still meets all of them.
 template <int NT, bool kFc1>
-__device__ void moe_multiply(const MoeParams& p, MoeShared& sh, const MoeRing& ring,
+__device__ void moe_multiply(const MoeParams& p, MoeShared& sh, const MoeRing<1>& ring,
                              const WaitCtx& wc, MoePlace& at, int& buf, bool& dead) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
-  const MoeUnits<kFc1> d(p, sh);
+  const MoeUnits<1, kFc1> d(p, sh);
   MoeTokens<NT, kFc1> tokens(p, sh, ring, d, at.stage);
 #pragma unroll 1
   for (int s = 0; s < ring.stages; ++s) tokens.issue();
@@ -560,7 +610,7 @@ __device__ void moe_multiply(const MoeParams& p, MoeShared& sh, const MoeRing& r
           for (int j = 0; j < NT; ++j) {
             x[i][j] = make_uint4(0, 0, 0, 0);  // past K's end, and past the expert's tokens
             if (j * 8 + g < n && (i0 + i) * 32 < left)
-              x[i][j] = *reinterpret_cast<const uint4*>(st + moe_slot(ring, i0 + i, j * 8 + g));
+              x[i][j] = *reinterpret_cast<const uint4*>(st + ring.slot(i0 + i, j * 8 + g));
           }
         }
         if (i0 + kHeld == 2) {  // every lane has read what it wants of the stage
@@ -576,56 +626,180 @@ __device__ void moe_multiply(const MoeParams& p, MoeShared& sh, const MoeRing& r
               moe_mma(c[j], l[i].z, h[i].z, l[i].w, h[i].w, x[i][j].z, x[i][j].w);
             }
       }
-      at.next(ring);
+      at.next(ring.stages);
       tokens.issue();  // into the slots just read
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j * 8 >= n) break;
-      float v = moe_reduce(sh, buf, c[j]);
+      const float v = moe_reduce(sh, buf, c[j]);
       buf ^= 1;
-      const int up = moe_thread() & 1, f = (moe_thread() >> 1) & 7;
-      const int t = j * 8 + (moe_thread() >> 4);
-      const size_t s = sh.off[e] + t;
-      if constexpr (kFc1) {
-        int feat = r0 + f;
-        if (p.gated) {
-          const float o = __shfl_xor_sync(0xffffffffu, v, 1);  // the gate's thread gets its up
-          v = v * sigmoid_f(v) * o;
-        } else {
-          float z;
-          f2_unpack(gelu_x2(f2_pack(v, v)), v, z);
-          feat += 8 * up;
-        }
-        if (t < n && feat < p.Fe && !(p.gated && up))
-          p.act[s * p.Fe + feat] = __float2bfloat16_rn(v);
-      } else {
-        const int r = r0 + f + 8 * up;
-        if (t < n && r < p.H) __stcg(p.pair_y + s * p.H + r, v);
-      }
+      moe_result<kFc1>(p, sh, e, n, r0, j, v);
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// The same for experts with many tokens, by the whole CTA: a unit is four tiles of 16 rows, one
+// for each group, and a stage's tokens are there once for all of them.  Of the tokens' tiles of
+// eight, group g copies j = g and g + 4, each warp its 64 of K; an asynchronous arrival of every
+// thread on the stage's barrier says that they are there.  A stage is filled again one stage
+// late, when the slower warps have left it too.
 template <bool kFc1>
-__device__ __forceinline__ void moe_phase(const MoeParams& p, MoeShared& sh, const MoeRing& ring,
-                                          const WaitCtx& wc, MoePlace& at, int& buf, bool& dead,
-                                          uint32_t barrier) {
-  if (sh.most <= 8)
-    moe_multiply<1, kFc1>(p, sh, ring, wc, at, buf, dead);
-  else if (sh.most <= 16)
-    moe_multiply<2, kFc1>(p, sh, ring, wc, at, buf, dead);
-  else if (sh.most <= 32)
-    moe_multiply<4, kFc1>(p, sh, ring, wc, at, buf, dead);
-  else
-    moe_multiply<8, kFc1>(p, sh, ring, wc, at, buf, dead);
-  moe_sync();  // the CTA's results are written
+__device__ void moe_multiply_cta(const MoeParams& p, MoeShared& sh, const MoeRing<4>& ring,
+                                 const WaitCtx& wc, MoePlace& at, MoePlace& to, int& buf,
+                                 bool& dead) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  const MoeUnits<4, kFc1> d(p, sh);
+  const __nv_bfloat16* src = (kFc1 ? p.X : p.act) + moe_col();
+  const uint32_t slot = ring.slot(0, g), step = ring.most * 64;
+  const uint32_t weights = moe_group() * kMoeStageW + g * (kMoeKc * 2) + moe_col() * 2;
+  int cu = d.first(0), ckc = 0, there = 0;  // of the copies: unit, stage in it, tiles (bits)
+  const __nv_bfloat16* row[2];
+  auto open = [&]() {
+    if (cu >= d.count) return;
+    const int e = sh.active[cu / d.per], off = sh.off[e], n = __popcll(sh.mask[e]);
+    there = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int t = (moe_group() + 4 * q) * 8 + g, s = off + min(t, n - 1);
+      if (t < n) there |= 1 << q;
+      row[q] = src + static_cast<size_t>(kFc1 ? sh.tok[s] : s) * d.len;
+    }
+  };
+  auto issue = [&]() {
+    if (cu >= d.count) return;
+    if (!dead) dead = !moe_wait(ring.empty + 8 * to.stage, to.phase ^ 1u, wc, kSiteMoeEmpty);
+    const uint32_t dst = ring.base + to.stage * ring.stage_bytes + slot + moe_group() * 512;
+    const int left = d.len - ckc * kMoeKc - moe_col();
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (there >> q & 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)  // zeros past K's end
+          moe_copy16_or_0(dst + i * step + q * 2048, left > i * 32 ? row[q] + i * 32 : src,
+                          left > i * 32);
+        row[q] += kMoeKc;
+      }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ring.full + 8 * to.stage)
+                 : "memory");
+    to.next(ring.stages);
+    if (++ckc == d.kcs) {
+      ckc = 0;
+      cu += d.step();
+      open();
+    }
+  };
+  open();
+#pragma unroll 1
+  for (int s = 0; s < ring.stages - 1; ++s) issue();
+#pragma unroll 1
+  for (int u = d.first(0); u < d.count; u += d.step()) {
+    const int a = u / d.per, e = sh.active[a];
+    const int r0 = (u - a * d.per) * d.rows + moe_group() * (d.rows / 4);
+    const int n = __popcll(sh.mask[e]);
+    // by the number of token tiles, without a branch in a stage
+    auto unit = [&](auto tiles) {
+      constexpr int NT = decltype(tiles)::value;
+      float c[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+#pragma unroll 1
+      for (int kc = 0; kc < d.kcs; ++kc) {
+        if (!dead) dead = !moe_wait(ring.full + 8 * at.stage, at.phase, wc, kSiteMoeFull);
+        const uint8_t* st = ring.ptr + at.stage * ring.stage_bytes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 l = *reinterpret_cast<const uint4*>(st + weights + i * 64);
+          const uint4 h = *reinterpret_cast<const uint4*>(st + weights + i * 64 + kMoeBox);
+          uint4 x[NT];  // (slots of tokens that the expert does not have: columns that are dropped)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            x[j] = *reinterpret_cast<const uint4*>(st + slot + i * step + j * 512);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) moe_mma(c[j], l.x, h.x, l.y, h.y, x[j].x, x[j].y);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) moe_mma(c[j], l.z, h.z, l.w, h.w, x[j].z, x[j].w);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty + 8 * at.stage);
+        at.next(ring.stages);
+        issue();
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float v = moe_reduce(sh, buf, c[j]);
+        buf ^= 1;
+        moe_result<kFc1>(p, sh, e, n, r0, j, v);
+      }
+    };
+    switch ((n + 7) >> 3) {
+      case 1: unit(std::integral_constant<int, 1>()); break;
+      case 2: unit(std::integral_constant<int, 2>()); break;
+      case 3: unit(std::integral_constant<int, 3>()); break;
+      case 4: unit(std::integral_constant<int, 4>()); break;
+      case 5: unit(std::integral_constant<int, 5>()); break;
+      case 6: unit(std::integral_constant<int, 6>()); break;
+      default: unit(std::integral_constant<int, 8>()); break;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// After a phase: the CTA's results are written, and those of all CTAs.
+__device__ __forceinline__ void moe_phase_end(const MoeParams& p, MoeShared& sh, uint32_t barrier) {
+  moe_sync();
   if (threadIdx.x == 0) {
     moe_grid_arrive(p);
     moe_grid_wait(p, sh, barrier);
   }
   moe_sync();
+}
+
+// fc1 and fc2, by all threads of a CTA.
+template <int kTiles>
+__device__ __forceinline__ void moe_experts(const MoeParams& p, MoeShared& sh, uint8_t* smem,
+                                            const CUtensorMap* m1, const CUtensorMap* m2) {
+  constexpr int kRings = kMoeGroups / kTiles;
+  const bool multiplies = threadIdx.x < kMoeThreads;
+  const int group = multiplies ? moe_group() : (threadIdx.x - kMoeThreads) >> 5;
+  const MoeRing<kTiles> ring(smem, sh, kTiles == 1 ? group : 0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRings; ++i)
+      for (int s = 0; s < ring.stages; ++s) {
+        // filled by the copying thread, and with kTiles 4 by every multiplying one
+        mbar_init(smem_u32(&sh.full[i][s]), kTiles == 1 ? 1 : 1 + kMoeThreads);
+        mbar_init(smem_u32(&sh.empty[i][s]), kMoeWarps / kRings);
+      }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  const WaitCtx wc{&sh.abort, &p.sync->err, p.wait_ns};
+  if (!multiplies) {
+    if ((threadIdx.x & 31) == 0 && group < kRings)
+      moe_copy_thread<kTiles>(p, sh, ring, wc, m1, m2, group);
+    return;
+  }
+  MoePlace at;
+  int buf = 0;
+  bool dead = false;
+  if constexpr (kTiles == 1) {
+    auto phase = [&](auto fc1) {
+      if (sh.most <= 8)
+        moe_multiply<1, fc1.value>(p, sh, ring, wc, at, buf, dead);
+      else
+        moe_multiply<2, fc1.value>(p, sh, ring, wc, at, buf, dead);
+    };
+    phase(std::true_type());
+    moe_phase_end(p, sh, 2);
+    phase(std::false_type());
+  } else {
+    MoePlace to;
+    moe_multiply_cta<true>(p, sh, ring, wc, at, to, buf, dead);
+    moe_phase_end(p, sh, 2);
+    moe_multiply_cta<false>(p, sh, ring, wc, at, to, buf, dead);
+  }
+  moe_phase_end(p, sh, 3);
 }
 
 // Y_t = sum over t's pairs, in the order of its choices, of w y.
@@ -673,28 +847,11 @@ __global__ void __launch_bounds__(kMoeBlock, 1)
   if (sh.abort == 0u) {
     if (multiplies) moe_route(p, sh);
     __syncthreads();
-    const int group = multiplies ? moe_group() : (threadIdx.x - kMoeThreads) >> 5;
-    const MoeRing ring(moe_smem, sh, group);
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < kMoeGroups; ++i)
-        for (int s = 0; s < ring.stages; ++s) {
-          mbar_init(smem_u32(&sh.full[i][s]), 1);
-          mbar_init(smem_u32(&sh.empty[i][s]), 4);
-        }
-      mbar_fence_init();
-    }
-    __syncthreads();
-    const WaitCtx wc{&sh.abort, &p.sync->err, p.wait_ns};
-    if (multiplies) {
-      MoePlace at;
-      int buf = 0;
-      bool dead = false;
-      moe_phase<true>(p, sh, ring, wc, at, buf, dead, 2);
-      moe_phase<false>(p, sh, ring, wc, at, buf, dead, 3);
-      moe_combine(p, sh);
-    } else if ((threadIdx.x & 31) == 0) {
-      moe_copy_thread(p, sh, ring, wc, &map_w1, &map_w2, group);
-    }
+    if (sh.most < kMoeSharedFrom)
+      moe_experts<1>(p, sh, moe_smem, &map_w1, &map_w2);
+    else
+      moe_experts<4>(p, sh, moe_smem, &map_w1, &map_w2);
+    if (multiplies) moe_combine(p, sh);
   }
   // the last CTA out leaves the barriers' word as it found it, after an expired wait too
   __syncthreads();

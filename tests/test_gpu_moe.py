@@ -177,6 +177,24 @@ def test_same_bits_stream_and_two_graphs():
         assert mlpb.mlpb_moe_last_device_error(p2.handle) == 0
 
 
+@pytest.mark.parametrize("T,F", [(17, 40), (24, 264), (33, 72), (41, 256), (55, 520), (64, 1032)])
+def test_tokens_of_an_expert(T, F):
+    """Every number of token tiles for one expert next to experts with few or none: a router that
+    sends all tokens to expert 1, and their second choice where it falls; several units a CTA."""
+    for H, act in ((264, "gelu"), (4104, "swiglu")):
+        d = list(_make(T, H, F, 9, act))
+        d[0][:, 0] = 8.0
+        d[1][1, 0] = 2.0
+        plan = mlpb.MoEDecode(64, H, F, 9, 2, act)
+        g = [t.cuda() for t in d]
+        out = plan.forward(*g)
+        assert (out[1][:, 0] == 1).sum() >= T - 1
+        _check(d, 2, act, True, out)
+        again = plan.forward(*g)
+        assert all(torch.equal(a, b) for a, b in zip(out, again))
+        assert mlpb.mlpb_moe_last_device_error(plan.handle) == 0
+
+
 def test_offsets_past_32_bits():
     """Weights of more than 2^32 elements: the last experts are those of a small layer with the
     same rows (the first ones, of zeros, have logits of zero and are not taken)."""
