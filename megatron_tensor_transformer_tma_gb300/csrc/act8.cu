@@ -14,8 +14,7 @@
 //
 // Measured, with the rate of the bytes above (a copy reaches 6.8 TB/s): GELU T8192 F20480 save
 // 124 us, 6.8 TB/s, grad 181 us, 6.5 TB/s; SwiGLU T16384 F11008 save 214 us, 6.8 TB/s, grad
-// 301 us, 6.0 TB/s (its mix has the most streams, three in and three out, and 80 registers a
-// thread: instructions issue in 55 % of its cycles, stalled on loads otherwise).
+// 277 us, 6.5 TB/s.
 #include <algorithm>
 
 #include "../../include/mlpb.h"
@@ -27,10 +26,12 @@ namespace mlpb {
 
 constexpr int kAct8Threads = 256;
 
-// Rows a thread has in flight: 4 of 8 features, 2 of 16.
-template <int V>
-constexpr int act8_rows() {
-  return 4 / V;
+// Rows a thread has in flight (v times 8 features).  Saving: 4 of 8 features or 2 of 16 (one:
+// GELU T8192 F20480 124 -> 132 us).  The gradient, which has more streams and registers: 2, or 1
+// where gated (SwiGLU T16384 F11008, 16 features: 1 row 277 us, 2 301, 4 347; F11016, 8 features:
+// 306, 326, 363).
+constexpr int act8_rows(int v, bool grad, bool gated) {
+  return grad ? (gated ? 1 : 2) : 4 / v;
 }
 
 // Where a thread works: its 8 V features start at column f of A's row, and its vectors of Z
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kAct8Threads) act8_save_kernel(
     const __nv_bfloat16* __restrict__ Z, __nv_bfloat16* __restrict__ A,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t T, int64_t F, int64_t F1,
     int64_t nb, int width, int blocks, int units, int ux_log2, int col_ctas) {
-  constexpr int kRows = act8_rows<V>();
+  constexpr int kRows = act8_rows(V, false, kGated);
   const int ux = 1 << ux_log2;
   const int rows_cta = (kAct8Threads >> ux_log2) * kRows;
   const int64_t rb = blockIdx.x / col_ctas;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kAct8Threads) act8_grad_kernel(
     const uint8_t* __restrict__ scales, __nv_bfloat16* __restrict__ dZ,
     __nv_bfloat16* __restrict__ A, int64_t T, int64_t F, int64_t F1, int64_t nb, int width,
     int blocks, int units, int ux_log2, int col_ctas) {
-  constexpr int kRows = act8_rows<V>();
+  constexpr int kRows = act8_rows(V, true, kGated);
   const int ux = 1 << ux_log2;
   const int rows_cta = (kAct8Threads >> ux_log2) * kRows;
   const int64_t rb = blockIdx.x / col_ctas;
@@ -307,7 +308,7 @@ struct Act8Dims {
 
 // `bits`: the pointers of the tensors that are read and written 32 bytes at a time, or'ed.
 static mlpb_status act8_dims(int32_t act, int64_t T, int64_t F, int32_t tp, uintptr_t bits,
-                             Act8Dims* d) {
+                             bool grad, Act8Dims* d) {
   if (act != MLPB_ACT_GELU_TANH && act != MLPB_ACT_SWIGLU) return MLPB_EINVAL;
   if (T < 0 || F <= 0 || tp < 1) return MLPB_EINVAL;
   if (F % tp != 0 || (F / tp) % 8 != 0) return MLPB_EUNSUPPORTED;
@@ -328,7 +329,7 @@ static mlpb_status act8_dims(int32_t act, int64_t T, int64_t F, int32_t tp, uint
   while ((1 << d->ux_log2) < d->units && (1 << d->ux_log2) < kAct8Threads) ++d->ux_log2;
   d->col_ctas = static_cast<int>((d->units + (1 << d->ux_log2) - 1) >> d->ux_log2);
   const int64_t rows_cta = static_cast<int64_t>(kAct8Threads >> d->ux_log2) *
-                           (d->wide ? act8_rows<2>() : act8_rows<1>());
+                           act8_rows(d->wide ? 2 : 1, grad, d->gated);
   const int64_t grid = (T + rows_cta - 1) / rows_cta * d->col_ctas;
   if (grid > 0x7fffffffll) return MLPB_EUNSUPPORTED;
   d->grid = static_cast<unsigned>(grid);
@@ -342,7 +343,7 @@ using namespace mlpb;
 extern "C" mlpb_status mlpb_act8_scales(int32_t act, int64_t ffn, int32_t tp, int64_t* per_row) {
   Act8Dims d;
   if (per_row == nullptr) return MLPB_EINVAL;
-  const mlpb_status st = act8_dims(act, 0, ffn, tp, 0, &d);
+  const mlpb_status st = act8_dims(act, 0, ffn, tp, 0, false, &d);
   if (st == MLPB_OK) *per_row = d.nb;
   return st;
 }
@@ -352,7 +353,8 @@ extern "C" mlpb_status mlpb_act8_save(int32_t act, int64_t tokens, int64_t ffn, 
                                       mlpb_stream_t stream) {
   Act8Dims d;
   const mlpb_status st = act8_dims(
-      act, tokens, ffn, tp, reinterpret_cast<uintptr_t>(Z) | reinterpret_cast<uintptr_t>(A), &d);
+      act, tokens, ffn, tp, reinterpret_cast<uintptr_t>(Z) | reinterpret_cast<uintptr_t>(A),
+      false, &d);
   if (st != MLPB_OK) return st;
   if (tokens > 0 && (!Z || !codes || !scales)) return MLPB_EINVAL;
   for (const void* p : {Z, static_cast<const void*>(A), static_cast<const void*>(codes)})
@@ -378,7 +380,7 @@ extern "C" mlpb_status mlpb_act8_grad(int32_t act, int64_t tokens, int64_t ffn, 
                                    reinterpret_cast<uintptr_t>(dA) |
                                        reinterpret_cast<uintptr_t>(dZ) |
                                        reinterpret_cast<uintptr_t>(A),
-                                   &d);
+                                   true, &d);
   if (st != MLPB_OK) return st;
   if (tokens > 0 && (!dA || !codes || !scales || !dZ)) return MLPB_EINVAL;
   for (const void* p : {dA, codes, static_cast<const void*>(dZ), static_cast<const void*>(A)})
