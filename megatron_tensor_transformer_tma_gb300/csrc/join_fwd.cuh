@@ -118,7 +118,11 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
   };
   for (int b = 0; b < p.nbuf; ++b) issue(b, row0 + b * step);
 
-  uint4 gpre[kVpt];
+  // With LayerNorm, gamma_pre too is read again for every row where the registers would spill:
+  // T8192 H8192 bf16 107 -> 95 us, H4096 59 -> 49, T11061 H2184 80 -> 73.  Where they hardly do,
+  // it costs: T16384 H5120 fp32 191 -> 196 us, T4373 H5400 49 -> 53.
+  constexpr bool kReread = kBeta && (kPlain ? kWpr != 5 : kWpr <= 4);
+  uint4 gpre[kReread ? 1 : kVpt];
   JoinVec gw[kBeta ? 1 : kVpt];                            // gate gamma_post
   uint4 gpost[kBeta ? kVpt : 1], gate[kBeta ? kVpt : 1];  // or each of them
   // the factors of the gate row `g` (every row's where p.G <= 1)
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
 #pragma unroll
   for (int k = 0; k < kVpt; ++k) {
     if constexpr (kBeta) gpost[k] = join_param(p.gamma_post, k, jc);
-    gpre[k] = join_param(p.gamma_pre, k, jc);
+    if constexpr (!kReread) gpre[k] = join_param(p.gamma_pre, k, jc);
   }
   factors(p.gate);
 
@@ -199,7 +203,10 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
 #pragma unroll
       for (int k = 0; k < kVpt; ++k) {
         JoinVec t;
-        join_unpack(gpre[k], t);
+        if constexpr (kReread)
+          join_unpack(join_param(p.gamma_pre, k, jc), t);
+        else
+          join_unpack(gpre[k], t);
         join_affine<kBeta>(v[k], mu_h, rs_h, t, p.beta_pre, k, jc);
         join_store<bf, false>(p.Xn + row * p.H, k, jc, v[k]);
       }
