@@ -24,11 +24,13 @@
 //
 // Measured (bandwidth over the bytes that a call cannot do without; the copy that the card
 // reaches is 6.8 TB/s): forward T 8192 H 8192 bf16, RMSNorms and a gate, 92 us, 5.8 TB/s;
-// backward 156 us, 5.2 TB/s, of which 143 the first pass; backward T 16384 H 4096 fp32,
+// backward 155 us, 5.2 TB/s, of which 143 the first pass; backward T 16384 H 4096 fp32,
 // LayerNorms, 265 us, 6.6 TB/s.  What keeps the bf16 backward from the last fifth is the chain
 // of a row (its reduction among it) with one row an SM in registers.  Ragged widths: RMS
-// T 3000 H 7000 30 us forward (83 %), 62 backward (60 %); LayerNorms T 11061 H 2184 81 and 98
-// (35 and 44 %), bound by instructions and the chain of their four reductions.
+// T 3000 H 7000 30 us forward (83 %), 62 backward (60 %); LayerNorms T 11061 H 2184 73 and 99
+// (39 and 43 %), bound by instructions and the chain of their four reductions.  A gate for each
+// token restarts a CTA's copies with every row: backward T 8192 H 8192 278 us (letting them run
+// on from group to group gained nothing there and cost the others 1-2 %).
 #pragma once
 
 #include <algorithm>
@@ -54,6 +56,7 @@ struct JoinParams {
   // the general backward's
   int wpr, rows;   // warps of a row, rows of a CTA
   int ring_bytes;  // of the ring
+  bool split;      // its rows walk groups of their own
   bool ragged;     // some of the threads' columns are past the row's end
   // forward (inputs of both)
   const void *X, *Y;

@@ -19,7 +19,8 @@
 // registers without LayerNorm's two plain sums, 64 with them), and each CTA leaves one row of
 // partial sums for a second launch to add up in a fixed order: no atomics, the same bits every
 // run.  So a CTA's rows are of one group: a group has blocks_per_group CTAs, or, with more
-// groups than CTAs, a CTA walks whole groups and adds each into its own partial row.
+// groups than CTAs, a CTA walks whole groups and adds each into its own partial row.  (Or each
+// row of a CTA does, where groups are short: p.split.)
 #pragma once
 
 #include "../../include/mlpb.h"
@@ -240,8 +241,13 @@ __global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
 
   const int bpg = p.blocks_per_group;
   const int groups = p.G > 0 ? p.G : 1;
-  const int walker = blockIdx.x / kCl;        // this CTA, or cluster
-  const int walkers = gridDim.x / kCl / bpg;  // of a turn: groups that a walker steps over
+  // A group is walked by bpg CTAs (or clusters), whose `at_once` rows are all the group's; or,
+  // with p.split, a walker is one row of a CTA.
+  constexpr bool kSeveral = !kPlain && kCl == 1 && (kWpr == -12 || kVpt == 1);  // rows of a CTA
+  const bool split = kSeveral && p.split;
+  const int at_once = split ? 1 : rows, place = split ? 0 : sub;
+  const int walker = split ? blockIdx.x * rows + sub : blockIdx.x / kCl;
+  const int walkers = (split ? gridDim.x * rows : gridDim.x / kCl) / bpg;  // groups of a turn
   int par = 0;
   bool first = true;
   if constexpr (kCl > 1) cluster_sync();  // the other CTA's shared memory is there
@@ -249,8 +255,8 @@ __global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
   for (int g = walker / bpg; g < groups; g += walkers) {
     // (below 2^31, and what is added beyond the end below 2^14)
     const uint32_t r_end = (g + 1u) * static_cast<uint32_t>(p.rows_per_group);
-    const uint32_t row0 = r_end - static_cast<uint32_t>(p.rows_per_group) + (walker % bpg) * rows + sub;
-    const uint32_t step = bpg * rows;
+    const uint32_t row0 = r_end - static_cast<uint32_t>(p.rows_per_group) + (walker % bpg) * at_once + place;
+    const uint32_t step = bpg * at_once;
     const bf* gate = p.gate != nullptr ? p.gate + static_cast<int64_t>(g) * p.H : nullptr;
 
     auto issue = [&](int b, uint32_t row) {
@@ -446,9 +452,9 @@ __global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
 
     // The end of this CTA's rows of the group: S1 and S0 over the CTA, and what they give.
     if (need_y) {
-      join_combine(s1, rows, comb);
-      if (kBeta) join_combine(s0, rows, comb);
-      if (sub == 0) {
+      join_combine(s1, at_once, comb);
+      if (kBeta) join_combine(s0, at_once, comb);
+      if (place == 0) {
         const int64_t slot = static_cast<int64_t>(walker) * p.H;
 #pragma unroll
         for (int k = 0; k < kVpt; ++k) {
@@ -499,9 +505,9 @@ __global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
   }
 
   if (has_pre) {
-    join_combine(a1, rows, comb);
-    if (kBeta) join_combine(a0, rows, comb);
-    if (sub == 0) {
+    join_combine(a1, at_once, comb);
+    if (kBeta) join_combine(a0, at_once, comb);
+    if (place == 0) {
       const int64_t slot = static_cast<int64_t>(walker) * p.H;
 #pragma unroll
       for (int k = 0; k < kVpt; ++k) {
@@ -535,7 +541,7 @@ static cudaError_t join_bwd_launch(JoinParams p, const JoinShape& sh, int grid, 
   const size_t late = (p.dXout != nullptr ? xs : 0) + (p.part_alpha != nullptr ? xs : 0);
   constexpr size_t kFactors = JoinFactors<kVpt, join_bwd_smem<kWpr, kBeta>()>::kBytes;
   // (the general ones' rows meet in memory of their own)
-  const size_t comb = sh.rows > 1 ? static_cast<size_t>(sh.threads) * kVpt * 32 : 0;
+  const size_t comb = sh.rows > 1 && !p.split ? static_cast<size_t>(sh.threads) * kVpt * 32 : 0;
   const size_t room = (208u << 10) / join_ctas(kWpr) - kFactors * sh.threads -
                       (kWpr < 0 ? comb : 0);
   const size_t stage = early + late;  // 160 KB an SM at most: one fits

@@ -188,6 +188,16 @@ def test_widths(H):
         _run(T, H, "none", "layer", T, True, *types)
 
 
+@pytest.mark.parametrize("T,H,G", [(5000, 264, 5000), (3000, 512, 1500), (2100, 1024, 2100),
+                                   (2000, 2048, 1000), (700, 4392, 700), (333, 9000, 333),
+                                   (1900, 72, 950), (40, 520, 40)])
+def test_many_short_groups(T, H, G):
+    """A gate for each token or pair: rows of a CTA in groups of their own, copies that run on from
+    a group to the next, walkers without a group."""
+    _run(T, H, "layer", "rms", G, True, BF, BF)
+    _run(T, H, "rms", "rms", G, False, F32, F32)
+
+
 def test_rows_of_two_ctas():
     """Above 8192 columns: in place, accumulated, captured, groups more and fewer than walkers."""
     for G in (2, 380):
