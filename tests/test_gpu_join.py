@@ -9,6 +9,8 @@ factors (the sum g xh, xh, rs): 200 u of the magnitudes of the terms; dY chains 
 bf16 outputs add half a step of their value, 2^-8 at most.  Xn and its statistics are compared
 with the norm of the stream that the GPU stored, which is how they are defined.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -363,6 +365,32 @@ def test_other_stream_and_two_graphs():
     for _, grads, *_ in graphs:
         for k, v in grads.items():
             assert torch.equal(v, got[k]), k
+
+
+def test_host_threads():
+    """Threads with plans of different sizes for the same kernels."""
+    wrong = []
+
+    def work(T, G, res):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            d = _make(T, 4096, "rms", "rms", G, res, BF, BF)
+            plan = mlpb.Join(T, 4096, "rms", "rms", G, EPS)
+            par = {k: d[k] for k in ("res_scale", "gate", "gamma_post", "gamma_pre")}
+            first = None
+            for i in range(60):
+                o = plan.forward(d["X"], d["Y"], **par)
+                g = plan.backward(d["X"], d["Y"], o[0], o[2], d["dXout"], d["dXn"], **par)
+                out = [o[0], o[1], g["dX"], g["dY"], g["dgamma_pre"]]
+                first = first or [t.clone() for t in out]
+                if not all(torch.equal(a, b) for a, b in zip(first, out)):
+                    wrong.append((T, i))
+    threads = [threading.Thread(target=work, args=a)
+               for a in ((4, 0, False), (1500, 1, True), (700, 0, False))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_offsets_past_32_bits():

@@ -195,6 +195,34 @@ def test_tokens_of_an_expert(T, F):
         assert mlpb.mlpb_moe_last_device_error(plan.handle) == 0
 
 
+def test_two_handles_at_once_and_forms_in_turn():
+    """Handles on two streams at the same time; one handle with calls of a few and of many tokens
+    an expert after each other; a call after another one left NaN in shared memory."""
+    d = [t.cuda() for t in _make(64, 1024, 520, 6, "swiglu")]
+    xs, hs = (d[0], d[0][:1].contiguous()), [mlpb.MoEDecode(64, 1024, 520, 6, 2) for _ in range(2)]
+    want = [[t.clone() for t in h.forward(x, *d[1:])] for h, x in zip(hs, xs)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in hs], [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(hs[i].forward(xs[i], *d[1:]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for o in outs[i] for a, b in zip(o, want[i]))
+    for T in (1, 64, 5, 40, 17, 2, 33):
+        x = d[0][:T].contiguous()
+        fresh = mlpb.MoEDecode(64, 1024, 520, 6, 2).forward(x, *d[1:])
+        assert all(torch.equal(a, b) for a, b in zip(hs[0].forward(x, *d[1:]), fresh))
+    odd = [t.cuda() for t in _make(64, 1000, 264, 4, "swiglu")]
+    plan = mlpb.MoEDecode(64, 1000, 264, 4, 2)
+    a = [t.clone() for t in plan.forward(*odd)]
+    hs[1].forward(torch.full_like(d[0], float("nan")), *d[1:])
+    assert all(torch.equal(u, v) for u, v in zip(a, plan.forward(*odd)))
+    for h in (*hs, plan):
+        assert mlpb.mlpb_moe_last_device_error(h.handle) == 0
+
+
 def test_offsets_past_32_bits():
     """Weights of more than 2^32 elements: the last experts are those of a small layer with the
     same rows (the first ones, of zeros, have logits of zero and are not taken)."""
