@@ -509,7 +509,7 @@ def mlpb_join_bwd(cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post
     bf, f32 = torch.bfloat16, torch.float32
     xt, yt = _join_types(cfg)
     row, vec, gates = (T, H), (H,), (cfg.gate_groups, H)
-    if workspace is not None and workspace.numel() * workspace.element_size() < _join_ws(cfg, dev):
+    if workspace is not None and workspace.nbytes < _join_ws_of(bytes(cfg), dev):
         raise ValueError("workspace: smaller than mlpb_join_workspace_size()")
     args = [ctypes.byref(cfg), _arg(X, xt, row, "X", dev), _arg(Y, yt, row, "Y", dev),
             _arg(Xout, xt, row, "Xout", dev), _arg(stats, f32, (T, 4), "stats", dev),
@@ -530,10 +530,15 @@ def mlpb_join_bwd(cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post
 
 
 def _join_ws(cfg, dev):
-    if dev == torch.cuda.current_device():
-        return mlpb_join_workspace_size(cfg)
+    dev = torch.device(dev)
+    return _join_ws_of(bytes(cfg), torch.cuda.current_device() if dev.index is None else dev.index)
+
+
+@functools.lru_cache(maxsize=1024)
+def _join_ws_of(cfg, dev):
+    """A function of the configuration's bytes and the device's number of SMs alone."""
     with torch.cuda.device(dev):
-        return mlpb_join_workspace_size(cfg)
+        return mlpb_join_workspace_size(mlpb_join_config.from_buffer_copy(cfg))
 
 
 @dataclasses.dataclass
@@ -812,7 +817,8 @@ class Join:
                  gamma_post=None, beta_post=None, gamma_pre=None, beta_pre=None, grads=None,
                  stream=None):
         """The gradients for dXout (None: zero) and dXn of forward()'s outputs; X and Y may be
-        None where the backward does not read them (include/mlpb.h)."""
+        None where the backward does not read them (include/mlpb.h).  `grads`: an alloc_grads()
+        to write into again (half of a small call's host time is its allocations)."""
         g = grads
         if g is None:
             with _on(stream):
