@@ -253,72 +253,6 @@ __device__ __forceinline__ void join_read(const uint8_t* src, int k,
   }
 }
 
-// A vector as it was copied: unpacked pair by pair, where the arithmetic wants it, it takes half
-// the registers.
-template <class E>
-struct JoinRaw {
-  static constexpr int kWords = 2 * static_cast<int>(sizeof(E));
-  uint32_t w[kWords];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ uint64_t pair(int i) const {
-    if constexpr (sizeof(E) == 4)
-      return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-    else
-      return join_pair(w[i]);
-  }
-  __device__ __forceinline__ void set(int i, uint64_t v) {  // rounds to E
-    float a, b;
-    f2_unpack(v, a, b);
-    if constexpr (sizeof(E) == 4) {
-      w[2 * i] = __float_as_uint(a);
-      w[2 * i + 1] = __float_as_uint(b);
-    } else {
-      w[i] = pack_bf16x2(a, b);
-    }
-  }
-  // vector k from the thread's slots
-  template <bool kSplit>
-  __device__ __forceinline__ void read(const uint8_t* src, int k) {
-    const uint32_t lane = threadIdx.x & 31;
-    if constexpr (!kSplit) {
-      const uint4 u = *reinterpret_cast<const uint4*>(src + (k * 32 + lane) * 16);
-      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* q = src + ((2 * k + h) * 32 + lane) * (4 * sizeof(E));
-        if constexpr (sizeof(E) == 4) {
-          const uint4 u = *reinterpret_cast<const uint4*>(q);
-          w[4 * h] = u.x, w[4 * h + 1] = u.y, w[4 * h + 2] = u.z, w[4 * h + 3] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(q);
-          w[2 * h] = u.x, w[2 * h + 1] = u.y;
-        }
-      }
-    }
-  }
-  // vector k into a row
-  template <bool kSplit, int kVpt, bool kFull>
-  __device__ __forceinline__ void store(E* row, int k, const JoinCols<kSplit, kVpt, kFull>& jc) const {
-    if constexpr (!kSplit) {
-      if (jc.ok(2 * k)) st_global_v4(row + jc.c[2 * k], make_uint4(w[0], w[1], w[2], w[3]));
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!jc.ok(2 * k + h)) continue;
-        if constexpr (sizeof(E) == 4)
-          *reinterpret_cast<uint4*>(row + jc.c[2 * k + h]) =
-              make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-        else
-          *reinterpret_cast<uint2*>(row + jc.c[2 * k + h]) = make_uint2(w[2 * h], w[2 * h + 1]);
-      }
-    }
-  }
-};
-
 // Vector k of a parameter, packed (zeros past its end, and where there is none).
 template <bool kSplit, int kVpt, bool kFull>
 __device__ __forceinline__ uint4 join_param(const __nv_bfloat16* p, int k,

@@ -136,7 +136,8 @@ struct JoinFactors {
   JoinVec w[kSmem ? 1 : kVpt];
   uint4* own;
   static constexpr size_t kBytes = kSmem ? 48 * kVpt : 0;  // of a thread
-  __device__ __forceinline__ JoinFactors(void* smem) : own(static_cast<uint4*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ JoinFactors(void* smem)
+      : own(static_cast<uint4*>(smem) + threadIdx.x) {}
   __device__ __forceinline__ void set_pre(int k, const uint4& v) {
     if constexpr (kSmem)
       own[3 * k * blockDim.x] = v;
@@ -162,7 +163,8 @@ struct JoinFactors {
     if constexpr (kSmem) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(own + (3 * k + 1 + h) * blockDim.x);
+        const ulonglong2 t =
+            *reinterpret_cast<const ulonglong2*>(own + (3 * k + 1 + h) * blockDim.x);
         v[2 * h] = t.x;
         v[2 * h + 1] = t.y;
       }
@@ -255,7 +257,8 @@ __global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
   for (int g = walker / bpg; g < groups; g += walkers) {
     // (below 2^31, and what is added beyond the end below 2^14)
     const uint32_t r_end = (g + 1u) * static_cast<uint32_t>(p.rows_per_group);
-    const uint32_t row0 = r_end - static_cast<uint32_t>(p.rows_per_group) + (walker % bpg) * at_once + place;
+    const uint32_t row0 = r_end - static_cast<uint32_t>(p.rows_per_group) +
+                          (walker % bpg) * at_once + place;
     const uint32_t step = bpg * at_once;
     const bf* gate = p.gate != nullptr ? p.gate + static_cast<int64_t>(g) * p.H : nullptr;
 
@@ -299,12 +302,12 @@ __global__ void __launch_bounds__(join_threads(kWpr), join_ctas(kWpr))
 
     int b = 0;
     float4 next = make_float4(0.f, 0.f, 0.f, 0.f);  // the next row's statistics, a row ahead
-    if (row0 < r_end) next = __ldg(reinterpret_cast<const float4*>(p.stats + static_cast<int64_t>(row0) * 4));
+    if (row0 < r_end) next = __ldg(reinterpret_cast<const float4*>(p.stats) + row0);
     for (uint32_t row = row0; row < r_end; row += step) {
       const int64_t at = static_cast<int64_t>(row) * p.H;
       const float4 stat = next;
       if (row + step < r_end)
-        next = __ldg(reinterpret_cast<const float4*>(p.stats + static_cast<int64_t>(row + step) * 4));
+        next = __ldg(reinterpret_cast<const float4*>(p.stats) + row + step);
       cp_async_wait_ring(p.nbuf);
       uint8_t* st = join_smem + mine + b * slots;
       const uint64_t mu_h = join_twice(stat.z), rs_h = join_twice(stat.w);

@@ -173,7 +173,8 @@ __device__ __forceinline__ int moe_warp() { return (threadIdx.x >> 5) & 3; }
 __device__ __forceinline__ float moe_reduce(MoeShared& sh, int buf, const float (&c)[4]) {
   const int lane = threadIdx.x & 31;
   float* part = sh.part[moe_group()][buf];
-  float2* t = reinterpret_cast<float2*>(part + moe_warp() * 128 + (lane & 3) * 32 + (lane >> 2) * 2);
+  float2* t =
+      reinterpret_cast<float2*>(part + moe_warp() * 128 + (lane & 3) * 32 + (lane >> 2) * 2);
   t[0] = make_float2(c[0], c[2]);
   t[8] = make_float2(c[1], c[3]);
   asm volatile("bar.sync %0, 128;" ::"r"(moe_group() + 2) : "memory");
@@ -573,7 +574,7 @@ __device__ __forceinline__ void moe_result(const MoeParams& p, const MoeShared& 
   }
 }
 
-// fc1 or fc2 with up to NT tiles of eight of an expert's tokens.  After a wait that expired
+// fc1 or fc2 with up to NT (1 or 2) tiles of eight of an expert's tokens.  After a wait that expired
 // (`dead`), a lane waits no more and works on with what the stages hold: the launch is lost and
 // reported, but every barrier that the warps share still meets all of them.
 template <int NT, bool kFc1>
@@ -597,35 +598,29 @@ __device__ void moe_multiply(const MoeParams& p, MoeShared& sh, const MoeRing<1>
       moe_wait_oldest(ring.stages);
       const uint8_t* st = ring.ptr + at.stage * ring.stage_bytes;
       const int left = d.len - kc * kMoeKc - moe_col();
-      constexpr int kHeld = NT <= 2 ? 2 : 1;  // steps whose tokens are in registers at once
+      uint4 l[2], h[2], x[2][NT];
 #pragma unroll
-      for (int i0 = 0; i0 < 2; i0 += kHeld) {
-        uint4 l[kHeld], h[kHeld], x[kHeld][NT];
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* w = st + g * (kMoeKc * 2) + (moe_col() + i * 32) * 2;
+        l[i] = *reinterpret_cast<const uint4*>(w);
+        h[i] = *reinterpret_cast<const uint4*>(w + kMoeBox);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          const uint8_t* w = st + g * (kMoeKc * 2) + (moe_col() + (i0 + i) * 32) * 2;
-          l[i] = *reinterpret_cast<const uint4*>(w);
-          h[i] = *reinterpret_cast<const uint4*>(w + kMoeBox);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            x[i][j] = make_uint4(0, 0, 0, 0);  // past K's end, and past the expert's tokens
-            if (j * 8 + g < n && (i0 + i) * 32 < left)
-              x[i][j] = *reinterpret_cast<const uint4*>(st + ring.slot(i0 + i, j * 8 + g));
-          }
+        for (int j = 0; j < NT; ++j) {
+          x[i][j] = make_uint4(0, 0, 0, 0);  // past K's end, and past the expert's tokens
+          if (j * 8 + g < n && i * 32 < left)
+            x[i][j] = *reinterpret_cast<const uint4*>(st + ring.slot(i, j * 8 + g));
         }
-        if (i0 + kHeld == 2) {  // every lane has read what it wants of the stage
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ring.empty + 8 * at.stage);
-        }
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            if (j * 8 < n) {
-              moe_mma(c[j], l[i].x, h[i].x, l[i].y, h[i].y, x[i][j].x, x[i][j].y);
-              moe_mma(c[j], l[i].z, h[i].z, l[i].w, h[i].w, x[i][j].z, x[i][j].w);
-            }
       }
+      __syncwarp();  // every lane has read what it wants of the stage
+      if (lane == 0) mbar_arrive(ring.empty + 8 * at.stage);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (j * 8 < n) {
+            moe_mma(c[j], l[i].x, h[i].x, l[i].y, h[i].y, x[i][j].x, x[i][j].y);
+            moe_mma(c[j], l[i].z, h[i].z, l[i].w, h[i].w, x[i][j].z, x[i][j].w);
+          }
       at.next(ring.stages);
       tokens.issue();  // into the slots just read
     }
@@ -681,7 +676,8 @@ __device__ void moe_multiply_cta(const MoeParams& p, MoeShared& sh, const MoeRin
                           left > i * 32);
         row[q] += kMoeKc;
       }
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ring.full + 8 * to.stage)
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
+                 ::"r"(ring.full + 8 * to.stage)
                  : "memory");
     to.next(ring.stages);
     if (++ckc == d.kcs) {
@@ -805,7 +801,8 @@ __device__ __forceinline__ void moe_experts(const MoeParams& p, MoeShared& sh, u
 // Y_t = sum over t's pairs, in the order of its choices, of w y.
 __device__ __forceinline__ void moe_combine(const MoeParams& p, const MoeShared& sh) {
   const int per = p.H / 8;
-  for (int i = blockIdx.x * kMoeThreads + threadIdx.x; i < p.T * per; i += gridDim.x * kMoeThreads) {
+  for (int i = blockIdx.x * kMoeThreads + threadIdx.x; i < p.T * per;
+       i += gridDim.x * kMoeThreads) {
     const int t = i / per, c = (i - t * per) * 8;
     float v[8];
 #pragma unroll
@@ -828,8 +825,8 @@ __device__ __forceinline__ void moe_combine(const MoeParams& p, const MoeShared&
 }
 
 __global__ void __launch_bounds__(kMoeBlock, 1)
-    moe_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w2,
-               const MoeParams p) {
+    moe_kernel(const __grid_constant__ CUtensorMap map_w1,
+               const __grid_constant__ CUtensorMap map_w2, const MoeParams p) {
   extern __shared__ __align__(128) uint8_t moe_smem[];
   MoeShared& sh = *reinterpret_cast<MoeShared*>(moe_smem + kMoeGroups * kMoeRing);
   const bool multiplies = threadIdx.x < kMoeThreads;
@@ -935,7 +932,8 @@ extern "C" mlpb_status mlpb_moe_create(const mlpb_moe_config* cfg, mlpb_moe** ou
                            static_cast<int>(kMoeSmem)) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moe_kernel, kMoeBlock, kMoeSmem) !=
           cudaSuccess ||
-      per_sm < 1 || cudaMalloc(reinterpret_cast<void**>(&h->sync), sizeof(MoeSync)) != cudaSuccess ||
+      per_sm < 1 ||
+      cudaMalloc(reinterpret_cast<void**>(&h->sync), sizeof(MoeSync)) != cudaSuccess ||
       cudaMemset(h->sync, 0, sizeof(MoeSync)) != cudaSuccess ||
       cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come
     if (h->sync) cudaFree(h->sync);
@@ -969,9 +967,11 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
   if (tokens > c.max_tokens) return MLPB_EUNSUPPORTED;
   if (!Wr || !W1 || !W2) return MLPB_EINVAL;
   if (tokens > 0 && (!X || !Y || !ids || !weights || !workspace)) return MLPB_EINVAL;
-  for (const void* q : {X, Wr, W1, W2, static_cast<const void*>(Y), static_cast<const void*>(workspace)})
+  for (const void* q :
+       {X, Wr, W1, W2, static_cast<const void*>(Y), static_cast<const void*>(workspace)})
     if (q && (reinterpret_cast<uintptr_t>(q) & 15u) != 0) return MLPB_EINVAL;
-  if ((reinterpret_cast<uintptr_t>(ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
+  if ((reinterpret_cast<uintptr_t>(ids) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
     return MLPB_EINVAL;
   int device = -1;
   if (cudaGetDevice(&device) != cudaSuccess) return MLPB_ECUDA;

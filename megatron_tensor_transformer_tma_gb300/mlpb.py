@@ -792,8 +792,8 @@ class Join:
                 Xn = self._rows(torch.bfloat16)
             if stats is None:
                 stats = torch.empty(self._stats, dtype=torch.float32, device=self.device)
-        mlpb_join_fwd(self.cfg, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre, Xout,
-                      Xn, stats, stream)
+        mlpb_join_fwd(self.cfg, X, Y, res_scale, gate, gamma_post, beta_post, gamma_pre, beta_pre,
+                      Xout, Xn, stats, stream)
         return Xout, Xn, stats
 
     def alloc_grads(self, res_scale=False):
