@@ -421,6 +421,11 @@ mlpb_status mlpb_join_bwd(const mlpb_join_config *cfg, const void *X, const void
  *     Y   = sum over a token's experts of w W2_e act(W1_e x)       (no biases)
  * Every routed expert's weights are read once for all of its tokens.  act(W1_e x) is rounded to
  * bf16 (the second product's operand); every sum is fp32. */
+#define MLPB_MOE_FAULT_INJECT 0x2u /* mlpb_moe_config.flags, test only: the handle's first launch \
+                                      never fills one stage of a ring, its second leaves out an \
+                                      arrival at a barrier of the grid; both end by their waits' \
+                                      limit (MLPB_ETIMEOUT), and the third is an ordinary one    */
+
 typedef struct {
   int32_t max_tokens; /* most tokens of a call, 1..64                                         */
   int32_t hidden;     /* a multiple of 8                                                      */
@@ -429,7 +434,7 @@ typedef struct {
   int32_t topk;       /* 1..16, at most experts                                               */
   int32_t act;        /* mlpb_act                                                             */
   int32_t normalize;  /* 1: the weights of a token sum to 1                                   */
-  uint32_t flags;     /* 0                                                                    */
+  uint32_t flags;     /* 0, or MLPB_MOE_FAULT_INJECT                                          */
 } mlpb_moe_config;
 
 typedef struct mlpb_moe mlpb_moe; /* opaque; owns a few device words and no tensors */

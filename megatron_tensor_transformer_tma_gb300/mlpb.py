@@ -41,6 +41,7 @@ MLPB_NORM_RMS = 2
 MLPB_JOIN_STREAM_F32 = 0x1
 MLPB_JOIN_BLOCK_F32 = 0x2
 MLPB_JOIN_ACCUMULATE_GRADS = 0x4
+MLPB_MOE_FAULT_INJECT = 0x2
 ACT8_BLOCK = 32  # features that share a scale byte of an 8-bit activation checkpoint
 
 # Every symbol include/mlpb.h declares.
