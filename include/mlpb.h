@@ -460,7 +460,8 @@ mlpb_status mlpb_moe_forward(mlpb_moe *h, int64_t tokens, const void *X, const v
                              float *weights, void *workspace, mlpb_stream_t stream);
 
 /* As mlpb_last_device_error, for a mixture-of-experts handle: MLPB_ETIMEOUT if a bounded wait
- * of its launches expired since the last call. */
+ * of its launches on `stream` so far expired since the last call.  The current device must be
+ * the handle's (EINVAL). */
 mlpb_status mlpb_moe_last_device_error(mlpb_moe *h, mlpb_stream_t stream);
 
 /* Static English text of a status code. */

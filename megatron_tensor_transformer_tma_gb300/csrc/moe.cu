@@ -1063,10 +1063,13 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
 
 extern "C" mlpb_status mlpb_moe_last_device_error(mlpb_moe* h, mlpb_stream_t stream) {
   if (h == nullptr) return MLPB_EINVAL;
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return MLPB_ECUDA;
+  if (device != h->device) return MLPB_EINVAL;  // `stream` would not be one of the handle's
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(s) != cudaSuccess) return MLPB_ECUDA;
   uint32_t v = 0;
-  if (cudaMemcpy(&v, &h->sync->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(&v, &h->sync->err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
     return MLPB_ECUDA;
   if (v == 0) return MLPB_OK;
   if (cudaMemsetAsync(&h->sync->err, 0, sizeof(uint32_t), s) != cudaSuccess ||

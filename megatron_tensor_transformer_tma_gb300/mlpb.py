@@ -201,19 +201,22 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _call_on(dev, name, args, stream):
-    """Calls a library function with `args` and a stream (None: the current one of device
-    `dev`), with that device current: the library launches on the current device."""
-    fn = getattr(load_library(), name)
+def _on_device(dev, fn, args, stream):
+    """The result of a library function for `args` and a stream (None: the current one of device
+    `dev`), with that device current: the library works on the current device."""
     if stream is None:
         s = _raw_stream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if dev == torch.cuda.current_device():
-        _check(fn(*args, s), name)
-    else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, s), name)
+        return fn(*args, s)
+    with torch.cuda.device(dev):
+        return fn(*args, s)
+
+
+def _call_on(dev, name, args, stream):
+    """The same by the function's name, raising for a status that is not MLPB_OK."""
+    _check(_on_device(dev, getattr(load_library(), name), args, stream), name)
 
 
 def _on(stream):
@@ -600,8 +603,9 @@ def mlpb_moe_forward(h: MoEHandle, X, Wr, W1, W2, Y, ids, weights, workspace, st
 
 
 def mlpb_moe_last_device_error(h: MoEHandle, stream=None) -> int:
-    """The status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
-    return load_library().mlpb_moe_last_device_error(h.ptr, _stream(stream))
+    """The status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising, after the work of
+    `stream` (None: the current one of the handle's device)."""
+    return _on_device(h.device, load_library().mlpb_moe_last_device_error, [h.ptr], stream)
 
 
 def mlpb_last_device_error(h: Handle, stream=None) -> int:
