@@ -219,13 +219,21 @@ def _call_on(dev, name, args, stream):
     _check(_on_device(dev, getattr(load_library(), name), args, stream), name)
 
 
-def _on(stream):
-    """A context in which new tensors belong to the stream that the call will run on."""
+def _on(stream, device):
+    """A context in which new tensors on `device` belong to the stream that the call will run on."""
     if stream is None:
         return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
+
+
+def _device(device):
+    """The torch.device of a plan; "cuda" is the device that is current now, for good."""
+    d = torch.device(device)
+    if d.type == "cuda" and d.index is None:
+        d = torch.device("cuda", torch.cuda.current_device())
+    return d
 
 
 def _stream(stream):
@@ -534,8 +542,7 @@ def mlpb_join_bwd(cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post
 
 
 def _join_ws(cfg, dev):
-    dev = torch.device(dev)
-    return _join_ws_of(bytes(cfg), torch.cuda.current_device() if dev.index is None else dev.index)
+    return _join_ws_of(bytes(cfg), _device(dev).index)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -741,7 +748,7 @@ class ActCheckpoint8:
 
     def __init__(self, tokens, ffn, tp=1, act="gelu", device="cuda"):
         self.tokens, self.ffn, self.tp, self.act = tokens, ffn, tp, act
-        self.device = torch.device(device)
+        self.device = _device(device)
         self.width = 2 * ffn if act == "swiglu" else ffn
         self.codes = torch.empty((tokens, self.width), dtype=torch.int8, device=self.device)
         self.scales = torch.empty((tokens, mlpb_act8_scales(act, ffn, tp)), dtype=torch.uint8,
@@ -752,14 +759,14 @@ class ActCheckpoint8:
 
     def save(self, Z, A=None, stream=None):
         if A is None:
-            with _on(stream):
+            with _on(stream, self.device):
                 A = self._new(self.ffn)
         mlpb_act8_save(self.act, Z, A, self.codes, self.scales, self.tp, stream)
         return A
 
     def grad(self, dA, dZ=None, A=None, codes=None, scales=None, stream=None):
         """(dZ, A); codes and scales other than the ones this object holds may be given."""
-        with _on(stream):
+        with _on(stream, self.device):
             dZ = self._new(self.width) if dZ is None else dZ
             A = self._new(self.ffn) if A is None else A
         mlpb_act8_grad(self.act, dA, self.codes if codes is None else codes,
@@ -776,7 +783,7 @@ class Join:
                  has_block=True, device="cuda"):
         self.cfg = make_join_config(tokens, hidden, post_norm, pre_norm, gate_groups, eps,
                                     stream_dtype, block_dtype, accumulate, has_block)
-        self.device = torch.device(device)
+        self.device = _device(device)
         self.workspace = torch.empty(_join_ws(self.cfg, self.device), dtype=torch.uint8,
                                      device=self.device)
         self._stream_dtype, self._has_block = stream_dtype, bool(has_block)
@@ -790,7 +797,7 @@ class Join:
                 gamma_pre=None, beta_pre=None, Xout=None, Xn=None, stats=None, stream=None):
         """(Xout, Xn, stats); Xout is None without a block, Xn without a pre norm.  Pass the
         stream X itself as Xout to update it in place."""
-        with _on(stream):
+        with _on(stream, self.device):
             if Xout is None and self._has_block:
                 Xout = self._rows(self._stream_dtype)
             if Xn is None and self._has_pre:
@@ -826,7 +833,7 @@ class Join:
         to write into again (half of a small call's host time is its allocations)."""
         g = grads
         if g is None:
-            with _on(stream):
+            with _on(stream, self.device):
                 g = self.alloc_grads(res_scale is not None)
         mlpb_join_bwd(self.cfg, X, Y, Xout, stats, res_scale, gate, gamma_post, beta_post,
                       gamma_pre, dXout, dXn, g["dX"], g["dY"], g["dres_scale"], g["dgate"],
@@ -842,7 +849,7 @@ class MoEDecode:
     def __init__(self, max_tokens, hidden, ffn, experts, topk, act="swiglu", normalize=True,
                  device="cuda"):
         self.cfg = make_moe_config(max_tokens, hidden, ffn, experts, topk, act, normalize)
-        self.device = torch.device(device)
+        self.device = _device(device)
         with torch.cuda.device(self.device):
             self.handle = mlpb_moe_create(self.cfg)
         self.workspace = torch.empty(mlpb_moe_workspace_size(self.handle), dtype=torch.uint8,
@@ -859,7 +866,7 @@ class MoEDecode:
 
     def forward(self, X, Wr, W1, W2, Y=None, ids=None, weights=None, stream=None):
         T, c = X.shape[0], self.cfg
-        with _on(stream):
+        with _on(stream, self.device):
             if Y is None:
                 Y = torch.empty((T, c.hidden), dtype=torch.bfloat16, device=self.device)
             if ids is None:
