@@ -330,7 +330,8 @@ mlpb_status mlpb_quantize_e4m3(const void *in, int64_t batches, int64_t rows, in
  * scale byte.  With amax the block's largest magnitude and k the largest integer, at most
  * 126, with amax 2^k <= 127 (k = 0 for zeros), each code is z 2^k rounded to the nearest
  * integer, ties to even, and the scale byte is 127 - k: a code c stands for c 2^(byte - 127),
- * exactly.  A block that holds an infinity or a NaN has the byte 255 and stands for NaN
+ * exactly.  (bf16's largest value would become 64 2^122, past the range: the block that holds it
+ * has k = -121 and ties towards zero, 127 for that value.)  A block that holds an infinity or a NaN has the byte 255 and stands for NaN
  * throughout (its codes mean nothing).
  *
  * mlpb_act8_scales: *per_row = scale bytes of a row (ceil(F / 32) for GELU,

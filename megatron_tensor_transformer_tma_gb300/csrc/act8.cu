@@ -147,8 +147,9 @@ __device__ __forceinline__ Act8Codes<V> act8_encode(const Act8Words<V>& u,
   for (int i = 0; i < 4 * V; ++i) m = absmax_bf16x2(m, u.w[i]);
 #pragma unroll
   for (int o = 1; o < 4 / V; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  scale = act8_scale_byte(max(m & 0xffffu, m >> 16));
-  const float f = act8_to_codes(scale);
+  const uint32_t amax = max(m & 0xffffu, m >> 16);
+  scale = act8_scale_byte(amax);
+  const float f = act8_to_codes(scale, amax);
   Act8Codes<V> q;
 #pragma unroll
   for (int i = 0; i < 2 * V; ++i)

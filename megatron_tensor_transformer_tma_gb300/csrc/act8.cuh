@@ -5,7 +5,9 @@
 // (k <= 126; k = 0 for a block of zeros), code = z 2^k rounded to the nearest integer, ties
 // to even, and the scale byte e = 127 - k is the biased exponent of a code's step 2^-k.
 // z 2^k, the rounding and code 2^-k are exact in fp32, and code 2^-k is exact in bf16 too
-// (7 bits of magnitude), so the codes are a pure function of the bf16 values.  Signed
+// (7 bits of magnitude), so the codes are a pure function of the bf16 values.  bf16's largest
+// value, 127.5 2^121, would so become 64 2^122, an infinity: its block has k = -121 all the same,
+// and codes rounded with ties towards zero (127 for it, half a step off like any other).  Signed
 // integers rather than E4M3: a block of 32 normal values reaches about 2 sigma, so the step
 // is 2^-6 to 2^-5 sigma everywhere, where E4M3's step is 2^-4 to 2^-3 of the value itself
 // (a million normal values, each format with its block's power-of-two scale: rms error 0.8 %
@@ -30,17 +32,20 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t m, uint32_t w) {
 }
 
 // Scale byte of a block from the bits of its largest |bf16| (exponent E, mantissa M):
-// 127 = (2 - 2^-6) 2^6, so k = 133 - E, one less when 1.M > 2 - 2^-6, that is M = 0x7f.
+// 127 = (2 - 2^-6) 2^6, so k = 133 - E, one less when 1.M > 2 - 2^-6, that is M = 0x7f, but not
+// below -121.
 __device__ __forceinline__ uint32_t act8_scale_byte(uint32_t amax16) {
   if (amax16 >= 0x7f80u) return kActNanScale;
   const int E = static_cast<int>(amax16 >> 7);
-  const int k = amax16 == 0u ? 0 : min(126, 133 - E - ((amax16 & 0x7fu) == 0x7fu ? 1 : 0));
+  const int k =
+      amax16 == 0u ? 0 : max(-121, min(126, 133 - E - ((amax16 & 0x7fu) == 0x7fu ? 1 : 0)));
   return static_cast<uint32_t>(127 - k);
 }
 
-// 2^k, the factor that takes values to codes, of a scale byte (any finite value for 255).
-__device__ __forceinline__ float act8_to_codes(uint32_t e) {
-  return __uint_as_float(min(254u - e, 253u) << 23);
+// 2^k, the factor that takes values to codes, of a scale byte and its block's largest |bf16| (any
+// finite value for 255; the next one below 2^k where that is bf16's largest).
+__device__ __forceinline__ float act8_to_codes(uint32_t e, uint32_t amax16) {
+  return __uint_as_float((min(254u - e, 253u) << 23) - (amax16 == 0x7f7fu ? 1u : 0u));
 }
 
 // 2^-k, a code's step; NaN for 255 (0 is the subnormal 2^-127).

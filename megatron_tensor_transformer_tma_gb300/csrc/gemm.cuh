@@ -170,8 +170,9 @@ __device__ __forceinline__ void store_act8x32(uint8_t* codes, uint8_t* scale,
   pack_bf16x32(v, w);
 #pragma unroll
   for (int e = 0; e < 16; ++e) m = absmax_bf16x2(m, w[e]);
-  const uint32_t sb = act8_scale_byte(max(m & 0xffffu, m >> 16));
-  const float f = act8_to_codes(sb);
+  const uint32_t amax = max(m & 0xffffu, m >> 16);
+  const uint32_t sb = act8_scale_byte(amax);
+  const float f = act8_to_codes(sb, amax);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float2 a = unpack_bf16x2(w[2 * e]), b = unpack_bf16x2(w[2 * e + 1]);

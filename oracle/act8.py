@@ -6,7 +6,9 @@ TEST INFRASTRUCTURE.  Only ``tests/`` may import this module.
 Blocks of 32 consecutive features of a segment (all F for GELU, each shard's gate and each
 shard's up features for SwiGLU) share a power-of-two scale 2^k, k the largest integer <= 126
 with amax 2^k <= 127 (0 for zeros); a code is rint(z 2^k), ties to even; the scale byte is
-127 - k, or 255 for a block with a non-finite value, which stands for NaN.
+127 - k, or 255 for a block with a non-finite value, which stands for NaN.  A block whose amax is
+bf16's largest value has k = -121 (at -122 its code would stand for 2^128) and rounds ties towards
+zero.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import numpy as np
 from .mlp import silu, silu_grad
 
 BLOCK = 32
+LARGEST = 255.0 * 2.0 ** 120  # of bf16
 
 
 def segments(ffn, tp, act):
@@ -43,9 +46,12 @@ def quantize(Z, ffn, tp, act):
                     k = 300
                     while amax * 2.0 ** k > 127.0:
                         k -= 1
-                    k = min(k, 126)
+                    k = max(-121, min(k, 126))
                 scales[t, s, b] = 127 - k
-                codes[t, s, b * BLOCK:(b + 1) * BLOCK] = np.rint(blk * 2.0 ** k)
+                q = blk * 2.0 ** k
+                if amax == LARGEST:
+                    q = q * (1.0 - 2.0 ** -24)
+                codes[t, s, b * BLOCK:(b + 1) * BLOCK] = np.rint(q)
     return codes.reshape(T, n * width), scales.reshape(T, n * nb)
 
 
