@@ -185,20 +185,23 @@ __device__ __forceinline__ float moe_reduce(MoeShared& sh, int buf, const float 
 }
 
 // ------------------------------------------------------------------ router
-__device__ __forceinline__ float moe_dot8(const uint4& a, const uint4& b, float s) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 u = unpack_bf16x2(x[i]), v = unpack_bf16x2(y[i]);
-    s = fmaf(u.x, v.x, s);
-    s = fmaf(u.y, v.y, s);
-  }
-  return s;
+__device__ __forceinline__ uint64_t moe_pair(uint32_t w) {
+  const float2 f = unpack_bf16x2(w);
+  return f2_pack(f.x, f.y);
+}
+
+// Eight products into four sums (two f32x2): a sum is rounded once for two of them.
+__device__ __forceinline__ void moe_dot8(const uint4& a, const uint4& b, uint64_t (&s)[2]) {
+  s[0] = f2_fma(moe_pair(a.x), moe_pair(b.x), s[0]);
+  s[1] = f2_fma(moe_pair(a.y), moe_pair(b.y), s[1]);
+  s[0] = f2_fma(moe_pair(a.z), moe_pair(b.z), s[0]);
+  s[1] = f2_fma(moe_pair(a.w), moe_pair(b.w), s[1]);
 }
 
 // A pair of expert and token at a time, K over all sixteen warps, or with more pairs than CTAs
 // four pairs, K over four warps each.  The code is kept short: it runs once, and fetching it
-// takes longer than running it.
+// takes longer than running it.  A logit takes at most 8 ceil(H / 4096) + 24 roundings (two for
+// each 8 of a lane's products in a sum, two to join its four, five in the warp, one for each warp).
 __device__ __forceinline__ void moe_logits(const MoeParams& p, MoeShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = p.E * p.T;
@@ -213,9 +216,13 @@ __device__ __forceinline__ void moe_logits(const MoeParams& p, MoeShared& sh) {
       const int t = pair / p.E, e = pair - t * p.E;
       const __nv_bfloat16* a = p.Wr + static_cast<size_t>(e) * p.H;
       const __nv_bfloat16* x = p.X + static_cast<size_t>(t) * p.H;
+      uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll 2
       for (int c = (sub * 32 + lane) * 8; c < p.H; c += w * 256)
-        acc = moe_dot8(ld_global_nc_v4(a + c), ld_global_nc_v4(x + c), acc);
+        moe_dot8(ld_global_nc_v4(a + c), ld_global_nc_v4(x + c), sums);
+      float lo, hi;
+      f2_unpack(f2_add(sums[0], sums[1]), lo, hi);
+      acc = lo + hi;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     }
