@@ -18,7 +18,8 @@
 // elements as its registers hold: 32 of a row in the forward, 16 in the backward, which keeps
 // column sums too.  (8 a thread, with twice to four times the threads: the backward of T 8192
 // H 8192 took 95 instructions an element and 290 us.)  And the usual call -- both norms, every
-// warp's columns all inside the row -- has an instantiation of its own (kPlain) without the
+// warp's columns all inside the row: H 1024, 2048, 4096 and 8192, in the forward 5120 and 16384
+// too -- has an instantiation of its own (kPlain) without the
 // masks and the checks of what there is, which are half of the general one's instructions.  A
 // CTA holds several rows where a row needs few warps.
 //
@@ -85,10 +86,14 @@ constexpr int join_rows(int wpr) { return wpr >= 8 ? 1 : 8 / wpr; }
 constexpr int join_threads(int wpr) { return wpr < 0 ? -32 * wpr : 32 * wpr * join_rows(wpr); }
 constexpr int join_ctas(int wpr) { return wpr < 0 ? 1 : 512 / join_threads(wpr); }  // of an SM
 
-// Warps of a row in the forward, of those that there are kernels for: 256 elements each up to H
-// 256, else 1024.
-inline int join_fwd_wpr(int64_t H) {
-  return H <= 1024 ? 1 : H <= 2048 ? 2 : H <= 4096 ? 4 : H == 5120 ? 5 : H <= 8192 ? 8 : 16;
+// Warps of a row in the forward: 256 elements each up to H 256, else 1024, rounded up to the next
+// of 1, 2, 4, 8 and 16.  Five warps between (three rows an SM instead of two) where LayerNorm's
+// instructions bound the call or the row fills them; RMS rows that do not are faster on eight
+// (T 7280 bf16: LayerNorms H 4608 77 us against 93, H 5112 85 against 93, RMS H 4608 53 against 50,
+// H 5112 55 against 52).
+inline int join_fwd_wpr(int64_t H, bool layer) {
+  if (H > 4096 && H <= 5120 && (layer || H % 1024 == 0)) return 5;
+  return H <= 1024 ? 1 : H <= 2048 ? 2 : H <= 4096 ? 4 : H <= 8192 ? 8 : 16;
 }
 
 // How a backward is laid out: vectors of a thread, warps of a row in one CTA, rows and threads of a
@@ -108,14 +113,17 @@ inline JoinShape join_shape_general(int vpt, int64_t H, int max, int64_t most, i
   return JoinShape{vpt, wpr, rows, 32 * wpr * rows, cluster};
 }
 
-// The backward's: plain instantiations for 16 elements a thread at these widths; the general ones
-// hold as many (8 up to H 256), on 12 warps of 168 registers where a row fits them (with
+// The backward's: plain instantiations, for 16 elements a thread, where whole rows fill an SM's 16
+// warps, that is at powers of two from 1024 to 8192 (H 8192 LayerNorms 108 us; other multiples of
+// 1024 leave warps idle and are as fast or faster in the general ones: T 6552 H 5120 bf16 RMS 92 us
+// against 107, fp32 LayerNorms 126 against 140, but bf16 LayerNorms 126 against 119).  The general
+// ones hold as many (8 up to H 256), on 12 warps of 168 registers where a row fits them (with
 // LayerNorm 16 of 128 registers spill: T 11061 H 2184, 119 us against 104; RMS T 7122 H 2936, 64
 // against 60), and above H 8192 with two CTAs a row (32 elements a thread in one CTA: T 610
 // H 9856 44 us against 30, T 1024 H 16384 with LayerNorm over 90 against 88; three CTAs of 12
 // warps there 128).
 inline bool join_bwd_has_plain(int64_t H) {
-  return H == 1024 || H == 2048 || H == 4096 || H == 5120 || H == 8192;
+  return H >= 1024 && H <= 8192 && (H & (H - 1)) == 0;
 }
 inline JoinShape join_bwd_shape(int64_t H, bool plain, int64_t most) {
   if (plain) return join_shape_plain(2, static_cast<int>(H / 512));

@@ -582,7 +582,6 @@ static cudaError_t join_bwd_pick(const JoinParams& p, const JoinShape& sh, bool 
       case 2: return join_bwd_launch<XT, YT, 2, 2, kBeta>(p, sh, grid, s);
       case 4: return join_bwd_launch<XT, YT, 2, 4, kBeta>(p, sh, grid, s);
       case 8: return join_bwd_launch<XT, YT, 2, 8, kBeta>(p, sh, grid, s);
-      case 10: return join_bwd_launch<XT, YT, 2, 10, kBeta>(p, sh, grid, s);
       default: return join_bwd_launch<XT, YT, 2, 16, kBeta>(p, sh, grid, s);
     }
   }

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(join_threads(kWpr), 512 / join_threads(kWpr))
 
   // With LayerNorm, gamma_pre too is read again for every row where the registers would spill:
   // T8192 H8192 bf16 107 -> 95 us, H4096 59 -> 49, T11061 H2184 80 -> 73.  Where they hardly do,
-  // it costs: T16384 H5120 fp32 191 -> 196 us, T4373 H5400 49 -> 53.
+  // it costs: T16384 H5120 fp32 (five warps, 136 registers) 191 -> 196 us, T4373 H5400 49 -> 53.
   constexpr bool kReread = kBeta && (kPlain ? kWpr != 5 : kWpr <= 4);
   uint4 gpre[kReread ? 1 : kVpt];
   JoinVec gw[kBeta ? 1 : kVpt];                            // gate gamma_post
@@ -243,7 +243,7 @@ static cudaError_t join_fwd_launch(JoinParams p, int num_sms, cudaStream_t s) {
 
 template <class XT, class YT, bool kBeta>
 static cudaError_t join_fwd_pick(const JoinParams& p, int num_sms, cudaStream_t s) {
-  switch (join_fwd_wpr(p.H)) {
+  switch (join_fwd_wpr(p.H, kBeta)) {
     case 1:
       return p.H <= 256 ? join_fwd_launch<XT, YT, 1, 1, kBeta>(p, num_sms, s)
                         : join_fwd_launch<XT, YT, 4, 1, kBeta>(p, num_sms, s);
