@@ -330,9 +330,9 @@ mlpb_status mlpb_quantize_e4m3(const void *in, int64_t batches, int64_t rows, in
  * scale byte.  With amax the block's largest magnitude and k the largest integer, at most
  * 126, with amax 2^k <= 127 (k = 0 for zeros), each code is z 2^k rounded to the nearest
  * integer, ties to even, and the scale byte is 127 - k: a code c stands for c 2^(byte - 127),
- * exactly.  (bf16's largest value would become 64 2^122, past the range: the block that holds it
- * has k = -121 and ties towards zero, 127 for that value.)  A block that holds an infinity or a NaN has the byte 255 and stands for NaN
- * throughout (its codes mean nothing).
+ * exactly.  (bf16's largest value would become 64 2^122, past the range: the block that holds
+ * it has k = -121 and ties towards zero, 127 for that value.)  A block that holds an infinity or
+ * a NaN has the byte 255 and stands for NaN throughout (its codes mean nothing).
  *
  * mlpb_act8_scales: *per_row = scale bytes of a row (ceil(F / 32) for GELU,
  * 2 tp ceil(Fs / 32) for SwiGLU).
@@ -455,7 +455,8 @@ mlpb_status mlpb_moe_workspace_size(const mlpb_moe *h, size_t *bytes);
  * [tokens][topk] int32 and weights [tokens][topk] fp32 receive the routing.  The launch is
  * cooperative (one CTA on every SM, which synchronise).  The current device must be the
  * handle's.  Calls of one handle, or with one workspace, must not overlap on the GPU (use one
- * stream, or a handle and a workspace for each; a captured graph counts as its call). */
+ * stream, or a handle and a workspace for each; a captured graph counts as its call, and the
+ * handle has to outlive it). */
 mlpb_status mlpb_moe_forward(mlpb_moe *h, int64_t tokens, const void *X, const void *Wr,
                              const void *W1, const void *W2, void *Y, int32_t *ids,
                              float *weights, void *workspace, mlpb_stream_t stream);

@@ -13,7 +13,7 @@
 // threads; every thread walks act8_rows() rows of its columns, whose loads are issued together.
 //
 // Measured, with the rate of the bytes above (a copy reaches 6.8 TB/s): GELU T8192 F20480 save
-// 124 us, 6.8 TB/s, grad 181 us, 6.5 TB/s; SwiGLU T16384 F11008 save 214 us, 6.8 TB/s, grad
+// 124 us, 6.8 TB/s, grad 183 us, 6.4 TB/s; SwiGLU T16384 F11008 save 214 us, 6.8 TB/s, grad
 // 277 us, 6.5 TB/s.
 #include <algorithm>
 
@@ -323,7 +323,7 @@ static mlpb_status act8_dims(int32_t act, int64_t T, int64_t F, int32_t tp, uint
   d->blocks = static_cast<int>(blocks);
   // 32-byte accesses where every row and segment starts on one: measured at GELU T8192 F20480,
   // save 137 us with 8 features a thread and 124 with 16 (6.8 TB/s), grad 230 and 181 (6.5 TB/s;
-  // there one exponential for both outputs counts too)
+  // there one exponential for both outputs counts too; 183 with the slope held finite)
   d->wide = width % 16 == 0 && (bits & 31u) == 0;
   d->units = static_cast<int>(segments * blocks * (d->wide ? 2 : 4));
   d->ux_log2 = 2;

@@ -27,8 +27,8 @@
 // Where an expert has more than 16 tokens, those copies, 512 bytes a token for every 8 KB of
 // weights, would leave one stage in a group's ring.  Then the CTA has one ring and works on
 // units of 64 rows, 16 for each group, and a stage holds its tokens once for all four: T 64
-// H 4096 Fe 1792 4 experts top 2 73 us (with rings of the groups 125; two groups with units of
-// 32 rows 154), 16 experts top 4 153 us (170); from 9 tokens on it loses (T 24 57 us against
+// H 4096 Fe 1792 4 experts top 2 75 us (with rings of the groups 125; two groups with units of
+// 32 rows 154), 16 experts top 4 151 us (170); from 9 tokens on it loses (T 24 57 us against
 // 51).
 // Two other ways to move the weights measured slower: cp.async of each lane's own fragments was
 // bound by instructions, about 200 a kilobyte (T 1: 4.1 TB/s over all); and bulk copies of
@@ -41,8 +41,8 @@
 // 16 consecutive bytes of a row.
 //
 // Measured, over the bytes of the routed experts' weights (a copy reaches 6.8 TB/s): SwiGLU T 1
-// H 4096 Fe 1376 top 8: 271 MB in 65 us, 4.2 TB/s; T 16 H 4096 Fe 688 128 experts top 8: 1.39 GB
-// in 228 us, 6.1 TB/s; T 64 H 5120 Fe 2560 32 experts top 4: 2.52 GB in 415 us, 6.1 TB/s.  At T 1
+// H 4096 Fe 1376 top 8: 271 MB in 66 us, 4.1 TB/s; T 16 H 4096 Fe 688 128 experts top 8: 1.39 GB
+// in 228 us, 6.1 TB/s; T 64 H 5120 Fe 2560 32 experts top 4: 2.52 GB in 412 us, 6.1 TB/s.  At T 1
 // the launch, router, choice and three barriers take 13 us of that, and fc1 ends between 35 and
 // 48 us by the part of the chip an SM is in (units claimed one by one instead measured 74 us in
 // all).
