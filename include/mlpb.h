@@ -416,12 +416,12 @@ mlpb_status mlpb_join_bwd(const mlpb_join_config *cfg, const void *X, const void
 
 /* A mixture-of-experts MLP for a few tokens (decoding), in one launch: the block's MLP with
  * `experts` experts in the place of its shards, of which every token takes `topk`.
- *     l   = X Wr^T                                  (router logits, fp32)
+ *     l   = X Wr^T                                  (to about 2^-40 of sum |x||wr|)
  *     ids = the topk experts of largest l, descending, equal ones by index (NaN last)
  *     w   = softmax(l) at ids, over all experts; divided by its sum over ids with `normalize`
  *     Y   = sum over a token's experts of w W2_e act(W1_e x)       (no biases)
  * Every routed expert's weights are read once for all of its tokens.  act(W1_e x) is rounded to
- * bf16 (the second product's operand); every sum is fp32. */
+ * bf16 (the second product's operand); every other sum is fp32. */
 #define MLPB_MOE_FAULT_INJECT 0x2u /* mlpb_moe_config.flags, test only: the handle's first launch \
                                       never fills one stage of a ring, its second leaves out an \
                                       arrival at a barrier of the grid; both end by their waits' \

@@ -6,7 +6,7 @@
 //
 // Bound by memory: up to 64 tokens share each expert's weights, which move once (a few flops a
 // byte).  One CTA an SM runs four phases with a barrier over the grid between them:
-//   router   a CTA takes one or four pairs of expert and token at a time;
+//   router   a CTA takes one, four or sixteen pairs of expert and token at a time;
 //   fc1      units of 16 weight rows (8 gate and the same 8 up features, or 16 for GELU) of one
 //            expert times that expert's tokens;
 //   fc2      the same with 16 output columns a unit, into fp32 rows y_s;
@@ -47,8 +47,8 @@
 // 48 us by the part of the chip an SM is in (units claimed one by one instead measured 74 us in
 // all).
 //
-// a is rounded to bf16, as every activation that a GEMM of this library reads; logits, softmax
-// and all sums are fp32.  Every wait is bounded (common.cuh).
+// a is rounded to bf16, as every activation that a GEMM of this library reads; logits are
+// pairs of fp32 values, softmax and all other sums fp32.  Every wait is bounded (common.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -89,7 +89,7 @@ struct MoeParams {
   __nv_bfloat16* Y;
   int32_t* ids;        // [T][K]
   float* weights;      // [T][K]
-  float* logits;       // [T][E] scratch
+  float2* logits;      // [T][E] scratch: fp32 and what that leaves out
   __nv_bfloat16* act;  // [T * K][Fe] scratch: a_s, pairs ordered by expert, then token
   float* pair_y;       // [T * K][H] scratch: y_s
   int T, H, Fe, E, K;
@@ -190,50 +190,90 @@ __device__ __forceinline__ uint64_t moe_pair(uint32_t w) {
   return f2_pack(f.x, f.y);
 }
 
-// Eight products into four sums (two f32x2): a sum is rounded once for two of them.
-__device__ __forceinline__ void moe_dot8(const uint4& a, const uint4& b, uint64_t (&s)[2]) {
-  s[0] = f2_fma(moe_pair(a.x), moe_pair(b.x), s[0]);
-  s[1] = f2_fma(moe_pair(a.y), moe_pair(b.y), s[1]);
-  s[0] = f2_fma(moe_pair(a.z), moe_pair(b.z), s[0]);
-  s[1] = f2_fma(moe_pair(a.w), moe_pair(b.w), s[1]);
+// s += x y for two values; what the sum's rounding loses goes into c.  The product of two bf16
+// is exact, so this is the error of one addition, by Knuth's two-sum (no order of magnitudes).
+__device__ __forceinline__ void moe_add2(uint64_t x, uint64_t y, uint64_t& s, uint64_t& c) {
+  const uint64_t t = f2_fma(x, y, s);
+  const uint64_t r = f2_sub(s, t);                          // -(what s took of x y)
+  const uint64_t lost = f2_add(f2_sub(s, f2_add(t, r)), f2_fma(x, y, r));
+  c = f2_add(c, lost);
+  s = t;
 }
 
-// A pair of expert and token at a time, K over all sixteen warps, or with more pairs than CTAs
-// four pairs, K over four warps each.  The code is kept short: it runs once, and fetching it
-// takes longer than running it.  A logit takes at most 8 ceil(H / 4096) + 24 roundings (two for
-// each 8 of a lane's products in a sum, two to join its four, five in the warp, one for each warp).
+// Eight products into four sums and what they lose (two f32x2 each).
+__device__ __forceinline__ void moe_dot8(const uint4& a, const uint4& b, uint64_t (&s)[2],
+                                         uint64_t (&c)[2]) {
+  moe_add2(moe_pair(a.x), moe_pair(b.x), s[0], c[0]);
+  moe_add2(moe_pair(a.y), moe_pair(b.y), s[1], c[1]);
+  moe_add2(moe_pair(a.z), moe_pair(b.z), s[0], c[0]);
+  moe_add2(moe_pair(a.w), moe_pair(b.w), s[1], c[1]);
+}
+
+// v = v + w, each a sum (x) and what it lost (y).
+__device__ __forceinline__ void moe_join(float2& v, float2 w) {
+  const float t = v.x + w.x, r = t - v.x;
+  v.y += w.y + ((v.x - (t - r)) + (w.x - r));
+  v.x = t;
+}
+
+// A lane's sums, as one.
+__device__ __forceinline__ float2 moe_total(const uint64_t (&s)[2], const uint64_t (&c)[2]) {
+  float2 a[2], b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f2_unpack(s[i], a[i].x, b[i].x);
+    f2_unpack(c[i], a[i].y, b[i].y);
+    moe_join(a[i], b[i]);
+  }
+  moe_join(a[0], a[1]);
+  return a[0];
+}
+
+// The sum over the lanes that differ in the bits up to `from`.
+__device__ __forceinline__ float2 moe_sum(float2 v, int from) {
+#pragma unroll 1
+  for (int o = from; o > 0; o >>= 1)
+    moe_join(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                            __shfl_xor_sync(0xffffffffu, v.y, o)));
+  return v;
+}
+
+// A pair of expert and token at a time, K over all sixteen warps; with more pairs than CTAs four
+// pairs, K over four warps each, and with many sixteen, a warp each (T 64 H 2048 256 experts 165
+// us, four warps 176; T 16 H 4096 128 experts 228, 230).  The code is kept short: it runs once, and
+// fetching it takes longer than running it.  A logit is right to about 2^-40 of its terms'
+// magnitudes, so that a token's experts are those of its exact logits whatever else is in the call;
+// with fp32 sums, whose order depends on the number of pairs, near ties went either way (T 16 227
+// us, T 64 H 5120 32 experts 412 against 413; in 64 bits 238 and 422).
 __device__ __forceinline__ void moe_logits(const MoeParams& p, MoeShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = p.E * p.T;
-  const int w = pairs <= static_cast<int>(gridDim.x) ? kMoeWarps : 4;  // warps of a pair
+  const int ctas = gridDim.x;
+  const int w = pairs <= ctas ? kMoeWarps : pairs <= 4 * ctas ? 4 : 1;  // warps of a pair
   const int at_once = kMoeWarps / w, sub = warp & (w - 1);
   int buf = 0;
 #pragma unroll 1
   for (int first = blockIdx.x * at_once; first < pairs; first += gridDim.x * at_once, buf ^= 1) {
     const int pair = first + warp / w;
-    float acc = 0.f;
+    const int t = pair / p.E, e = pair - t * p.E;
+    float2* part = reinterpret_cast<float2*>(sh.part[0][buf]);
     if (pair < pairs) {
-      const int t = pair / p.E, e = pair - t * p.E;
       const __nv_bfloat16* a = p.Wr + static_cast<size_t>(e) * p.H;
       const __nv_bfloat16* x = p.X + static_cast<size_t>(t) * p.H;
-      uint64_t sums[2] = {0ull, 0ull};
-#pragma unroll 2
+      uint64_t sums[2] = {0ull, 0ull}, lost[2] = {0ull, 0ull};
+#pragma unroll 4
       for (int c = (sub * 32 + lane) * 8; c < p.H; c += w * 256)
-        moe_dot8(ld_global_nc_v4(a + c), ld_global_nc_v4(x + c), sums);
-      float lo, hi;
-      f2_unpack(f2_add(sums[0], sums[1]), lo, hi);
-      acc = lo + hi;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        moe_dot8(ld_global_nc_v4(a + c), ld_global_nc_v4(x + c), sums, lost);
+      const float2 v = moe_sum(moe_total(sums, lost), 16);
+      if (lane == 0) part[warp] = v;
     }
-    if (lane == 0) sh.part[0][buf][warp] = acc;
     moe_sync();
-    if (pair < pairs && sub == 0 && lane == 0) {
-      float s = 0.f;
-#pragma unroll 1
-      for (int k = 0; k < w; ++k) s += sh.part[0][buf][warp + k];
-      const int t = pair / p.E;
-      __stcg(p.logits + static_cast<size_t>(t) * p.E + (pair - t * p.E), s);
+    if (pair < pairs && sub == 0) {
+      float2 v = moe_sum(lane < w ? part[warp + lane] : make_float2(0.f, 0.f), w / 2);
+      if (v.y != v.y) v.y = 0.f;  // an infinite sum's loss reads NaN
+      const float l = v.x + v.y;
+      if (lane == 0)
+        __stcg(p.logits + static_cast<size_t>(t) * p.E + e, make_float2(l, v.y - (l - v.x)));
     }
   }
 }
@@ -252,14 +292,17 @@ __device__ __forceinline__ void moe_choose(const MoeParams& p, MoeShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int t = warp; t < p.T; t += kMoeWarps) {
     float l[kPer];
-    uint32_t key[kPer];
+    uint32_t key[kPer], low[kPer];  // order by the fp32 logit, then by what it leaves out
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = i * 32 + lane;
       const bool in = e < p.E;
-      l[i] = in ? __ldcg(p.logits + static_cast<size_t>(t) * p.E + e) : -INFINITY;
-      key[i] = in ? moe_key(l[i]) : 0u;
+      const float2 v = in ? __ldcg(p.logits + static_cast<size_t>(t) * p.E + e)
+                          : make_float2(-INFINITY, 0.f);
+      l[i] = v.x;
+      key[i] = in ? moe_key(v.x) : 0u;
+      low[i] = moe_key(v.y);
       top = fmaxf(top, l[i]);
     }
 #pragma unroll
@@ -273,18 +316,21 @@ __device__ __forceinline__ void moe_choose(const MoeParams& p, MoeShared& sh) {
     float mine = 0.f;  // lane k keeps the k-th choice
     int mine_e = 0;
     for (int k = 0; k < p.K; ++k) {
-      uint32_t best = 0u;
+      uint32_t best = 0u, next = 0u;
       int at = 0x7fffffff;
       float val = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (key[i] > best) {  // the lowest index of a lane's equals comes first
+        if (key[i] > best || (key[i] == best && low[i] > next)) {  // a lane's lowest index first
           best = key[i];
+          next = low[i];
           at = i * 32 + lane;
           val = l[i];
         }
       const uint32_t all = __reduce_max_sync(0xffffffffu, best);
-      const int e = __reduce_min_sync(0xffffffffu, best == all ? at : 0x7fffffff);
+      if (best != all) next = 0u;
+      const uint32_t most = __reduce_max_sync(0xffffffffu, next);
+      const int e = __reduce_min_sync(0xffffffffu, next == most ? at : 0x7fffffff);
       val = __shfl_sync(0xffffffffu, val, e & 31);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
@@ -933,7 +979,7 @@ static bool moe_map(const mlpb_moe* h, CUtensorMap* m, const void* base, uint64_
 }
 
 static size_t moe_logits_bytes(const mlpb_moe_config& c) {
-  return moe_align(static_cast<size_t>(c.max_tokens) * c.experts * 4);
+  return moe_align(static_cast<size_t>(c.max_tokens) * c.experts * 8);
 }
 
 static size_t moe_act_bytes(const mlpb_moe_config& c) {
@@ -1036,7 +1082,7 @@ extern "C" mlpb_status mlpb_moe_forward(mlpb_moe* h, int64_t tokens, const void*
   p.Y = static_cast<__nv_bfloat16*>(Y);
   p.ids = ids;
   p.weights = weights;
-  p.logits = static_cast<float*>(workspace);
+  p.logits = static_cast<float2*>(workspace);
   uint8_t* ws = static_cast<uint8_t*>(workspace) + moe_logits_bytes(c);
   p.act = reinterpret_cast<__nv_bfloat16*>(ws);
   p.pair_y = reinterpret_cast<float*>(ws + moe_act_bytes(c));

@@ -32,3 +32,32 @@ def test_additions_of_half_a_step(T, E, H, ones):
     want = torch.softmax(l, 1).gather(1, ids.cpu().long())
     D = (8 * -(-H // 4096) + 24) * U * l.max().item()
     assert ((w.cpu().double() - want).abs() <= (2 * D + 16 * U) * want).all()
+
+
+@pytest.mark.parametrize("T,E,K,H", [(64, 256, 16, 1032), (20, 64, 8, 4096), (1, 128, 16, 4104),
+                                     (3, 8, 8, 8192)])
+def test_near_ties(T, E, K, H):
+    """Experts in pairs whose logits differ by 2^-27, far below what fp32 sums resolve (half a step
+    of a sum of one is 2^-25 or more): their order is that of the 64-bit logits, which 64-bit sums
+    give to 2^-45, and the kernel to 2^-40 sum |x||wr| < 2^-32; and a token alone has the experts
+    that it has among others."""
+    g = torch.Generator().manual_seed(T + E + H)
+    X = torch.randn(T, H, generator=g)
+    Wr = torch.randn(E // 2, H, generator=g) * H ** -0.5
+    X[:, 5] = torch.randint(0, 2, (T,), generator=g) * 2.0 - 1
+    Wr[:, 5] = 2.0 ** -20 * (1 + torch.randint(0, 127, (E // 2,), generator=g) / 128)
+    other = Wr.clone()
+    other[:, 5] += 2.0 ** -27
+    X, Wr = X.to(BF), torch.cat([Wr, other]).to(BF)
+    assert (X.double().abs() @ Wr.double().abs().T).max() < 256
+    l = X.double() @ Wr.double().T
+    want = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :K]
+    plan = mlpb.MoEDecode(T, H, 8, E, K, "gelu", False)
+    d = (Wr.cuda(), torch.zeros(E, 8, H, dtype=BF, device="cuda"),
+         torch.zeros(E, H, 8, dtype=BF, device="cuda"))
+    ids, w = plan.forward(X.cuda(), *d)[1:]
+    assert mlpb.mlpb_moe_last_device_error(plan.handle) == 0
+    assert torch.equal(ids.cpu().long(), want)
+    for t in (0, T // 2, T - 1):
+        alone = plan.forward(X[t:t + 1].cuda(), *d)
+        assert torch.equal(alone[1][0], ids[t])
