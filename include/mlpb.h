@@ -466,6 +466,78 @@ mlpb_status mlpb_moe_forward(mlpb_moe *h, int64_t tokens, const void *X, const v
  * the handle's (EINVAL). */
 mlpb_status mlpb_moe_last_device_error(mlpb_moe *h, mlpb_stream_t stream);
 
+/* Block-scaled E4M3: one power-of-two scale for each 128 consecutive columns of a row, or for each
+ * 128 x 128 block (`square`, for weights, whose codes and transposed codes then are the same).
+ * With amax the block's largest magnitude and k the largest integer, at most 126, with amax 2^k
+ * <= 448 (k = 0 for zeros), a code is e4m3(x 2^k), nearest, ties to even, and the scale byte is
+ * 127 - k: a code c stands for c 2^(byte - 127), exactly.  A block that holds an infinity or a NaN
+ * has the byte 255 and stands for NaN throughout.
+ *   codes   [rows][ld] bytes, ld = columns rounded up to 16 (mlpb_b128_sizes); the pad holds 0
+ *   scales  byte of (row, kb = column / 128) at
+ *             ((kb / 4) * ceil(rows / 128) + row / 128) * 512
+ *               + (row % 32) * 16 + (row % 128) / 32 * 4 + kb % 4,
+ *           the order in which the tensor cores take them; bytes past the end hold 127
+ *
+ * mlpb_b128_sizes: *ld and the bytes of the scales of a [rows][cols] matrix.
+ * mlpb_b128_quantize: x [rows][cols], bf16 or (x_f32 = 1) fp32, to codes q and scales qs of x
+ * and/or codes qt and scales qts of its transpose [cols][rows] (blocks along its own columns);
+ * either pair may be NULL, not both.  cols % 8 == 0, both at most 2^20 (else MLPB_EUNSUPPORTED);
+ * tensors 16-byte aligned; outputs overlap no input.  rows = 0 does nothing.  No handle, no
+ * workspace; allocates nothing. */
+mlpb_status mlpb_b128_sizes(int64_t rows, int64_t cols, int64_t *ld, size_t *scale_bytes);
+mlpb_status mlpb_b128_quantize(const void *x, int32_t x_f32, int64_t rows, int64_t cols,
+                               int32_t square, void *q, void *qs, void *qt, void *qts,
+                               mlpb_stream_t stream);
+
+/* A linear layer on block-scaled E4M3 operands, forward and backward ("Why Megatron-LM Matters" /
+ * "Key Features": mixed precision down to FP8; finer than the one scale for a tensor of
+ * MLPB_FLAG_FP8, at the same rate: the tensor cores apply the scales):
+ *     Y = Xq Wq^T,   dX = dYq Wq,   dW = (dY^T)q ((X^T)q)^T
+ * where (.)q rounds blocks of 128 along the axis that is summed over, and W blocks of 128 x 128.
+ * Products of codes are exact, sums fp32. */
+#define MLPB_LINEAR8_OUT_F32 0x1u      /* Y and dX are fp32 (else bf16)                       */
+#define MLPB_LINEAR8_FAULT_INJECT 0x2u /* test only, as MLPB_FLAG_FAULT_INJECT: the first     \
+                                          product's first stage is never filled               */
+
+typedef struct {
+  int64_t max_tokens; /* most rows of a call, 1..2^20                  */
+  int64_t inputs;     /* K: a multiple of 8, at most 2^20              */
+  int64_t outputs;    /* N: a multiple of 8, at most 2^20              */
+  uint32_t flags;     /* MLPB_LINEAR8_*                                */
+} mlpb_linear8_config;
+
+typedef struct mlpb_linear8 mlpb_linear8; /* opaque; owns a device word and no tensors */
+
+/* Validates *cfg and allocates the handle on the current device; EINVAL for null arguments or
+ * values out of range, EUNSUPPORTED for sizes outside those above. */
+mlpb_status mlpb_linear8_create(const mlpb_linear8_config *cfg, mlpb_linear8 **out);
+void mlpb_linear8_destroy(mlpb_linear8 *h);
+
+/* Bytes of the workspace of the calls below (codes and scales of X, or of dY and dY^T). */
+mlpb_status mlpb_linear8_workspace_size(const mlpb_linear8 *h, size_t *bytes);
+
+/* Forward of `tokens` <= max_tokens rows (0 does nothing): X [tokens][inputs] bf16; Wq, Ws the
+ * codes and scales of W [outputs][inputs] (mlpb_b128_quantize, square); Y [tokens][outputs].
+ * Xt, Xts, NULL in serving, receive codes and scales of X^T [inputs][tokens] for the backward.
+ * The current device must be the handle's.  Calls that share a workspace must not overlap on the
+ * GPU (a captured graph counts as its call, and the handle has to outlive it). */
+mlpb_status mlpb_linear8_forward(mlpb_linear8 *h, int64_t tokens, const void *X, const void *Wq,
+                                 const void *Ws, void *Y, void *Xt, void *Xts, void *workspace,
+                                 mlpb_stream_t stream);
+
+/* Backward for dY [tokens][outputs] bf16, with as many tokens as the forward that wrote Xt and
+ * Xts; Wt, Wts the codes and scales of W^T [inputs][outputs] of the same quantization.  dX
+ * [tokens][inputs] or dW [outputs][inputs] fp32 may be NULL, not both (nor are their operands
+ * read then).  accumulate: dW is added into.  tokens = 0 writes a zero dW, or leaves it as it is
+ * when accumulating. */
+mlpb_status mlpb_linear8_backward(mlpb_linear8 *h, int64_t tokens, const void *dY, const void *Wt,
+                                  const void *Wts, const void *Xt, const void *Xts, void *dX,
+                                  float *dW, int32_t accumulate, void *workspace,
+                                  mlpb_stream_t stream);
+
+/* As mlpb_moe_last_device_error, for a linear layer's handle. */
+mlpb_status mlpb_linear8_last_device_error(mlpb_linear8 *h, mlpb_stream_t stream);
+
 /* Static English text of a status code. */
 const char *mlpb_status_str(mlpb_status s);
 

@@ -1,0 +1,261 @@
+// A linear layer on block-scaled E4M3 operands: handle, workspace, tensor maps, launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <new>
+
+#include "../../include/mlpb.h"
+#include "common.cuh"
+#include "linear8.cuh"
+
+using namespace mlpb;
+
+struct mlpb_linear8 {
+  mlpb_linear8_config cfg;
+  int device, max_clusters;
+  bool fault_pending;
+  uint32_t* err;
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+};
+
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+size_t code_bytes(int64_t rows, int64_t cols) {
+  return align256(static_cast<size_t>(rows * b128_ld(cols)));
+}
+
+size_t scale_bytes(int64_t rows, int64_t cols) {
+  return static_cast<size_t>(b128_scale_bytes(rows, cols));
+}
+
+// A quantized matrix: codes [rows][ld] and scales.
+struct Quantized {
+  uint8_t *codes, *scales;
+  int64_t rows, cols;
+};
+
+Quantized quantized(const void* codes, const void* scales, int64_t rows, int64_t cols) {
+  return Quantized{static_cast<uint8_t*>(const_cast<void*>(codes)),
+                   static_cast<uint8_t*>(const_cast<void*>(scales)), rows, cols};
+}
+
+// The next one of the workspace.
+Quantized take(uint8_t*& at, int64_t rows, int64_t cols) {
+  Quantized q{at, at + code_bytes(rows, cols), rows, cols};
+  at += code_bytes(rows, cols) + scale_bytes(rows, cols);
+  return q;
+}
+
+bool encode(const mlpb_linear8* h, CUtensorMap* m, CUtensorMapDataType type, const void* base,
+            uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+            uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {stride};
+  const cuuint32_t box[2] = {box_inner, box_outer}, steps[2] = {1, 1};
+  return h->encode(m, type, 2, const_cast<void*>(base), dims, strides, box, steps,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Codes in tiles of 128 rows by 128 bytes; what is past the edges reads zero.
+bool map_codes(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
+  const uint64_t ld = static_cast<uint64_t>(b128_ld(q.cols));
+  return encode(h, m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, ld, static_cast<uint64_t>(q.rows), ld,
+                kB128, kB128, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scales as rows of 512 bytes: group of four blocks by group, 128-row tile by tile.
+bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
+  return encode(h, m, CU_TENSOR_MAP_DATA_TYPE_UINT32, q.scales, kB128Chunk / 4,
+                static_cast<uint64_t>(b128_scale_bytes(q.rows, q.cols) / kB128Chunk), kB128Chunk,
+                kB128Chunk / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// C [a.rows][b.rows] (+)= A B^T over the columns that both have.
+mlpb_status product(mlpb_linear8* h, const Quantized& a, const Quantized& b, void* C, bool f32,
+                    bool accumulate, cudaStream_t s) {
+  B128Maps m;
+  if (!map_codes(h, &m.a, a) || !map_codes(h, &m.b, b) || !map_scales(h, &m.sa, a) ||
+      !map_scales(h, &m.sb, b))
+    return MLPB_ECUDA;
+  B128Params p{};
+  p.M = static_cast<int>(a.rows);
+  p.N = static_cast<int>(b.rows);
+  p.num_pm = static_cast<int>(cdiv(a.rows, 256));
+  p.num_n = static_cast<int>(cdiv(b.rows, 256));
+  p.num_kb = static_cast<int>(b128_blocks(a.cols));
+  p.a_tiles = static_cast<int>(b128_blocks(a.rows));
+  p.b_tiles = static_cast<int>(b128_blocks(b.rows));
+  p.out_f32 = f32 ? 1 : 0;
+  p.accumulate = accumulate ? 1 : 0;
+  p.C = C;
+  p.err = h->err;
+  p.wait_ns = kDefaultWaitNs;
+  p.fault_inject = h->fault_pending ? 1 : 0;
+  h->fault_pending = false;
+  const int clusters = std::min(p.num_pm * p.num_n, h->max_clusters);
+  return launch_b128_gemm(m, p, clusters, s) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
+}
+
+mlpb_status quantize(const void* x, bool f32, int64_t rows, int64_t cols, const Quantized* q,
+                     const Quantized* qt, cudaStream_t s) {
+  return launch_b128_quantize(x, f32, rows, cols, false, q ? q->codes : nullptr,
+                              q ? q->scales : nullptr, qt ? qt->codes : nullptr,
+                              qt ? qt->scales : nullptr, s) == cudaSuccess
+             ? MLPB_OK
+             : MLPB_ECUDA;
+}
+
+// The current device is the handle's.
+mlpb_status on_device(const mlpb_linear8* h) {
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return MLPB_ECUDA;
+  return device == h->device ? MLPB_OK : MLPB_EINVAL;
+}
+
+}  // namespace
+
+extern "C" mlpb_status mlpb_linear8_create(const mlpb_linear8_config* cfg, mlpb_linear8** out) {
+  if (cfg == nullptr || out == nullptr) return MLPB_EINVAL;
+  *out = nullptr;
+  const mlpb_linear8_config& c = *cfg;
+  if (c.max_tokens < 1 || c.inputs < 1 || c.outputs < 1 ||
+      (c.flags & ~(MLPB_LINEAR8_OUT_F32 | MLPB_LINEAR8_FAULT_INJECT)) != 0)
+    return MLPB_EINVAL;
+  constexpr int64_t most = int64_t{1} << 20;
+  if (c.max_tokens > most || c.inputs > most || c.outputs > most || c.inputs % 8 != 0 ||
+      c.outputs % 8 != 0)
+    return MLPB_EUNSUPPORTED;
+  mlpb_linear8* h = new (std::nothrow) mlpb_linear8();
+  if (h == nullptr) return MLPB_ENOMEM;
+  h->cfg = c;
+  h->fault_pending = (c.flags & MLPB_LINEAR8_FAULT_INJECT) != 0;
+  h->err = nullptr;
+  int major = 0, minor = 0;
+  if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, h->device) != cudaSuccess) {
+    delete h;
+    return MLPB_ECUDA;
+  }
+  if (major != 10 || minor != 3) {
+    delete h;
+    return MLPB_EUNSUPPORTED;
+  }
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found{};
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess || fn == nullptr) {
+    delete h;
+    return MLPB_ECUDA;
+  }
+  h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  if (b128_gemm_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
+      cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||
+      cudaMemset(h->err, 0, sizeof(uint32_t)) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come
+    if (h->err) cudaFree(h->err);
+    delete h;
+    return MLPB_ECUDA;
+  }
+  *out = h;
+  return MLPB_OK;
+}
+
+extern "C" void mlpb_linear8_destroy(mlpb_linear8* h) {
+  if (h == nullptr) return;
+  if (h->err) cudaFree(h->err);
+  delete h;
+}
+
+extern "C" mlpb_status mlpb_linear8_workspace_size(const mlpb_linear8* h, size_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MLPB_EINVAL;
+  const mlpb_linear8_config& c = h->cfg;
+  const size_t x = code_bytes(c.max_tokens, c.inputs) + scale_bytes(c.max_tokens, c.inputs);
+  const size_t dy = code_bytes(c.max_tokens, c.outputs) + scale_bytes(c.max_tokens, c.outputs) +
+                    code_bytes(c.outputs, c.max_tokens) + scale_bytes(c.outputs, c.max_tokens);
+  *bytes = std::max(x, dy);
+  return MLPB_OK;
+}
+
+extern "C" mlpb_status mlpb_linear8_forward(mlpb_linear8* h, int64_t tokens, const void* X,
+                                            const void* Wq, const void* Ws, void* Y, void* Xt,
+                                            void* Xts, void* workspace, mlpb_stream_t stream) {
+  if (h == nullptr || tokens < 0) return MLPB_EINVAL;
+  const mlpb_linear8_config& c = h->cfg;
+  if (tokens > c.max_tokens) return MLPB_EUNSUPPORTED;
+  if (!Wq || !Ws || (Xt == nullptr) != (Xts == nullptr)) return MLPB_EINVAL;
+  if (tokens > 0 && (!X || !Y || !workspace)) return MLPB_EINVAL;
+  for (const void* q : {X, Wq, Ws, static_cast<const void*>(Y), static_cast<const void*>(Xt),
+                        static_cast<const void*>(Xts), static_cast<const void*>(workspace)})
+    if (!aligned16(q)) return MLPB_EINVAL;
+  mlpb_status st = on_device(h);
+  if (st != MLPB_OK || tokens == 0) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  const Quantized x = take(at, tokens, c.inputs);
+  const Quantized w = quantized(Wq, Ws, c.outputs, c.inputs);
+  const Quantized xt = quantized(Xt, Xts, c.inputs, tokens);
+  st = quantize(X, false, tokens, c.inputs, &x, Xt ? &xt : nullptr, s);
+  if (st != MLPB_OK) return st;
+  return product(h, x, w, Y, (c.flags & MLPB_LINEAR8_OUT_F32) != 0, false, s);
+}
+
+extern "C" mlpb_status mlpb_linear8_backward(mlpb_linear8* h, int64_t tokens, const void* dY,
+                                             const void* Wt, const void* Wts, const void* Xt,
+                                             const void* Xts, void* dX, float* dW,
+                                             int32_t accumulate, void* workspace,
+                                             mlpb_stream_t stream) {
+  if (h == nullptr || tokens < 0 || (accumulate != 0 && accumulate != 1)) return MLPB_EINVAL;
+  const mlpb_linear8_config& c = h->cfg;
+  if (tokens > c.max_tokens) return MLPB_EUNSUPPORTED;
+  if (tokens > 0 && (!dY || !workspace || (!dX && !dW) || (dX && (!Wt || !Wts)) ||
+                     (dW && (!Xt || !Xts))))
+    return MLPB_EINVAL;
+  for (const void* q :
+       {dY, Wt, Wts, Xt, Xts, static_cast<const void*>(dX), static_cast<const void*>(dW),
+        static_cast<const void*>(workspace)})
+    if (!aligned16(q)) return MLPB_EINVAL;
+  mlpb_status st = on_device(h);
+  if (st != MLPB_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    if (dW != nullptr && accumulate == 0 &&
+        cudaMemsetAsync(dW, 0, static_cast<size_t>(c.inputs * c.outputs) * 4, s) != cudaSuccess)
+      return MLPB_ECUDA;
+    return MLPB_OK;
+  }
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  const Quantized dy = take(at, tokens, c.outputs), dyt = take(at, c.outputs, tokens);
+  st = quantize(dY, false, tokens, c.outputs, dX ? &dy : nullptr, dW ? &dyt : nullptr, s);
+  if (st == MLPB_OK && dX != nullptr)
+    st = product(h, dy, quantized(Wt, Wts, c.inputs, c.outputs), dX,
+                 (c.flags & MLPB_LINEAR8_OUT_F32) != 0, false, s);
+  if (st == MLPB_OK && dW != nullptr)
+    st = product(h, dyt, quantized(Xt, Xts, c.inputs, tokens), dW, true, accumulate != 0, s);
+  return st;
+}
+
+extern "C" mlpb_status mlpb_linear8_last_device_error(mlpb_linear8* h, mlpb_stream_t stream) {
+  if (h == nullptr) return MLPB_EINVAL;
+  const mlpb_status st = on_device(h);  // `stream` would not be one of the handle's
+  if (st != MLPB_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  if (cudaMemcpyAsync(&v, h->err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MLPB_ECUDA;
+  if (v == 0) return MLPB_OK;
+  if (cudaMemsetAsync(h->err, 0, sizeof(uint32_t), s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MLPB_ECUDA;
+  return MLPB_ETIMEOUT;
+}

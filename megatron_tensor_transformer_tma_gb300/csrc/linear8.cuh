@@ -1,0 +1,33 @@
+// Launch parameters of the products of block-scaled E4M3 operands (linear8.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "b128.cuh"
+
+namespace mlpb {
+
+// C [M][N] (+)= A B^T for A [M][K] and B [N][K] in block-scaled E4M3.
+struct B128Params {
+  int M, N;
+  int num_pm, num_n, num_kb;  // pairs of M tiles, N tiles, 128-deep k-blocks
+  int a_tiles, b_tiles;       // 128-row tiles that the scales have
+  int raster_group;
+  int out_f32;     // C is fp32 (else bf16)
+  int accumulate;  // C += (fp32)
+  void* C;
+  uint32_t* err;
+  uint64_t wait_ns;
+  int fault_inject;
+};
+
+struct B128Maps {
+  CUtensorMap a, b, sa, sb;
+};
+
+cudaError_t b128_gemm_set_attrs(int* max_clusters);
+cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters, cudaStream_t s);
+
+}  // namespace mlpb

@@ -42,6 +42,8 @@ MLPB_JOIN_STREAM_F32 = 0x1
 MLPB_JOIN_BLOCK_F32 = 0x2
 MLPB_JOIN_ACCUMULATE_GRADS = 0x4
 MLPB_MOE_FAULT_INJECT = 0x2
+MLPB_LINEAR8_OUT_F32 = 0x1
+MLPB_LINEAR8_FAULT_INJECT = 0x2
 ACT8_BLOCK = 32  # features that share a scale byte of an 8-bit activation checkpoint
 
 # Every symbol include/mlpb.h declares.
@@ -54,6 +56,9 @@ EXPORTED = (
     "mlpb_join_workspace_size", "mlpb_join_fwd", "mlpb_join_bwd",
     "mlpb_moe_create", "mlpb_moe_destroy", "mlpb_moe_workspace_size", "mlpb_moe_forward",
     "mlpb_moe_last_device_error",
+    "mlpb_b128_sizes", "mlpb_b128_quantize",
+    "mlpb_linear8_create", "mlpb_linear8_destroy", "mlpb_linear8_workspace_size",
+    "mlpb_linear8_forward", "mlpb_linear8_backward", "mlpb_linear8_last_device_error",
 )
 
 
@@ -76,6 +81,11 @@ class mlpb_join_config(ctypes.Structure):
 class mlpb_moe_config(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int32) for k in ("max_tokens", "hidden", "ffn", "experts", "topk",
                                               "act", "normalize")] + [("flags", ctypes.c_uint32)]
+
+
+class mlpb_linear8_config(ctypes.Structure):
+    _fields_ = [("max_tokens", ctypes.c_int64), ("inputs", ctypes.c_int64),
+                ("outputs", ctypes.c_int64), ("flags", ctypes.c_uint32)]
 
 
 class mlpb_kernel_time(ctypes.Structure):
@@ -133,6 +143,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mlpb_moe_workspace_size": (I, [H, ctypes.POINTER(Z)]),
         "mlpb_moe_forward": (I, [H, I64] + [P] * 9),
         "mlpb_moe_last_device_error": (I, [H, P]),
+        "mlpb_b128_sizes": (I, [I64, I64, ctypes.POINTER(I64), ctypes.POINTER(Z)]),
+        "mlpb_b128_quantize": (I, [P, I32, I64, I64, I32] + [P] * 5),
+        "mlpb_linear8_create": (I, [ctypes.POINTER(mlpb_linear8_config), ctypes.POINTER(H)]),
+        "mlpb_linear8_destroy": (None, [H]),
+        "mlpb_linear8_workspace_size": (I, [H, ctypes.POINTER(Z)]),
+        "mlpb_linear8_forward": (I, [H, I64] + [P] * 8),
+        "mlpb_linear8_backward": (I, [H, I64] + [P] * 7 + [I32, P, P]),
+        "mlpb_linear8_last_device_error": (I, [H, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -615,6 +633,137 @@ def mlpb_moe_last_device_error(h: MoEHandle, stream=None) -> int:
     return _on_device(h.device, load_library().mlpb_moe_last_device_error, [h.ptr], stream)
 
 
+@functools.lru_cache(maxsize=4096)
+def mlpb_b128_sizes(rows, cols):
+    """(bytes of a row of codes, bytes of the scales) of a block-scaled E4M3 [rows][cols] matrix."""
+    ld, n = ctypes.c_int64(), ctypes.c_size_t()
+    _check(load_library().mlpb_b128_sizes(rows, cols, ctypes.byref(ld), ctypes.byref(n)),
+           "mlpb_b128_sizes")
+    return ld.value, n.value
+
+
+def b128_empty(rows, cols, device):
+    """Uninitialised codes [rows][ld] and scales of a [rows][cols] matrix (uint8)."""
+    ld, n = mlpb_b128_sizes(rows, cols)
+    return (torch.empty((rows, ld), dtype=torch.uint8, device=device),
+            torch.empty(n, dtype=torch.uint8, device=device))
+
+
+def _b128_args(q, rows, cols, name, dev):
+    """Pointers of a (codes, scales) pair, or of None."""
+    if q is None:
+        return [None, None]
+    ld, n = mlpb_b128_sizes(rows, cols)
+    return [_arg(q[0], torch.uint8, (rows, ld), name + " codes", dev),
+            _arg(q[1], torch.uint8, (n,), name + " scales", dev)]
+
+
+def mlpb_b128_quantize(x, q=None, qt=None, square=False, stream=None):
+    """Block-scaled E4M3 (include/mlpb.h) of a bf16 or fp32 matrix x [rows][cols] into q and/or of
+    its transpose into qt, each a (codes, scales) pair of b128_empty()."""
+    dev = _cuda_index(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows][cols], got {tuple(x.shape)}")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x: expected bfloat16 or float32, got {x.dtype}")
+    rows, cols = x.shape
+    args = [_arg(x, x.dtype, x.shape, "x", dev), 1 if x.dtype == torch.float32 else 0, rows, cols,
+            1 if square else 0, *_b128_args(q, rows, cols, "q", dev),
+            *_b128_args(qt, cols, rows, "qt", dev)]
+    _call_on(dev, "mlpb_b128_quantize", args, stream)
+
+
+def b128_values(q, rows, cols):
+    """What a (codes, scales) pair stands for, as fp64 [rows][cols] (torch operations: for tests
+    and inspection; fp32's largest values are rounded to 2^128)."""
+    codes, scales = q
+    n = -(-cols // 128)
+    tiles = -(-rows // 128)
+    e = scales.view(-1, tiles, 32, 4, 4).permute(1, 3, 2, 0, 4).reshape(tiles * 128, -1)[:rows, :n]
+    v = codes[:, :cols].contiguous().view(torch.float8_e4m3fn).double()
+    e = e.to(torch.int32).repeat_interleave(128, 1)[:, :cols]
+    return torch.where(e == 255, torch.full_like(v, float("nan")), v * torch.exp2(e.double() - 127))
+
+
+@dataclasses.dataclass
+class Linear8Handle:
+    ptr: int
+    cfg: mlpb_linear8_config
+    device: int  # CUDA device number it was created on
+    workspace_bytes: int
+
+
+def mlpb_linear8_create(cfg: mlpb_linear8_config) -> Linear8Handle:
+    """A linear layer's handle on the current CUDA device."""
+    lib, h, n = load_library(), ctypes.c_void_p(), ctypes.c_size_t()
+    _check(lib.mlpb_linear8_create(ctypes.byref(cfg), ctypes.byref(h)), "mlpb_linear8_create")
+    _check(lib.mlpb_linear8_workspace_size(h.value, ctypes.byref(n)),
+           "mlpb_linear8_workspace_size")
+    return Linear8Handle(h.value, cfg, torch.cuda.current_device(), n.value)
+
+
+def mlpb_linear8_destroy(h: Linear8Handle):
+    if h is not None and h.ptr:
+        load_library().mlpb_linear8_destroy(h.ptr)
+        h.ptr = 0
+
+
+def mlpb_linear8_workspace_size(h: Linear8Handle) -> int:
+    return h.workspace_bytes
+
+
+def _linear8_rows(h, t, cols, name):
+    """(device, rows) of a call's first tensor [rows][cols]."""
+    dev = _cuda_index(t, name)
+    if dev != h.device:
+        raise ValueError(f"{name}: on cuda:{dev}, the handle on cuda:{h.device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [tokens][{cols}], got {tuple(t.shape)}")
+    return dev, t.shape[0]
+
+
+def _workspace(ws, need, dev):
+    if ws is None:
+        return None
+    p = _arg(ws, torch.uint8, ws.shape, "workspace", dev)
+    if ws.numel() < need:
+        raise ValueError(f"workspace: {ws.numel()} bytes, {need} are needed")
+    return p
+
+
+def _linear8_out(c):
+    return torch.float32 if c.flags & MLPB_LINEAR8_OUT_F32 else torch.bfloat16
+
+
+def mlpb_linear8_forward(h, X, Wq, Y, Xt=None, workspace=None, stream=None):
+    """Y = X W^T for the rows of X (include/mlpb.h); Wq, and Xt for the backward, are (codes,
+    scales) pairs."""
+    c = h.cfg
+    K, N = c.inputs, c.outputs
+    dev, T = _linear8_rows(h, X, K, "X")
+    args = [h.ptr, T, _arg(X, torch.bfloat16, (T, K), "X", dev), *_b128_args(Wq, N, K, "Wq", dev),
+            _arg(Y, _linear8_out(c), (T, N), "Y", dev), *_b128_args(Xt, K, T, "Xt", dev),
+            _workspace(workspace, h.workspace_bytes, dev)]
+    _call_on(dev, "mlpb_linear8_forward", args, stream)
+
+
+def mlpb_linear8_backward(h, dY, Wt, Xt, dX, dW, accumulate=False, workspace=None, stream=None):
+    """dX = dY W and dW (+)= dY^T X; either output may be None."""
+    c = h.cfg
+    K, N = c.inputs, c.outputs
+    dev, T = _linear8_rows(h, dY, N, "dY")
+    args = [h.ptr, T, _arg(dY, torch.bfloat16, (T, N), "dY", dev), *_b128_args(Wt, K, N, "Wt", dev),
+            *_b128_args(Xt, K, T, "Xt", dev), _arg(dX, _linear8_out(c), (T, K), "dX", dev),
+            _arg(dW, torch.float32, (N, K), "dW", dev), 1 if accumulate else 0,
+            _workspace(workspace, h.workspace_bytes, dev)]
+    _call_on(dev, "mlpb_linear8_backward", args, stream)
+
+
+def mlpb_linear8_last_device_error(h: Linear8Handle, stream=None) -> int:
+    """The status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
+    return _on_device(h.device, load_library().mlpb_linear8_last_device_error, [h.ptr], stream)
+
+
 def mlpb_last_device_error(h: Handle, stream=None) -> int:
     """Returns the status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
     return load_library().mlpb_last_device_error(h.ptr, _stream(stream))
@@ -875,3 +1024,83 @@ class MoEDecode:
                 weights = torch.empty((T, c.topk), dtype=torch.float32, device=self.device)
         mlpb_moe_forward(self.handle, X, Wr, W1, W2, Y, ids, weights, self.workspace, stream)
         return Y, ids, weights
+
+
+class Linear8:
+    """A linear layer y = x W^T on E4M3 operands with a scale for each block of 128, for up to
+    max_tokens rows.  load() lays the weight out (again after each update); forward() and
+    backward() as in include/mlpb.h.  Owns the weight's codes (with `training`, its transpose's
+    too), what a forward keeps of X for the backward, and the workspace."""
+
+    def __init__(self, max_tokens, inputs, outputs, training=True, out_dtype=torch.bfloat16,
+                 device="cuda", flags=0):
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"out_dtype: bfloat16 or float32, not {out_dtype}")
+        self.handle = None
+        self.cfg = mlpb_linear8_config(max_tokens, inputs, outputs, flags | (
+            MLPB_LINEAR8_OUT_F32 if out_dtype == torch.float32 else 0))
+        self.device, self.training, self.out_dtype = _device(device), training, out_dtype
+        with torch.cuda.device(self.device):
+            self.handle = mlpb_linear8_create(self.cfg)
+        self.workspace = torch.empty(self.handle.workspace_bytes, dtype=torch.uint8,
+                                     device=self.device)
+        self.Wq = b128_empty(outputs, inputs, self.device)
+        self.Wt = b128_empty(inputs, outputs, self.device) if training else None
+        self._saved = None
+        if training:  # one buffer for any number of tokens
+            ld, n = mlpb_b128_sizes(inputs, max_tokens)
+            self._saved = torch.empty(inputs * ld + n, dtype=torch.uint8, device=self.device)
+
+    def close(self):
+        mlpb_linear8_destroy(self.handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def load(self, W, stream=None):
+        """Quantizes the weight W [outputs][inputs] (bf16 or fp32) in blocks of 128 x 128."""
+        if tuple(W.shape) != (self.cfg.outputs, self.cfg.inputs):
+            raise ValueError(f"W: expected shape {(self.cfg.outputs, self.cfg.inputs)}, "
+                             f"got {tuple(W.shape)}")
+        mlpb_b128_quantize(W, self.Wq, self.Wt, True, stream)
+
+    def saved(self, tokens):
+        """The (codes, scales) of X^T that forward() writes for this many tokens."""
+        ld, n = mlpb_b128_sizes(self.cfg.inputs, tokens)
+        m = self.cfg.inputs * ld
+        return self._saved[:m].view(self.cfg.inputs, ld), self._saved[m:m + n]
+
+    def forward(self, X, Y=None, Xt=None, stream=None):
+        """Y [tokens][outputs].  With `training`, Xt (or this object) receives X^T for the
+        backward."""
+        T = X.shape[0]
+        if Y is None:
+            with _on(stream, self.device):
+                Y = torch.empty((T, self.cfg.outputs), dtype=self.out_dtype, device=self.device)
+        if Xt is None and self.training and T <= self.cfg.max_tokens:
+            Xt = self.saved(T)
+        mlpb_linear8_forward(self.handle, X, self.Wq, Y, Xt, self.workspace, stream)
+        return Y
+
+    def backward(self, dY, dX=None, dW=None, Xt=None, accumulate=False, input_grad=True,
+                 stream=None):
+        """(dX, dW) for the rows of the last forward, or for an Xt that a forward wrote; with
+        `accumulate` dW is added into; without `input_grad` dX is not computed."""
+        if not self.training:
+            raise ValueError("Linear8: made with training=False")
+        if accumulate and dW is None:
+            raise ValueError("dW: nothing given to add into")
+        T, c = dY.shape[0], self.cfg
+        with _on(stream, self.device):
+            if dX is None and input_grad:
+                dX = torch.empty((T, c.inputs), dtype=self.out_dtype, device=self.device)
+            if dW is None:
+                dW = torch.empty((c.outputs, c.inputs), dtype=torch.float32, device=self.device)
+        if Xt is None and T <= c.max_tokens:
+            Xt = self.saved(T)
+        mlpb_linear8_backward(self.handle, dY, self.Wt, Xt, dX, dW, accumulate, self.workspace,
+                              stream)
+        return dX, dW
