@@ -538,6 +538,59 @@ mlpb_status mlpb_linear8_backward(mlpb_linear8 *h, int64_t tokens, const void *d
 /* As mlpb_moe_last_device_error, for a linear layer's handle. */
 mlpb_status mlpb_linear8_last_device_error(mlpb_linear8 *h, mlpb_stream_t stream);
 
+/* Orthogonalised updates of weights, by Newton-Schulz products ("From Install to Your First
+ * Model" and the sharded optimizer's section of the source tour name the optimizer's step, which
+ * this library's weight gradients feed): for `batch` matrices [rows][cols] -- a weight's shards, as
+ * dW1, dW2 lie --
+ *     X_0 = U / |U|_F,  X <- a X + (b A + c A A) X, A = X X^T   (`steps` times),  O = X
+ * (X <- a X + X (b A + c A A), A = X^T X, with more rows than columns), and, in
+ * mlpb_muon_step,
+ *     M <- momentum M + G,   U = G + momentum M (nesterov) or M
+ *     W <- (1 - lr weight_decay) W - lr scale O
+ * A zero matrix stays zero; one with an infinity or a NaN becomes NaN, alone.
+ * Products take fp16 operands with fixed scales, sums and both products' diagonals are fp32, X
+ * keeps 22 bits between the steps: O is off by some 5e-4 of its size. */
+#define MLPB_MUON_FAULT_INJECT 0x1u /* test only, as MLPB_FLAG_FAULT_INJECT: the first product's \
+                                       first stage is never filled                              */
+
+typedef struct {
+  int64_t batch;      /* matrices, 1..65535                                                     */
+  int64_t rows, cols; /* of each, 1..65536                                                      */
+  int32_t steps;      /* 1..64                                                                  */
+  int32_t nesterov;   /* mlpb_muon_step: 1 U = G + momentum M, 0 U = M                           */
+  float coef[3];      /* a, b, c: singular values from [0, 1] have to stay below 2               */
+  float momentum;     /* [0, 1)                                                                 */
+  float weight_decay;
+  float scale;        /* of the update, such as 0.2 sqrt(max(rows, cols))                       */
+  uint32_t flags;     /* 0, or MLPB_MUON_FAULT_INJECT                                           */
+} mlpb_muon_config;
+
+typedef struct mlpb_muon mlpb_muon; /* opaque; owns a device word and no tensors */
+
+/* Validates *cfg and allocates the handle on the current device; EINVAL for null arguments or
+ * values out of range, EUNSUPPORTED for sizes and coefficients outside those above. */
+mlpb_status mlpb_muon_create(const mlpb_muon_config *cfg, mlpb_muon **out);
+void mlpb_muon_destroy(mlpb_muon *h);
+
+/* Bytes of the workspace of the calls below (three fp16 copies of X, two symmetric matrices of the
+ * smaller side). */
+mlpb_status mlpb_muon_workspace_size(const mlpb_muon *h, size_t *bytes);
+
+/* O [batch][rows][cols] bf16 from U, bf16 or (u_f32 = 1) fp32 (O may not overlap U).  16-byte
+ * aligned tensors.  The current device must be the handle's.  Calls that share a workspace must
+ * not overlap on the GPU (a captured graph counts as its call, and the handle has to outlive it). */
+mlpb_status mlpb_muon_orthogonalize(mlpb_muon *h, const void *U, int32_t u_f32, void *O,
+                                    void *workspace, mlpb_stream_t stream);
+
+/* One step: G, M, W [batch][rows][cols] fp32, M and W updated in place; Wb, unless NULL, receives
+ * the new W in bf16; lr one fp32 on the device (a captured graph then takes any schedule).  No two
+ * of the tensors overlap. */
+mlpb_status mlpb_muon_step(mlpb_muon *h, const float *G, float *M, float *W, void *Wb,
+                           const float *lr, void *workspace, mlpb_stream_t stream);
+
+/* As mlpb_moe_last_device_error, for an update's handle. */
+mlpb_status mlpb_muon_last_device_error(mlpb_muon *h, mlpb_stream_t stream);
+
 /* Static English text of a status code. */
 const char *mlpb_status_str(mlpb_status s);
 

@@ -2,4 +2,4 @@
 (libmlpb) and its thin ctypes binding."""
 from .mlpb import *  # noqa: F401,F403
 from .mlpb import (ActCheckpoint8, Join, Linear8, MLPBlock, MLPBError,  # noqa: F401
-                   MLPBranch, MoEDecode, load_library)
+                   MLPBranch, MoEDecode, Muon, load_library)

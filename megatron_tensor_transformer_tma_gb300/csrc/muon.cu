@@ -1,0 +1,311 @@
+// Orthogonalised updates of weights: handle, workspace, tensor maps, the launches of a call.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "../../include/mlpb.h"
+#include "common.cuh"
+#include "gemm_params.h"
+#include "muon.cuh"
+
+using namespace mlpb;
+
+struct mlpb_muon {
+  mlpb_muon_config cfg;
+  int device, max_clusters;
+  bool tall, fault_pending;
+  int n, ldx, ldn;
+  uint32_t* err;
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+};
+
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct Layout {
+  float4* part;
+  __half *x0, *x1, *xl, *e, *d;
+  float *diag, *beta;
+  size_t bytes;
+};
+
+Layout layout(const mlpb_muon* h, void* workspace) {
+  const mlpb_muon_config& c = h->cfg;
+  uint8_t* const base = static_cast<uint8_t*>(workspace);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base + at;
+    at += align256(bytes);
+    return p;
+  };
+  const size_t x = static_cast<size_t>(c.batch * c.rows) * h->ldx * 2;
+  const size_t s = static_cast<size_t>(c.batch) * h->n * h->ldn * 2;
+  const size_t v = static_cast<size_t>(c.batch) * h->ldn * 4;
+  Layout l;
+  l.part = reinterpret_cast<float4*>(
+      take(static_cast<size_t>(c.batch) * muon_partials(c.rows * c.cols, c.batch) * 16));
+  l.x0 = reinterpret_cast<__half*>(take(x));
+  l.x1 = reinterpret_cast<__half*>(take(x));
+  l.xl = reinterpret_cast<__half*>(take(x));
+  l.e = reinterpret_cast<__half*>(take(s));
+  l.d = reinterpret_cast<__half*>(take(s));
+  l.diag = reinterpret_cast<float*>(take(v));
+  l.beta = reinterpret_cast<float*>(take(v));
+  l.bytes = at;
+  return l;
+}
+
+bool encode(const mlpb_muon* h, CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
+                   const_cast<void*>(base), dims, strides, box, steps,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Matrices [batch][rows][ld] as operands whose K runs along a row: 128 rows by 64 columns.
+bool map_k(const mlpb_muon* h, CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+           uint64_t ld) {
+  const cuuint64_t dims[3] = {cols, rows, static_cast<cuuint64_t>(h->cfg.batch)};
+  const cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
+  const cuuint32_t box[3] = {kBK, kBM, 1};
+  return encode(h, m, base, 3, dims, strides, box);
+}
+
+// The same with K along a column: two 64-wide chunks of 64 rows.
+bool map_mn(const mlpb_muon* h, CUtensorMap* m, const void* base, uint64_t rows, uint64_t ld) {
+  const cuuint64_t dims[4] = {64, rows, ld / 64, static_cast<cuuint64_t>(h->cfg.batch)};
+  const cuuint64_t strides[3] = {ld * 2, 128, rows * ld * 2};
+  const cuuint32_t box[4] = {64, kBK, 2, 1};
+  return encode(h, m, base, 4, dims, strides, box);
+}
+
+bool map_x(const mlpb_muon* h, CUtensorMap* m, const void* base, bool mn) {
+  const mlpb_muon_config& c = h->cfg;
+  return mn ? map_mn(h, m, base, c.rows, h->ldx) : map_k(h, m, base, c.rows, c.cols, h->ldx);
+}
+
+// The steps, the last of them into what `p` names.
+mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* workspace,
+                    cudaStream_t s) {
+  const mlpb_muon_config& c = h->cfg;
+  const Layout l = layout(h, workspace);
+  CUtensorMap k[2], mn[2], e, d;
+  for (int i = 0; i < 2; ++i) {
+    __half* x = i == 0 ? l.x0 : l.x1;
+    if (!map_x(h, &k[i], x, false) || !map_x(h, &mn[i], x, true)) return MLPB_ECUDA;
+  }
+  if (!map_k(h, &e, l.e, h->n, h->n, h->ldn) || !map_k(h, &d, l.d, h->n, h->n, h->ldn))
+    return MLPB_ECUDA;
+  if (launch_muon_norm(in, l.part, s) != cudaSuccess ||
+      launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, s) != cudaSuccess)
+    return MLPB_ECUDA;
+  p.batch = static_cast<int>(c.batch);
+  p.rows = static_cast<int>(c.rows);
+  p.cols = static_cast<int>(c.cols);
+  p.n = h->n;
+  p.ldx = h->ldx;
+  p.ldn = h->ldn;
+  p.a = c.coef[0];
+  p.b = c.coef[1];
+  p.c = c.coef[2];
+  p.xl = l.xl;
+  p.e = l.e;
+  p.d = l.d;
+  p.diag = l.diag;
+  p.beta = l.beta;
+  p.err = h->err;
+  p.wait_ns = kDefaultWaitNs;
+  p.fault_inject = h->fault_pending ? 1 : 0;
+  h->fault_pending = false;
+  const int tiles = static_cast<int>(cdiv(h->n, 256));
+  for (int i = 0; i < c.steps; ++i) {
+    const int from = i & 1;
+    p.xh = from == 0 ? l.x0 : l.x1;
+    p.xh_out = from == 0 ? l.x1 : l.x0;
+    p.num_pm = p.num_n = tiles;
+    p.units = p.batch * (tiles * (tiles + 1) / 2);
+    p.num_kb = static_cast<int>(cdiv(h->tall ? c.rows : c.cols, kBK));
+    const CUtensorMap& x = h->tall ? mn[from] : k[from];
+    if (launch_ortho(OrthoOp::Gram, h->tall, x, x, p, std::min(p.units, h->max_clusters), s) !=
+        cudaSuccess)
+      return MLPB_ECUDA;
+    p.fault_inject = 0;
+    p.num_kb = static_cast<int>(cdiv(h->n, kBK));
+    if (launch_ortho(OrthoOp::Poly, h->tall, e, e, p, std::min(p.units, h->max_clusters), s) !=
+        cudaSuccess)
+      return MLPB_ECUDA;
+    p.num_pm = static_cast<int>(cdiv(c.rows, 256));
+    p.num_n = static_cast<int>(cdiv(c.cols, 256));
+    p.units = p.batch * p.num_pm * p.num_n;
+    if (launch_ortho(i == c.steps - 1 ? OrthoOp::Last : OrthoOp::Apply, h->tall,
+                     h->tall ? k[from] : d, h->tall ? d : mn[from], p,
+                     std::min(p.units, h->max_clusters), s) != cudaSuccess)
+      return MLPB_ECUDA;
+  }
+  return MLPB_OK;
+}
+
+// Whether singular values that start in [0, 1] stay below 2, where the fp16 formats' fixed scales
+// hold every operand (b A + c A A below 60).
+bool coefficients_fit(const mlpb_muon_config& c) {
+  for (int i = 0; i <= 4096; ++i) {
+    double s = i / 4096.0;
+    for (int k = 0; k < c.steps; ++k) {
+      const double q = s * s;
+      if (std::fabs(c.coef[1]) * q + std::fabs(c.coef[2]) * q * q > 60.0) return false;
+      s = std::fabs(s * (c.coef[0] + q * (c.coef[1] + c.coef[2] * q)));
+      if (!(s < 2.0)) return false;
+    }
+  }
+  return true;
+}
+
+mlpb_status on_device(const mlpb_muon* h) {
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return MLPB_ECUDA;
+  return device == h->device ? MLPB_OK : MLPB_EINVAL;
+}
+
+}  // namespace
+
+extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon** out) {
+  if (cfg == nullptr || out == nullptr) return MLPB_EINVAL;
+  *out = nullptr;
+  const mlpb_muon_config& c = *cfg;
+  if (c.batch < 1 || c.rows < 1 || c.cols < 1 || c.steps < 1 || (c.nesterov != 0 && c.nesterov != 1) ||
+      (c.flags & ~MLPB_MUON_FAULT_INJECT) != 0)
+    return MLPB_EINVAL;
+  for (float f : {c.coef[0], c.coef[1], c.coef[2], c.weight_decay, c.scale})
+    if (!std::isfinite(f)) return MLPB_EINVAL;
+  if (!(c.momentum >= 0.0f && c.momentum < 1.0f)) return MLPB_EINVAL;
+  if (c.batch > 65535 || c.rows > 65536 || c.cols > 65536 || c.steps > 64 ||
+      c.batch * cdiv(c.rows, 256) * cdiv(c.cols, 256) > (int64_t{1} << 30) || !coefficients_fit(c))
+    return MLPB_EUNSUPPORTED;
+  mlpb_muon* h = new (std::nothrow) mlpb_muon();
+  if (h == nullptr) return MLPB_ENOMEM;
+  h->cfg = c;
+  h->tall = c.rows > c.cols;
+  h->n = static_cast<int>(std::min(c.rows, c.cols));
+  h->ldx = static_cast<int>(cdiv(c.cols, kOrthoLd)) * kOrthoLd;
+  h->ldn = static_cast<int>(cdiv(h->n, kOrthoLd)) * kOrthoLd;
+  h->fault_pending = (c.flags & MLPB_MUON_FAULT_INJECT) != 0;
+  h->err = nullptr;
+  int major = 0, minor = 0;
+  if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, h->device) != cudaSuccess) {
+    delete h;
+    return MLPB_ECUDA;
+  }
+  if (major != 10 || minor != 3) {
+    delete h;
+    return MLPB_EUNSUPPORTED;
+  }
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found{};
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess || fn == nullptr) {
+    delete h;
+    return MLPB_ECUDA;
+  }
+  h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  if (ortho_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
+      cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||
+      cudaMemset(h->err, 0, sizeof(uint32_t)) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come
+    if (h->err) cudaFree(h->err);
+    delete h;
+    return MLPB_ECUDA;
+  }
+  *out = h;
+  return MLPB_OK;
+}
+
+extern "C" void mlpb_muon_destroy(mlpb_muon* h) {
+  if (h == nullptr) return;
+  if (h->err) cudaFree(h->err);
+  delete h;
+}
+
+extern "C" mlpb_status mlpb_muon_workspace_size(const mlpb_muon* h, size_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MLPB_EINVAL;
+  *bytes = layout(h, nullptr).bytes;
+  return MLPB_OK;
+}
+
+extern "C" mlpb_status mlpb_muon_orthogonalize(mlpb_muon* h, const void* U, int32_t u_f32, void* O,
+                                               void* workspace, mlpb_stream_t stream) {
+  if (h == nullptr || !U || !O || !workspace || (u_f32 != 0 && u_f32 != 1)) return MLPB_EINVAL;
+  for (const void* q : {U, static_cast<const void*>(O), static_cast<const void*>(workspace)})
+    if (!aligned16(q)) return MLPB_EINVAL;
+  const mlpb_status st = on_device(h);
+  if (st != MLPB_OK) return st;
+  MuonInput in{};
+  in.g = U;
+  in.g_f32 = u_f32;
+  in.batch = h->cfg.batch;
+  in.rows = h->cfg.rows;
+  in.cols = h->cfg.cols;
+  OrthoParams p{};
+  p.out = static_cast<__nv_bfloat16*>(O);
+  return iterate(h, in, p, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mlpb_status mlpb_muon_step(mlpb_muon* h, const float* G, float* M, float* W, void* Wb,
+                                      const float* lr, void* workspace, mlpb_stream_t stream) {
+  if (h == nullptr || !G || !M || !W || !lr || !workspace) return MLPB_EINVAL;
+  for (const void* q : {static_cast<const void*>(G), static_cast<const void*>(M),
+                        static_cast<const void*>(W), static_cast<const void*>(Wb),
+                        static_cast<const void*>(workspace)})
+    if (!aligned16(q)) return MLPB_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(lr) & 3u) != 0) return MLPB_EINVAL;
+  const mlpb_status st = on_device(h);
+  if (st != MLPB_OK) return st;
+  const mlpb_muon_config& c = h->cfg;
+  MuonInput in{};
+  in.g = G;
+  in.m = M;
+  in.g_f32 = 1;
+  in.nesterov = c.nesterov;
+  in.momentum = c.momentum;
+  in.batch = c.batch;
+  in.rows = c.rows;
+  in.cols = c.cols;
+  OrthoParams p{};
+  p.w = W;
+  p.wb = static_cast<__nv_bfloat16*>(Wb);
+  p.lr = lr;
+  p.decay = c.weight_decay;
+  p.scale = c.scale;
+  return iterate(h, in, p, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mlpb_status mlpb_muon_last_device_error(mlpb_muon* h, mlpb_stream_t stream) {
+  if (h == nullptr) return MLPB_EINVAL;
+  const mlpb_status st = on_device(h);  // `stream` would not be one of the handle's
+  if (st != MLPB_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  if (cudaMemcpyAsync(&v, h->err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MLPB_ECUDA;
+  if (v == 0) return MLPB_OK;
+  if (cudaMemsetAsync(h->err, 0, sizeof(uint32_t), s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MLPB_ECUDA;
+  return MLPB_ETIMEOUT;
+}

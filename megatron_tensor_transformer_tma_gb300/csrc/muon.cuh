@@ -1,0 +1,85 @@
+// Newton-Schulz orthogonalisation on the tensor cores: number formats, launch parameters.
+//
+// X <- a X + (b A + c A A) X with A = X X^T (or X <- a X + X (b A + c A A), A = X^T X, when X has
+// more rows than columns).  With n the smaller side, two of the three products are symmetric
+// n x n matrices, of which only the tiles on and below the diagonal are computed.
+//
+// Operands are fp16, which has eight times bf16's precision at the same rate; values have fixed
+// scales, since singular values stay below 2 (the host checks the coefficients).  What would cost
+// precision is kept out of the products:
+//   - X is hi + lo, two fp16 parts (22 bits); the product takes hi, a X both.
+//   - The diagonal d of A is fp32 and its part E off the diagonal fp16:
+//       A A = E E + (d_i + d_j) E_ij + delta_ij d_i^2,
+//     so the identity that A comes near is not rounded.  Likewise b A + c A A + a I = D + diag(beta)
+//     and X' = beta X + D X: a X and most of (b A + c A A) X cancel (3.4 - 2.7 near the end), and
+//     do so in fp32.
+// Against 64 bits the result is off by 3e-4 to 7e-4 of its size (Gaussian, low-rank and decaying
+// spectra); with the diagonals in the products it is 1e-3 to 3e-3, with bf16 operands 1e-2 to
+// 2e-2.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace mlpb {
+
+constexpr float kXScale = 4096.0f;    // X, E are stored times 2^12
+constexpr float kXInv = 1.0f / 4096.0f;
+constexpr float kDScale = 1024.0f;    // D times 2^10
+constexpr float kEEInv = kXInv * kXInv;            // a product's scale: 2^-24
+constexpr float kDXInv = kXInv / kDScale;          // 2^-22
+constexpr int kOrthoLd = 64;  // rows of X, E and D are padded to multiples of 64 (X's with zeros)
+
+enum class OrthoOp : int {
+  Gram = 0,  // E, d from X
+  Poly,      // D, beta from E, d
+  Apply,     // X' from D, beta, X
+  Last,      // as Apply, into the result
+};
+
+struct OrthoParams {
+  int batch, rows, cols, n;  // n = min(rows, cols)
+  int ldx, ldn;              // elements of a row of X; of E and D
+  int num_pm, num_n;         // 256-row and 256-column tiles of a matrix
+  int units;                 // tiles of all matrices (on and below the diagonal for Gram, Poly)
+  int num_kb;                // 64-deep k-blocks
+  float a, b, c;
+  const __half* xh;  // Apply: X
+  __half* xh_out;    // Apply: X'
+  __half* xl;        // the low parts, rewritten in place
+  __half* e;
+  __half* d;
+  float* diag;  // d [batch][ldn]
+  float* beta;  // [batch][ldn]
+  // Last: O bf16, or the weight's update W <- (1 - lr wd) W - lr scale O
+  __nv_bfloat16* out;
+  float* w;
+  __nv_bfloat16* wb;  // a bf16 copy of the updated W, or NULL
+  const float* lr;
+  float decay, scale;
+  uint32_t* err;
+  uint64_t wait_ns;
+  int fault_inject;
+};
+
+cudaError_t ortho_set_attrs(int* max_clusters);
+cudaError_t launch_ortho(OrthoOp op, bool tall, const CUtensorMap& a, const CUtensorMap& b,
+                         const OrthoParams& p, int clusters, cudaStream_t s);
+
+// muon_prepare.cu.  U = G + momentum M' with M' = momentum M + G (nesterov), or M', or (M NULL) G
+// itself; X = U / |U| in two fp16 parts.
+struct MuonInput {
+  const void* g;  // fp32, or bf16 (M NULL)
+  float* m;
+  int g_f32, nesterov;
+  float momentum;
+  int64_t batch, rows, cols;
+};
+int muon_partials(int64_t elems, int64_t batch);
+cudaError_t launch_muon_norm(const MuonInput& in, float4* part, cudaStream_t s);
+cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* xh, __half* xh_other,
+                              __half* xl, int ldx, cudaStream_t s);
+
+}  // namespace mlpb

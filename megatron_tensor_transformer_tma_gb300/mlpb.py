@@ -44,6 +44,7 @@ MLPB_JOIN_ACCUMULATE_GRADS = 0x4
 MLPB_MOE_FAULT_INJECT = 0x2
 MLPB_LINEAR8_OUT_F32 = 0x1
 MLPB_LINEAR8_FAULT_INJECT = 0x2
+MLPB_MUON_FAULT_INJECT = 0x1
 ACT8_BLOCK = 32  # features that share a scale byte of an 8-bit activation checkpoint
 
 # Every symbol include/mlpb.h declares.
@@ -59,6 +60,8 @@ EXPORTED = (
     "mlpb_b128_sizes", "mlpb_b128_quantize",
     "mlpb_linear8_create", "mlpb_linear8_destroy", "mlpb_linear8_workspace_size",
     "mlpb_linear8_forward", "mlpb_linear8_backward", "mlpb_linear8_last_device_error",
+    "mlpb_muon_create", "mlpb_muon_destroy", "mlpb_muon_workspace_size",
+    "mlpb_muon_orthogonalize", "mlpb_muon_step", "mlpb_muon_last_device_error",
 )
 
 
@@ -86,6 +89,14 @@ class mlpb_moe_config(ctypes.Structure):
 class mlpb_linear8_config(ctypes.Structure):
     _fields_ = [("max_tokens", ctypes.c_int64), ("inputs", ctypes.c_int64),
                 ("outputs", ctypes.c_int64), ("flags", ctypes.c_uint32)]
+
+
+class mlpb_muon_config(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
+                ("coef", ctypes.c_float * 3), ("momentum", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
 
 
 class mlpb_kernel_time(ctypes.Structure):
@@ -151,6 +162,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mlpb_linear8_forward": (I, [H, I64] + [P] * 8),
         "mlpb_linear8_backward": (I, [H, I64] + [P] * 7 + [I32, P, P]),
         "mlpb_linear8_last_device_error": (I, [H, P]),
+        "mlpb_muon_create": (I, [ctypes.POINTER(mlpb_muon_config), ctypes.POINTER(H)]),
+        "mlpb_muon_destroy": (None, [H]),
+        "mlpb_muon_workspace_size": (I, [H, ctypes.POINTER(Z)]),
+        "mlpb_muon_orthogonalize": (I, [H, P, I32, P, P, P]),
+        "mlpb_muon_step": (I, [H] + [P] * 7),
+        "mlpb_muon_last_device_error": (I, [H, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -764,6 +781,79 @@ def mlpb_linear8_last_device_error(h: Linear8Handle, stream=None) -> int:
     return _on_device(h.device, load_library().mlpb_linear8_last_device_error, [h.ptr], stream)
 
 
+@dataclasses.dataclass
+class MuonHandle:
+    ptr: int
+    cfg: mlpb_muon_config
+    device: int  # CUDA device number it was created on
+    workspace_bytes: int
+
+
+def make_muon_config(rows, cols, batch=1, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
+                     momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0,
+                     flags=0) -> mlpb_muon_config:
+    return mlpb_muon_config(batch, rows, cols, steps, 1 if nesterov else 0,
+                            (ctypes.c_float * 3)(*coefficients), momentum, weight_decay, scale,
+                            flags)
+
+
+def mlpb_muon_create(cfg: mlpb_muon_config) -> MuonHandle:
+    """An orthogonalised update's handle on the current CUDA device."""
+    lib, h, n = load_library(), ctypes.c_void_p(), ctypes.c_size_t()
+    _check(lib.mlpb_muon_create(ctypes.byref(cfg), ctypes.byref(h)), "mlpb_muon_create")
+    _check(lib.mlpb_muon_workspace_size(h.value, ctypes.byref(n)), "mlpb_muon_workspace_size")
+    return MuonHandle(h.value, cfg, torch.cuda.current_device(), n.value)
+
+
+def mlpb_muon_destroy(h: MuonHandle):
+    if h is not None and h.ptr:
+        load_library().mlpb_muon_destroy(h.ptr)
+        h.ptr = 0
+
+
+def mlpb_muon_workspace_size(h: MuonHandle) -> int:
+    return h.workspace_bytes
+
+
+def _muon_shape(h, t, name):
+    """(device, shape) of a call's tensors: [rows][cols] matrices in any number of leading
+    dimensions that make up the batch."""
+    dev, c = _cuda_index(t, name), h.cfg
+    if dev != h.device:
+        raise ValueError(f"{name}: on cuda:{dev}, the handle on cuda:{h.device}")
+    if t.dim() < 2 or tuple(t.shape[-2:]) != (c.rows, c.cols) \
+            or t.numel() != c.batch * c.rows * c.cols:
+        raise ValueError(f"{name}: expected {c.batch} matrices of shape {(c.rows, c.cols)}, "
+                         f"got {tuple(t.shape)}")
+    return dev, t.shape
+
+
+def mlpb_muon_orthogonalize(h, U, O, workspace, stream=None):
+    """O (bf16) from U (bf16 or fp32), both [..., rows, cols] (include/mlpb.h)."""
+    dev, shape = _muon_shape(h, U, "U")
+    if U.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"U: expected bfloat16 or float32, got {U.dtype}")
+    args = [h.ptr, _arg(U, U.dtype, shape, "U", dev), 1 if U.dtype == torch.float32 else 0,
+            _arg(O, torch.bfloat16, shape, "O", dev), _workspace(workspace, h.workspace_bytes, dev)]
+    _call_on(dev, "mlpb_muon_orthogonalize", args, stream)
+
+
+def mlpb_muon_step(h, G, M, W, lr, workspace, Wb=None, stream=None):
+    """The momentum M and the weight W (fp32, in place) for the gradient G, and W in bf16 unless Wb
+    is None; lr a CUDA tensor of one fp32."""
+    dev, shape = _muon_shape(h, W, "W")
+    f32 = torch.float32
+    args = [h.ptr, _arg(G, f32, shape, "G", dev), _arg(M, f32, shape, "M", dev),
+            _arg(W, f32, shape, "W", dev), _arg(Wb, torch.bfloat16, shape, "Wb", dev),
+            _arg(lr, f32, (1,), "lr", dev), _workspace(workspace, h.workspace_bytes, dev)]
+    _call_on(dev, "mlpb_muon_step", args, stream)
+
+
+def mlpb_muon_last_device_error(h: MuonHandle, stream=None) -> int:
+    """The status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
+    return _on_device(h.device, load_library().mlpb_muon_last_device_error, [h.ptr], stream)
+
+
 def mlpb_last_device_error(h: Handle, stream=None) -> int:
     """Returns the status code (MLPB_OK, MLPB_ETIMEOUT, MLPB_ECUDA) without raising."""
     return load_library().mlpb_last_device_error(h.ptr, _stream(stream))
@@ -1104,3 +1194,43 @@ class Linear8:
         mlpb_linear8_backward(self.handle, dY, self.Wt, Xt, dX, dW, accumulate, self.workspace,
                               stream)
         return dX, dW
+
+
+class Muon:
+    """The orthogonalised update of `batch` matrices [rows][cols], such as the shards of a weight
+    (dW1 [t][2][Fs][H] is 2 t matrices): orthogonalize() alone, or step() with momentum, decay and
+    the weight's update.  Owns a handle and its workspace."""
+
+    def __init__(self, rows, cols, batch=1, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
+                 momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0, device="cuda",
+                 flags=0):
+        self.handle = None
+        self.cfg = make_muon_config(rows, cols, batch, steps, coefficients, momentum, nesterov,
+                                    weight_decay, scale, flags)
+        self.device = _device(device)
+        with torch.cuda.device(self.device):
+            self.handle = mlpb_muon_create(self.cfg)
+        self.workspace = torch.empty(self.handle.workspace_bytes, dtype=torch.uint8,
+                                     device=self.device)
+
+    def close(self):
+        mlpb_muon_destroy(self.handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def orthogonalize(self, U, O=None, stream=None):
+        """O, bf16 in the shape of U (bf16 or fp32)."""
+        if O is None:
+            with _on(stream, self.device):
+                O = torch.empty(U.shape, dtype=torch.bfloat16, device=self.device)
+        mlpb_muon_orthogonalize(self.handle, U, O, self.workspace, stream)
+        return O
+
+    def step(self, W, M, G, lr, Wb=None, stream=None):
+        """Updates the momentum M and the weight W (fp32) in place for the gradient G; Wb, if
+        given, receives W in bf16.  lr: a CUDA tensor of one fp32."""
+        mlpb_muon_step(self.handle, G, M, W, lr, self.workspace, Wb, stream)
