@@ -1,14 +1,20 @@
 // The products of a Newton-Schulz step (muon.cuh) on the tensor cores, for a batch of matrices.
 //
-// The pipeline is that of gemm.cuh (pairs of CTAs, 256 x 256 tiles, a 7-stage TMA ring, two
-// accumulators in tensor memory, bounded waits), on fp16 operands.  The symmetric products (Gram,
-// Poly) compute the tiles on and below the diagonal and write those below it twice, the second
-// time transposed: a warp's 32 rows are 32 consecutive elements of each mirrored row.
+// The pipeline is that of gemm.cuh (pairs of CTAs, 256 x 256 tiles, a TMA ring, two accumulators
+// in tensor memory, bounded waits), on fp16 operands.  The symmetric products (Gram, Poly) compute
+// the tiles on and below the diagonal and write those below it twice, the second time transposed.
 //   wide (rows <= cols)   Gram  A, B = X        K-major   K = cols
 //                         Apply A = D K-major, B = X MN-major, K = rows; beta by row
 //   tall                  Gram  A, B = X        MN-major  K = rows
 //                         Apply A = X, B = D    K-major   K = cols; beta by column
 //   Poly                  A, B = E              K-major   K = n
+//
+// An element of X' takes 8 bytes in and out beside 2 n operations, as much of the memory's time as
+// of the tensor cores' at n = 1376, so the epilogue's tiles go through shared memory by TMA: each
+// epilogue warp has two slots for 32 rows by 64 columns, computes in place, stores the box, and
+// loads the box after next when the store has read it.  (Rows read and written by their threads,
+// 16 bytes a lane, took 540 us for 16 matrices of 1376 x 4096, four times the product: every
+// access touches 32 lines.)  The ring has 5 stages for that, 4 where W's fp32 boxes come too.
 #include <algorithm>
 
 #include "gemm.cuh"
@@ -69,195 +75,380 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-__device__ __forceinline__ void load_half32(const __half* p, float (&v)[32]) {
+// Eight values of a 16-byte piece.
+__device__ __forceinline__ void unpack_half8(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p + 8 * q));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_half2(w[e]);
-      v[8 * q + 2 * e] = f.x;
-      v[8 * q + 2 * e + 1] = f.y;
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack_half2(w[e]);
+    v[2 * e] = f.x;
+    v[2 * e + 1] = f.y;
   }
 }
 
-__device__ __forceinline__ void store_half32(__half* p, const float (&v)[32]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    st_global_v4(p + 8 * q,
-                 make_uint4(pack_half2(v[8 * q], v[8 * q + 1]),
-                            pack_half2(v[8 * q + 2], v[8 * q + 3]),
-                            pack_half2(v[8 * q + 4], v[8 * q + 5]),
-                            pack_half2(v[8 * q + 6], v[8 * q + 7])));
+__device__ __forceinline__ uint4 pack_half8(const float (&v)[8]) {
+  return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]),
+                    pack_half2(v[6], v[7]));
 }
 
-// v[e] of a row's 32 columns from `col` on, without its diagonal element, which is returned (0
-// where the chunk has none).
-__device__ __forceinline__ float take_diagonal(float (&v)[32], int m, int col) {
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ void sts2(uint32_t a, __half h) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__half_as_ushort(h)) : "memory");
+}
+
+constexpr int kEpiRows = 32, kEpiCols = 64;
+constexpr int kEpiBox = kEpiRows * kEpiCols * 2;  // 4 KB: rows of 128 bytes, 128-byte swizzle
+
+template <OrthoOp Op>
+struct OrthoSmem {
+  static constexpr int stages = Op == OrthoOp::Last ? 4 : 5;
+  // a slot: the first box, and a second one (low part, mirrored box) or W's two
+  static constexpr int slot = Op == OrthoOp::Last ? 3 * kEpiBox : 2 * kEpiBox;
+  static constexpr int epi = 4 * 2 * slot;
+  static constexpr int bytes = stages * kPairStageBytes + epi + 1024 + 512;
+  static_assert(bytes <= 232448, "shared memory of a CTA");
+  static constexpr bool loads = Op != OrthoOp::Gram;
+};
+
+// Address of the 16-byte piece j of a box's row.
+__device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int j) {
+  return box + row * 128 + ((j ^ (row & 7)) << 4);
+}
+
+// A warp's boxes in order: columns of 64 of a tile, tile after tile.
+template <OrthoOp Op>
+struct BoxWalk {
+  int u, sub, subs;
+  OrthoTile t;
+  __device__ __forceinline__ void enter(const OrthoParams& p) {
+    if (u >= p.units) return;
+    t = ortho_tile<Op>(u, p);
+    const int width = (Op == OrthoOp::Gram || Op == OrthoOp::Poly) ? p.n : p.cols;
+    subs = min(kBN / kEpiCols, (width - t.nt * kBN + kEpiCols - 1) / kEpiCols);
+    sub = 0;
+  }
+  __device__ __forceinline__ void next(const OrthoParams& p, int step) {
+    if (++sub == subs) {
+      u += step;
+      enter(p);
+    }
+  }
+};
+
+// Loads a box's inputs into its slot; one lane.
+template <OrthoOp Op>
+__device__ __forceinline__ void load_box(const BoxWalk<Op>& w, int row0, uint32_t slot,
+                                         uint32_t bar, const OrthoMaps& m, const OrthoParams& p) {
+  const int col = w.t.nt * kBN + w.sub * kEpiCols;
+  const bool second =
+      Op == OrthoOp::Apply || (Op == OrthoOp::Last && p.w != nullptr && !p.ragged);
+  constexpr int more = Op == OrthoOp::Last ? 2 : 1;
+  mbar_arrive_expect_tx(bar, kEpiBox * (second ? 1 + more : 1));
+  tma_load_3d(slot, &m.in0, bar, col, row0, w.t.b);
+  if (second) {
+    tma_load_3d(slot + kEpiBox, &m.in1, bar, col, row0, w.t.b);
+    if (Op == OrthoOp::Last)
+      tma_load_3d(slot + 2 * kEpiBox, &m.in1, bar, col + 32, row0, w.t.b);
+  }
+}
+
+// A box of a symmetric product: rows m of the thread, 64 columns; the diagonal's element apart.
+template <OrthoOp Op>
+__device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slot, int lane, int m,
+                                              int col, const OrthoTile& t, float dm,
+                                              const OrthoParams& p) {
+  if constexpr (Op == OrthoOp::Gram) {
+#pragma unroll
+    for (int e = 0; e < kEpiCols; ++e) v[e] *= kXInv;  // A times 2^12
+  }
   float d = 0.0f;
+  if (t.mp == t.nt) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (col + e == m) {
-      d = v[e];
-      v[e] = 0.0f;
+    for (int e = 0; e < kEpiCols; ++e)
+      if (col + e == m) {
+        d = v[e];
+        v[e] = 0.0f;
+      }
+    if (m >= col && m < col + kEpiCols && m < p.n) {
+      const size_t at = static_cast<size_t>(t.b) * p.ldn + m;
+      if constexpr (Op == OrthoOp::Gram)
+        p.diag[at] = d * kXInv;
+      else
+        p.beta[at] = p.a + dm * fmaf(p.c, dm, p.b) + p.c * (d * kEEInv);
     }
-  return d;
-}
-
-// A symmetric matrix's chunk: row m, columns [col, col + 32), and below the diagonal tiles the
-// mirrored column.  Rows have 32 elements from `col` on: they are padded to multiples of 64.
-__device__ __forceinline__ void store_symmetric(__half* S, int m, int col, int n, int ld,
-                                                bool mirror, const float (&v)[32]) {
-  if (m >= n) return;
-  store_half32(S + static_cast<size_t>(m) * ld + col, v);
-  if (mirror) {
+  }
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (col + e < n) S[static_cast<size_t>(col + e) * ld + m] = __float2half_rn(v[e]);
+  for (int j = 0; j < 8; ++j) {
+    float r[8];
+    const uint32_t at = box_piece(slot, lane, j);
+    if constexpr (Op == OrthoOp::Poly) {
+      float e16[8];
+      unpack_half8(lds16(at), e16);
+      // rows of 64 elements: inside the buffer, though not all are of the matrix
+      const float* dj = p.diag + static_cast<size_t>(t.b) * p.ldn + col + 8 * j;
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(dj)),
+                   y = __ldcg(reinterpret_cast<const float4*>(dj + 4));
+      const float dd[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float lin = fmaf(p.c, dm + dd[i], p.b) * (kXInv * kDScale);
+        r[i] = fmaf(lin, e16[i], (p.c * (kEEInv * kDScale)) * v[8 * j + i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = v[8 * j + i];
+    }
+    sts16(at, pack_half8(r));
+    if (t.mp != t.nt) {  // its column, 32 consecutive elements of a row across the warp
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sts2(slot + kEpiBox + (8 * j + i) * 64 + lane * 2, __float2half_rn(r[i]));
+    }
   }
 }
 
+// A box of X' or of the result.
 template <OrthoOp Op, bool kTall>
-__device__ __forceinline__ void ortho_epilogue(uint32_t tacc, int row, int rank, const OrthoTile& t,
+__device__ __forceinline__ void apply_box(const float (&v)[kEpiCols], uint32_t slot, int lane,
+                                          int col, const OrthoTile& t, float bm, float keep,
+                                          float step, const OrthoParams& p) {
+  const float* beta = p.beta + static_cast<size_t>(t.b) * p.ldn + col;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t at = box_piece(slot, lane, j);
+    float x[8], b[8], r[8];
+    unpack_half8(lds16(at), x);
+    if constexpr (Op == OrthoOp::Apply) {
+      float lo[8];
+      unpack_half8(lds16(at + kEpiBox), lo);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += lo[i];
+    }
+    if constexpr (kTall) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(beta + 8 * j)),
+                   z = __ldcg(reinterpret_cast<const float4*>(beta + 8 * j + 4));
+      const float q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = q[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = bm;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = fmaf(b[i], x[i], v[8 * j + i] * (1.0f / kDScale));
+    if constexpr (Op == OrthoOp::Apply) {  // X' times 2^12, in two parts
+      sts16(at, pack_half8(r));
+      if (p.low_out) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] -= __half2float(__float2half_rn(r[i]));
+        sts16(at + kEpiBox, pack_half8(r));
+      }
+    } else {
+      // W's pieces: four columns each, columns 32 on in the second box
+      const uint32_t w0 = box_piece(slot + kEpiBox * (1 + j / 4), lane, (2 * j) & 7);
+      const uint32_t w1 = box_piece(slot + kEpiBox * (1 + j / 4), lane, (2 * j + 1) & 7);
+      if (p.w == nullptr || p.ragged) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] *= kXInv;
+      } else {
+        const uint4 y = lds16(w0), z = lds16(w1);
+        const uint32_t q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = fmaf(-step, r[i], keep * __uint_as_float(q[i]));
+      }
+      if (p.w != nullptr || p.ragged) {
+        sts16(w0, make_uint4(__float_as_uint(r[0]), __float_as_uint(r[1]), __float_as_uint(r[2]),
+                             __float_as_uint(r[3])));
+        sts16(w1, make_uint4(__float_as_uint(r[4]), __float_as_uint(r[5]), __float_as_uint(r[6]),
+                             __float_as_uint(r[7])));
+      }
+      if (!p.ragged && (p.w == nullptr || p.wb != nullptr))
+        sts16(at, make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]),
+                             pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7])));
+    }
+  }
+}
+
+// The result's box where rows are no multiple of 16 bytes: from W's boxes row by row.
+__device__ __forceinline__ void ragged_rows(uint32_t slot, int lane, int row0, int col,
+                                            const OrthoTile& t, float keep, float step,
+                                            const OrthoParams& p) {
+  for (int r = 0; r < kEpiRows && row0 + r < p.rows; ++r) {
+    const size_t o = (static_cast<size_t>(t.b) * p.rows + row0 + r) * p.cols + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = lane + 32 * h;
+      if (col + c >= p.cols) continue;
+      float v;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(v)
+                   : "r"(box_piece(slot + kEpiBox * (1 + h), r, lane >> 2) + (lane & 3) * 4));
+      if (p.w == nullptr) {
+        p.out[o + c] = __float2bfloat16_rn(v);
+      } else {
+        const float w = fmaf(-step * 4096.0f, v, keep * p.w[o + c]);
+        p.w[o + c] = w;
+        if (p.wb != nullptr) p.wb[o + c] = __float2bfloat16_rn(w);
+      }
+    }
+  }
+}
+
+// One epilogue warp: the 32 accumulator rows of its lane quarter, box by box.
+template <OrthoOp Op, bool kTall>
+__device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tfull0,
+                                               uint32_t tempty0, uint32_t tempty_lead,
+                                               uint32_t boxes, uint32_t box_bar, int quarter,
+                                               int lane, int rank, int cid, int nclusters,
+                                               const WaitCtx& wc, const OrthoMaps& maps,
                                                const OrthoParams& p) {
-  const int m = (t.mp * 2 + rank) * kBM + row;
-  const int n0 = t.nt * kBN;
-  if constexpr (Op == OrthoOp::Gram || Op == OrthoOp::Poly) {
-    const size_t at = static_cast<size_t>(t.b) * p.n * p.ldn;
-    const float* diag = p.diag + static_cast<size_t>(t.b) * p.ldn;
-    float dm = 0.0f;
-    if (Op == OrthoOp::Poly && m < p.n) dm = __ldg(diag + m);
+  using Sm = OrthoSmem<Op>;
+  const int row = (rank * kBM) + quarter * 32;  // of a tile's 256
+  float keep = 0.0f, step = 0.0f;
+  if (Op == OrthoOp::Last && p.w != nullptr) {
+    const float lr = __ldg(p.lr);
+    keep = 1.0f - lr * p.decay;
+    step = lr * p.scale * kXInv;
+  }
+  BoxWalk<Op> at, ahead;
+  at.u = ahead.u = cid;
+  at.enter(p);
+  ahead.enter(p);
+  int issued = 0;
+  if constexpr (Sm::loads) {
+    if (lane == 0)
+      for (; issued < 2 && ahead.u < p.units; ++issued, ahead.next(p, nclusters))
+        load_box<Op>(ahead, ahead.t.mp * 256 + row, boxes + issued * Sm::slot,
+                     box_bar + 8 * issued, maps, p);
+  }
+  int it = 0, q = 0;
+  bool good = true;
+  while (good && at.u < p.units) {
+    const int buf = it & 1;
+    int ok = 1;
+    if (lane == 0)
+      ok = wait_bounded(tfull0 + 8 * buf, (it >> 1) & 1, wc, kSiteEpiAccFull) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+    __syncwarp();
+    tc_fence_after();
+    const OrthoTile t = at.t;
+    const int subs = at.subs;
+    const int row0 = t.mp * 256 + row, m = row0 + lane;
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kBN;
+    float dm = 0.0f;  // the row's d or beta
+    if (Op == OrthoOp::Poly && m < p.n)
+      dm = __ldcg(p.diag + static_cast<size_t>(t.b) * p.ldn + m);
+    if ((Op == OrthoOp::Apply || Op == OrthoOp::Last) && !kTall && m < p.rows)
+      dm = __ldcg(p.beta + static_cast<size_t>(t.b) * p.ldn + m);
 #pragma unroll 1
-    for (int c = 0; c < kBN / 32; ++c) {
-      const int col = n0 + c * 32;
-      if (col >= p.n) break;
-      __syncwarp();  // rows past the end and the diagonal's lanes went ways of their own
-      float v[32];
-      tmem_load_f32x32(tacc + c * 32, v);
-      const bool on = t.mp == t.nt && m >= col && m < col + 32;
-      if constexpr (Op == OrthoOp::Gram) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] *= kXInv;  // A times 2^12
-        if (on) {
-          const float d = take_diagonal(v, m, col);
-          if (m < p.n) p.diag[static_cast<size_t>(t.b) * p.ldn + m] = d * kXInv;
+    for (int sub = 0; sub < subs; ++sub, ++q) {
+      const int col = t.nt * kBN + sub * kEpiCols;
+      const uint32_t slot = boxes + (q & 1) * Sm::slot;
+      if constexpr (Sm::loads) {
+        if (lane == 0)
+          ok = wait_bounded(box_bar + 8 * (q & 1), (q >> 1) & 1, wc, kSiteEpiAccFull) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          good = false;
+          break;
         }
-        store_symmetric(p.e + at, m, col, p.n, p.ldn, t.mp != t.nt, v);
+        if (lane == 0) --issued;
       } else {
-        if (on) {
-          const float d = take_diagonal(v, m, col);
-          if (m < p.n)
-            p.beta[static_cast<size_t>(t.b) * p.ldn + m] =
-                p.a + dm * fmaf(p.c, dm, p.b) + p.c * (d * kEEInv);
+        if (lane == 0) bulk_wait_read<1>();  // the slot's last store
+      }
+      __syncwarp();
+      float v[kEpiCols];
+      {
+        uint32_t r0[32], r1[32];
+        tmem_ld_32x32b_x32(tacc + sub * kEpiCols, r0);
+        tmem_ld_32x32b_x32(tacc + sub * kEpiCols + 32, r1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = __uint_as_float(r0[e]);
+          v[32 + e] = __uint_as_float(r1[e]);
         }
-        if (m < p.n) {
-          float e16[32];
-          load_half32(p.e + at + static_cast<size_t>(m) * p.ldn + col, e16);
-          const float* dj = diag + col;  // 16-byte aligned: rows of 64
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 d4 = __ldg(reinterpret_cast<const float4*>(dj + 4 * q));
-            const float d[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 4 * q + i;
-              const float lin = fmaf(p.c, dm + d[i], p.b) * (kXInv * kDScale);
-              v[e] = fmaf(lin, e16[e], (p.c * (kEEInv * kDScale)) * v[e]);
+      }
+      if (sub == subs - 1) {  // the accumulator is free
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(tempty0 + 8 * buf);
+          else mbar_arrive_remote(tempty_lead + 8 * buf);
+        }
+      }
+      if constexpr (Op == OrthoOp::Gram || Op == OrthoOp::Poly)
+        symmetric_box<Op>(v, slot, lane, m, col, t, dm, p);
+      else
+        apply_box<Op, kTall>(v, slot, lane, col, t, dm, keep, step, p);
+      if (Op == OrthoOp::Last && p.ragged) {
+        __syncwarp();
+        ragged_rows(slot, lane, row0, col, t, keep, step, p);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int height = (Op == OrthoOp::Gram || Op == OrthoOp::Poly) ? p.n : p.rows;
+        if (row0 < height) {
+          if constexpr (Op == OrthoOp::Gram || Op == OrthoOp::Poly) {
+            tma_store_3d(&maps.out0, slot, col, row0, t.b);
+            if (t.mp != t.nt) tma_store_3d(&maps.mirror, slot + kEpiBox, row0, col, t.b);
+          } else if constexpr (Op == OrthoOp::Apply) {
+            tma_store_3d(&maps.out0, slot, col, row0, t.b);
+            if (p.low_out) tma_store_3d(&maps.out1, slot + kEpiBox, col, row0, t.b);
+          } else if (!p.ragged) {
+            if (p.w == nullptr || p.wb != nullptr) tma_store_3d(&maps.out0, slot, col, row0, t.b);
+            if (p.w != nullptr) {
+              tma_store_3d(&maps.in1, slot + kEpiBox, col, row0, t.b);
+              if (col + 32 < p.cols)
+                tma_store_3d(&maps.in1, slot + 2 * kEpiBox, col + 32, row0, t.b);
             }
           }
         }
-        store_symmetric(p.d + at, m, col, p.n, p.ldn, t.mp != t.nt, v);
-      }
-    }
-  } else {
-    const bool row_ok = m < p.rows;
-    const float* beta = p.beta + static_cast<size_t>(t.b) * p.ldn;
-    const float bm = !kTall && row_ok ? __ldg(beta + m) : 0.0f;
-    const size_t rm = static_cast<size_t>(t.b) * p.rows + m;
-    float keep = 0.0f, step = 0.0f;
-    if (Op == OrthoOp::Last && p.w != nullptr) {
-      const float lr = __ldg(p.lr);
-      keep = 1.0f - lr * p.decay;
-      step = lr * p.scale * kXInv;
-    }
-#pragma unroll 1
-    for (int c = 0; c < kBN / 32; ++c) {
-      const int col = n0 + c * 32;
-      if (col >= p.cols) break;
-      __syncwarp();  // rows past the end went a way of their own
-      float v[32];
-      tmem_load_f32x32(tacc + c * 32, v);
-      if (!row_ok) continue;
-      float hi[32], lo[32];
-      load_half32(p.xh + rm * p.ldx + col, hi);
-      load_half32(p.xl + rm * p.ldx + col, lo);
-      if constexpr (kTall) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 b4 = __ldg(reinterpret_cast<const float4*>(beta + col + 4 * q));
-          const float b[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 4 * q + i;
-            const float be = col + e < p.cols ? b[i] : 0.0f;  // what is behind the last is no number
-            v[e] = fmaf(be, hi[e] + lo[e], v[e] * (1.0f / kDScale));
+        bulk_commit();
+        if constexpr (Sm::loads) {
+          if (ahead.u < p.units) {
+            bulk_wait_read<0>();
+            load_box<Op>(ahead, ahead.t.mp * 256 + row, slot, box_bar + 8 * (q & 1), maps, p);
+            ++issued;
+            ahead.next(p, nclusters);
           }
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = fmaf(bm, hi[e] + lo[e], v[e] * (1.0f / kDScale));
       }
-      if constexpr (Op == OrthoOp::Apply) {  // X' times 2^12, in two parts
-#pragma unroll
-        for (int e = 0; e < 32; ++e) lo[e] = v[e] - __half2float(__float2half_rn(v[e]));
-        store_half32(p.xh_out + rm * p.ldx + col, v);
-        store_half32(p.xl + rm * p.ldx + col, lo);
-      } else {
-        const size_t o = rm * p.cols + col;
-        const int nv = min(32, p.cols - col);
-        if (p.w == nullptr) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= kXInv;
-          if (p.cols % 8 == 0) {
-            store_bf16x32(p.out + o, nv, v);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e < nv) p.out[o + e] = __float2bfloat16_rn(v[e]);
-          }
-        } else if (p.cols % 8 == 0) {
-          float w[32];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (4 * q < nv) x = __ldcg(reinterpret_cast<const float4*>(p.w + o + 4 * q));
-            w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = fmaf(-step, v[e], keep * w[e]);
-          store_f32x32(p.w + o, nv, w);
-          if (p.wb != nullptr) store_bf16x32(p.wb + o, nv, w);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e < nv) {
-              const float w = fmaf(-step, v[e], keep * p.w[o + e]);
-              p.w[o + e] = w;
-              if (p.wb != nullptr) p.wb[o + e] = __float2bfloat16_rn(w);
-            }
-        }
-      }
+      __syncwarp();
     }
+    at.u += nclusters;
+    at.enter(p);
+    ++it;
+  }
+  if (lane == 0) {
+    // after an expired wait: the boxes that are still to come
+    if constexpr (Sm::loads)
+      for (int i = 0; i < issued; ++i, ++q)
+        wait_drain(box_bar + 8 * (q & 1), (q >> 1) & 1, wc);
+    bulk_wait_all();
   }
 }
 
 template <OrthoOp Op, bool kTall>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    ortho_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const OrthoParams p) {
-  constexpr int S = kPairStages;
+    ortho_kernel(const __grid_constant__ OrthoMaps maps, const OrthoParams p) {
+  using Sm = OrthoSmem<Op>;
+  constexpr int S = Sm::stages;
   constexpr bool a_mn = OrthoMajor<Op, kTall>::a_mn, b_mn = OrthoMajor<Op, kTall>::b_mn;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -265,14 +456,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t sA0 = base;
   const uint32_t sB0 = base + S * kPairAStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kPairStageBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kPairStageBytes + Sm::epi);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = smem_u32(bars + S);
   const uint32_t tfull0 = smem_u32(bars + 2 * S);
   const uint32_t tempty0 = smem_u32(bars + 2 * S + 2);
   const uint32_t drain = smem_u32(bars + 2 * S + 4);
+  const uint32_t box0 = smem_u32(bars + 2 * S + 5);  // two slots of four epilogue warps
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -291,10 +483,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(tempty0 + 8 * b, 8);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(box0 + 8 * i, 1);
     *abort_flag = 0u;
     mbar_fence_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+    if (Sm::loads) tma_prefetch_desc(&maps.in0);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
@@ -304,6 +498,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tc_fence_after();
   cluster_sync();
+  pdl_launch_next();
+  pdl_wait();  // what follows reads what the kernel before this one has written
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full_lead = mapa_shared(full0, 0);
   const uint32_t tempty_lead = mapa_shared(tempty0, 0);
@@ -331,14 +527,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           } else if (leader) {
             const uint32_t fb = full0 + 8 * stage;
             mbar_arrive_expect_tx(fb, 2 * kPairStageBytes);
-            ortho_load<a_mn, false>(sa, &tmA, fb, kb * kBK, ra, t.b);
-            ortho_load<b_mn, false>(sb, &tmB, fb, kb * kBK, rb, t.b);
+            ortho_load<a_mn, false>(sa, &maps.a, fb, kb * kBK, ra, t.b);
+            ortho_load<b_mn, false>(sb, &maps.b, fb, kb * kBK, rb, t.b);
             armed |= 1u << stage;
             armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           } else {
             const uint32_t fb = full_lead + 8 * stage;
-            ortho_load<a_mn, true>(sa, &tmA, fb, kb * kBK, ra, t.b);
-            ortho_load<b_mn, true>(sb, &tmB, fb, kb * kBK, rb, t.b);
+            ortho_load<a_mn, true>(sa, &maps.a, fb, kb * kBK, ra, t.b);
+            ortho_load<b_mn, true>(sb, &maps.b, fb, kb * kBK, rb, t.b);
             armed = 1u;
           }
           if (++stage == S) {
@@ -401,29 +597,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    int it = 0;
-    for (int u = cid; u < p.units; u += nclusters, ++it) {
-      const int buf = it & 1;
-      const uint32_t acc_par = (it >> 1) & 1;
-      int ok = 1;
-      if (lane == 0)
-        ok = wait_bounded(tfull0 + 8 * buf, acc_par, wc, kSiteEpiAccFull) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      __syncwarp();
-      tc_fence_after();
-      const OrthoTile t = ortho_tile<Op>(u, p);
-      ortho_epilogue<Op, kTall>(
-          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kBN, row, rank, t, p);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(tempty0 + 8 * buf);
-        else mbar_arrive_remote(tempty_lead + 8 * buf);
-      }
-    }
+    ortho_epilogue<Op, kTall>(tmem_base, tfull0, tempty0, tempty_lead,
+                              base + S * kPairStageBytes + (warp - 2) * 2 * Sm::slot,
+                              box0 + 16 * (warp - 2), warp & 3, lane, rank, cid, nclusters, wc,
+                              maps, p);
   }
 
   tc_fence_before();
@@ -436,55 +613,70 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-using OrthoKernel = void (*)(const CUtensorMap, const CUtensorMap, const OrthoParams);
+using OrthoKernel = void (*)(const OrthoMaps, const OrthoParams);
 
-static OrthoKernel ortho_kernel_of(OrthoOp op, bool tall) {
-  switch (op) {
-    case OrthoOp::Gram:
-      return tall ? ortho_kernel<OrthoOp::Gram, true> : ortho_kernel<OrthoOp::Gram, false>;
-    case OrthoOp::Poly:  // the same for both
-      return ortho_kernel<OrthoOp::Poly, false>;
-    case OrthoOp::Apply:
-      return tall ? ortho_kernel<OrthoOp::Apply, true> : ortho_kernel<OrthoOp::Apply, false>;
-    default:
-      return tall ? ortho_kernel<OrthoOp::Last, true> : ortho_kernel<OrthoOp::Last, false>;
-  }
+template <OrthoOp Op, bool kTall>
+static cudaError_t attr_of() {
+  return cudaFuncSetAttribute(ortho_kernel<Op, kTall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              OrthoSmem<Op>::bytes);
 }
 
-static void ortho_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clusters,
+// Launched so that it may begin while the kernel before it ends (pdl_wait).
+static void ortho_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clusters, int smem,
                          cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2), 1, 1);
   cfg.blockDim = dim3(kGemmThreads, 1, 1);
-  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
+}
+
+template <OrthoOp Op, bool kTall>
+static cudaError_t launch_as(const OrthoMaps& m, const OrthoParams& p, int clusters,
+                             cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ortho_config(cfg, attr, clusters, OrthoSmem<Op>::bytes, s);
+  return cudaLaunchKernelEx(&cfg, ortho_kernel<Op, kTall>, m, p);
 }
 
 cudaError_t ortho_set_attrs(int* max_clusters) {
-  for (OrthoOp op : {OrthoOp::Gram, OrthoOp::Poly, OrthoOp::Apply, OrthoOp::Last})
-    for (bool tall : {false, true}) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_kernel_of(op, tall)),
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
-      if (e != cudaSuccess) return e;
-    }
+  for (cudaError_t e :
+       {attr_of<OrthoOp::Gram, false>(), attr_of<OrthoOp::Gram, true>(),
+        attr_of<OrthoOp::Poly, false>(), attr_of<OrthoOp::Apply, false>(),
+        attr_of<OrthoOp::Apply, true>(), attr_of<OrthoOp::Last, false>(),
+        attr_of<OrthoOp::Last, true>()})
+    if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  ortho_config(cfg, attr, 2, nullptr);
-  return cudaOccupancyMaxActiveClusters(max_clusters, ortho_kernel_of(OrthoOp::Gram, false), &cfg);
+  cudaLaunchAttribute attr[2];
+  ortho_config(cfg, attr, 2, OrthoSmem<OrthoOp::Last>::bytes, nullptr);
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(max_clusters, ortho_kernel<OrthoOp::Last, false>, &cfg);
 }
 
-cudaError_t launch_ortho(OrthoOp op, bool tall, const CUtensorMap& a, const CUtensorMap& b,
-                         const OrthoParams& p, int clusters, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  ortho_config(cfg, attr, clusters, s);
-  return cudaLaunchKernelEx(&cfg, ortho_kernel_of(op, tall), a, b, p);
+cudaError_t launch_ortho(OrthoOp op, bool tall, const OrthoMaps& m, const OrthoParams& p,
+                         int clusters, cudaStream_t s) {
+  switch (op) {
+    case OrthoOp::Gram:
+      return tall ? launch_as<OrthoOp::Gram, true>(m, p, clusters, s)
+                  : launch_as<OrthoOp::Gram, false>(m, p, clusters, s);
+    case OrthoOp::Poly:  // the same for both
+      return launch_as<OrthoOp::Poly, false>(m, p, clusters, s);
+    case OrthoOp::Apply:
+      return tall ? launch_as<OrthoOp::Apply, true>(m, p, clusters, s)
+                  : launch_as<OrthoOp::Apply, false>(m, p, clusters, s);
+    case OrthoOp::Last:
+      return tall ? launch_as<OrthoOp::Last, true>(m, p, clusters, s)
+                  : launch_as<OrthoOp::Last, false>(m, p, clusters, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace mlpb

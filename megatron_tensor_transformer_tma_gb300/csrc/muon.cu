@@ -65,36 +65,55 @@ Layout layout(const mlpb_muon* h, void* workspace) {
   return l;
 }
 
-bool encode(const mlpb_muon* h, CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box) {
+bool encode(const mlpb_muon* h, CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+            CUtensorMapSwizzle swizzle) {
   const cuuint32_t steps[4] = {1, 1, 1, 1};
-  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
-                   const_cast<void*>(base), dims, strides, box, steps,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return h->encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
+                   box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
-// Matrices [batch][rows][ld] as operands whose K runs along a row: 128 rows by 64 columns.
-bool map_k(const mlpb_muon* h, CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
-           uint64_t ld) {
-  const cuuint64_t dims[3] = {cols, rows, static_cast<cuuint64_t>(h->cfg.batch)};
-  const cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
-  const cuuint32_t box[3] = {kBK, kBM, 1};
-  return encode(h, m, base, 3, dims, strides, box);
+// Matrices [batch][rows][ld] in boxes of some rows by some columns.
+struct Matrices {
+  const void* base;
+  int64_t rows, cols, ld;
+};
+
+bool map_box(const mlpb_muon* h, CUtensorMap* m, const Matrices& x, CUtensorMapDataType type,
+             uint64_t size, uint32_t box_cols, uint32_t box_rows, bool swizzled) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(x.cols), static_cast<cuuint64_t>(x.rows),
+                              static_cast<cuuint64_t>(h->cfg.batch)};
+  const cuuint64_t strides[2] = {x.ld * size, static_cast<cuuint64_t>(x.rows) * x.ld * size};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  return encode(h, m, type, x.base, 3, dims, strides, box,
+                swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// The same with K along a column: two 64-wide chunks of 64 rows.
-bool map_mn(const mlpb_muon* h, CUtensorMap* m, const void* base, uint64_t rows, uint64_t ld) {
-  const cuuint64_t dims[4] = {64, rows, ld / 64, static_cast<cuuint64_t>(h->cfg.batch)};
-  const cuuint64_t strides[3] = {ld * 2, 128, rows * ld * 2};
+// As operands whose K runs along a row: 128 rows by 64 columns.
+bool map_k(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
+  return map_box(h, m, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, kBK, kBM, true);
+}
+
+// With K along a column: two 64-wide chunks of 64 rows.
+bool map_mn(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(x.rows),
+                              static_cast<cuuint64_t>(x.ld / 64),
+                              static_cast<cuuint64_t>(h->cfg.batch)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.ld) * 2, 128,
+                                 static_cast<cuuint64_t>(x.rows) * x.ld * 2};
   const cuuint32_t box[4] = {64, kBK, 2, 1};
-  return encode(h, m, base, 4, dims, strides, box);
+  return encode(h, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x.base, 4, dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-bool map_x(const mlpb_muon* h, CUtensorMap* m, const void* base, bool mn) {
-  const mlpb_muon_config& c = h->cfg;
-  return mn ? map_mn(h, m, base, c.rows, h->ldx) : map_k(h, m, base, c.rows, c.cols, h->ldx);
+// The epilogue's boxes of 32 rows by 64 columns, and mirrored.
+bool map_tile(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
+  return map_box(h, m, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, 64, 32, true);
+}
+bool map_mirror(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
+  return map_box(h, m, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, 32, 64, false);
 }
 
 // The steps, the last of them into what `p` names.
@@ -102,28 +121,47 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
                     cudaStream_t s) {
   const mlpb_muon_config& c = h->cfg;
   const Layout l = layout(h, workspace);
-  CUtensorMap k[2], mn[2], e, d;
-  for (int i = 0; i < 2; ++i) {
-    __half* x = i == 0 ? l.x0 : l.x1;
-    if (!map_x(h, &k[i], x, false) || !map_x(h, &mn[i], x, true)) return MLPB_ECUDA;
+  const Matrices x[2] = {{l.x0, c.rows, c.cols, h->ldx}, {l.x1, c.rows, c.cols, h->ldx}};
+  const Matrices low{l.xl, c.rows, c.cols, h->ldx};
+  const Matrices e{l.e, h->n, h->n, h->ldn}, d{l.d, h->n, h->n, h->ldn};
+  OrthoMaps gram[2], poly, apply[2], last;  // by the buffer that X is in
+  bool ok = map_k(h, &poly.a, e) && map_tile(h, &poly.in0, e) && map_tile(h, &poly.out0, d) &&
+            map_mirror(h, &poly.mirror, d);
+  poly.b = poly.in1 = poly.out1 = poly.a;
+  const int buffers = c.steps > 1 ? 2 : 1;
+  for (int i = 0; i < buffers && ok; ++i) {
+    OrthoMaps& g = gram[i];
+    OrthoMaps& y = apply[i];
+    ok = (h->tall ? map_mn(h, &g.a, x[i]) : map_k(h, &g.a, x[i])) && map_tile(h, &g.out0, e) &&
+         map_mirror(h, &g.mirror, e);
+    g.b = g.in0 = g.in1 = g.out1 = g.a;
+    ok = ok && (h->tall ? map_k(h, &y.a, x[i]) && map_k(h, &y.b, d)
+                        : map_k(h, &y.a, d) && map_mn(h, &y.b, x[i])) &&
+         map_tile(h, &y.in0, x[i]) && map_tile(h, &y.in1, low) && map_tile(h, &y.out0, x[1 - i]);
+    y.out1 = y.mirror = y.in1;
   }
-  if (!map_k(h, &e, l.e, h->n, h->n, h->ldn) || !map_k(h, &d, l.d, h->n, h->n, h->ldn))
-    return MLPB_ECUDA;
-  if (launch_muon_norm(in, l.part, s) != cudaSuccess ||
+  last = apply[(c.steps - 1) & 1];
+  p.ragged = c.cols % 8 != 0 ? 1 : 0;
+  if (ok && !p.ragged) {
+    if (p.w != nullptr)
+      ok = map_box(h, &last.in1, {p.w, c.rows, c.cols, c.cols}, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                   32, 32, true);
+    const void* half = p.w != nullptr ? p.wb : p.out;
+    if (ok && half != nullptr)
+      ok = map_box(h, &last.out0, {half, c.rows, c.cols, c.cols}, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   2, 64, 32, true);
+  }
+  if (!ok || launch_muon_norm(in, l.part, s) != cudaSuccess ||
       launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, s) != cudaSuccess)
     return MLPB_ECUDA;
   p.batch = static_cast<int>(c.batch);
   p.rows = static_cast<int>(c.rows);
   p.cols = static_cast<int>(c.cols);
   p.n = h->n;
-  p.ldx = h->ldx;
   p.ldn = h->ldn;
   p.a = c.coef[0];
   p.b = c.coef[1];
   p.c = c.coef[2];
-  p.xl = l.xl;
-  p.e = l.e;
-  p.d = l.d;
   p.diag = l.diag;
   p.beta = l.beta;
   p.err = h->err;
@@ -132,27 +170,24 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   h->fault_pending = false;
   const int tiles = static_cast<int>(cdiv(h->n, 256));
   for (int i = 0; i < c.steps; ++i) {
-    const int from = i & 1;
-    p.xh = from == 0 ? l.x0 : l.x1;
-    p.xh_out = from == 0 ? l.x1 : l.x0;
+    const bool is_last = i == c.steps - 1;
     p.num_pm = p.num_n = tiles;
     p.units = p.batch * (tiles * (tiles + 1) / 2);
     p.num_kb = static_cast<int>(cdiv(h->tall ? c.rows : c.cols, kBK));
-    const CUtensorMap& x = h->tall ? mn[from] : k[from];
-    if (launch_ortho(OrthoOp::Gram, h->tall, x, x, p, std::min(p.units, h->max_clusters), s) !=
-        cudaSuccess)
+    if (launch_ortho(OrthoOp::Gram, h->tall, gram[i & 1], p, std::min(p.units, h->max_clusters),
+                     s) != cudaSuccess)
       return MLPB_ECUDA;
     p.fault_inject = 0;
     p.num_kb = static_cast<int>(cdiv(h->n, kBK));
-    if (launch_ortho(OrthoOp::Poly, h->tall, e, e, p, std::min(p.units, h->max_clusters), s) !=
+    if (launch_ortho(OrthoOp::Poly, h->tall, poly, p, std::min(p.units, h->max_clusters), s) !=
         cudaSuccess)
       return MLPB_ECUDA;
     p.num_pm = static_cast<int>(cdiv(c.rows, 256));
     p.num_n = static_cast<int>(cdiv(c.cols, 256));
     p.units = p.batch * p.num_pm * p.num_n;
-    if (launch_ortho(i == c.steps - 1 ? OrthoOp::Last : OrthoOp::Apply, h->tall,
-                     h->tall ? k[from] : d, h->tall ? d : mn[from], p,
-                     std::min(p.units, h->max_clusters), s) != cudaSuccess)
+    p.low_out = i < c.steps - 2 ? 1 : 0;
+    if (launch_ortho(is_last ? OrthoOp::Last : OrthoOp::Apply, h->tall, is_last ? last : apply[i & 1],
+                     p, std::min(p.units, h->max_clusters), s) != cudaSuccess)
       return MLPB_ECUDA;
   }
   return MLPB_OK;

@@ -7,7 +7,8 @@
 // Operands are fp16, which has eight times bf16's precision at the same rate; values have fixed
 // scales, since singular values stay below 2 (the host checks the coefficients).  What would cost
 // precision is kept out of the products:
-//   - X is hi + lo, two fp16 parts (22 bits); the product takes hi, a X both.
+//   - X is hi + lo, two fp16 parts (22 bits); the product takes hi, a X both.  (The last step's X
+//     is hi alone: what it loses is not amplified any more.)
 //   - The diagonal d of A is fp32 and its part E off the diagonal fp16:
 //       A A = E E + (d_i + d_j) E_ij + delta_ij d_i^2,
 //     so the identity that A comes near is not rounded.  Likewise b A + c A A + a I = D + diag(beta)
@@ -41,22 +42,19 @@ enum class OrthoOp : int {
 
 struct OrthoParams {
   int batch, rows, cols, n;  // n = min(rows, cols)
-  int ldx, ldn;              // elements of a row of X; of E and D
+  int ldn;                   // elements of a row of E, D, diag and beta
   int num_pm, num_n;         // 256-row and 256-column tiles of a matrix
   int units;                 // tiles of all matrices (on and below the diagonal for Gram, Poly)
   int num_kb;                // 64-deep k-blocks
   float a, b, c;
-  const __half* xh;  // Apply: X
-  __half* xh_out;    // Apply: X'
-  __half* xl;        // the low parts, rewritten in place
-  __half* e;
-  __half* d;
   float* diag;  // d [batch][ldn]
   float* beta;  // [batch][ldn]
+  int low_out;  // Apply: X' has a low part (the last step's X is the high part alone)
   // Last: O bf16, or the weight's update W <- (1 - lr wd) W - lr scale O
   __nv_bfloat16* out;
   float* w;
   __nv_bfloat16* wb;  // a bf16 copy of the updated W, or NULL
+  int ragged;         // rows of out, w, wb that no tensor map takes (cols % 8 != 0)
   const float* lr;
   float decay, scale;
   uint32_t* err;
@@ -64,9 +62,19 @@ struct OrthoParams {
   int fault_inject;
 };
 
+// The operands' maps, and those of the epilogue's boxes of 32 rows by 64 columns (W: 32 by 32).
+struct OrthoMaps {
+  CUtensorMap a, b;
+  CUtensorMap in0;     // Poly: E;  Apply, Last: X
+  CUtensorMap in1;     // Apply: its low part;  Last: W
+  CUtensorMap out0;    // Gram: E;  Poly: D;  Apply: X';  Last: O or W's bf16 copy
+  CUtensorMap out1;    // Apply: its low part
+  CUtensorMap mirror;  // Gram: E;  Poly: D in boxes of 64 rows by 32 columns
+};
+
 cudaError_t ortho_set_attrs(int* max_clusters);
-cudaError_t launch_ortho(OrthoOp op, bool tall, const CUtensorMap& a, const CUtensorMap& b,
-                         const OrthoParams& p, int clusters, cudaStream_t s);
+cudaError_t launch_ortho(OrthoOp op, bool tall, const OrthoMaps& m, const OrthoParams& p,
+                         int clusters, cudaStream_t s);
 
 // muon_prepare.cu.  U = G + momentum M' with M' = momentum M + G (nesterov), or M', or (M NULL) G
 // itself; X = U / |U| in two fp16 parts.

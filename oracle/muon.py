@@ -46,15 +46,16 @@ def _half(x, scale):
 
 def rounded(U, steps=5, coef=COEF):
     """With X, the part of A off its diagonal and that of b A + c A A + a I as fp16 operands, scaled
-    by 2^12, 2^12 and 2^10, diagonals apart, and X in two fp16 parts between the steps."""
+    by 2^12, 2^12 and 2^10, diagonals apart, and X in two fp16 parts between the steps (one before the
+    last)."""
     a, b, c = coef
     X = normalized(U)
     tall = X.shape[0] > X.shape[1]
     if tall:
         X = X.T
-    for _ in range(steps):
+    for i in range(steps):
         hi = _half(X, 4096.0)
-        X = hi + _half(X - hi, 4096.0)
+        X = hi + (_half(X - hi, 4096.0) if i < steps - 1 else 0.0)
         A = hi @ hi.T
         d = np.diag(A).copy()
         E = _half(A - np.diag(d), 4096.0)
