@@ -20,6 +20,7 @@ struct mlpb_muon {
   int device, max_clusters;
   bool tall, fault_pending;
   int n, ldx, ldn;
+  int small;  // CTAs of a cluster that keeps a matrix in shared memory; 0: tiles of tensor cores
   uint32_t* err;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
 };
@@ -120,6 +121,11 @@ bool map_mirror(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
 mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* workspace,
                     cudaStream_t s) {
   const mlpb_muon_config& c = h->cfg;
+  p.a = c.coef[0];
+  p.b = c.coef[1];
+  p.c = c.coef[2];
+  if (h->small > 0)
+    return launch_muon_small(in, p, c.steps, h->small, s) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
   const Layout l = layout(h, workspace);
   const Matrices x[2] = {{l.x0, c.rows, c.cols, h->ldx}, {l.x1, c.rows, c.cols, h->ldx}};
   const Matrices low{l.xl, c.rows, c.cols, h->ldx};
@@ -159,9 +165,6 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   p.cols = static_cast<int>(c.cols);
   p.n = h->n;
   p.ldn = h->ldn;
-  p.a = c.coef[0];
-  p.b = c.coef[1];
-  p.c = c.coef[2];
   p.diag = l.diag;
   p.beta = l.beta;
   p.err = h->err;
@@ -238,8 +241,9 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
   h->ldn = static_cast<int>(cdiv(h->n, kOrthoLd)) * kOrthoLd;
   h->fault_pending = (c.flags & MLPB_MUON_FAULT_INJECT) != 0;
   h->err = nullptr;
-  int major = 0, minor = 0;
+  int major = 0, minor = 0, sms = 0;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, h->device) != cudaSuccess) {
     delete h;
@@ -258,6 +262,16 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
     return MLPB_ECUDA;
   }
   h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  const int64_t length = std::max(c.rows, c.cols);
+  h->small = muon_small_cluster(h->n, length, c.batch, sms);
+  if (h->small > 0) {
+    bool fits = false;
+    if (muon_small_set_attrs(h->n, length, h->small, &fits) != cudaSuccess) {
+      delete h;
+      return MLPB_ECUDA;
+    }
+    if (!fits) h->small = 0;
+  }
   if (ortho_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
       cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->err, 0, sizeof(uint32_t)) != cudaSuccess ||
@@ -278,7 +292,7 @@ extern "C" void mlpb_muon_destroy(mlpb_muon* h) {
 
 extern "C" mlpb_status mlpb_muon_workspace_size(const mlpb_muon* h, size_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MLPB_EINVAL;
-  *bytes = layout(h, nullptr).bytes;
+  *bytes = h->small > 0 ? 256 : layout(h, nullptr).bytes;
   return MLPB_OK;
 }
 

@@ -6,80 +6,12 @@
 
 #include <algorithm>
 
-#include "common.cuh"
-#include "muon.cuh"
+#include "muon_update.cuh"
 
 namespace mlpb {
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepMaxParts = 512;
-
-// U of four consecutive elements (n of them valid), M written back by the first pass.
-template <bool kFirst, typename T>
-__device__ __forceinline__ void update4(const T* g, float* m, int n, bool vec, float mu,
-                                        int nesterov, float (&u)[4]) {
-  if constexpr (sizeof(T) == 2) {
-    if (vec) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(g));
-      const float2 x = unpack_bf16x2(w.x), y = unpack_bf16x2(w.y);
-      u[0] = x.x; u[1] = x.y; u[2] = y.x; u[3] = y.y;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = e < n ? __bfloat162float(g[e]) : 0.0f;
-    }
-  } else {
-    if (vec) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(g));
-      u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = e < n ? g[e] : 0.0f;
-    }
-    if (m != nullptr) {
-      float v[4];
-      if (vec) {
-        const float4 x = *reinterpret_cast<const float4*>(m);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = e < n ? m[e] : 0.0f;
-      }
-      if constexpr (kFirst) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(mu, v[e], u[e]);
-        if (vec) {
-          *reinterpret_cast<float4*>(m) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < n) m[e] = v[e];
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = nesterov ? fmaf(mu, v[e], u[e]) : v[e];
-    }
-  }
-}
-
-// Sums of squares in three ranges (after Blue, 1978), so that neither large nor small values
-// leave fp32's range: x small of 2^-40, large of 2^40, the rest.
-constexpr float kTiny = 9.094947017729282e-13f;   // 2^-40
-constexpr float kHuge = 1.099511627776e12f;       // 2^40
-constexpr float kUp = 1.2089258196146292e24f;     // 2^80
-constexpr float kDown = 8.271806125530277e-25f;   // 2^-80
-
-__device__ __forceinline__ void add_square(float x, float4& s) {
-  const float a = fabsf(x);
-  if (a < kTiny) {
-    const float y = x * kUp;
-    s.x = fmaf(y, y, s.x);
-  } else if (a <= kHuge) {
-    s.y = fmaf(x, x, s.y);
-  } else {  // NaN too
-    const float y = x * kDown;
-    s.z = fmaf(y, y, s.z);
-  }
-}
+constexpr int kPrepMaxParts = kPrepThreads;
 
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) muon_norm_kernel(const MuonInput in,
@@ -96,17 +28,7 @@ __global__ void __launch_bounds__(kPrepThreads) muon_norm_kernel(const MuonInput
     float u[4];
     const int n = static_cast<int>(min(static_cast<int64_t>(4), elems - i));
     update4<true>(g + i, m == nullptr ? nullptr : m + i, n, vec, in.momentum, in.nesterov, u);
-    const float a = fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])));
-    const float b = fminf(fminf(fabsf(u[0]), fabsf(u[1])), fminf(fabsf(u[2]), fabsf(u[3])));
-    if (b >= kTiny && a <= kHuge) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s.y = fmaf(u[e], u[e], s.y);
-      // max and min leave a NaN out: it is added by the comparisons' failing elsewhere
-      s.z += (u[0] + u[1] + u[2] + u[3]) * 0.0f;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) add_square(u[e], s);
-    }
+    add_squares4(u, s);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
@@ -127,31 +49,6 @@ __global__ void __launch_bounds__(kPrepThreads) muon_norm_kernel(const MuonInput
   }
 }
 
-// x = (u s1) s2 for u / |U|: two factors, since 1 / |U| may be past fp32's range.  A warp's work;
-// the order of the sum is fixed.
-__device__ __forceinline__ void norm_factors(const float4* part, int parts, float& s1, float& s2) {
-  double t = 0.0;
-  for (int i = threadIdx.x & 31; i < parts; i += 32) {
-    const float4 p = part[i];
-    t += static_cast<double>(p.x) * 6.842277657836021e-49 + static_cast<double>(p.y) +
-         static_cast<double>(p.z) * 1.461501637330903e48;  // 2^-160, 2^160
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  const double norm = sqrt(t);
-  s2 = 1.0f;
-  if (norm == 0.0) {  // a zero matrix stays zero
-    s1 = 0.0f;
-  } else if (!(norm < 1e60)) {  // a NaN goes through; with infinities NaN at them, zero elsewhere
-    s1 = isnan(norm) ? static_cast<float>(norm) : 0.0f;
-  } else {
-    int e;
-    const double f = frexp(norm, &e);  // norm = f 2^e; e in [-148, 160]
-    s1 = ldexpf(1.0f, -(e / 2));
-    s2 = ldexpf(static_cast<float>(1.0 / f), -(e - e / 2));
-  }
-}
-
 // X's two parts, eight columns of a row a thread; the pad of both buffers of X is zero.
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads)
@@ -160,15 +57,20 @@ __global__ void __launch_bounds__(kPrepThreads)
                       __half* __restrict__ xl, int ldx) {
   __shared__ float factors[2];
   const int64_t b = blockIdx.y;
-  if (threadIdx.x < 32) {
-    float f1, f2;
-    norm_factors(part + b * parts, parts, f1, f2);
+  {  // a part a thread: muon_partials() is at most the number of threads
+    __shared__ double warps[kPrepThreads / 32];
+    double t = static_cast<int>(threadIdx.x) < parts ? whole_square(part[b * parts + threadIdx.x])
+                                                     : 0.0;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = t;
+    __syncthreads();
     if (threadIdx.x == 0) {
-      factors[0] = f1;
-      factors[1] = f2;
+      for (int w = 1; w < kPrepThreads / 32; ++w) t += warps[w];
+      norm_factors(t, factors[0], factors[1]);
     }
+    __syncthreads();
   }
-  __syncthreads();
   const float s1 = factors[0], s2 = factors[1] * kXScale;
   const int64_t elems = in.rows * in.cols;
   const int groups = ldx / 8;
@@ -228,7 +130,7 @@ cudaError_t launch_muon_norm(const MuonInput& in, float4* part, cudaStream_t s) 
 cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* xh,
                               __half* xh_other, __half* xl, int ldx, cudaStream_t s) {
   const int64_t pieces = in.rows * (ldx / 8);
-  const int64_t most = std::max<int64_t>(1, 4864 / in.batch);
+  const int64_t most = std::max<int64_t>(1, 1216 / in.batch);
   const dim3 grid(static_cast<unsigned>(
                       std::min<int64_t>(most, (pieces + kPrepThreads - 1) / kPrepThreads)),
                   static_cast<unsigned>(in.batch));

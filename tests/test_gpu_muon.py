@@ -42,7 +42,11 @@ def _close(got, U, half=True, steps=5, coef=muon.COEF, scale=1.0, more=0.0):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 40), (2, 40, 1), (1, 16, 16), (3, 33, 77), (2, 130, 65), (1, 64, 1032),
-          (1, 300, 257), (2, 257, 600), (1, 520, 264), (1, 128, 256), (5, 96, 128), (1, 700, 700)]
+          (1, 300, 257), (2, 257, 600), (1, 520, 264), (1, 128, 256), (5, 96, 128), (1, 700, 700),
+          # in shared memory: sides around 32 and 128, one CTA and clusters, long sides that no
+          # longer fit
+          (1, 32, 2000), (3, 2001, 31), (1, 97, 1000), (2, 128, 4096), (1, 4100, 128), (40, 20, 70),
+          (1, 127, 4097), (1, 9000, 60), (200, 8, 8), (1, 24, 8300)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -112,7 +116,8 @@ def test_zero_infinite_and_nan_matrices_keep_to_themselves():
         assert torch.equal(O[i], want[i])
 
 
-@pytest.mark.parametrize("shape", [(2, 2, 40, 72), (3, 130, 48), (1, 77, 33)])
+@pytest.mark.parametrize("shape", [(2, 2, 40, 72), (3, 130, 48), (1, 77, 33), (2, 200, 264),
+                                   (1, 333, 141)])
 @pytest.mark.parametrize("nesterov", [True, False])
 def test_step(shape, nesterov):
     n, (r, c) = int(np.prod(shape[:-2])), shape[-2:]
@@ -174,7 +179,7 @@ def test_refusals():
         plan.orthogonalize(U.half())
     with pytest.raises(ValueError, match="are needed"):
         mlpb.mlpb_muon_orthogonalize(plan.handle, U, torch.empty_like(U, dtype=BF),
-                                     plan.workspace[:256])
+                                     plan.workspace[:64])
     with pytest.raises(mlpb.MLPBError):
         mlpb.mlpb_muon_orthogonalize(plan.handle, U, None, plan.workspace)
     with pytest.raises(TypeError):
@@ -186,7 +191,7 @@ def test_refusals():
 
 
 def test_an_expired_wait_is_reported_and_the_next_call_is_right():
-    U = _randn(1, 1, 300, 520)
+    U = _randn(1, 1, 300, 520)  # not a matrix that lies in shared memory: nothing waits there
     want = mlpb.Muon(300, 520).orthogonalize(U)
     hurt = mlpb.Muon(300, 520, flags=mlpb.MLPB_MUON_FAULT_INJECT)
     hurt.orthogonalize(U)
