@@ -11,10 +11,15 @@
 //
 // An element of X' takes 8 bytes in and out beside 2 n operations, as much of the memory's time as
 // of the tensor cores' at n = 1376, so the epilogue's tiles go through shared memory by TMA: each
-// epilogue warp has two slots for 32 rows by 64 columns, computes in place, stores the box, and
-// loads the box after next when the store has read it.  (Rows read and written by their threads,
+// of eight epilogue warps has a slot for 32 rows by 64 columns, computes in place, stores the box,
+// and loads its next box when the store has read it.  (Rows read and written by their threads,
 // 16 bytes a lane, took 540 us for 16 matrices of 1376 x 4096, four times the product: every
 // access touches 32 lines.)  The ring has 5 stages for that, 4 where W's fp32 boxes come too.
+//
+// Few tiles leave pairs idle and the epilogue in the open.  Then tiles are 256 x 128 (the rule is
+// at ortho_narrow in muon.cu), and the symmetric products' K is cut into ranges (`split`), whose
+// fp32 sums go to the workspace; for each 32 x 64 box the warp that comes last adds the ranges in
+// their order, so that the bits do not depend on who it is, and goes on with the sum.
 #include <algorithm>
 
 #include "gemm.cuh"
@@ -28,26 +33,43 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bo
 }
 
 struct OrthoTile {
-  int b, mp, nt;
+  int b, mp, nt;     // matrix, tile of 256 rows, tile of BN columns
+  int part, parts;   // range of K
+  bool mirror;       // below the diagonal: its transpose is stored too
 };
 
 template <OrthoOp Op>
+constexpr bool kSymmetric = Op == OrthoOp::Gram || Op == OrthoOp::Poly;
+
+template <OrthoOp Op, int BN>
 __device__ __forceinline__ OrthoTile ortho_tile(int u, const OrthoParams& p) {
   OrthoTile t;
-  if constexpr (Op == OrthoOp::Gram || Op == OrthoOp::Poly) {
-    const int per = p.num_pm * (p.num_pm + 1) / 2;
-    t.b = u / per;
-    const int i = u - t.b * per;  // row by row below the diagonal
-    t.mp = static_cast<int>((sqrtf(8.0f * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
-    while (t.mp * (t.mp + 1) / 2 > i) --t.mp;
-    while ((t.mp + 1) * (t.mp + 2) / 2 <= i) ++t.mp;
-    t.nt = i - t.mp * (t.mp + 1) / 2;
+  t.part = 0;
+  t.parts = 1;
+  t.mirror = false;
+  if constexpr (kSymmetric<Op>) {
+    t.parts = p.split;
+    t.part = u % p.split;
+    u /= p.split;
+    // row by row of 256, with R columns tiles in each more: R mp (mp + 1) / 2 tiles before row mp
+    constexpr int R = 256 / BN;
+    t.b = u / p.per_matrix;
+    const int i = u - t.b * p.per_matrix;
+    t.mp = static_cast<int>((sqrtf(8.0f / R * static_cast<float>(i) + 1.0f) - 1.0f) * 0.5f);
+    while (R * t.mp * (t.mp + 1) / 2 > i) --t.mp;
+    while (R * (t.mp + 1) * (t.mp + 2) / 2 <= i) ++t.mp;
+    t.nt = i - R * t.mp * (t.mp + 1) / 2;
+    t.mirror = t.nt < R * t.mp;
   } else {
-    const int per = p.num_pm * p.num_n;
-    t.b = u / per;
-    tile_coords(u - t.b * per, p.num_pm, p.num_n, 8, t.mp, t.nt);
+    t.b = u / p.per_matrix;
+    tile_coords(u - t.b * p.per_matrix, p.num_pm, p.num_n, 8, t.mp, t.nt);
   }
   return t;
+}
+
+__device__ __forceinline__ void ortho_range(const OrthoTile& t, int num_kb, int& kb0, int& kb1) {
+  kb0 = num_kb * t.part / t.parts;
+  kb1 = num_kb * (t.part + 1) / t.parts;
 }
 
 template <OrthoOp Op, bool kTall>
@@ -105,54 +127,68 @@ __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
                : "memory");
 }
 
-__device__ __forceinline__ void sts2(uint32_t a, __half h) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__half_as_ushort(h)) : "memory");
+__device__ __forceinline__ void sts2(uint32_t a, uint32_t low) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(low)) : "memory");
 }
 
 constexpr int kEpiRows = 32, kEpiCols = 64;
 constexpr int kEpiBox = kEpiRows * kEpiCols * 2;  // 4 KB: rows of 128 bytes, 128-byte swizzle
 
-template <OrthoOp Op>
+constexpr int kEpiWarps = 8;
+constexpr int kOrthoThreads = 64 + 32 * kEpiWarps;
+
+template <OrthoOp Op, int BN>
 struct OrthoSmem {
-  static constexpr int stages = Op == OrthoOp::Last ? 4 : 5;
+  static constexpr int b_stage = BN / 2 * kBK * 2;
+  static constexpr int stage = kPairAStage + b_stage;
+  static constexpr int stages = (Op == OrthoOp::Last ? 4 : 5) + (BN == 128 ? 1 : 0);
   // a slot: the first box, and a second one (low part, mirrored box) or W's two
   static constexpr int slot = Op == OrthoOp::Last ? 3 * kEpiBox : 2 * kEpiBox;
-  static constexpr int epi = 4 * 2 * slot;
-  static constexpr int bytes = stages * kPairStageBytes + epi + 1024 + 512;
+  static constexpr int epi = kEpiWarps * slot;
+  static constexpr int bytes = stages * stage + epi + 1024 + 512;
   static_assert(bytes <= 232448, "shared memory of a CTA");
   static constexpr bool loads = Op != OrthoOp::Gram;
 };
+
+// Boxes of 64 columns that the matrix has in a tile.
+template <OrthoOp Op, int BN>
+__device__ __forceinline__ int ortho_boxes(const OrthoTile& t, const OrthoParams& p) {
+  const int width = kSymmetric<Op> ? p.n : p.cols;
+  return min(BN / kEpiCols, (width - t.nt * BN + kEpiCols - 1) / kEpiCols);
+}
 
 // Address of the 16-byte piece j of a box's row.
 __device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int j) {
   return box + row * 128 + ((j ^ (row & 7)) << 4);
 }
 
-// A warp's boxes in order: columns of 64 of a tile, tile after tile.
-template <OrthoOp Op>
+// A warp's boxes in order: of the 64-column boxes of a tile those of its half, tile after tile.
+template <OrthoOp Op, int BN>
 struct BoxWalk {
-  int u, sub, subs;
+  int u, sub, subs;  // the tile, the box in it, the boxes that the matrix has there
   OrthoTile t;
-  __device__ __forceinline__ void enter(const OrthoParams& p) {
-    if (u >= p.units) return;
-    t = ortho_tile<Op>(u, p);
-    const int width = (Op == OrthoOp::Gram || Op == OrthoOp::Poly) ? p.n : p.cols;
-    subs = min(kBN / kEpiCols, (width - t.nt * kBN + kEpiCols - 1) / kEpiCols);
-    sub = 0;
+  __device__ __forceinline__ void find(int half, const OrthoParams& p, int step) {
+    for (; u < p.units; u += step) {
+      t = ortho_tile<Op, BN>(u, p);
+      subs = ortho_boxes<Op, BN>(t, p);
+      sub = half;
+      if (sub < subs) return;
+    }
   }
-  __device__ __forceinline__ void next(const OrthoParams& p, int step) {
-    if (++sub == subs) {
+  __device__ __forceinline__ void next(int half, const OrthoParams& p, int step) {
+    sub += 2;
+    if (sub >= subs) {
       u += step;
-      enter(p);
+      find(half, p, step);
     }
   }
 };
 
 // Loads a box's inputs into its slot; one lane.
-template <OrthoOp Op>
-__device__ __forceinline__ void load_box(const BoxWalk<Op>& w, int row0, uint32_t slot,
+template <OrthoOp Op, int BN>
+__device__ __forceinline__ void load_box(const BoxWalk<Op, BN>& w, int row0, uint32_t slot,
                                          uint32_t bar, const OrthoMaps& m, const OrthoParams& p) {
-  const int col = w.t.nt * kBN + w.sub * kEpiCols;
+  const int col = w.t.nt * BN + w.sub * kEpiCols;
   const bool second =
       Op == OrthoOp::Apply || (Op == OrthoOp::Last && p.w != nullptr && !p.ragged);
   constexpr int more = Op == OrthoOp::Last ? 2 : 1;
@@ -165,17 +201,25 @@ __device__ __forceinline__ void load_box(const BoxWalk<Op>& w, int row0, uint32_
   }
 }
 
+// Vectors along a box's columns are held by the warp, two elements a lane.
+struct ColumnPair {
+  float lo, hi;  // of columns lane, 32 + lane
+  __device__ __forceinline__ float at(int e) const {
+    return __shfl_sync(0xffffffffu, e < 32 ? lo : hi, e & 31);
+  }
+};
+
 // A box of a symmetric product: rows m of the thread, 64 columns; the diagonal's element apart.
 template <OrthoOp Op>
 __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slot, int lane, int m,
                                               int col, const OrthoTile& t, float dm,
-                                              const OrthoParams& p) {
+                                              const ColumnPair& dj, const OrthoParams& p) {
   if constexpr (Op == OrthoOp::Gram) {
 #pragma unroll
     for (int e = 0; e < kEpiCols; ++e) v[e] *= kXInv;  // A times 2^12
   }
-  float d = 0.0f;
-  if (t.mp == t.nt) {
+  if (!t.mirror) {
+    float d = 0.0f;
 #pragma unroll
     for (int e = 0; e < kEpiCols; ++e)
       if (col + e == m) {
@@ -189,6 +233,7 @@ __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slo
       else
         p.beta[at] = p.a + dm * fmaf(p.c, dm, p.b) + p.c * (d * kEEInv);
     }
+    __syncwarp();
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -197,25 +242,22 @@ __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slo
     if constexpr (Op == OrthoOp::Poly) {
       float e16[8];
       unpack_half8(lds16(at), e16);
-      // rows of 64 elements: inside the buffer, though not all are of the matrix
-      const float* dj = p.diag + static_cast<size_t>(t.b) * p.ldn + col + 8 * j;
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(dj)),
-                   y = __ldcg(reinterpret_cast<const float4*>(dj + 4));
-      const float dd[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float lin = fmaf(p.c, dm + dd[i], p.b) * (kXInv * kDScale);
+        const float lin = fmaf(p.c, dm + dj.at(8 * j + i), p.b) * (kXInv * kDScale);
         r[i] = fmaf(lin, e16[i], (p.c * (kEEInv * kDScale)) * v[8 * j + i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) r[i] = v[8 * j + i];
     }
-    sts16(at, pack_half8(r));
-    if (t.mp != t.nt) {  // its column, 32 consecutive elements of a row across the warp
+    const uint4 h = pack_half8(r);
+    sts16(at, h);
+    if (t.mirror) {  // its column, 32 consecutive elements of a row across the warp
+      const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+      const uint32_t to = slot + kEpiBox + 8 * j * 64 + lane * 2;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sts2(slot + kEpiBox + (8 * j + i) * 64 + lane * 2, __float2half_rn(r[i]));
+      for (int i = 0; i < 8; ++i) sts2(to + i * 64, w[i >> 1] >> (16 * (i & 1)));
     }
   }
 }
@@ -223,9 +265,8 @@ __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slo
 // A box of X' or of the result.
 template <OrthoOp Op, bool kTall>
 __device__ __forceinline__ void apply_box(const float (&v)[kEpiCols], uint32_t slot, int lane,
-                                          int col, const OrthoTile& t, float bm, float keep,
-                                          float step, const OrthoParams& p) {
-  const float* beta = p.beta + static_cast<size_t>(t.b) * p.ldn + col;
+                                          float bm, const ColumnPair& bj, float keep, float step,
+                                          const OrthoParams& p) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t at = box_piece(slot, lane, j);
@@ -238,11 +279,8 @@ __device__ __forceinline__ void apply_box(const float (&v)[kEpiCols], uint32_t s
       for (int i = 0; i < 8; ++i) x[i] += lo[i];
     }
     if constexpr (kTall) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(beta + 8 * j)),
-                   z = __ldcg(reinterpret_cast<const float4*>(beta + 8 * j + 4));
-      const float q[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = q[i];
+      for (int i = 0; i < 8; ++i) b[i] = bj.at(8 * j + i);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[i] = bm;
@@ -307,15 +345,29 @@ __device__ __forceinline__ void ragged_rows(uint32_t slot, int lane, int row0, i
   }
 }
 
-// One epilogue warp: the 32 accumulator rows of its lane quarter, box by box.
-template <OrthoOp Op, bool kTall>
+// An accumulator's box, as 64 values of the thread's row.
+__device__ __forceinline__ void load_acc_box(uint32_t taddr, float (&v)[kEpiCols]) {
+  uint32_t r0[32], r1[32];
+  tmem_ld_32x32b_x32(taddr, r0);
+  tmem_ld_32x32b_x32(taddr + 32, r1);
+  tmem_ld_wait();
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    v[e] = __uint_as_float(r0[e]);
+    v[32 + e] = __uint_as_float(r1[e]);
+  }
+}
+
+// One epilogue warp: the 32 accumulator rows of its lane quarter, the boxes of its half.
+template <OrthoOp Op, bool kTall, int BN>
 __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tfull0,
                                                uint32_t tempty0, uint32_t tempty_lead,
-                                               uint32_t boxes, uint32_t box_bar, int quarter,
-                                               int lane, int rank, int cid, int nclusters,
-                                               const WaitCtx& wc, const OrthoMaps& maps,
-                                               const OrthoParams& p) {
-  using Sm = OrthoSmem<Op>;
+                                               uint32_t slot, uint32_t box_bar, int ewarp,
+                                               int quarter, int lane, int rank, int cid,
+                                               int nclusters, const WaitCtx& wc,
+                                               const OrthoMaps& maps, const OrthoParams& p) {
+  using Sm = OrthoSmem<Op, BN>;
+  const int half = ewarp >> 2;
   const int row = (rank * kBM) + quarter * 32;  // of a tile's 256
   float keep = 0.0f, step = 0.0f;
   if (Op == OrthoOp::Last && p.w != nullptr) {
@@ -323,21 +375,29 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
     keep = 1.0f - lr * p.decay;
     step = lr * p.scale * kXInv;
   }
-  BoxWalk<Op> at, ahead;
-  at.u = ahead.u = cid;
-  at.enter(p);
-  ahead.enter(p);
-  int issued = 0;
+  BoxWalk<Op, BN> ahead;
+  ahead.u = cid;
+  ahead.find(half, p, nclusters);
+  bool coming = false;  // a box on its way into the slot
   if constexpr (Sm::loads) {
-    if (lane == 0)
-      for (; issued < 2 && ahead.u < p.units; ++issued, ahead.next(p, nclusters))
-        load_box<Op>(ahead, ahead.t.mp * 256 + row, boxes + issued * Sm::slot,
-                     box_bar + 8 * issued, maps, p);
+    if (ahead.u < p.units) {
+      if (lane == 0) load_box<Op, BN>(ahead, ahead.t.mp * 256 + row, slot, box_bar, maps, p);
+      coming = true;
+      ahead.next(half, p, nclusters);
+    }
   }
-  int it = 0, q = 0;
+  int it = 0;
+  uint32_t box_parity = 0;
   bool good = true;
-  while (good && at.u < p.units) {
+  for (int u = cid; u < p.units && good; u += nclusters, ++it) {
     const int buf = it & 1;
+    const OrthoTile t = ortho_tile<Op, BN>(u, p);
+    const int subs = ortho_boxes<Op, BN>(t, p);
+    const int row0 = t.mp * 256 + row, m = row0 + lane;
+    const size_t vec = static_cast<size_t>(t.b) * p.ldn;  // of diag and beta
+    float dm = 0.0f;  // the row's d or beta
+    if (Op == OrthoOp::Poly && m < p.n) dm = __ldcg(p.diag + vec + m);
+    if (!kSymmetric<Op> && !kTall && m < p.rows) dm = __ldcg(p.beta + vec + m);
     int ok = 1;
     if (lane == 0)
       ok = wait_bounded(tfull0 + 8 * buf, (it >> 1) & 1, wc, kSiteEpiAccFull) ? 1 : 0;
@@ -345,45 +405,98 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
     if (!ok) break;
     __syncwarp();
     tc_fence_after();
-    const OrthoTile t = at.t;
-    const int subs = at.subs;
-    const int row0 = t.mp * 256 + row, m = row0 + lane;
-    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kBN;
-    float dm = 0.0f;  // the row's d or beta
-    if (Op == OrthoOp::Poly && m < p.n)
-      dm = __ldcg(p.diag + static_cast<size_t>(t.b) * p.ldn + m);
-    if ((Op == OrthoOp::Apply || Op == OrthoOp::Last) && !kTall && m < p.rows)
-      dm = __ldcg(p.beta + static_cast<size_t>(t.b) * p.ldn + m);
+    const uint32_t tacc =
+        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * BN);
+    bool mine = true;  // this warp goes on with the boxes
+    float4* part = nullptr;
+    if (kSymmetric<Op> && t.parts > 1) {
+      // this range's sums, [tile][range][CTA][warp][box of the half][16][lane]
+      constexpr int kBoxes = BN / 128;
+      const size_t per_range = static_cast<size_t>(2 * kEpiWarps) * kBoxes * 16 * 32;
+      const size_t tile = static_cast<size_t>(u / t.parts);
+      part = p.partial + tile * t.parts * per_range +
+             static_cast<size_t>((rank * kEpiWarps + ewarp) * kBoxes) * 16 * 32 + lane;
+      for (int sub = half, i = 0; sub < subs; sub += 2, ++i) {
+        float v[kEpiCols];
+        load_acc_box(tacc + sub * kEpiCols, v);
+        float4* to = part + t.part * per_range + i * 16 * 32;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          to[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+      }
+      __threadfence();
+      __syncwarp();
+      int before = 0;
+      if (lane == 0) {
+        uint32_t* count = p.counts + (tile * 2 + rank) * kEpiWarps + ewarp;
+        before = static_cast<int>(atomicAdd(count, 1u));
+        if (before == t.parts - 1) *count = 0u;  // for the next product
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      __threadfence();
+      mine = before == t.parts - 1;
+    }
+    if (half >= subs || !mine) {  // no box of this tile, or no more to do with it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(tempty0 + 8 * buf);
+        else mbar_arrive_remote(tempty_lead + 8 * buf);
+      }
+      if (Sm::loads && half < subs && lane == 0) {  // its box has come for nothing
+        wait_drain(box_bar, box_parity, wc);
+      }
+      if (Sm::loads && half < subs) coming = false;  // split: a pair has one tile
+      continue;
+    }
 #pragma unroll 1
-    for (int sub = 0; sub < subs; ++sub, ++q) {
-      const int col = t.nt * kBN + sub * kEpiCols;
-      const uint32_t slot = boxes + (q & 1) * Sm::slot;
+    for (int sub = half; sub < subs; sub += 2) {
+      const int col = t.nt * BN + sub * kEpiCols;
+      ColumnPair cj{0.0f, 0.0f};
+      if (Op == OrthoOp::Poly || (!kSymmetric<Op> && kTall)) {
+        const float* c = (Op == OrthoOp::Poly ? p.diag : p.beta) + vec + col;
+        const int width = kSymmetric<Op> ? p.n : p.cols;
+        if (col + lane < width) cj.lo = __ldcg(c + lane);
+        if (col + 32 + lane < width) cj.hi = __ldcg(c + 32 + lane);
+      }
       if constexpr (Sm::loads) {
-        if (lane == 0)
-          ok = wait_bounded(box_bar + 8 * (q & 1), (q >> 1) & 1, wc, kSiteEpiAccFull) ? 1 : 0;
+        if (lane == 0) ok = wait_bounded(box_bar, box_parity, wc, kSiteEpiAccFull) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
           good = false;
           break;
         }
-        if (lane == 0) --issued;
+        box_parity ^= 1u;
+        coming = false;
       } else {
-        if (lane == 0) bulk_wait_read<1>();  // the slot's last store
+        if (lane == 0) bulk_wait_read<0>();  // the slot's last store
       }
       __syncwarp();
       float v[kEpiCols];
-      {
-        uint32_t r0[32], r1[32];
-        tmem_ld_32x32b_x32(tacc + sub * kEpiCols, r0);
-        tmem_ld_32x32b_x32(tacc + sub * kEpiCols + 32, r1);
-        tmem_ld_wait();
+      if (kSymmetric<Op> && t.parts > 1) {
+        constexpr size_t per_range = static_cast<size_t>(2 * kEpiWarps) * (BN / 128) * 16 * 32;
+        const float4* from = part + (sub >> 1) * 16 * 32;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] = __uint_as_float(r0[e]);
-          v[32 + e] = __uint_as_float(r1[e]);
+        for (int e = 0; e < kEpiCols; ++e) v[e] = 0.0f;
+        for (int r = 0; r < t.parts; ++r) {
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
+            float4 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __ldcg(from + r * per_range + (h + e) * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[4 * (h + e)] += x[e].x;
+              v[4 * (h + e) + 1] += x[e].y;
+              v[4 * (h + e) + 2] += x[e].z;
+              v[4 * (h + e) + 3] += x[e].w;
+            }
+          }
         }
+      } else {
+        load_acc_box(tacc + sub * kEpiCols, v);
       }
-      if (sub == subs - 1) {  // the accumulator is free
+      if (sub + 2 >= subs) {  // the accumulator is free
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -391,10 +504,10 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
           else mbar_arrive_remote(tempty_lead + 8 * buf);
         }
       }
-      if constexpr (Op == OrthoOp::Gram || Op == OrthoOp::Poly)
-        symmetric_box<Op>(v, slot, lane, m, col, t, dm, p);
+      if constexpr (kSymmetric<Op>)
+        symmetric_box<Op>(v, slot, lane, m, col, t, dm, cj, p);
       else
-        apply_box<Op, kTall>(v, slot, lane, col, t, dm, keep, step, p);
+        apply_box<Op, kTall>(v, slot, lane, dm, cj, keep, step, p);
       if (Op == OrthoOp::Last && p.ragged) {
         __syncwarp();
         ragged_rows(slot, lane, row0, col, t, keep, step, p);
@@ -402,11 +515,11 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        const int height = (Op == OrthoOp::Gram || Op == OrthoOp::Poly) ? p.n : p.rows;
+        const int height = kSymmetric<Op> ? p.n : p.rows;
         if (row0 < height) {
-          if constexpr (Op == OrthoOp::Gram || Op == OrthoOp::Poly) {
+          if constexpr (kSymmetric<Op>) {
             tma_store_3d(&maps.out0, slot, col, row0, t.b);
-            if (t.mp != t.nt) tma_store_3d(&maps.mirror, slot + kEpiBox, row0, col, t.b);
+            if (t.mirror) tma_store_3d(&maps.mirror, slot + kEpiBox, row0, col, t.b);
           } else if constexpr (Op == OrthoOp::Apply) {
             tma_store_3d(&maps.out0, slot, col, row0, t.b);
             if (p.low_out) tma_store_3d(&maps.out1, slot + kEpiBox, col, row0, t.b);
@@ -420,34 +533,30 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
           }
         }
         bulk_commit();
-        if constexpr (Sm::loads) {
-          if (ahead.u < p.units) {
+      }
+      if constexpr (Sm::loads) {
+        if (ahead.u < p.units) {
+          if (lane == 0) {
             bulk_wait_read<0>();
-            load_box<Op>(ahead, ahead.t.mp * 256 + row, slot, box_bar + 8 * (q & 1), maps, p);
-            ++issued;
-            ahead.next(p, nclusters);
+            load_box<Op, BN>(ahead, ahead.t.mp * 256 + row, slot, box_bar, maps, p);
           }
+          coming = true;
+          ahead.next(half, p, nclusters);
         }
       }
       __syncwarp();
     }
-    at.u += nclusters;
-    at.enter(p);
-    ++it;
   }
   if (lane == 0) {
-    // after an expired wait: the boxes that are still to come
-    if constexpr (Sm::loads)
-      for (int i = 0; i < issued; ++i, ++q)
-        wait_drain(box_bar + 8 * (q & 1), (q >> 1) & 1, wc);
+    if (Sm::loads && coming) wait_drain(box_bar, box_parity, wc);  // after an expired wait
     bulk_wait_all();
   }
 }
 
-template <OrthoOp Op, bool kTall>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+template <OrthoOp Op, bool kTall, int BN>
+__global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoMaps maps, const OrthoParams p) {
-  using Sm = OrthoSmem<Op>;
+  using Sm = OrthoSmem<Op, BN>;
   constexpr int S = Sm::stages;
   constexpr bool a_mn = OrthoMajor<Op, kTall>::a_mn, b_mn = OrthoMajor<Op, kTall>::b_mn;
   extern __shared__ uint8_t smem_raw[];
@@ -456,7 +565,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t sA0 = base;
   const uint32_t sB0 = base + S * kPairAStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kPairStageBytes + Sm::epi);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * Sm::stage + Sm::epi);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const uint32_t full0 = smem_u32(bars);
@@ -464,7 +573,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tfull0 = smem_u32(bars + 2 * S);
   const uint32_t tempty0 = smem_u32(bars + 2 * S + 2);
   const uint32_t drain = smem_u32(bars + 2 * S + 4);
-  const uint32_t box0 = smem_u32(bars + 2 * S + 5);  // two slots of four epilogue warps
+  const uint32_t box0 = smem_u32(bars + 2 * S + 5);  // the epilogue warps' slots
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -480,10 +589,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 8);
+      mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < 8; ++i) mbar_init(box0 + 8 * i, 1);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(box0 + 8 * i, 1);
     *abort_flag = 0u;
     mbar_fence_init();
     tma_prefetch_desc(&maps.a);
@@ -491,7 +600,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (Sm::loads) tma_prefetch_desc(&maps.in0);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_alloc_pair(smem_u32(tmem_slot), 2 * BN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -513,20 +622,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t armed = 0, armed_par = 0;
       bool skip_once = p.fault_inject != 0 && cid == 0 && leader;
       for (int u = cid; u < p.units; u += nclusters) {
-        const OrthoTile t = ortho_tile<Op>(u, p);
-        const int ra = (t.mp * 2 + rank) * kBM, rb = t.nt * kBN + 128 * rank;
+        const OrthoTile t = ortho_tile<Op, BN>(u, p);
+        const int ra = (t.mp * 2 + rank) * kBM, rb = t.nt * BN + BN / 2 * rank;
+        int kb0, kb1;
+        ortho_range(t, p.num_kb, kb0, kb1);
         bool ok = true;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
             break;
           }
-          const uint32_t sa = sA0 + stage * kPairAStage, sb = sB0 + stage * kPairBStage;
+          const uint32_t sa = sA0 + stage * kPairAStage, sb = sB0 + stage * Sm::b_stage;
           if (skip_once) {
             skip_once = false;  // fault injection: this stage is never armed
           } else if (leader) {
             const uint32_t fb = full0 + 8 * stage;
-            mbar_arrive_expect_tx(fb, 2 * kPairStageBytes);
+            mbar_arrive_expect_tx(fb, 2 * Sm::stage);
             ortho_load<a_mn, false>(sa, &maps.a, fb, kb * kBK, ra, t.b);
             ortho_load<b_mn, false>(sb, &maps.b, fb, kb * kBK, rb, t.b);
             armed |= 1u << stage;
@@ -557,7 +668,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---------------------------------------------------------------- MMA issuer (pair)
-      constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, kBN, a_mn, b_mn);
+      constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN, a_mn, b_mn);
       const uint64_t adesc0 = a_mn ? sdesc(sA0, kChunk, 1024, 2u) : sdesc(sA0, 16, 1024, 2u);
       const uint64_t bdesc0 = b_mn ? sdesc(sB0, kChunk, 1024, 2u) : sdesc(sB0, 16, 1024, 2u);
       constexpr uint32_t kAk = (a_mn ? 2048u : 32u) >> 4, kBk = (b_mn ? 2048u : 32u) >> 4;
@@ -569,20 +680,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t acc_par = (it >> 1) & 1;
         if (!wait_bounded(tempty0 + 8 * buf, acc_par ^ 1u, wc, kSiteMmaAccEmpty)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + buf * kBN;
+        const uint32_t d = tmem_base + buf * BN;
+        const OrthoTile t = ortho_tile<Op, BN>(u, p);
+        int kb0, kb1;
+        ortho_range(t, p.num_kb, kb0, kb1);
         bool ok = true;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(full0 + 8 * stage, phase, wc, kSiteMmaFull)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t as = adesc0 + static_cast<uint32_t>(stage) * (kPairAStage >> 4);
-          const uint64_t bs = bdesc0 + static_cast<uint32_t>(stage) * (kPairBStage >> 4);
+          const uint64_t bs = bdesc0 + static_cast<uint32_t>(stage) * (Sm::b_stage >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16_pair(d, as + kk * kAk, bs + kk * kBk, idesc,
-                           (kb != 0 || kk != 0) ? 1u : 0u);
+                           (kb != kb0 || kk != 0) ? 1u : 0u);
           umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
           if (++stage == S) {
             stage = 0;
@@ -597,10 +711,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    ortho_epilogue<Op, kTall>(tmem_base, tfull0, tempty0, tempty_lead,
-                              base + S * kPairStageBytes + (warp - 2) * 2 * Sm::slot,
-                              box0 + 16 * (warp - 2), warp & 3, lane, rank, cid, nclusters, wc,
-                              maps, p);
+    ortho_epilogue<Op, kTall, BN>(tmem_base, tfull0, tempty0, tempty_lead,
+                                  base + S * Sm::stage + (warp - 2) * Sm::slot,
+                                  box0 + 8 * (warp - 2), warp - 2, warp & 3, lane, rank, cid,
+                                  nclusters, wc, maps, p);
   }
 
   tc_fence_before();
@@ -609,23 +723,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   cluster_sync();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc_pair(tmem_base, kTmemCols);
+    tmem_dealloc_pair(tmem_base, 2 * BN);
   }
 }
 
-using OrthoKernel = void (*)(const OrthoMaps, const OrthoParams);
-
 template <OrthoOp Op, bool kTall>
 static cudaError_t attr_of() {
-  return cudaFuncSetAttribute(ortho_kernel<Op, kTall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              OrthoSmem<Op>::bytes);
+  const cudaError_t e =
+      cudaFuncSetAttribute(ortho_kernel<Op, kTall, 128>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, OrthoSmem<Op, 128>::bytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(ortho_kernel<Op, kTall, 256>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 OrthoSmem<Op, 256>::bytes);
 }
 
 // Launched so that it may begin while the kernel before it ends (pdl_wait).
 static void ortho_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clusters, int smem,
                          cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2), 1, 1);
-  cfg.blockDim = dim3(kGemmThreads, 1, 1);
+  cfg.blockDim = dim3(kOrthoThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -643,8 +760,10 @@ static cudaError_t launch_as(const OrthoMaps& m, const OrthoParams& p, int clust
                              cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  ortho_config(cfg, attr, clusters, OrthoSmem<Op>::bytes, s);
-  return cudaLaunchKernelEx(&cfg, ortho_kernel<Op, kTall>, m, p);
+  ortho_config(cfg, attr, clusters,
+               p.narrow ? OrthoSmem<Op, 128>::bytes : OrthoSmem<Op, 256>::bytes, s);
+  return p.narrow ? cudaLaunchKernelEx(&cfg, ortho_kernel<Op, kTall, 128>, m, p)
+                  : cudaLaunchKernelEx(&cfg, ortho_kernel<Op, kTall, 256>, m, p);
 }
 
 cudaError_t ortho_set_attrs(int* max_clusters) {
@@ -656,9 +775,10 @@ cudaError_t ortho_set_attrs(int* max_clusters) {
     if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  ortho_config(cfg, attr, 2, OrthoSmem<OrthoOp::Last>::bytes, nullptr);
+  ortho_config(cfg, attr, 2, OrthoSmem<OrthoOp::Last, 256>::bytes, nullptr);
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(max_clusters, ortho_kernel<OrthoOp::Last, false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_clusters, ortho_kernel<OrthoOp::Last, false, 256>,
+                                        &cfg);
 }
 
 cudaError_t launch_ortho(OrthoOp op, bool tall, const OrthoMaps& m, const OrthoParams& p,

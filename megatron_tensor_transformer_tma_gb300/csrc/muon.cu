@@ -37,8 +37,56 @@ struct Layout {
   float4* part;
   __half *x0, *x1, *xl, *e, *d;
   float *diag, *beta;
+  float4* partial;
+  uint32_t* counts;
   size_t bytes;
 };
+
+// The tiles of a product over all matrices.
+struct Tiling {
+  int narrow, num_pm, num_n, per_matrix, split, units, num_kb;
+  int tiles() const { return units / split; }
+};
+
+// Tiles of 128 columns where those of 256 would be fewer than two for each pair of SMs: twice the
+// tiles keep the pairs evenly busy and leave half the epilogue after the last product.
+bool ortho_narrow(int64_t wide_tiles, int clusters) { return wide_tiles < 2 * clusters; }
+
+Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, int64_t depth) {
+  const int64_t batch = h->cfg.batch;
+  Tiling t;
+  t.num_pm = static_cast<int>(cdiv(rows, 256));
+  auto count = [&](int bn) {
+    t.num_n = static_cast<int>(cdiv(cols, bn));
+    if (!symmetric) return t.num_pm * t.num_n;
+    const int r = 256 / bn;  // the last row of tiles may lack some at its end
+    return r * t.num_pm * (t.num_pm + 1) / 2 - (r * t.num_pm - t.num_n);
+  };
+  t.per_matrix = count(256);
+  t.narrow = ortho_narrow(batch * t.per_matrix, h->max_clusters) ? 1 : 0;
+  if (t.narrow) t.per_matrix = count(128);
+  t.num_kb = static_cast<int>(cdiv(depth, kBK));
+  const int tiles = static_cast<int>(batch) * t.per_matrix;
+  t.split = 1;
+  // Ranges of K: no more than fill the pairs, none shorter than four k-blocks, and no more than
+  // balance a k-block's time with that of adding a range's sums (about one and a half of it).
+  if (symmetric && 2 * tiles <= h->max_clusters) {
+    const int balance = static_cast<int>(std::sqrt(t.num_kb / 1.5));
+    t.split = std::max(1, std::min({h->max_clusters / tiles, t.num_kb / 4, balance}));
+  }
+  t.units = tiles * t.split;
+  return t;
+}
+
+Tiling gram_tiling(const mlpb_muon* h) {
+  return tiling(h, true, h->n, h->n, std::max(h->cfg.rows, h->cfg.cols));
+}
+Tiling poly_tiling(const mlpb_muon* h) { return tiling(h, true, h->n, h->n, h->n); }
+Tiling apply_tiling(const mlpb_muon* h) {
+  return tiling(h, false, h->cfg.rows, h->cfg.cols, h->n);
+}
+
+constexpr int kCounts = 16;  // counters of a tile: two CTAs' epilogue warps
 
 Layout layout(const mlpb_muon* h, void* workspace) {
   const mlpb_muon_config& c = h->cfg;
@@ -62,6 +110,15 @@ Layout layout(const mlpb_muon* h, void* workspace) {
   l.d = reinterpret_cast<__half*>(take(s));
   l.diag = reinterpret_cast<float*>(take(v));
   l.beta = reinterpret_cast<float*>(take(v));
+  const Tiling gram = gram_tiling(h), poly = poly_tiling(h);
+  l.partial = nullptr;
+  l.counts = nullptr;
+  if (gram.split > 1 || poly.split > 1) {
+    const int units = std::max(gram.split > 1 ? gram.units : 0, poly.split > 1 ? poly.units : 0);
+    l.partial = reinterpret_cast<float4*>(
+        take(static_cast<size_t>(units) * 256 * (gram.narrow ? 128 : 256) * 4));
+    l.counts = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(gram.tiles()) * kCounts * 4));
+  }
   l.bytes = at;
   return l;
 }
@@ -92,19 +149,20 @@ bool map_box(const mlpb_muon* h, CUtensorMap* m, const Matrices& x, CUtensorMapD
                 swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// As operands whose K runs along a row: 128 rows by 64 columns.
-bool map_k(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
-  return map_box(h, m, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, kBK, kBM, true);
+// As operands whose K runs along a row: `size` (128 or 64) rows by 64 columns.
+bool map_k(const mlpb_muon* h, CUtensorMap* m, const Matrices& x, int size) {
+  return map_box(h, m, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, kBK, static_cast<uint32_t>(size),
+                 true);
 }
 
-// With K along a column: two 64-wide chunks of 64 rows.
-bool map_mn(const mlpb_muon* h, CUtensorMap* m, const Matrices& x) {
+// With K along a column: `size` / 64 chunks, 64 wide, of 64 rows.
+bool map_mn(const mlpb_muon* h, CUtensorMap* m, const Matrices& x, int size) {
   const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(x.rows),
                               static_cast<cuuint64_t>(x.ld / 64),
                               static_cast<cuuint64_t>(h->cfg.batch)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.ld) * 2, 128,
                                  static_cast<cuuint64_t>(x.rows) * x.ld * 2};
-  const cuuint32_t box[4] = {64, kBK, 2, 1};
+  const cuuint32_t box[4] = {64, kBK, static_cast<cuuint32_t>(size / 64), 1};
   return encode(h, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x.base, 4, dims, strides, box,
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
@@ -131,18 +189,21 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   const Matrices low{l.xl, c.rows, c.cols, h->ldx};
   const Matrices e{l.e, h->n, h->n, h->ldn}, d{l.d, h->n, h->n, h->ldn};
   OrthoMaps gram[2], poly, apply[2], last;  // by the buffer that X is in
-  bool ok = map_k(h, &poly.a, e) && map_tile(h, &poly.in0, e) && map_tile(h, &poly.out0, d) &&
-            map_mirror(h, &poly.mirror, d);
-  poly.b = poly.in1 = poly.out1 = poly.a;
+  const Tiling tg = gram_tiling(h), tp = poly_tiling(h), ta = apply_tiling(h);
+  const int bs = tg.narrow ? 64 : 128, ba = ta.narrow ? 64 : 128;  // a CTA's rows of B
+  bool ok = map_k(h, &poly.a, e, 128) && map_k(h, &poly.b, e, bs) && map_tile(h, &poly.in0, e) &&
+            map_tile(h, &poly.out0, d) && map_mirror(h, &poly.mirror, d);
+  poly.in1 = poly.out1 = poly.a;
   const int buffers = c.steps > 1 ? 2 : 1;
   for (int i = 0; i < buffers && ok; ++i) {
     OrthoMaps& g = gram[i];
     OrthoMaps& y = apply[i];
-    ok = (h->tall ? map_mn(h, &g.a, x[i]) : map_k(h, &g.a, x[i])) && map_tile(h, &g.out0, e) &&
-         map_mirror(h, &g.mirror, e);
-    g.b = g.in0 = g.in1 = g.out1 = g.a;
-    ok = ok && (h->tall ? map_k(h, &y.a, x[i]) && map_k(h, &y.b, d)
-                        : map_k(h, &y.a, d) && map_mn(h, &y.b, x[i])) &&
+    ok = (h->tall ? map_mn(h, &g.a, x[i], 128) && map_mn(h, &g.b, x[i], bs)
+                  : map_k(h, &g.a, x[i], 128) && map_k(h, &g.b, x[i], bs)) &&
+         map_tile(h, &g.out0, e) && map_mirror(h, &g.mirror, e);
+    g.in0 = g.in1 = g.out1 = g.a;
+    ok = ok && (h->tall ? map_k(h, &y.a, x[i], 128) && map_k(h, &y.b, d, ba)
+                        : map_k(h, &y.a, d, 128) && map_mn(h, &y.b, x[i], ba)) &&
          map_tile(h, &y.in0, x[i]) && map_tile(h, &y.in1, low) && map_tile(h, &y.out0, x[1 - i]);
     y.out1 = y.mirror = y.in1;
   }
@@ -158,7 +219,8 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
                    2, 64, 32, true);
   }
   if (!ok || launch_muon_norm(in, l.part, s) != cudaSuccess ||
-      launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, s) != cudaSuccess)
+      launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, l.counts,
+                        l.counts ? tg.tiles() * kCounts : 0, s) != cudaSuccess)
     return MLPB_ECUDA;
   p.batch = static_cast<int>(c.batch);
   p.rows = static_cast<int>(c.rows);
@@ -171,26 +233,25 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   p.wait_ns = kDefaultWaitNs;
   p.fault_inject = h->fault_pending ? 1 : 0;
   h->fault_pending = false;
-  const int tiles = static_cast<int>(cdiv(h->n, 256));
-  for (int i = 0; i < c.steps; ++i) {
-    const bool is_last = i == c.steps - 1;
-    p.num_pm = p.num_n = tiles;
-    p.units = p.batch * (tiles * (tiles + 1) / 2);
-    p.num_kb = static_cast<int>(cdiv(h->tall ? c.rows : c.cols, kBK));
-    if (launch_ortho(OrthoOp::Gram, h->tall, gram[i & 1], p, std::min(p.units, h->max_clusters),
-                     s) != cudaSuccess)
-      return MLPB_ECUDA;
+  p.partial = l.partial;
+  p.counts = l.counts;
+  auto run = [&](OrthoOp op, const Tiling& t, const OrthoMaps& maps) {
+    p.narrow = t.narrow;
+    p.num_pm = t.num_pm;
+    p.num_n = t.num_n;
+    p.per_matrix = t.per_matrix;
+    p.split = t.split;
+    p.units = t.units;
+    p.num_kb = t.num_kb;
+    const cudaError_t err =
+        launch_ortho(op, h->tall, maps, p, std::min(t.units, h->max_clusters), s);
     p.fault_inject = 0;
-    p.num_kb = static_cast<int>(cdiv(h->n, kBK));
-    if (launch_ortho(OrthoOp::Poly, h->tall, poly, p, std::min(p.units, h->max_clusters), s) !=
-        cudaSuccess)
-      return MLPB_ECUDA;
-    p.num_pm = static_cast<int>(cdiv(c.rows, 256));
-    p.num_n = static_cast<int>(cdiv(c.cols, 256));
-    p.units = p.batch * p.num_pm * p.num_n;
+    return err == cudaSuccess;
+  };
+  for (int i = 0; i < c.steps; ++i) {
     p.low_out = i < c.steps - 2 ? 1 : 0;
-    if (launch_ortho(is_last ? OrthoOp::Last : OrthoOp::Apply, h->tall, is_last ? last : apply[i & 1],
-                     p, std::min(p.units, h->max_clusters), s) != cudaSuccess)
+    if (!run(OrthoOp::Gram, tg, gram[i & 1]) || !run(OrthoOp::Poly, tp, poly) ||
+        !(i == c.steps - 1 ? run(OrthoOp::Last, ta, last) : run(OrthoOp::Apply, ta, apply[i & 1])))
       return MLPB_ECUDA;
   }
   return MLPB_OK;

@@ -43,9 +43,14 @@ enum class OrthoOp : int {
 struct OrthoParams {
   int batch, rows, cols, n;  // n = min(rows, cols)
   int ldn;                   // elements of a row of E, D, diag and beta
-  int num_pm, num_n;         // 256-row and 256-column tiles of a matrix
-  int units;                 // tiles of all matrices (on and below the diagonal for Gram, Poly)
+  int narrow;                // tiles of 128 columns, not 256
+  int num_pm, num_n;         // 256-row tiles and column tiles of a matrix
+  int per_matrix;            // tiles of a matrix (on and below the diagonal for Gram, Poly)
+  int split;                 // Gram, Poly: ranges of K; then no more units than pairs
+  int units;                 // tiles of all matrices, times split
   int num_kb;                // 64-deep k-blocks
+  float4* partial;           // the ranges' sums
+  uint32_t* counts;          // ranges that are done, for each tile, CTA and epilogue warp; zeros
   float a, b, c;
   float* diag;  // d [batch][ldn]
   float* beta;  // [batch][ldn]
@@ -88,7 +93,8 @@ struct MuonInput {
 int muon_partials(int64_t elems, int64_t batch);
 cudaError_t launch_muon_norm(const MuonInput& in, float4* part, cudaStream_t s);
 cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* xh, __half* xh_other,
-                              __half* xl, int ldx, cudaStream_t s);
+                              __half* xl, int ldx, uint32_t* counts, int num_counts,
+                              cudaStream_t s);  // and counts = 0
 
 // muon_small.cu: the whole update in one launch, for n <= 128 and lengths that a cluster's shared
 // memory holds; 0 CTAs: it does not.
