@@ -204,29 +204,44 @@ __device__ __forceinline__ void load_box(const BoxWalk<Op, BN>& w, int row0, uin
 // Vectors along a box's columns are held by the warp, two elements a lane.
 struct ColumnPair {
   float lo, hi;  // of columns lane, 32 + lane
-  __device__ __forceinline__ float at(int e) const {
-    return __shfl_sync(0xffffffffu, e < 32 ? lo : hi, e & 31);
+  // of column e of the half box that begins with piece j0
+  __device__ __forceinline__ float at(int j0, int e) const {
+    return __shfl_sync(0xffffffffu, j0 == 0 ? lo : hi, e);
   }
 };
 
-// A box of a symmetric product: rows m of the thread, 64 columns; the diagonal's element apart.
+// The same box into L2, before its slot is free.
+template <OrthoOp Op, int BN>
+__device__ __forceinline__ void prefetch_box(const BoxWalk<Op, BN>& w, int row0,
+                                             const OrthoMaps& m, const OrthoParams& p) {
+  const int col = w.t.nt * BN + w.sub * kEpiCols;
+  tma_prefetch_3d(&m.in0, col, row0, w.t.b);
+  if (Op == OrthoOp::Apply || (Op == OrthoOp::Last && p.w != nullptr && !p.ragged)) {
+    tma_prefetch_3d(&m.in1, col, row0, w.t.b);
+    if (Op == OrthoOp::Last) tma_prefetch_3d(&m.in1, col + 32, row0, w.t.b);
+  }
+}
+
+// Half a box of a symmetric product (pieces j0 to j0 + 3 of the thread's row m); the diagonal's
+// element apart.
 template <OrthoOp Op>
-__device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slot, int lane, int m,
-                                              int col, const OrthoTile& t, float dm,
+__device__ __forceinline__ void symmetric_box(float (&v)[32], int j0, uint32_t slot, int lane,
+                                              int m, int col, const OrthoTile& t, float dm,
                                               const ColumnPair& dj, const OrthoParams& p) {
   if constexpr (Op == OrthoOp::Gram) {
 #pragma unroll
-    for (int e = 0; e < kEpiCols; ++e) v[e] *= kXInv;  // A times 2^12
+    for (int e = 0; e < 32; ++e) v[e] *= kXInv;  // A times 2^12
   }
   if (!t.mirror) {
+    const int on = m - col - 8 * j0;
     float d = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kEpiCols; ++e)
-      if (col + e == m) {
+    for (int e = 0; e < 32; ++e)
+      if (e == on) {
         d = v[e];
         v[e] = 0.0f;
       }
-    if (m >= col && m < col + kEpiCols && m < p.n) {
+    if (on >= 0 && on < 32 && m < p.n) {
       const size_t at = static_cast<size_t>(t.b) * p.ldn + m;
       if constexpr (Op == OrthoOp::Gram)
         p.diag[at] = d * kXInv;
@@ -236,7 +251,8 @@ __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slo
     __syncwarp();
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int q = 0; q < 4; ++q) {
+    const int j = j0 + q;
     float r[8];
     const uint32_t at = box_piece(slot, lane, j);
     if constexpr (Op == OrthoOp::Poly) {
@@ -244,12 +260,12 @@ __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slo
       unpack_half8(lds16(at), e16);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float lin = fmaf(p.c, dm + dj.at(8 * j + i), p.b) * (kXInv * kDScale);
-        r[i] = fmaf(lin, e16[i], (p.c * (kEEInv * kDScale)) * v[8 * j + i]);
+        const float lin = fmaf(p.c, dm + dj.at(j0, 8 * q + i), p.b) * (kXInv * kDScale);
+        r[i] = fmaf(lin, e16[i], (p.c * (kEEInv * kDScale)) * v[8 * q + i]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = v[8 * j + i];
+      for (int i = 0; i < 8; ++i) r[i] = v[8 * q + i];
     }
     const uint4 h = pack_half8(r);
     sts16(at, h);
@@ -262,13 +278,14 @@ __device__ __forceinline__ void symmetric_box(float (&v)[kEpiCols], uint32_t slo
   }
 }
 
-// A box of X' or of the result.
+// Half a box of X' or of the result.
 template <OrthoOp Op, bool kTall>
-__device__ __forceinline__ void apply_box(const float (&v)[kEpiCols], uint32_t slot, int lane,
+__device__ __forceinline__ void apply_box(const float (&v)[32], int j0, uint32_t slot, int lane,
                                           float bm, const ColumnPair& bj, float keep, float step,
                                           const OrthoParams& p) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int q = 0; q < 4; ++q) {
+    const int j = j0 + q;
     const uint32_t at = box_piece(slot, lane, j);
     float x[8], b[8], r[8];
     unpack_half8(lds16(at), x);
@@ -280,13 +297,13 @@ __device__ __forceinline__ void apply_box(const float (&v)[kEpiCols], uint32_t s
     }
     if constexpr (kTall) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = bj.at(8 * j + i);
+      for (int i = 0; i < 8; ++i) b[i] = bj.at(j0, 8 * q + i);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[i] = bm;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = fmaf(b[i], x[i], v[8 * j + i] * (1.0f / kDScale));
+    for (int i = 0; i < 8; ++i) r[i] = fmaf(b[i], x[i], v[8 * q + i] * (1.0f / kDScale));
     if constexpr (Op == OrthoOp::Apply) {  // X' times 2^12, in two parts
       sts16(at, pack_half8(r));
       if (p.low_out) {
@@ -342,19 +359,6 @@ __device__ __forceinline__ void ragged_rows(uint32_t slot, int lane, int row0, i
         if (p.wb != nullptr) p.wb[o + c] = __float2bfloat16_rn(w);
       }
     }
-  }
-}
-
-// An accumulator's box, as 64 values of the thread's row.
-__device__ __forceinline__ void load_acc_box(uint32_t taddr, float (&v)[kEpiCols]) {
-  uint32_t r0[32], r1[32];
-  tmem_ld_32x32b_x32(taddr, r0);
-  tmem_ld_32x32b_x32(taddr + 32, r1);
-  tmem_ld_wait();
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    v[e] = __uint_as_float(r0[e]);
-    v[32 + e] = __uint_as_float(r1[e]);
   }
 }
 
@@ -417,12 +421,15 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
       part = p.partial + tile * t.parts * per_range +
              static_cast<size_t>((rank * kEpiWarps + ewarp) * kBoxes) * 16 * 32 + lane;
       for (int sub = half, i = 0; sub < subs; sub += 2, ++i) {
-        float v[kEpiCols];
-        load_acc_box(tacc + sub * kEpiCols, v);
         float4* to = part + t.part * per_range + i * 16 * 32;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          to[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        for (int h = 0; h < 2; ++h) {
+          float v[32];
+          tmem_load_f32x32(tacc + sub * kEpiCols + 32 * h, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            to[(8 * h + e) * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
       }
       __threadfence();
       __syncwarp();
@@ -468,46 +475,50 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
         }
         box_parity ^= 1u;
         coming = false;
+        if (lane == 0 && ahead.u < p.units)
+          prefetch_box<Op, BN>(ahead, ahead.t.mp * 256 + row, maps, p);
       } else {
         if (lane == 0) bulk_wait_read<0>();  // the slot's last store
       }
       __syncwarp();
-      float v[kEpiCols];
-      if (kSymmetric<Op> && t.parts > 1) {
-        constexpr size_t per_range = static_cast<size_t>(2 * kEpiWarps) * (BN / 128) * 16 * 32;
-        const float4* from = part + (sub >> 1) * 16 * 32;
 #pragma unroll
-        for (int e = 0; e < kEpiCols; ++e) v[e] = 0.0f;
-        for (int r = 0; r < t.parts; ++r) {
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        if (kSymmetric<Op> && t.parts > 1) {
+          constexpr size_t per_range = static_cast<size_t>(2 * kEpiWarps) * (BN / 128) * 16 * 32;
+          const float4* from = part + ((sub >> 1) * 16 + 8 * h) * 32;
 #pragma unroll
-          for (int h = 0; h < 16; h += 8) {
+          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+#pragma unroll 2
+          for (int r = 0; r < t.parts; ++r) {
             float4 x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __ldcg(from + r * per_range + (h + e) * 32);
+            for (int e = 0; e < 8; ++e) x[e] = __ldcg(from + r * per_range + e * 32);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              v[4 * (h + e)] += x[e].x;
-              v[4 * (h + e) + 1] += x[e].y;
-              v[4 * (h + e) + 2] += x[e].z;
-              v[4 * (h + e) + 3] += x[e].w;
+              v[4 * e] += x[e].x;
+              v[4 * e + 1] += x[e].y;
+              v[4 * e + 2] += x[e].z;
+              v[4 * e + 3] += x[e].w;
             }
           }
+        } else {
+          tmem_load_f32x32(tacc + sub * kEpiCols + 32 * h, v);
         }
-      } else {
-        load_acc_box(tacc + sub * kEpiCols, v);
-      }
-      if (sub + 2 >= subs) {  // the accumulator is free
-        tc_fence_before();
+        if (h == 1 && sub + 2 >= subs) {  // the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive(tempty0 + 8 * buf);
+            else mbar_arrive_remote(tempty_lead + 8 * buf);
+          }
+        }
+        if constexpr (kSymmetric<Op>)
+          symmetric_box<Op>(v, 4 * h, slot, lane, m, col, t, dm, cj, p);
+        else
+          apply_box<Op, kTall>(v, 4 * h, slot, lane, dm, cj, keep, step, p);
         __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(tempty0 + 8 * buf);
-          else mbar_arrive_remote(tempty_lead + 8 * buf);
-        }
       }
-      if constexpr (kSymmetric<Op>)
-        symmetric_box<Op>(v, slot, lane, m, col, t, dm, cj, p);
-      else
-        apply_box<Op, kTall>(v, slot, lane, dm, cj, keep, step, p);
       if (Op == OrthoOp::Last && p.ragged) {
         __syncwarp();
         ragged_rows(slot, lane, row0, col, t, keep, step, p);

@@ -42,40 +42,57 @@ struct Layout {
   size_t bytes;
 };
 
+constexpr int kMaxSplit = 16;
+
 // The tiles of a product over all matrices.
 struct Tiling {
   int narrow, num_pm, num_n, per_matrix, split, units, num_kb;
   int tiles() const { return units / split; }
+  size_t partial_bytes() const {
+    return split > 1 ? static_cast<size_t>(units) * 256 * (narrow ? 128 : 256) * 4 : 0;
+  }
 };
 
-// Tiles of 128 columns where those of 256 would be fewer than two for each pair of SMs: twice the
-// tiles keep the pairs evenly busy and leave half the epilogue after the last product.
-bool ortho_narrow(int64_t wide_tiles, int clusters) { return wide_tiles < 2 * clusters; }
-
+// Tiles of 256 or 128 columns, and for the symmetric products ranges of K: what is estimated to
+// end first, in the time of a k-block (0.26 us).  That is the same for both widths: a ring of five
+// or six stages keeps up with 256 columns and no more, so that narrow tiles pay where they are all
+// in the first wave and leave half the epilogue (a box of 64 columns for each of its warps: four
+// k-blocks) after the last product.  Ranges cost the sums' way through L2 and one addition for
+// each.
 Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, int64_t depth) {
   const int64_t batch = h->cfg.batch;
-  Tiling t;
-  t.num_pm = static_cast<int>(cdiv(rows, 256));
-  auto count = [&](int bn) {
+  Tiling best{};
+  double least = 0.0;
+  for (int narrow = 0; narrow < 2; ++narrow) {
+    const int bn = narrow ? 128 : 256;
+    Tiling t;
+    t.narrow = narrow;
+    t.num_pm = static_cast<int>(cdiv(rows, 256));
     t.num_n = static_cast<int>(cdiv(cols, bn));
-    if (!symmetric) return t.num_pm * t.num_n;
-    const int r = 256 / bn;  // the last row of tiles may lack some at its end
-    return r * t.num_pm * (t.num_pm + 1) / 2 - (r * t.num_pm - t.num_n);
-  };
-  t.per_matrix = count(256);
-  t.narrow = ortho_narrow(batch * t.per_matrix, h->max_clusters) ? 1 : 0;
-  if (t.narrow) t.per_matrix = count(128);
-  t.num_kb = static_cast<int>(cdiv(depth, kBK));
-  const int tiles = static_cast<int>(batch) * t.per_matrix;
-  t.split = 1;
-  // Ranges of K: no more than fill the pairs, none shorter than four k-blocks, and no more than
-  // balance a k-block's time with that of adding a range's sums (about one and a half of it).
-  if (symmetric && 2 * tiles <= h->max_clusters) {
-    const int balance = static_cast<int>(std::sqrt(t.num_kb / 1.5));
-    t.split = std::max(1, std::min({h->max_clusters / tiles, t.num_kb / 4, balance}));
+    t.num_kb = static_cast<int>(cdiv(depth, kBK));
+    t.per_matrix = t.num_pm * t.num_n;
+    if (symmetric) {
+      const int r = 256 / bn;  // the last row of tiles may lack some at its end
+      t.per_matrix = r * t.num_pm * (t.num_pm + 1) / 2 - (r * t.num_pm - t.num_n);
+    }
+    const int64_t tiles = batch * t.per_matrix;
+    const int boxes = narrow ? 1 : 2;
+    for (t.split = 1; t.split <= kMaxSplit; ++t.split) {
+      if (t.split > 1 && (!symmetric || tiles * t.split > h->max_clusters ||
+                          t.split > t.num_kb))
+        break;
+      t.units = static_cast<int>(tiles) * t.split;
+      double cost = static_cast<double>(cdiv(t.units, h->max_clusters)) *
+                        cdiv(t.num_kb, t.split) +
+                    4.0 * boxes;
+      if (t.split > 1) cost += 5.0 + 0.7 * t.split * boxes;
+      if (best.split == 0 || cost < least) {
+        best = t;
+        least = cost;
+      }
+    }
   }
-  t.units = tiles * t.split;
-  return t;
+  return best;
 }
 
 Tiling gram_tiling(const mlpb_muon* h) {
@@ -86,7 +103,10 @@ Tiling apply_tiling(const mlpb_muon* h) {
   return tiling(h, false, h->cfg.rows, h->cfg.cols, h->n);
 }
 
-constexpr int kCounts = 16;  // counters of a tile: two CTAs' epilogue warps
+// Counters of ranges that are done: of each tile, for two CTAs' eight epilogue warps.
+size_t count_bytes(const mlpb_muon* h) {
+  return static_cast<size_t>(std::max(gram_tiling(h).tiles(), poly_tiling(h).tiles())) * 16 * 4;
+}
 
 Layout layout(const mlpb_muon* h, void* workspace) {
   const mlpb_muon_config& c = h->cfg;
@@ -114,10 +134,8 @@ Layout layout(const mlpb_muon* h, void* workspace) {
   l.partial = nullptr;
   l.counts = nullptr;
   if (gram.split > 1 || poly.split > 1) {
-    const int units = std::max(gram.split > 1 ? gram.units : 0, poly.split > 1 ? poly.units : 0);
-    l.partial = reinterpret_cast<float4*>(
-        take(static_cast<size_t>(units) * 256 * (gram.narrow ? 128 : 256) * 4));
-    l.counts = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(gram.tiles()) * kCounts * 4));
+    l.partial = reinterpret_cast<float4*>(take(std::max(gram.partial_bytes(), poly.partial_bytes())));
+    l.counts = reinterpret_cast<uint32_t*>(take(count_bytes(h)));
   }
   l.bytes = at;
   return l;
@@ -190,16 +208,17 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   const Matrices e{l.e, h->n, h->n, h->ldn}, d{l.d, h->n, h->n, h->ldn};
   OrthoMaps gram[2], poly, apply[2], last;  // by the buffer that X is in
   const Tiling tg = gram_tiling(h), tp = poly_tiling(h), ta = apply_tiling(h);
-  const int bs = tg.narrow ? 64 : 128, ba = ta.narrow ? 64 : 128;  // a CTA's rows of B
-  bool ok = map_k(h, &poly.a, e, 128) && map_k(h, &poly.b, e, bs) && map_tile(h, &poly.in0, e) &&
+  // a CTA's rows of B
+  const int bg = tg.narrow ? 64 : 128, bp = tp.narrow ? 64 : 128, ba = ta.narrow ? 64 : 128;
+  bool ok = map_k(h, &poly.a, e, 128) && map_k(h, &poly.b, e, bp) && map_tile(h, &poly.in0, e) &&
             map_tile(h, &poly.out0, d) && map_mirror(h, &poly.mirror, d);
   poly.in1 = poly.out1 = poly.a;
   const int buffers = c.steps > 1 ? 2 : 1;
   for (int i = 0; i < buffers && ok; ++i) {
     OrthoMaps& g = gram[i];
     OrthoMaps& y = apply[i];
-    ok = (h->tall ? map_mn(h, &g.a, x[i], 128) && map_mn(h, &g.b, x[i], bs)
-                  : map_k(h, &g.a, x[i], 128) && map_k(h, &g.b, x[i], bs)) &&
+    ok = (h->tall ? map_mn(h, &g.a, x[i], 128) && map_mn(h, &g.b, x[i], bg)
+                  : map_k(h, &g.a, x[i], 128) && map_k(h, &g.b, x[i], bg)) &&
          map_tile(h, &g.out0, e) && map_mirror(h, &g.mirror, e);
     g.in0 = g.in1 = g.out1 = g.a;
     ok = ok && (h->tall ? map_k(h, &y.a, x[i], 128) && map_k(h, &y.b, d, ba)
@@ -220,7 +239,7 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   }
   if (!ok || launch_muon_norm(in, l.part, s) != cudaSuccess ||
       launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, l.counts,
-                        l.counts ? tg.tiles() * kCounts : 0, s) != cudaSuccess)
+                        l.counts ? static_cast<int>(count_bytes(h) / 4) : 0, s) != cudaSuccess)
     return MLPB_ECUDA;
   p.batch = static_cast<int>(c.batch);
   p.rows = static_cast<int>(c.rows);
