@@ -2,10 +2,11 @@
 //
 // Reads of 2 (or 4) bytes and writes of one or two bytes an element bound it.  A CTA takes one
 // 128 x 128 tile, so that every block of the matrix and of its transpose lies in one CTA and the
-// tile is read from memory once: each thread keeps eight 16-byte pieces (eight rows apart in
-// groups of 16 lanes a row) in flight, the rows' maxima come from shuffles of 16 lanes, and the
-// tile goes through shared memory for the columns, of which a thread takes two over 32 rows
-// (32 bytes of two rows of the transpose: whole sectors).
+// tile is read from memory once.  Four lanes hold a row (four 16-byte pieces each, all in flight
+// before the first is used), so that its maximum takes two exchanges; pieces are kept as loaded,
+// bf16 in pairs (one instruction for two maxima), and the tile goes through shared memory for the
+// columns, of which a thread takes two over 32 rows (32 bytes of two rows of the transpose: whole
+// sectors).
 #include <algorithm>
 
 #include "../../include/mlpb.h"
@@ -16,43 +17,132 @@ namespace mlpb {
 
 constexpr int kQThreads = 256;
 
+// Eight consecutive elements of a row, as loaded.
+template <typename T>
+struct Piece;
+
+template <>
+struct Piece<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld_global_nc_v4(p); }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void keep(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+  // Codes of the eight values times f.
+  __device__ __forceinline__ uint2 codes(float f) const;
+};
+
+template <>
+struct Piece<float> {
+  uint4 u, v;
+  __device__ __forceinline__ void load(const float* p) {
+    u = ld_global_nc_v4(p);
+    v = ld_global_nc_v4(p + 4);
+  }
+  __device__ __forceinline__ void clear() { u = v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void keep(float* p) const {
+    reinterpret_cast<uint4*>(p)[0] = u;
+    reinterpret_cast<uint4*>(p)[1] = v;
+  }
+  __device__ __forceinline__ uint2 codes(float f) const {
+    return make_uint2(b128_pack4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                 __uint_as_float(u.w), f),
+                      b128_pack4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                 __uint_as_float(v.w), f));
+  }
+};
+
+// The larger magnitudes of two pairs of bf16 (a NaN's is the largest).
+__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// A pair of bf16 as two floats.
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ uint2 Piece<__nv_bfloat16>::codes(float f) const {
+  return make_uint2(b128_pack4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y), f),
+                    b128_pack4(bf_lo(u.z), bf_hi(u.z), bf_lo(u.w), bf_hi(u.w), f));
+}
+
+// Magnitudes as fp32 bits: of pieces of a row, of pairs of a column.
+__device__ __forceinline__ uint32_t magnitude(const Piece<__nv_bfloat16> (&p)[4]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m = absmax2(m, p[j].u.x);
+    m = absmax2(m, p[j].u.y);
+    m = absmax2(m, p[j].u.z);
+    m = absmax2(m, p[j].u.w);
+  }
+  return max(m << 16, m & 0xffff0000u);
+}
+
+__device__ __forceinline__ uint32_t magnitude(const Piece<float> (&p)[4]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w[8] = {p[j].u.x, p[j].u.y, p[j].u.z, p[j].u.w,
+                           p[j].v.x, p[j].v.y, p[j].v.z, p[j].v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, w[e] & 0x7fffffffu);
+  }
+  return m;
+}
+
+// Two columns' elements of a row, as kept in shared memory.
+template <typename T>
+struct Pair;
+
+template <>
+struct Pair<__nv_bfloat16> {
+  uint32_t w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    w = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ float lo() const { return bf_lo(w); }
+  __device__ __forceinline__ float hi() const { return bf_hi(w); }
+};
+
+template <>
+struct Pair<float> {
+  float2 f;
+  __device__ __forceinline__ void load(const float* p) { f = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ float lo() const { return f.x; }
+  __device__ __forceinline__ float hi() const { return f.y; }
+};
+
+__device__ __forceinline__ void column_magnitudes(const Pair<__nv_bfloat16> (&c)[32],
+                                                  uint32_t (&m)[2]) {
+  uint32_t a = 0u;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) a = absmax2(a, c[r].w);
+  m[0] = a << 16;
+  m[1] = a & 0xffff0000u;
+}
+
+__device__ __forceinline__ void column_magnitudes(const Pair<float> (&c)[32], uint32_t (&m)[2]) {
+  m[0] = m[1] = 0u;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) {
+    m[0] = max(m[0], __float_as_uint(c[r].f.x) & 0x7fffffffu);
+    m[1] = max(m[1], __float_as_uint(c[r].f.y) & 0x7fffffffu);
+  }
+}
+
 template <typename T>
 struct QTile {
-  // a row's stride leaves the columns' reads (consecutive words of a row) and the rows' 16-byte
-  // writes free of conflicts
-  static constexpr int kStride = kB128 + 16 / static_cast<int>(sizeof(T));
+  // Strides of 80 (bf16) and 132 (fp32) words: a quarter of a warp's 16-byte stores (two rows of
+  // four pieces) and the reads of consecutive pairs of a row meet no bank twice.
+  static constexpr int kStride = sizeof(T) == 2 ? 160 : 132;
   T v[kB128 * kStride];
   uint32_t colmax[4][kB128];
   uint32_t rowmax[kQThreads / 32];
 };
-
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8], __nv_bfloat16* keep) {
-  const uint4 u = ld_global_nc_v4(p);
-  *reinterpret_cast<uint4*>(keep) = u;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = unpack_bf16x2(w[e]);
-    v[2 * e] = f.x;
-    v[2 * e + 1] = f.y;
-  }
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&v)[8], float* keep) {
-  const uint4 a = ld_global_nc_v4(p), b = ld_global_nc_v4(p + 4);
-  reinterpret_cast<uint4*>(keep)[0] = a;
-  reinterpret_cast<uint4*>(keep)[1] = b;
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
-}
-
-__device__ __forceinline__ float2 pair_at(const __nv_bfloat16* p) {
-  return unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p));
-}
-__device__ __forceinline__ float2 pair_at(const float* p) {
-  return *reinterpret_cast<const float2*>(p);
-}
 
 // The scale byte of row `row` (of the `tiles` x 128 rows that have bytes) and block kb, and those
 // of the blocks after the last one that share its word.
@@ -66,7 +156,7 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t tiles, int64_t row
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
     b128_quantize_kernel(const T* __restrict__ x, int64_t R, int64_t C, int square,
                          uint8_t* __restrict__ q, uint8_t* __restrict__ qs,
                          uint8_t* __restrict__ qt, uint8_t* __restrict__ qts) {
@@ -77,37 +167,34 @@ __global__ void __launch_bounds__(kQThreads)
   const int64_t c0 = cb * kB128, r0 = rb * kB128;
   const int64_t cblocks = gridDim.x, rblocks = gridDim.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ch = (tid & 15) * 8, rr = tid >> 4;  // this thread's columns, its rows mod 16
-  const bool col_ok = c0 + ch < C;
+  const int ch = (tid & 3) * 8, rr = tid >> 2;  // columns ch + 32 j of rows rr, rr + 64
 
-  float v[8][8];
+  Piece<T> p[2][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 16 + rr;
-    if (col_ok && r0 + r < R) {
-      load8(x + (r0 + r) * C + c0 + ch, v[i], sh.v + r * S + ch);
-    } else {
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] = 0.0f;
-        sh.v[r * S + ch + e] = T(0.0f);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int64_t row = r0 + rr + 64 * i, col = c0 + ch + 32 * j;
+      if (row < R && col < C) p[i][j].load(x + row * C + col);
+      else p[i][j].clear();
     }
+  uint32_t m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m[i] = magnitude(p[i]);
+    m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+    m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
   }
-  uint32_t m[8];
   uint32_t all = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] = 0u;  // magnitudes order like their bits, NaN above infinity
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m[i] = max(m[i], __float_as_uint(v[i][e]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
-    all = max(all, m[i]);
-  }
   if (square) {
-    all = max(all, __shfl_xor_sync(0xffffffffu, all, 16));
+    all = __reduce_max_sync(0xffffffffu, max(m[0], m[1]));
     if (lane == 0) sh.rowmax[warp] = all;
+  }
+  if (qt != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[i][j].keep(sh.v + (rr + 64 * i) * S + ch + 32 * j);
   }
   __syncthreads();
   if (square) {
@@ -118,38 +205,36 @@ __global__ void __launch_bounds__(kQThreads)
   if (q != nullptr) {
     const int64_t ld = b128_ld(C);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 16 + rr;
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = r0 + rr + 64 * i;
       const uint32_t byte = b128_scale_byte(square ? all : m[i]);
       const float f = b128_to_codes(byte);
-      if ((tid & 15) == 0) put_scale(qs, rblocks, r0 + r, cb, cblocks, r0 + r < R ? byte : kB128One);
-      if (r0 + r < R && c0 + ch < ld)
-        *reinterpret_cast<uint2*>(q + (r0 + r) * ld + c0 + ch) =
-            make_uint2(b128_pack4(v[i][0], v[i][1], v[i][2], v[i][3], f),
-                       b128_pack4(v[i][4], v[i][5], v[i][6], v[i][7], f));
+      if ((tid & 3) == 0) put_scale(qs, rblocks, row, cb, cblocks, row < R ? byte : kB128One);
+      if (row < R) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t col = c0 + ch + 32 * j;
+          if (col < ld) *reinterpret_cast<uint2*>(q + row * ld + col) = p[i][j].codes(f);
+        }
+      }
     }
   }
   if (qt == nullptr) return;
   const int j = (tid & 63) * 2, g = tid >> 6;  // two columns, rows [32 g, 32 g + 32)
-  const T* col = sh.v + (g * 32) * S + j;
-  uint32_t mt[2];
-  if (square) {
-    mt[0] = mt[1] = all;
-  } else {
-    mt[0] = mt[1] = 0u;
+  Pair<T> c[32];
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      const float2 f = pair_at(col + r * S);
-      mt[0] = max(mt[0], __float_as_uint(f.x) & 0x7fffffffu);
-      mt[1] = max(mt[1], __float_as_uint(f.y) & 0x7fffffffu);
-    }
-    sh.colmax[g][j] = mt[0];
-    sh.colmax[g][j + 1] = mt[1];
+  for (int r = 0; r < 32; ++r) c[r].load(sh.v + (g * 32 + r) * S + j);
+  uint32_t mt[2] = {all, all};
+  if (!square) {
+    column_magnitudes(c, mt);
+    *reinterpret_cast<uint2*>(&sh.colmax[g][j]) = make_uint2(mt[0], mt[1]);
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      mt[e] = max(max(sh.colmax[0][j + e], sh.colmax[1][j + e]),
-                  max(sh.colmax[2][j + e], sh.colmax[3][j + e]));
+    for (int k = 0; k < 4; ++k) {
+      const uint2 o = *reinterpret_cast<const uint2*>(&sh.colmax[k][j]);
+      mt[0] = max(mt[0], o.x);
+      mt[1] = max(mt[1], o.y);
+    }
   }
   const int64_t ldt = b128_ld(R);
   const uint32_t b0 = b128_scale_byte(mt[0]), b1 = b128_scale_byte(mt[1]);
@@ -165,11 +250,9 @@ __global__ void __launch_bounds__(kQThreads)
     uint32_t w0[4], w1[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float2 f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = pair_at(col + (h * 16 + e * 4 + i) * S);
-      w0[e] = b128_pack4(f[0].x, f[1].x, f[2].x, f[3].x, f0);
-      w1[e] = b128_pack4(f[0].y, f[1].y, f[2].y, f[3].y, f1);
+      const int r = h * 16 + e * 4;
+      w0[e] = b128_pack4(c[r].lo(), c[r + 1].lo(), c[r + 2].lo(), c[r + 3].lo(), f0);
+      w1[e] = b128_pack4(c[r].hi(), c[r + 1].hi(), c[r + 2].hi(), c[r + 3].hi(), f1);
     }
     uint8_t* o = qt + (c0 + j) * ldt + r0 + g * 32 + h * 16;
     st_global_v4(o, make_uint4(w0[0], w0[1], w0[2], w0[3]));

@@ -38,9 +38,9 @@ __host__ __device__ constexpr int64_t b128_scale_bytes(int64_t rows, int64_t col
 __device__ __forceinline__ uint32_t b128_scale_byte(uint32_t amax_bits) {
   if (amax_bits >= 0x7f800000u) return kB128Nan;
   if (amax_bits == 0u) return kB128One;
-  int e;
-  const float m = frexpf(__uint_as_float(amax_bits), &e);  // 448 = 0.875 2^9
-  const int k = min(m <= 0.875f ? 9 - e : 8 - e, 126);
+  // 448 = 1.75 2^8; below 2^-126 every k is past 126
+  const int e = static_cast<int>(amax_bits >> 23) - 127;
+  const int k = min(((amax_bits & 0x7fffffu) <= 0x600000u ? 8 : 7) - e, 126);
   return static_cast<uint32_t>(127 - k);
 }
 

@@ -560,7 +560,7 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
   }
   if (lane == 0) {
     if (Sm::loads && coming) wait_drain(box_bar, box_parity, wc);  // after an expired wait
-    bulk_wait_all();
+    bulk_wait_read<0>();  // what follows waits for the whole grid
   }
 }
 

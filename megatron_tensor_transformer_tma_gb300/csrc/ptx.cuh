@@ -141,11 +141,6 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-// Waits until the thread's bulk groups have been written.
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
 // ------------------------------------------------------------------ dependent launches
 // Lets the next kernel of the stream begin (up to its own pdl_wait) once every CTA has come here.
 __device__ __forceinline__ void pdl_launch_next() {
