@@ -5,8 +5,9 @@
 // tile is read from memory once.  Four lanes hold a row (four 16-byte pieces each, all in flight
 // before the first is used), so that its maximum takes two exchanges; pieces are kept as loaded,
 // bf16 in pairs (one instruction for two maxima), and the tile goes through shared memory for the
-// columns, of which a thread takes two over 32 rows (32 bytes of two rows of the transpose: whole
-// sectors).
+// columns, of which a thread takes two over 32 rows, and the transposed codes once more, so that
+// rows leave whole (written by their threads, each store touched 32 lines: 143 us for T8192 x
+// 20480 in both layouts).
 #include <algorithm>
 
 #include "../../include/mlpb.h"
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
                          uint8_t* __restrict__ q, uint8_t* __restrict__ qs,
                          uint8_t* __restrict__ qt, uint8_t* __restrict__ qts) {
   extern __shared__ __align__(16) uint8_t q_smem[];
+  pdl_launch_next();
   QTile<T>& sh = *reinterpret_cast<QTile<T>*>(q_smem);
   constexpr int S = QTile<T>::kStride;
   const int64_t cb = blockIdx.x, rb = blockIdx.y;
@@ -242,11 +244,12 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
     put_scale(qts, cblocks, c0 + j, rb, rblocks, c0 + j < C ? b0 : kB128One);
     put_scale(qts, cblocks, c0 + j + 1, rb, rblocks, c0 + j + 1 < C ? b1 : kB128One);
   }
-  if (c0 + j >= C) return;  // C is even
   const float f0 = b128_to_codes(b0), f1 = b128_to_codes(b1);
+  if (square) __syncthreads();  // the columns have been read (else: above)
+  // Rows of the transpose as 128 bytes, in whole pieces of 16 that trade places by pairs of rows.
+  uint8_t* codes = reinterpret_cast<uint8_t*>(sh.v);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (r0 + g * 32 + h * 16 >= ldt) break;
     uint32_t w0[4], w1[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -254,9 +257,18 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
       w0[e] = b128_pack4(c[r].lo(), c[r + 1].lo(), c[r + 2].lo(), c[r + 3].lo(), f0);
       w1[e] = b128_pack4(c[r].hi(), c[r + 1].hi(), c[r + 2].hi(), c[r + 3].hi(), f1);
     }
-    uint8_t* o = qt + (c0 + j) * ldt + r0 + g * 32 + h * 16;
-    st_global_v4(o, make_uint4(w0[0], w0[1], w0[2], w0[3]));
-    st_global_v4(o + ldt, make_uint4(w1[0], w1[1], w1[2], w1[3]));
+    uint8_t* o = codes + j * kB128 + (((g * 2 + h) ^ ((j >> 1) & 7)) << 4);
+    *reinterpret_cast<uint4*>(o) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+    *reinterpret_cast<uint4*>(o + kB128) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int col = i * 32 + (tid >> 3), piece = tid & 7;
+    if (c0 + col < C && r0 + piece * 16 < ldt)
+      st_global_v4(qt + (c0 + col) * ldt + r0 + piece * 16,
+                   *reinterpret_cast<const uint4*>(codes + col * kB128 +
+                                                   ((piece ^ ((col >> 1) & 7)) << 4)));
   }
 }
 

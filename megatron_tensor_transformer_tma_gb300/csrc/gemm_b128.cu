@@ -12,6 +12,11 @@
 //   warps 2..9  epilogue.  The accumulator takes 256 of the 512 columns and scales 32 more, so
 //               there is no second one: eight warps take the tile into 128 registers a thread
 //               and release it before they convert and store.
+//
+// An accumulation in the tensor cores cuts off instead of rounding: sums come out too small, by
+// 6e-7 of their size after 64 k-blocks and in proportion.  So an fp32 result's sum is taken in
+// chunks of 64 k-blocks, each added to the stored result in fp32 (a tile is in L2 then, and the
+// next chunk's products run meanwhile): dW of 16384 tokens is off by as much as that of 8192.
 #include <algorithm>
 
 #include "../../include/mlpb.h"
@@ -23,6 +28,7 @@ namespace mlpb {
 constexpr int kMxStages = 6;
 constexpr int kMxThreads = 320;
 constexpr int kMxEpiWarps = 8;
+constexpr int kMxChunk = 64;                   // k-blocks summed in the tensor cores, fp32 results
 constexpr int kMxScaleBytes = 3 * kB128Chunk;  // 128 A rows, 256 B rows
 constexpr int kMxScaleCol = 256;               // tensor-memory column of the first scales
 constexpr int kMxScaleCols = 16;               // 4 of A, 8 of B, twice
@@ -191,11 +197,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int stage = 0;
       uint32_t phase = 0, sbuf = 0;
       int it = 0;
-      for (int u = cid; u < num_units; u += nclusters, ++it) {
-        if (!wait_bounded(tempty, (it & 1) ^ 1u, wc, kSiteMmaAccEmpty)) break;
-        tc_fence_after();
-        bool ok = true;
+      bool ok = true;
+      for (int u = cid; u < num_units && ok; u += nclusters) {
         for (int kb = 0; kb < p.num_kb; ++kb) {
+          const int in_chunk = kb & (p.chunk - 1);
+          if (in_chunk == 0) {
+            if (!wait_bounded(tempty, (it & 1) ^ 1u, wc, kSiteMmaAccEmpty)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
           if (!wait_bounded(full0 + 8 * stage, phase, wc, kSiteMmaFull)) {
             ok = false;
             break;
@@ -217,15 +229,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_mx_pair(tmem_base, as + kk * 2, bs + kk * 2, idesc, sfa, sfa + 4,
-                         (kb != 0 || kk != 0) ? 1u : 0u);
+                         (in_chunk != 0 || kk != 0) ? 1u : 0u);
           umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
+          if (in_chunk == p.chunk - 1 || kb == p.num_kb - 1) {
+            umma_commit_pair_mc(tfull, 0x3);
+            ++it;
+          }
         }
-        if (!ok) break;
-        umma_commit_pair_mc(tfull, 0x3);
       }
       umma_commit_pair(drain);
       wait_drain(drain, 0, wc);
@@ -237,8 +251,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int row = quarter * 32 + lane;
     const uint32_t tacc =
         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128u * half;
-    int it = 0;
-    for (int u = cid; u < num_units; u += nclusters, ++it) {
+    const int chunks = (p.num_kb + p.chunk - 1) / p.chunk;
+    const int turns = (num_units - cid + nclusters - 1) / nclusters * chunks;
+    for (int it = 0; it < turns; ++it) {
+      const int chunk = it % chunks, u = cid + it / chunks * nclusters;
       int ok = 1;
       if (lane == 0) ok = wait_bounded(tfull, it & 1, wc, kSiteEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[c][e]);
         if (p.out_f32) {
           float* C = static_cast<float*>(p.C) + o + 32 * c;
-          if (p.accumulate) add_f32x32(C, nv, f);
+          if (p.accumulate || chunk > 0) add_f32x32(C, nv, f);
           store_f32x32(C, nv, f);
         } else {
           store_bf16x32(static_cast<__nv_bfloat16*>(p.C) + o + 32 * c, nv, f);
@@ -302,6 +318,8 @@ static void pair_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
 }
+
+int b128_chunk(bool out_f32) { return out_f32 ? kMxChunk : 1 << 30; }
 
 cudaError_t b128_gemm_set_attrs(int* max_clusters) {
   cudaError_t e = cudaFuncSetAttribute(gemm_b128_kernel,

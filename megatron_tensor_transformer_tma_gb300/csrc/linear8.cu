@@ -15,6 +15,7 @@ using namespace mlpb;
 struct mlpb_linear8 {
   mlpb_linear8_config cfg;
   int device, max_clusters;
+  int few_slots[kFewSlots];
   bool fault_pending;
   uint32_t* err;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
@@ -64,11 +65,11 @@ bool encode(const mlpb_linear8* h, CUtensorMap* m, CUtensorMapDataType type, con
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Codes in tiles of 128 rows by 128 bytes; what is past the edges reads zero.
-bool map_codes(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
+// Codes in tiles of `rows` (128) rows by 128 bytes; what is past the edges reads zero.
+bool map_codes(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q, int rows) {
   const uint64_t ld = static_cast<uint64_t>(b128_ld(q.cols));
   return encode(h, m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, ld, static_cast<uint64_t>(q.rows), ld,
-                kB128, kB128, CU_TENSOR_MAP_SWIZZLE_128B);
+                kB128, static_cast<uint32_t>(rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Scales as rows of 512 bytes: group of four blocks by group, 128-row tile by tile.
@@ -78,11 +79,19 @@ bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
                 kB128Chunk / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Whether a product goes to the kernel for few tiles: at most 128 rows of C, or fewer tiles of
+// 256 x 256 than half the pairs of SMs.
+bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n) {
+  return m <= 128 || 2 * cdiv(m, 256) * cdiv(n, 256) <= h->max_clusters;
+}
+
 // C [a.rows][b.rows] (+)= A B^T over the columns that both have.
 mlpb_status product(mlpb_linear8* h, const Quantized& a, const Quantized& b, void* C, bool f32,
                     bool accumulate, cudaStream_t s) {
   B128Maps m;
-  if (!map_codes(h, &m.a, a) || !map_codes(h, &m.b, b) || !map_scales(h, &m.sa, a) ||
+  const bool few = few_tiles(h, a.rows, b.rows);
+  if (!map_codes(h, &m.a, a, few ? b128_few_columns(a.rows) : kB128) ||
+      !map_codes(h, &m.b, b, kB128) || !map_scales(h, &m.sa, a) ||
       !map_scales(h, &m.sb, b))
     return MLPB_ECUDA;
   B128Params p{};
@@ -95,11 +104,14 @@ mlpb_status product(mlpb_linear8* h, const Quantized& a, const Quantized& b, voi
   p.b_tiles = static_cast<int>(b128_blocks(b.rows));
   p.out_f32 = f32 ? 1 : 0;
   p.accumulate = accumulate ? 1 : 0;
+  p.chunk = b128_chunk(f32);
   p.C = C;
   p.err = h->err;
   p.wait_ns = kDefaultWaitNs;
   p.fault_inject = h->fault_pending ? 1 : 0;
   h->fault_pending = false;
+  if (few)
+    return launch_b128_few(m, p, h->few_slots, s) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
   const int clusters = std::min(p.num_pm * p.num_n, h->max_clusters);
   return launch_b128_gemm(m, p, clusters, s) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
 }
@@ -159,6 +171,7 @@ extern "C" mlpb_status mlpb_linear8_create(const mlpb_linear8_config* cfg, mlpb_
   }
   h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   if (b128_gemm_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
+      b128_few_set_attrs(h->few_slots) != cudaSuccess || h->few_slots[0] < 1 ||
       cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->err, 0, sizeof(uint32_t)) != cudaSuccess ||
       cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come

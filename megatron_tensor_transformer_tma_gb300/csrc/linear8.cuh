@@ -17,6 +17,7 @@ struct B128Params {
   int raster_group;
   int out_f32;     // C is fp32 (else bf16)
   int accumulate;  // C += (fp32)
+  int chunk;       // k-blocks of a sum in the tensor cores, a power of two
   void* C;
   uint32_t* err;
   uint64_t wait_ns;
@@ -27,7 +28,17 @@ struct B128Maps {
   CUtensorMap a, b, sa, sb;
 };
 
+// k-blocks of a sum in the tensor cores for an fp32 result (bf16: all of them).
+int b128_chunk(bool out_f32);
 cudaError_t b128_gemm_set_attrs(int* max_clusters);
 cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters, cudaStream_t s);
+
+// gemm_b128_few.cu: the same with few tiles.  `slots`: clusters of 1, 2, 4 and 8 CTAs that are
+// resident at once; the box of m.a has b128_few_columns(M) rows.
+constexpr int kFewSlots = 4;
+int b128_few_columns(int64_t b_rows);
+cudaError_t b128_few_set_attrs(int* slots);
+cudaError_t launch_b128_few(const B128Maps& m, const B128Params& p, const int* slots,
+                            cudaStream_t s);
 
 }  // namespace mlpb
