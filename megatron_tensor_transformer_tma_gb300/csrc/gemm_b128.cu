@@ -15,8 +15,8 @@
 //
 // An accumulation in the tensor cores cuts off instead of rounding: sums come out too small, by
 // 6e-7 of their size after 64 k-blocks and in proportion.  So an fp32 result's sum is taken in
-// chunks of 64 k-blocks, each added to the stored result in fp32 (a tile is in L2 then, and the
-// next chunk's products run meanwhile): dW of 16384 tokens is off by as much as that of 8192.
+// chunks of 64 k-blocks, which are added in the epilogue's registers: dW of 16384 tokens is off by
+// as much as that of 8192.
 #include <algorithm>
 
 #include "../../include/mlpb.h"
@@ -76,6 +76,8 @@ __device__ __forceinline__ void issue_scales(const CUtensorMap* ma, const CUtens
   ld2<kPeer>(dst + 2 * kB128Chunk, mb, bar, 0, rb + min(2 * nt + 1, p.b_tiles - 1));
 }
 
+// kChunked: sums longer than a chunk (a kernel of its own: the others keep no sums between chunks).
+template <bool kChunked>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_b128_kernel(const __grid_constant__ B128Maps maps, const B128Params p) {
   constexpr int S = kMxStages;
@@ -131,6 +133,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   const WaitCtx wc{abort_flag, p.err, p.wait_ns};
   const int num_units = p.num_pm * p.num_n;
+  // a pair's turns: its tiles, each in chunks of K
+  const int chunks = kChunked ? (p.num_kb + p.chunk - 1) / p.chunk : 1;
+  const int turns = (num_units - cid + nclusters - 1) / nclusters * chunks;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -196,18 +201,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       constexpr uint32_t byte1 = idesc_mx_e4m3(2 * kBM, kBN, 1) - idesc0;
       int stage = 0;
       uint32_t phase = 0, sbuf = 0;
-      int it = 0;
-      bool ok = true;
-      for (int u = cid; u < num_units && ok; u += nclusters) {
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          const int in_chunk = kb & (p.chunk - 1);
-          if (in_chunk == 0) {
-            if (!wait_bounded(tempty, (it & 1) ^ 1u, wc, kSiteMmaAccEmpty)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-          }
+      for (int it = 0; it < turns; ++it) {
+        const int kb0 = kChunked ? it % chunks * p.chunk : 0;
+        const int kb1 = kChunked ? min(p.num_kb, kb0 + p.chunk) : p.num_kb;
+        if (!wait_bounded(tempty, (it & 1) ^ 1u, wc, kSiteMmaAccEmpty)) break;
+        tc_fence_after();
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(full0 + 8 * stage, phase, wc, kSiteMmaFull)) {
             ok = false;
             break;
@@ -229,17 +229,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_mx_pair(tmem_base, as + kk * 2, bs + kk * 2, idesc, sfa, sfa + 4,
-                         (in_chunk != 0 || kk != 0) ? 1u : 0u);
+                         (kb != kb0 || kk != 0) ? 1u : 0u);
           umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
-          if (in_chunk == p.chunk - 1 || kb == p.num_kb - 1) {
-            umma_commit_pair_mc(tfull, 0x3);
-            ++it;
-          }
         }
+        if (!ok) break;
+        umma_commit_pair_mc(tfull, 0x3);
       }
       umma_commit_pair(drain);
       wait_drain(drain, 0, wc);
@@ -251,26 +249,40 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int row = quarter * 32 + lane;
     const uint32_t tacc =
         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128u * half;
-    const int chunks = (p.num_kb + p.chunk - 1) / p.chunk;
-    const int turns = (num_units - cid + nclusters - 1) / nclusters * chunks;
+    uint32_t v[4][32];  // the tile's sums
     for (int it = 0; it < turns; ++it) {
-      const int chunk = it % chunks, u = cid + it / chunks * nclusters;
+      const int chunk = kChunked ? it % chunks : 0;
+      const int u = cid + (kChunked ? it / chunks : it) * nclusters;
       int ok = 1;
       if (lane == 0) ok = wait_bounded(tfull, it & 1, wc, kSiteEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       __syncwarp();
       tc_fence_after();
-      uint32_t v[4][32];
+      if (!kChunked || chunk == 0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tacc + 32 * c, v[c]);
-      tmem_ld_wait();
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tacc + 32 * c, v[c]);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tacc + 16 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            uint32_t& sum = v[c >> 1][16 * (c & 1) + e];
+            sum = __float_as_uint(__uint_as_float(sum) + __uint_as_float(r[e]));
+          }
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (leader) mbar_arrive(tempty);
         else mbar_arrive_remote(tempty_lead);
       }
+      if (kChunked && chunk != chunks - 1) continue;
       int mp, nt;
       tile_coords(u, p.num_pm, p.num_n, p.raster_group, mp, nt);
       const int m = (mp * 2 + rank) * kBM + row;
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[c][e]);
         if (p.out_f32) {
           float* C = static_cast<float*>(p.C) + o + 32 * c;
-          if (p.accumulate || chunk > 0) add_f32x32(C, nv, f);
+          if (p.accumulate) add_f32x32(C, nv, f);
           store_f32x32(C, nv, f);
         } else {
           store_bf16x32(static_cast<__nv_bfloat16*>(p.C) + o + 32 * c, nv, f);
@@ -322,13 +334,16 @@ static void pair_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int 
 int b128_chunk(bool out_f32) { return out_f32 ? kMxChunk : 1 << 30; }
 
 cudaError_t b128_gemm_set_attrs(int* max_clusters) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_b128_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
-  if (e != cudaSuccess) return e;
+  for (cudaError_t e :
+       {cudaFuncSetAttribute(gemm_b128_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMxSmem),
+        cudaFuncSetAttribute(gemm_b128_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMxSmem)})
+    if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   pair_config(cfg, attr, 2, nullptr);
-  return cudaOccupancyMaxActiveClusters(max_clusters, gemm_b128_kernel, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_clusters, gemm_b128_kernel<true>, &cfg);
 }
 
 cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters,
@@ -336,7 +351,8 @@ cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int cluster
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   pair_config(cfg, attr, clusters, s);
-  return cudaLaunchKernelEx(&cfg, gemm_b128_kernel, m, p);
+  return p.num_kb > p.chunk ? cudaLaunchKernelEx(&cfg, gemm_b128_kernel<true>, m, p)
+                            : cudaLaunchKernelEx(&cfg, gemm_b128_kernel<false>, m, p);
 }
 
 }  // namespace mlpb

@@ -80,8 +80,10 @@ bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
 }
 
 // Whether a product goes to the kernel for few tiles: at most 128 rows of C, or fewer tiles of
-// 256 x 256 than half the pairs of SMs.
-bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n) {
+// 256 x 256 than half the pairs of SMs; not where an fp32 sum is long enough for chunks, which
+// that kernel does not have.
+bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n, int64_t k, bool f32) {
+  if (b128_blocks(k) > b128_chunk(f32)) return false;
   return m <= 128 || 2 * cdiv(m, 256) * cdiv(n, 256) <= h->max_clusters;
 }
 
@@ -89,7 +91,7 @@ bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n) {
 mlpb_status product(mlpb_linear8* h, const Quantized& a, const Quantized& b, void* C, bool f32,
                     bool accumulate, cudaStream_t s) {
   B128Maps m;
-  const bool few = few_tiles(h, a.rows, b.rows);
+  const bool few = few_tiles(h, a.rows, b.rows, a.cols, f32);
   if (!map_codes(h, &m.a, a, few ? b128_few_columns(a.rows) : kB128) ||
       !map_codes(h, &m.b, b, kB128) || !map_scales(h, &m.sa, a) ||
       !map_scales(h, &m.sb, b))

@@ -110,6 +110,35 @@ def test_layer(T, K, N, out):
     assert serving.forward(X[:0]).shape == (0, N)
 
 
+def _scaled(values):
+    """What the library stands for as float64: blocks quantized by the oracle's rule, vectorised."""
+    x = values.double()
+    R, C = x.shape
+    b = torch.nn.functional.pad(x, (0, -C % 128)).view(R, -1, 128)
+    m, e = torch.frexp(b.abs().amax(-1, keepdim=True))
+    k = torch.where(m <= 0.875, 9 - e, 8 - e).double()
+    q = (b * torch.exp2(k)).float().to(torch.float8_e4m3fn).double() * torch.exp2(-k)
+    return q.view(R, -1)[:, :C]
+
+
+@pytest.mark.parametrize("T,K,N", [(16500, 136, 264), (24700, 264, 8), (9000, 1032, 2056)])
+def test_long_sums(T, K, N):
+    """dW over more tokens than one sum in the tensor cores: chunks of 64 blocks.  Each chunk's
+    error is that of its own length; their additions round, 2^-24 of a partial sum each."""
+    X, dY = _randn(1, T, K), _randn(2, T, N, std=1e-3)
+    plan = mlpb.Linear8(T, K, N)
+    plan.load(_randn(3, N, K))
+    plan.forward(X)
+    dW = plan.backward(dY, input_grad=False)[1].double()
+    a, b = _scaled(dY.t()), _scaled(X.t())
+    want, mags = a @ b.t(), a.abs() @ b.abs().t()
+    chunks = -(-T // 8192)
+    tol = (min(T, 8192) / 32 + 4) * 2.0 ** -22 * mags + chunks * 2.0 ** -24 * mags
+    assert bool(((dW - want).abs() <= tol).all())
+    # the size of the whole error does not grow with the number of chunks
+    assert float((dW - want).norm() / want.norm()) < 1e-6
+
+
 def test_values_that_are_not_finite_stay_in_their_rows():
     T, K, N = 40, 384, 256
     X, W, dY = _randn(1, T, K), _randn(2, N, K), _randn(3, T, N)
