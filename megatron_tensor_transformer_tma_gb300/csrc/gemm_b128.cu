@@ -25,15 +25,29 @@
 
 namespace mlpb {
 
-constexpr int kMxStages = 6;
 constexpr int kMxThreads = 320;
 constexpr int kMxEpiWarps = 8;
 constexpr int kMxChunk = 64;                   // k-blocks summed in the tensor cores, fp32 results
 constexpr int kMxScaleBytes = 3 * kB128Chunk;  // 128 A rows, 256 B rows
+constexpr int kMxStagedBelow = 32;             // k-blocks
+constexpr int kMxBox = 4096;                    // 32 rows of 128 bytes of a result
 constexpr int kMxScaleCol = 256;               // tensor-memory column of the first scales
 constexpr int kMxScaleCols = 16;               // 4 of A, 8 of B, twice
-constexpr int kMxSmem = kMxStages * (kPairStageBytes + kMxScaleBytes) + 1024 + 256;
-static_assert(kMxSmem <= 232448, "shared memory of a CTA");
+
+// How a tile's results leave.
+enum class MxOut {
+  Direct,   // from the threads of their rows; behind the next tile's products where K is long
+  Staged,   // through shared memory by TMA: two slots of 4 KB a warp, and two stages fewer
+  Chunked,  // as Direct, of sums longer than a chunk
+};
+
+template <MxOut O>
+struct MxSmem {
+  static constexpr int stages = O == MxOut::Staged ? 4 : 6;
+  static constexpr int slots = O == MxOut::Staged ? kMxEpiWarps * 2 * kMxBox : 0;
+  static constexpr int bytes = stages * (kPairStageBytes + kMxScaleBytes) + slots + 2048 + 256;
+  static_assert(bytes <= 232448, "shared memory of a CTA");
+};
 static_assert(kPairAStage == 128 * 128 && kPairBStage == 128 * 128, "E4M3 tiles");
 
 // Instruction descriptor of kind::mxf8f6f4: E4M3 operands, both K-major, UE8M0 scales; the scale
@@ -76,11 +90,12 @@ __device__ __forceinline__ void issue_scales(const CUtensorMap* ma, const CUtens
   ld2<kPeer>(dst + 2 * kB128Chunk, mb, bar, 0, rb + min(2 * nt + 1, p.b_tiles - 1));
 }
 
-// kChunked: sums longer than a chunk (a kernel of its own: the others keep no sums between chunks).
-template <bool kChunked>
+template <MxOut O>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_b128_kernel(const __grid_constant__ B128Maps maps, const B128Params p) {
-  constexpr int S = kMxStages;
+  using Sm = MxSmem<O>;
+  constexpr int S = Sm::stages;
+  constexpr bool kChunked = O == MxOut::Chunked;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -88,7 +103,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const uint32_t sA0 = base;
   const uint32_t sB0 = base + S * kPairAStage;
   const uint32_t sc0 = base + S * kPairStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * (kPairStageBytes + kMxScaleBytes));
+  const uint32_t slots = (sc0 + S * kMxScaleBytes + 1023u) & ~1023u;  // boxes begin on 1024 bytes
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (slots + Sm::slots - base));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 3);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const uint32_t full0 = smem_u32(bars);
@@ -127,6 +143,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   __syncthreads();
   tc_fence_after();
   cluster_sync();
+  pdl_launch_next();
+  pdl_wait();  // an operand may come from the kernel before this one
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full_lead = mapa_shared(full0, 0);
   const uint32_t tempty_lead = mapa_shared(tempty, 0);
@@ -194,7 +212,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---------------------------------------------------------------- MMA issuer (pair)
-      static_assert(kMxSmem < 256 * 1024, "descriptor address field");
+      static_assert(Sm::bytes < 256 * 1024, "descriptor address field");
       const uint64_t adesc0 = sdesc(sA0, 16, 1024, 2u), bdesc0 = sdesc(sB0, 16, 1024, 2u);
       const uint64_t sdesc0 = sdesc(sc0, 16, 128, 0u);  // 8-row groups of 128 bytes
       constexpr uint32_t idesc0 = idesc_mx_e4m3(2 * kBM, kBN, 0);
@@ -246,7 +264,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // ------------------------------------------------------------------ epilogue
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;  // columns [128 half, 128 half + 128) of the tile
-    const int row = quarter * 32 + lane;
     const uint32_t tacc =
         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128u * half;
     uint32_t v[4][32];  // the tile's sums
@@ -285,8 +302,45 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       if (kChunked && chunk != chunks - 1) continue;
       int mp, nt;
       tile_coords(u, p.num_pm, p.num_n, p.raster_group, mp, nt);
-      const int m = (mp * 2 + rank) * kBM + row;
+      const int m0 = (mp * 2 + rank) * kBM + quarter * 32, m = m0 + lane;
       const int n0 = nt * kBN + 128 * half;
+      if constexpr (O == MxOut::Staged) {
+        if (m0 >= p.M) continue;  // the warp's rows, all of them
+        const int width = p.out_f32 ? 32 : 64;  // columns of a box
+        const int boxes = min(128 / width, (p.N - n0 + width - 1) / width);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q >= boxes) break;
+          const uint32_t box = slots + ((warp - 2) * 2 + (q & 1)) * kMxBox;
+          if (lane == 0) bulk_wait_read<1>();  // the slot's last box
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t to = box + lane * 128 + ((j ^ (lane & 7)) << 4);
+            uint4 w;
+            if (p.out_f32) {
+              w = make_uint4(v[q][4 * j], v[q][4 * j + 1], v[q][4 * j + 2], v[q][4 * j + 3]);
+            } else {  // boxes 0 and 1: sums of chunks 2 q and 2 q + 1
+              const uint32_t* x = &v[(2 * q + j / 4) & 3][8 * (j & 3)];
+              w = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                             pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                             pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                             pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w.x), "r"(w.y),
+                         "r"(w.z), "r"(w.w)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (p.accumulate) tma_add_2d(&maps.c, box, n0 + q * width, m0);
+            else tma_store_2d(&maps.c, box, n0 + q * width, m0);
+            bulk_commit();
+          }
+        }
+        continue;
+      }
       if (m >= p.M) continue;
       const size_t o = static_cast<size_t>(m) * p.N + n0;
 #pragma unroll
@@ -305,6 +359,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
       }
     }
+    if (O == MxOut::Staged && lane == 0) bulk_wait_read<0>();
   }
 
   tc_fence_before();
@@ -317,42 +372,59 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   }
 }
 
+template <MxOut O>
 static void pair_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clusters,
                         cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2), 1, 1);
   cfg.blockDim = dim3(kMxThreads, 1, 1);
-  cfg.dynamicSmemBytes = kMxSmem;
+  cfg.dynamicSmemBytes = MxSmem<O>::bytes;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it begins with pdl_wait
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
+}
+
+template <MxOut O>
+static cudaError_t launch_out(const B128Maps& m, const B128Params& p, int clusters,
+                              cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  pair_config<O>(cfg, attr, clusters, s);
+  return cudaLaunchKernelEx(&cfg, gemm_b128_kernel<O>, m, p);
+}
+
+template <MxOut O>
+static cudaError_t attrs_of() {
+  return cudaFuncSetAttribute(gemm_b128_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              MxSmem<O>::bytes);
 }
 
 int b128_chunk(bool out_f32) { return out_f32 ? kMxChunk : 1 << 30; }
 
 cudaError_t b128_gemm_set_attrs(int* max_clusters) {
   for (cudaError_t e :
-       {cudaFuncSetAttribute(gemm_b128_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMxSmem),
-        cudaFuncSetAttribute(gemm_b128_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMxSmem)})
+       {attrs_of<MxOut::Direct>(), attrs_of<MxOut::Staged>(), attrs_of<MxOut::Chunked>()})
     if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  pair_config(cfg, attr, 2, nullptr);
-  return cudaOccupancyMaxActiveClusters(max_clusters, gemm_b128_kernel<true>, &cfg);
+  cudaLaunchAttribute attr[2];
+  pair_config<MxOut::Chunked>(cfg, attr, 2, nullptr);
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(max_clusters, gemm_b128_kernel<MxOut::Chunked>, &cfg);
 }
+
+// Staged where the products of a tile (0.13 us a k-block) no longer hide its stores by threads.
+bool b128_staged(int num_kb) { return num_kb < kMxStagedBelow; }
 
 cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters,
                              cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  pair_config(cfg, attr, clusters, s);
-  return p.num_kb > p.chunk ? cudaLaunchKernelEx(&cfg, gemm_b128_kernel<true>, m, p)
-                            : cudaLaunchKernelEx(&cfg, gemm_b128_kernel<false>, m, p);
+  if (p.num_kb > p.chunk) return launch_out<MxOut::Chunked>(m, p, clusters, s);
+  return b128_staged(p.num_kb) ? launch_out<MxOut::Staged>(m, p, clusters, s)
+                               : launch_out<MxOut::Direct>(m, p, clusters, s);
 }
 
 }  // namespace mlpb

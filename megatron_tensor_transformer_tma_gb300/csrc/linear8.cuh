@@ -26,10 +26,12 @@ struct B128Params {
 
 struct B128Maps {
   CUtensorMap a, b, sa, sb;
+  CUtensorMap c;  // C in boxes of 32 rows by 128 bytes, where b128_staged says so
 };
 
 // k-blocks of a sum in the tensor cores for an fp32 result (bf16: all of them).
 int b128_chunk(bool out_f32);
+bool b128_staged(int num_kb);
 cudaError_t b128_gemm_set_attrs(int* max_clusters);
 cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters, cudaStream_t s);
 
