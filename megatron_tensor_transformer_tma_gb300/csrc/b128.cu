@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
                          uint8_t* __restrict__ q, uint8_t* __restrict__ qs,
                          uint8_t* __restrict__ qt, uint8_t* __restrict__ qts) {
   extern __shared__ __align__(16) uint8_t q_smem[];
-  pdl_launch_next();
+  pdl_wait();         // x may come from the kernel before this one
+  pdl_launch_next();  // after it: what the next kernel reads early is final as well
   QTile<T>& sh = *reinterpret_cast<QTile<T>*>(q_smem);
   constexpr int S = QTile<T>::kStride;
   const int64_t cb = blockIdx.x, rb = blockIdx.y;
@@ -281,11 +282,19 @@ static cudaError_t launch_as(const void* x, int64_t R, int64_t C, bool square, v
         b128_quantize_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid(static_cast<unsigned>(b128_blocks(C)), static_cast<unsigned>(b128_blocks(R)));
-  b128_quantize_kernel<T><<<grid, kQThreads, smem, s>>>(
-      static_cast<const T*>(x), R, C, square ? 1 : 0, static_cast<uint8_t*>(q),
-      static_cast<uint8_t*>(qs), static_cast<uint8_t*>(qt), static_cast<uint8_t*>(qts));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(b128_blocks(C)), static_cast<unsigned>(b128_blocks(R)));
+  cfg.blockDim = dim3(kQThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it begins with pdl_wait
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, b128_quantize_kernel<T>, static_cast<const T*>(x), R, C,
+                            square ? 1 : 0, static_cast<uint8_t*>(q), static_cast<uint8_t*>(qs),
+                            static_cast<uint8_t*>(qt), static_cast<uint8_t*>(qts));
 }
 
 cudaError_t launch_b128_quantize(const void* x, bool f32, int64_t rows, int64_t cols, bool square,
