@@ -1163,16 +1163,27 @@ class Linear8:
         m = self.cfg.inputs * ld
         return self._saved[:m].view(self.cfg.inputs, ld), self._saved[m:m + n]
 
+    def _saved_args(self, tokens, Xt):
+        """Pointers of the X^T that a call writes or reads: a given one, or this object's."""
+        if Xt is not None:
+            return _b128_args(Xt, self.cfg.inputs, tokens, "Xt", self.device.index)
+        p = self._saved.data_ptr()  # as saved(), without its views
+        return [p, p + self.cfg.inputs * ((tokens + 15) // 16 * 16)]
+
     def forward(self, X, Y=None, Xt=None, stream=None):
         """Y [tokens][outputs].  With `training`, Xt (or this object) receives X^T for the
         backward."""
-        T = X.shape[0]
+        h, c, dev = self.handle, self.cfg, self.device.index
+        T = _linear8_rows(h, X, c.inputs, "X")[1]
         if Y is None:
             with _on(stream, self.device):
-                Y = torch.empty((T, self.cfg.outputs), dtype=self.out_dtype, device=self.device)
-        if Xt is None and self.training and T <= self.cfg.max_tokens:
-            Xt = self.saved(T)
-        mlpb_linear8_forward(self.handle, X, self.Wq, Y, Xt, self.workspace, stream)
+                Y = torch.empty((T, c.outputs), dtype=self.out_dtype, device=self.device)
+        args = [h.ptr, T, _arg(X, torch.bfloat16, (T, c.inputs), "X", dev),
+                self.Wq[0].data_ptr(), self.Wq[1].data_ptr(),
+                _arg(Y, self.out_dtype, (T, c.outputs), "Y", dev),
+                *(self._saved_args(T, Xt) if Xt is not None or self.training else (None, None)),
+                self.workspace.data_ptr()]
+        _call_on(dev, "mlpb_linear8_forward", args, stream)
         return Y
 
     def backward(self, dY, dX=None, dW=None, Xt=None, accumulate=False, input_grad=True,
@@ -1183,16 +1194,19 @@ class Linear8:
             raise ValueError("Linear8: made with training=False")
         if accumulate and dW is None:
             raise ValueError("dW: nothing given to add into")
-        T, c = dY.shape[0], self.cfg
+        h, c, dev = self.handle, self.cfg, self.device.index
+        T = _linear8_rows(h, dY, c.outputs, "dY")[1]
         with _on(stream, self.device):
             if dX is None and input_grad:
                 dX = torch.empty((T, c.inputs), dtype=self.out_dtype, device=self.device)
             if dW is None:
                 dW = torch.empty((c.outputs, c.inputs), dtype=torch.float32, device=self.device)
-        if Xt is None and T <= c.max_tokens:
-            Xt = self.saved(T)
-        mlpb_linear8_backward(self.handle, dY, self.Wt, Xt, dX, dW, accumulate, self.workspace,
-                              stream)
+        args = [h.ptr, T, _arg(dY, torch.bfloat16, (T, c.outputs), "dY", dev),
+                self.Wt[0].data_ptr(), self.Wt[1].data_ptr(), *self._saved_args(T, Xt),
+                _arg(dX, self.out_dtype, (T, c.inputs), "dX", dev),
+                _arg(dW, torch.float32, (c.outputs, c.inputs), "dW", dev),
+                1 if accumulate else 0, self.workspace.data_ptr()]
+        _call_on(dev, "mlpb_linear8_backward", args, stream)
         return dX, dW
 
 
