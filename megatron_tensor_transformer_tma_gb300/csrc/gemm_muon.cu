@@ -17,9 +17,10 @@
 // access touches 32 lines.)  The ring has 5 stages for that, 4 where W's fp32 boxes come too.
 //
 // Few tiles leave pairs idle and the epilogue in the open.  Then tiles are 256 x 128 (the rule is
-// at ortho_narrow in muon.cu), and the symmetric products' K is cut into ranges (`split`), whose
-// fp32 sums go to the workspace; for each 32 x 64 box the warp that comes last adds the ranges in
-// their order, so that the bits do not depend on who it is, and goes on with the sum.
+// at tiling() in muon.cu), and the symmetric products' K is cut into ranges (`split`), whose fp32
+// sums go to the workspace for ortho_fold_kernel, which adds them in their order on all SMs and
+// does what the epilogue does.  (The warp that comes last doing that in the product's own kernel
+// took 8 us for three ranges of 1376 x 1376: a fence, an atomic and a quarter of the SMs.)
 #include <algorithm>
 
 #include "gemm.cuh"
@@ -362,6 +363,12 @@ __device__ __forceinline__ void ragged_rows(uint32_t slot, int lane, int row0, i
   }
 }
 
+// Where a 32 x 64 box of a range's sums begins: [unit][CTA][epilogue warp][box of its half][16][32].
+template <int BN>
+__device__ __forceinline__ size_t partial_box(int unit, int rank, int ewarp, int i) {
+  return ((static_cast<size_t>(unit) * 2 + rank) * kEpiWarps + ewarp) * (BN / 128) * 512 + i * 512;
+}
+
 // One epilogue warp: the 32 accumulator rows of its lane quarter, the boxes of its half.
 template <OrthoOp Op, bool kTall, int BN>
 __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tfull0,
@@ -382,6 +389,7 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
   BoxWalk<Op, BN> ahead;
   ahead.u = cid;
   ahead.find(half, p, nclusters);
+  if (kSymmetric<Op> && p.split > 1) ahead.u = p.units;  // no boxes here
   bool coming = false;  // a box on its way into the slot
   if constexpr (Sm::loads) {
     if (ahead.u < p.units) {
@@ -411,49 +419,28 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
     tc_fence_after();
     const uint32_t tacc =
         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * BN);
-    bool mine = true;  // this warp goes on with the boxes
-    float4* part = nullptr;
-    if (kSymmetric<Op> && t.parts > 1) {
-      // this range's sums, [tile][range][CTA][warp][box of the half][16][lane]
-      constexpr int kBoxes = BN / 128;
-      const size_t per_range = static_cast<size_t>(2 * kEpiWarps) * kBoxes * 16 * 32;
-      const size_t tile = static_cast<size_t>(u / t.parts);
-      part = p.partial + tile * t.parts * per_range +
-             static_cast<size_t>((rank * kEpiWarps + ewarp) * kBoxes) * 16 * 32 + lane;
+    const bool split = kSymmetric<Op> && p.split > 1;
+    if (split) {  // this range's sums as they lie in the registers
+      float4* part = p.partial + partial_box<BN>(u, rank, ewarp, 0) + lane;
       for (int sub = half, i = 0; sub < subs; sub += 2, ++i) {
-        float4* to = part + t.part * per_range + i * 16 * 32;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[32];
           tmem_load_f32x32(tacc + sub * kEpiCols + 32 * h, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            to[(8 * h + e) * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            part[(i * 16 + 8 * h + e) * 32] =
+                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       }
-      __threadfence();
-      __syncwarp();
-      int before = 0;
-      if (lane == 0) {
-        uint32_t* count = p.counts + (tile * 2 + rank) * kEpiWarps + ewarp;
-        before = static_cast<int>(atomicAdd(count, 1u));
-        if (before == t.parts - 1) *count = 0u;  // for the next product
-      }
-      before = __shfl_sync(0xffffffffu, before, 0);
-      __threadfence();
-      mine = before == t.parts - 1;
     }
-    if (half >= subs || !mine) {  // no box of this tile, or no more to do with it
+    if (half >= subs || split) {  // no box of this tile
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(tempty0 + 8 * buf);
         else mbar_arrive_remote(tempty_lead + 8 * buf);
       }
-      if (Sm::loads && half < subs && lane == 0) {  // its box has come for nothing
-        wait_drain(box_bar, box_parity, wc);
-      }
-      if (Sm::loads && half < subs) coming = false;  // split: a pair has one tile
       continue;
     }
 #pragma unroll 1
@@ -484,27 +471,7 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
-        if (kSymmetric<Op> && t.parts > 1) {
-          constexpr size_t per_range = static_cast<size_t>(2 * kEpiWarps) * (BN / 128) * 16 * 32;
-          const float4* from = part + ((sub >> 1) * 16 + 8 * h) * 32;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-#pragma unroll 2
-          for (int r = 0; r < t.parts; ++r) {
-            float4 x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __ldcg(from + r * per_range + e * 32);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              v[4 * e] += x[e].x;
-              v[4 * e + 1] += x[e].y;
-              v[4 * e + 2] += x[e].z;
-              v[4 * e + 3] += x[e].w;
-            }
-          }
-        } else {
-          tmem_load_f32x32(tacc + sub * kEpiCols + 32 * h, v);
-        }
+        tmem_load_f32x32(tacc + sub * kEpiCols + 32 * h, v);
         if (h == 1 && sub + 2 >= subs) {  // the accumulator is free
           tc_fence_before();
           __syncwarp();
@@ -738,6 +705,135 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   }
 }
 
+// The sums of a symmetric product's ranges: a CTA adds those of one box, in their order, and
+// stores what the product's own epilogue would.  A thread has one row's columns 4 g .. 4 g + 3 for
+// four g; the box goes through shared memory so that rows and mirrored rows leave whole.
+constexpr int kFoldThreads = 128;
+
+template <OrthoOp Op, int BN>
+__global__ void __launch_bounds__(kFoldThreads) ortho_fold_kernel(const OrthoParams p) {
+  constexpr int kPitch = kEpiCols + 8;
+  __shared__ __align__(16) __half box[kEpiRows * kPitch];
+  pdl_launch_next();
+  pdl_wait();
+  constexpr int kBoxes = BN / 128;
+  int at = blockIdx.x;
+  const int i = at % kBoxes;
+  at /= kBoxes;
+  const int ewarp = at % kEpiWarps;
+  at /= kEpiWarps;
+  const int rank = at & 1, u = (at >> 1) * p.split;
+  const OrthoTile t = ortho_tile<Op, BN>(u, p);
+  const int sub = (ewarp >> 2) + 2 * i, quarter = (ewarp + 2) & 3;
+  const int row0 = t.mp * 256 + rank * kBM + quarter * kEpiRows;
+  const int col0 = t.nt * BN + sub * kEpiCols;
+  if (row0 >= p.n || col0 >= p.n) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int m = row0 + lane;
+  const size_t vec = static_cast<size_t>(t.b) * p.ldn;
+  const size_t mat = static_cast<size_t>(t.b) * p.n * p.ldn;
+  float4 s[4];
+  const float4* from = p.partial + partial_box<BN>(u, rank, ewarp, i) + lane;
+  const size_t range = partial_box<BN>(1, 0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s[k] = __ldcg(from + (warp + 4 * k) * 32);
+#pragma unroll 4
+  for (int r = 1; r < p.split; ++r) {
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = __ldcg(from + r * range + (warp + 4 * k) * 32);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s[k].x += x[k].x;
+      s[k].y += x[k].y;
+      s[k].z += x[k].z;
+      s[k].w += x[k].w;
+    }
+  }
+  const float dm = Op == OrthoOp::Poly && m < p.n ? __ldcg(p.diag + vec + m) : 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = (warp + 4 * k) * 4, col = col0 + c;
+    const float v[4] = {s[k].x, s[k].y, s[k].z, s[k].w};
+    float r[4];
+    if constexpr (Op == OrthoOp::Gram) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r[e] = v[e] * kXInv;  // A times 2^12
+        if (col + e == m) {
+          if (m < p.n) p.diag[vec + m] = r[e] * kXInv;
+          r[e] = 0.0f;
+        }
+      }
+    } else {
+      float e16[4] = {0.f, 0.f, 0.f, 0.f}, dj[4] = {0.f, 0.f, 0.f, 0.f};
+      if (m < p.n) {  // rows of 64 elements: inside the buffer
+        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p.e + mat +
+                                                              static_cast<size_t>(m) * p.ldn + col));
+        const float2 a = unpack_half2(w.x), b = unpack_half2(w.y);
+        e16[0] = a.x;
+        e16[1] = a.y;
+        e16[2] = b.x;
+        e16[3] = b.y;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < p.n) dj[e] = __ldcg(p.diag + vec + col + e);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lin = fmaf(p.c, dm + dj[e], p.b) * (kXInv * kDScale);
+        r[e] = fmaf(lin, e16[e], (p.c * (kEEInv * kDScale)) * v[e]);
+        if (col + e == m) {
+          if (m < p.n) p.beta[vec + m] = p.a + dm * fmaf(p.c, dm, p.b) + p.c * (v[e] * kEEInv);
+          r[e] = 0.0f;
+        }
+        if (col + e >= p.n) r[e] = 0.0f;  // E's pad is nobody's
+      }
+    }
+    *reinterpret_cast<uint2*>(box + lane * kPitch + c) =
+        make_uint2(pack_half2(r[0], r[1]), pack_half2(r[2], r[3]));
+  }
+  __syncthreads();
+  __half* out = (Op == OrthoOp::Gram ? p.e : p.d) + mat;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int q = threadIdx.x + k * kFoldThreads;
+    const int r = q >> 3, c = (q & 7) * 8;  // eight pieces a row
+    if (row0 + r < p.n && col0 + c < p.n)
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(row0 + r) * p.ldn + col0 + c) =
+          *reinterpret_cast<const uint4*>(box + r * kPitch + c);
+  }
+  if (!t.mirror) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int q = threadIdx.x + k * kFoldThreads;
+    const int c = q >> 2, r = (q & 3) * 8;  // four pieces a mirrored row
+    if (col0 + c < p.n && row0 + r < p.n) {
+      __half h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = box[(r + e) * kPitch + c];
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(col0 + c) * p.ldn + row0 + r) =
+          *reinterpret_cast<const uint4*>(h);
+    }
+  }
+}
+
+template <OrthoOp Op>
+static cudaError_t launch_fold(const OrthoParams& p, cudaStream_t s) {
+  const int boxes = p.units / p.split * 2 * kEpiWarps * (p.narrow ? 1 : 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(boxes));
+  cfg.blockDim = dim3(kFoldThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.narrow ? cudaLaunchKernelEx(&cfg, ortho_fold_kernel<Op, 128>, p)
+                  : cudaLaunchKernelEx(&cfg, ortho_fold_kernel<Op, 256>, p);
+}
+
 template <OrthoOp Op, bool kTall>
 static cudaError_t attr_of() {
   const cudaError_t e =
@@ -794,12 +890,15 @@ cudaError_t ortho_set_attrs(int* max_clusters) {
 
 cudaError_t launch_ortho(OrthoOp op, bool tall, const OrthoMaps& m, const OrthoParams& p,
                          int clusters, cudaStream_t s) {
+  cudaError_t e = cudaErrorInvalidValue;
   switch (op) {
     case OrthoOp::Gram:
-      return tall ? launch_as<OrthoOp::Gram, true>(m, p, clusters, s)
-                  : launch_as<OrthoOp::Gram, false>(m, p, clusters, s);
+      e = tall ? launch_as<OrthoOp::Gram, true>(m, p, clusters, s)
+               : launch_as<OrthoOp::Gram, false>(m, p, clusters, s);
+      return e == cudaSuccess && p.split > 1 ? launch_fold<OrthoOp::Gram>(p, s) : e;
     case OrthoOp::Poly:  // the same for both
-      return launch_as<OrthoOp::Poly, false>(m, p, clusters, s);
+      e = launch_as<OrthoOp::Poly, false>(m, p, clusters, s);
+      return e == cudaSuccess && p.split > 1 ? launch_fold<OrthoOp::Poly>(p, s) : e;
     case OrthoOp::Apply:
       return tall ? launch_as<OrthoOp::Apply, true>(m, p, clusters, s)
                   : launch_as<OrthoOp::Apply, false>(m, p, clusters, s);
@@ -807,7 +906,7 @@ cudaError_t launch_ortho(OrthoOp op, bool tall, const OrthoMaps& m, const OrthoP
       return tall ? launch_as<OrthoOp::Last, true>(m, p, clusters, s)
                   : launch_as<OrthoOp::Last, false>(m, p, clusters, s);
   }
-  return cudaErrorInvalidValue;
+  return e;
 }
 
 }  // namespace mlpb

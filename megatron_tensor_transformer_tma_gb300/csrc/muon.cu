@@ -38,7 +38,6 @@ struct Layout {
   __half *x0, *x1, *xl, *e, *d;
   float *diag, *beta;
   float4* partial;
-  uint32_t* counts;
   size_t bytes;
 };
 
@@ -47,7 +46,6 @@ constexpr int kMaxSplit = 16;
 // The tiles of a product over all matrices.
 struct Tiling {
   int narrow, num_pm, num_n, per_matrix, split, units, num_kb;
-  int tiles() const { return units / split; }
   size_t partial_bytes() const {
     return split > 1 ? static_cast<size_t>(units) * 256 * (narrow ? 128 : 256) * 4 : 0;
   }
@@ -57,8 +55,8 @@ struct Tiling {
 // end first, in the time of a k-block (0.26 us).  That is the same for both widths: a ring of five
 // or six stages keeps up with 256 columns and no more, so that narrow tiles pay where they are all
 // in the first wave and leave half the epilogue (a box of 64 columns for each of its warps: four
-// k-blocks) after the last product.  Ranges cost the sums' way through L2 and one addition for
-// each.
+// k-blocks) after the last product.  Ranges cost the sums' way through L2 and a launch that adds
+// them.
 Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, int64_t depth) {
   const int64_t batch = h->cfg.batch;
   Tiling best{};
@@ -85,7 +83,7 @@ Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, in
       double cost = static_cast<double>(cdiv(t.units, h->max_clusters)) *
                         cdiv(t.num_kb, t.split) +
                     4.0 * boxes;
-      if (t.split > 1) cost += 5.0 + 0.7 * t.split * boxes;
+      if (t.split > 1) cost += 12.0 + 0.3 * t.split;
       if (best.split == 0 || cost < least) {
         best = t;
         least = cost;
@@ -101,11 +99,6 @@ Tiling gram_tiling(const mlpb_muon* h) {
 Tiling poly_tiling(const mlpb_muon* h) { return tiling(h, true, h->n, h->n, h->n); }
 Tiling apply_tiling(const mlpb_muon* h) {
   return tiling(h, false, h->cfg.rows, h->cfg.cols, h->n);
-}
-
-// Counters of ranges that are done: of each tile, for two CTAs' eight epilogue warps.
-size_t count_bytes(const mlpb_muon* h) {
-  return static_cast<size_t>(std::max(gram_tiling(h).tiles(), poly_tiling(h).tiles())) * 16 * 4;
 }
 
 Layout layout(const mlpb_muon* h, void* workspace) {
@@ -130,13 +123,8 @@ Layout layout(const mlpb_muon* h, void* workspace) {
   l.d = reinterpret_cast<__half*>(take(s));
   l.diag = reinterpret_cast<float*>(take(v));
   l.beta = reinterpret_cast<float*>(take(v));
-  const Tiling gram = gram_tiling(h), poly = poly_tiling(h);
-  l.partial = nullptr;
-  l.counts = nullptr;
-  if (gram.split > 1 || poly.split > 1) {
-    l.partial = reinterpret_cast<float4*>(take(std::max(gram.partial_bytes(), poly.partial_bytes())));
-    l.counts = reinterpret_cast<uint32_t*>(take(count_bytes(h)));
-  }
+  l.partial = reinterpret_cast<float4*>(
+      take(std::max(gram_tiling(h).partial_bytes(), poly_tiling(h).partial_bytes())));
   l.bytes = at;
   return l;
 }
@@ -238,8 +226,7 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
                    2, 64, 32, true);
   }
   if (!ok || launch_muon_norm(in, l.part, s) != cudaSuccess ||
-      launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, l.counts,
-                        l.counts ? static_cast<int>(count_bytes(h) / 4) : 0, s) != cudaSuccess)
+      launch_muon_split(in, l.part, l.x0, l.x1, l.xl, h->ldx, s) != cudaSuccess)
     return MLPB_ECUDA;
   p.batch = static_cast<int>(c.batch);
   p.rows = static_cast<int>(c.rows);
@@ -253,7 +240,8 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   p.fault_inject = h->fault_pending ? 1 : 0;
   h->fault_pending = false;
   p.partial = l.partial;
-  p.counts = l.counts;
+  p.e = l.e;
+  p.d = l.d;
   auto run = [&](OrthoOp op, const Tiling& t, const OrthoMaps& maps) {
     p.narrow = t.narrow;
     p.num_pm = t.num_pm;

@@ -50,7 +50,7 @@ struct OrthoParams {
   int units;                 // tiles of all matrices, times split
   int num_kb;                // 64-deep k-blocks
   float4* partial;           // the ranges' sums
-  uint32_t* counts;          // ranges that are done, for each tile, CTA and epilogue warp; zeros
+  __half *e, *d;             // [batch][n][ldn], for the sums of ranges
   float a, b, c;
   float* diag;  // d [batch][ldn]
   float* beta;  // [batch][ldn]
@@ -93,8 +93,7 @@ struct MuonInput {
 int muon_partials(int64_t elems, int64_t batch);
 cudaError_t launch_muon_norm(const MuonInput& in, float4* part, cudaStream_t s);
 cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* xh, __half* xh_other,
-                              __half* xl, int ldx, uint32_t* counts, int num_counts,
-                              cudaStream_t s);  // and counts = 0
+                              __half* xl, int ldx, cudaStream_t s);
 
 // muon_small.cu: the whole update in one launch, for n <= 128 and lengths that a cluster's shared
 // memory holds; 0 CTAs: it does not.

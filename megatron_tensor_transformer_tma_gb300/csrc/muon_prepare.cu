@@ -54,11 +54,8 @@ template <typename T>
 __global__ void __launch_bounds__(kPrepThreads)
     muon_split_kernel(const MuonInput in, const float4* __restrict__ part, int parts,
                       __half* __restrict__ xh, __half* __restrict__ xh_other,
-                      __half* __restrict__ xl, int ldx, uint32_t* __restrict__ counts,
-                      int num_counts) {
+                      __half* __restrict__ xl, int ldx) {
   __shared__ float factors[2];
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < num_counts; i += kPrepThreads) counts[i] = 0u;
   const int64_t b = blockIdx.y;
   {  // a part a thread: muon_partials() is at most the number of threads
     __shared__ double warps[kPrepThreads / 32];
@@ -131,8 +128,7 @@ cudaError_t launch_muon_norm(const MuonInput& in, float4* part, cudaStream_t s) 
 }
 
 cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* xh,
-                              __half* xh_other, __half* xl, int ldx, uint32_t* counts, int num_counts,
-                              cudaStream_t s) {
+                              __half* xh_other, __half* xl, int ldx, cudaStream_t s) {
   const int64_t pieces = in.rows * (ldx / 8);
   const int64_t most = std::max<int64_t>(1, 1216 / in.batch);
   const dim3 grid(static_cast<unsigned>(
@@ -140,12 +136,10 @@ cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* x
                   static_cast<unsigned>(in.batch));
   const int parts = muon_partials(in.rows * in.cols, in.batch);
   if (in.g_f32)
-    muon_split_kernel<float><<<grid, kPrepThreads, 0, s>>>(in, part, parts, xh, xh_other, xl, ldx,
-                                                              counts, num_counts);
+    muon_split_kernel<float><<<grid, kPrepThreads, 0, s>>>(in, part, parts, xh, xh_other, xl, ldx);
   else
     muon_split_kernel<__nv_bfloat16>
-        <<<grid, kPrepThreads, 0, s>>>(in, part, parts, xh, xh_other, xl, ldx,
-                                                              counts, num_counts);
+        <<<grid, kPrepThreads, 0, s>>>(in, part, parts, xh, xh_other, xl, ldx);
   return cudaGetLastError();
 }
 
