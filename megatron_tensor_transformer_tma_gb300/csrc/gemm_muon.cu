@@ -389,6 +389,7 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
   BoxWalk<Op, BN> ahead;
   ahead.u = cid;
   ahead.find(half, p, nclusters);
+  pdl_wait();
   if (kSymmetric<Op> && p.split > 1) ahead.u = p.units;  // no boxes here
   bool coming = false;  // a box on its way into the slot
   if constexpr (Sm::loads) {
@@ -468,7 +469,7 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
         if (lane == 0) bulk_wait_read<0>();  // the slot's last store
       }
       __syncwarp();
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float v[32];
         tmem_load_f32x32(tacc + sub * kEpiCols + 32 * h, v);
@@ -585,8 +586,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   __syncthreads();
   tc_fence_after();
   cluster_sync();
-  pdl_launch_next();
-  pdl_wait();  // what follows reads what the kernel before this one has written
+  pdl_launch_next();  // the roles wait for the kernel before this one where they first need it
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full_lead = mapa_shared(full0, 0);
   const uint32_t tempty_lead = mapa_shared(tempty0, 0);
@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       uint32_t phase = 0;
       uint32_t armed = 0, armed_par = 0;
       bool skip_once = p.fault_inject != 0 && cid == 0 && leader;
+      bool first = true;
       for (int u = cid; u < p.units; u += nclusters) {
         const OrthoTile t = ortho_tile<Op, BN>(u, p);
         const int ra = (t.mp * 2 + rank) * kBM, rb = t.nt * BN + BN / 2 * rank;
@@ -611,6 +612,10 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
             break;
           }
           const uint32_t sa = sA0 + stage * kPairAStage, sb = sB0 + stage * Sm::b_stage;
+          if (first) {
+            first = false;
+            pdl_wait();
+          }
           if (skip_once) {
             skip_once = false;  // fault injection: this stage is never armed
           } else if (leader) {
@@ -709,13 +714,15 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
 // stores what the product's own epilogue would.  A thread has one row's columns 4 g .. 4 g + 3 for
 // four g; the box goes through shared memory so that rows and mirrored rows leave whole.
 constexpr int kFoldThreads = 128;
+constexpr int kFoldBox = kEpiRows * kEpiCols * 4;
 
 template <OrthoOp Op, int BN>
 __global__ void __launch_bounds__(kFoldThreads) ortho_fold_kernel(const OrthoParams p) {
   constexpr int kPitch = kEpiCols + 8;
   __shared__ __align__(16) __half box[kEpiRows * kPitch];
-  pdl_launch_next();
-  pdl_wait();
+  __shared__ __align__(8) uint64_t bar_mem[2];
+  __shared__ uint32_t abort_word;
+  extern __shared__ __align__(128) uint8_t fold_smem[];
   constexpr int kBoxes = BN / 128;
   int at = blockIdx.x;
   const int i = at % kBoxes;
@@ -728,29 +735,43 @@ __global__ void __launch_bounds__(kFoldThreads) ortho_fold_kernel(const OrthoPar
   const int row0 = t.mp * 256 + rank * kBM + quarter * kEpiRows;
   const int col0 = t.nt * BN + sub * kEpiCols;
   if (row0 >= p.n || col0 >= p.n) return;
+  // Each range's box is 8 KB in one piece: bulk copies, all in flight.  (Loads by threads, sixteen
+  // each, took 2.3 us a round: 9 us for sixteen ranges.)
+  const uint32_t bar = smem_u32(bar_mem), ring = smem_u32(fold_smem);
+  if (threadIdx.x == 0) {
+    abort_word = 0u;
+    mbar_init(bar, 1);
+    mbar_fence_init();
+    pdl_wait();
+    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.split) * kFoldBox);
+    for (int r = 0; r < p.split; ++r)
+      bulk_load(ring + r * kFoldBox,
+                p.partial + partial_box<BN>(u, rank, ewarp, i) + r * partial_box<BN>(1, 0, 0, 0),
+                kFoldBox, bar);
+  } else {
+    pdl_wait();
+  }
+  pdl_launch_next();
+  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int m = row0 + lane;
   const size_t vec = static_cast<size_t>(t.b) * p.ldn;
   const size_t mat = static_cast<size_t>(t.b) * p.n * p.ldn;
-  float4 s[4];
-  const float4* from = p.partial + partial_box<BN>(u, rank, ewarp, i) + lane;
-  const size_t range = partial_box<BN>(1, 0, 0, 0);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) s[k] = __ldcg(from + (warp + 4 * k) * 32);
+  const float dm = Op == OrthoOp::Poly && m < p.n ? __ldcg(p.diag + vec + m) : 0.0f;
+  const WaitCtx wc{&abort_word, p.err, p.wait_ns};
+  wait_bounded(bar, 0, wc, kSiteEpiAccFull);
+  float4 s[4] = {};
+  const float4* from = reinterpret_cast<const float4*>(fold_smem) + warp * 32 + lane;
 #pragma unroll 4
-  for (int r = 1; r < p.split; ++r) {
-    float4 x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = __ldcg(from + r * range + (warp + 4 * k) * 32);
+  for (int r = 0; r < p.split; ++r)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      s[k].x += x[k].x;
-      s[k].y += x[k].y;
-      s[k].z += x[k].z;
-      s[k].w += x[k].w;
+      const float4 x = from[r * (kFoldBox / 16) + k * 128];
+      s[k].x += x.x;
+      s[k].y += x.y;
+      s[k].z += x.z;
+      s[k].w += x.w;
     }
-  }
-  const float dm = Op == OrthoOp::Poly && m < p.n ? __ldcg(p.diag + vec + m) : 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int c = (warp + 4 * k) * 4, col = col0 + c;
@@ -824,6 +845,7 @@ static cudaError_t launch_fold(const OrthoParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(boxes));
   cfg.blockDim = dim3(kFoldThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.split) * kFoldBox;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -873,9 +895,20 @@ static cudaError_t launch_as(const OrthoMaps& m, const OrthoParams& p, int clust
                   : cudaLaunchKernelEx(&cfg, ortho_kernel<Op, kTall, 256>, m, p);
 }
 
+template <OrthoOp Op>
+static cudaError_t fold_attr_of() {
+  const int most = kOrthoMaxSplit * kFoldBox;
+  const cudaError_t e = cudaFuncSetAttribute(ortho_fold_kernel<Op, 128>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(ortho_fold_kernel<Op, 256>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 cudaError_t ortho_set_attrs(int* max_clusters) {
   for (cudaError_t e :
-       {attr_of<OrthoOp::Gram, false>(), attr_of<OrthoOp::Gram, true>(),
+       {fold_attr_of<OrthoOp::Gram>(), fold_attr_of<OrthoOp::Poly>(),
+        attr_of<OrthoOp::Gram, false>(), attr_of<OrthoOp::Gram, true>(),
         attr_of<OrthoOp::Poly, false>(), attr_of<OrthoOp::Apply, false>(),
         attr_of<OrthoOp::Apply, true>(), attr_of<OrthoOp::Last, false>(),
         attr_of<OrthoOp::Last, true>()})

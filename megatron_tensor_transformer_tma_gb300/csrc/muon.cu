@@ -41,8 +41,6 @@ struct Layout {
   size_t bytes;
 };
 
-constexpr int kMaxSplit = 16;
-
 // The tiles of a product over all matrices.
 struct Tiling {
   int narrow, num_pm, num_n, per_matrix, split, units, num_kb;
@@ -75,7 +73,7 @@ Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, in
     }
     const int64_t tiles = batch * t.per_matrix;
     const int boxes = narrow ? 1 : 2;
-    for (t.split = 1; t.split <= kMaxSplit; ++t.split) {
+    for (t.split = 1; t.split <= kOrthoMaxSplit; ++t.split) {
       if (t.split > 1 && (!symmetric || tiles * t.split > h->max_clusters ||
                           t.split > t.num_kb))
         break;

@@ -31,6 +31,7 @@ constexpr float kXInv = 1.0f / 4096.0f;
 constexpr float kDScale = 1024.0f;    // D times 2^10
 constexpr float kEEInv = kXInv * kXInv;            // a product's scale: 2^-24
 constexpr float kDXInv = kXInv / kDScale;          // 2^-22
+constexpr int kOrthoMaxSplit = 16;  // ranges of K
 constexpr int kOrthoLd = 64;  // rows of X, E and D are padded to multiples of 64 (X's with zeros)
 
 enum class OrthoOp : int {
