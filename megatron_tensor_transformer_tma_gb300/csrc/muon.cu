@@ -186,6 +186,7 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   p.a = c.coef[0];
   p.b = c.coef[1];
   p.c = c.coef[2];
+  p.err = h->err;
   if (h->small > 0)
     return launch_muon_small(in, p, c.steps, h->small, s) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
   const Layout l = layout(h, workspace);
@@ -233,7 +234,6 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   p.ldn = h->ldn;
   p.diag = l.diag;
   p.beta = l.beta;
-  p.err = h->err;
   p.wait_ns = kDefaultWaitNs;
   p.fault_inject = h->fault_pending ? 1 : 0;
   h->fault_pending = false;

@@ -3,20 +3,19 @@
 //
 // With n <= 128 a product is a few million operations on one tile, and the launches, pipeline
 // starts and trips through L2 of fifteen tensor-core launches cost far more than the products
-// (one 64 x 4096 matrix: 190 us; here profiles give its time in the table below).  Each CTA keeps a
-// slab of the longer side, X [n][slab] in two fp16 parts (muon.cuh has the number formats); a tall
-// matrix is transposed as it is read and written, since the polynomial of X^T is that of X
-// transposed.  A step is
-//   1. each CTA's share of X X^T over its slab (mma.sync; 16 warps, 32 x 32 blocks, the slab split
-//      between warps where there are fewer than 16 blocks);
+// (64 x 4096: 194 us).  Each CTA keeps a slab of the longer side, X [n][slab] in two fp16 parts
+// (muon.cuh has the number formats); a tall matrix is transposed as it is read and written, since
+// the polynomial of X^T is that of X transposed.  A step is
+//   1. each CTA's share of X X^T over its slab;
 //   2. the sum over CTAs, in rank order: each CTA adds one slice through distributed shared memory
 //      and writes E and d to all;
 //   3. E E, D and beta, by every CTA for itself;
-//   4. X <- beta X + D X in place: a warp takes 16 columns, holds them all in registers as operands
-//      and overwrites them.
-// Two barriers of the cluster a step.  mma.sync instead of tcgen05: fragments go between
-// registers and both layouts of shared memory without descriptors, tensor memory or a pipeline to
-// start, and the products are not what bounds it.
+//   4. X <- beta X + D X in place, 512 columns at a time.
+// Two barriers of the cluster a step.  The products are single tcgen05 chains of M = 128 (rows past
+// n are of whatever lies behind and are not read back) that a thread issues between barriers of the
+// CTA: with mma.sync, a sixteenth of the rate here, they were two thirds of the time at n = 128
+// (128 x 4096: 102 us).  X, E and D lie in chunks of 64 columns, rows of 128 bytes with the 128-byte
+// swizzle: the K-major operand of 1, 3 and 4 (D) and, the same bytes, the MN-major one of 4 (X).
 #include <algorithm>
 
 #include "muon_update.cuh"
@@ -29,30 +28,37 @@ constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kSmallMaxN = 128;
 constexpr int kSmallMaxCluster = 16;
 constexpr size_t kSmallMaxSmem = 232448;
+// More than half an SM's shared memory, and more than gemm_b128_few.cu leaves: no other CTA that
+// takes tensor memory is on the same SM.  (Two clusters that meet on two SMs could each hold there
+// what the other's second CTA waits for.)
+constexpr size_t kSmallMinSmem = 122880;
+constexpr int kSmallTmem = 512;
+constexpr int kSmallBlock = 256;  // columns of a chain of step 4; two in tensor memory
 
 struct SmallShape {
   int np;    // n rounded up to 32
-  int ns;    // elements of a row of E and D: np rounded up to 64
   int slab;  // columns of X in a CTA, a multiple of 64
-  int splits;  // of the slab in step 1
   __host__ __device__ size_t x_bytes() const { return static_cast<size_t>(np) * slab * 2; }
-  __host__ __device__ size_t e_bytes() const { return static_cast<size_t>(np) * ns * 2; }
+  __host__ __device__ size_t e_bytes() const {
+    return static_cast<size_t>(np) * ((np + 63) / 64) * 128;
+  }
   // the partial sums, later D
   __host__ __device__ size_t p_bytes() const {
-    return static_cast<size_t>(splits) * np * np * 4;
+    const size_t sums = static_cast<size_t>(np) * np * 4;
+    return sums > e_bytes() ? sums : e_bytes();
   }
+  __host__ __device__ size_t used() const { return 2 * x_bytes() + e_bytes() + p_bytes(); }
+  // A chain reads 128 rows of its chunk, whatever np is: what lies behind the last one is there too.
   __host__ __device__ size_t bytes() const {
-    return 2 * x_bytes() + e_bytes() + p_bytes() + 2 * kSmallMaxN * 4 + 512;
+    const size_t b = used() + static_cast<size_t>(128 - np) * 128 + 2 * kSmallMaxN * 4 + 512 + 1024;
+    return b > kSmallMinSmem ? b : kSmallMinSmem;
   }
 };
 
 static SmallShape small_shape(int n, int64_t length, int cluster) {
   SmallShape s;
   s.np = (n + 31) / 32 * 32;
-  s.ns = (s.np + 63) / 64 * 64;
   s.slab = static_cast<int>((length + cluster * 64 - 1) / (cluster * 64)) * 64;
-  const int blocks = (s.np / 32) * (s.np / 32);
-  s.splits = std::max(1, kSmallWarps / blocks);
   return s;
 }
 
@@ -67,35 +73,59 @@ struct SmallParams {
   __nv_bfloat16* wb;
   const float* lr;
   float decay, scale;
+  uint32_t* err;
+  uint64_t wait_ns;
 };
 
-// Element (row, col) of a swizzled matrix of fp16: 16-byte pieces of a row change places within
-// groups of eight, so that eight rows' pieces of one column lie in different banks.
-__device__ __forceinline__ int swz(int row, int col, int stride) {
-  return row * stride + ((((col >> 3) ^ (row & 7)) << 3) | (col & 7));
+// Element (row, col) of a matrix in chunks of 64 columns: within a row's 128 bytes 16-byte pieces
+// trade places by the row modulo 8.
+__device__ __forceinline__ int swz(int row, int col, int np) {
+  return ((col >> 6) * np + row) * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
 }
 
-__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void ldm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
+__device__ __forceinline__ void umma_f16_one(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+  tmem_ld_wait();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[e]);
+}
+
+// S S^T over `depth` columns of a matrix in chunks: 128 rows by np.
+__device__ __forceinline__ void chain_square(uint32_t d, uint32_t s, int np, int depth) {
+  const uint32_t idesc = idesc_bf16_f32(128, np, false, false) & ~((1u << 7) | (1u << 10));
+  const uint64_t desc = sdesc(s, 16, 1024, 2u);
+  for (int k = 0; k < depth; k += 16) {
+    const uint64_t at = desc + static_cast<uint32_t>(((k >> 6) * np * 128 + (k & 63) * 2) >> 4);
+    umma_f16_one(d, at, at, idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+// D X for `cols` columns (at most 256) of X from column c on: 128 rows.
+__device__ __forceinline__ void chain_apply(uint32_t d, uint32_t dm, uint32_t x, int np, int c,
+                                            int cols) {
+  const uint32_t idesc = idesc_bf16_f32(128, cols, false, true) & ~((1u << 7) | (1u << 10));
+  const uint64_t adesc = sdesc(dm, 16, 1024, 2u);
+  const uint64_t bdesc =
+      sdesc(x + (c >> 6) * np * 128, static_cast<uint32_t>(np) * 128, 1024, 2u);
+  for (int k = 0; k < np; k += 16)
+    umma_f16_one(d,
+                 adesc + static_cast<uint32_t>(((k >> 6) * np * 128 + (k & 63) * 2) >> 4),
+                 bdesc + static_cast<uint32_t>((k * 128) >> 4), idesc, k > 0 ? 1u : 0u);
 }
 
 __device__ __forceinline__ float4 ld_remote4(uint32_t cluster_addr) {
@@ -119,73 +149,6 @@ __device__ __forceinline__ void st_remote4(uint32_t cluster_addr, float v) {
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// A block of S S^T, 16 I x 8 J elements at rows i0 and j0, over columns [k0, k1) of a swizzled
-// matrix.  Rows of fragments begin at multiples of 8, so that a lane's swizzle is its own.
-template <int I, int J>
-__device__ __forceinline__ void block_product(float (&acc)[I][J][4], uint32_t s, int stride, int i0,
-                                              int j0, int k0, int k1, int lane) {
-#pragma unroll
-  for (int i = 0; i < I; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-  const uint32_t a0 = s + 2 * (i0 + (lane & 15)) * stride;  // rows, then columns 8 on
-  const uint32_t b0 = s + 2 * (j0 + (lane & 7) + ((lane >> 4) << 3)) * stride;  // the other way
-  const int ap = lane >> 4, bp = (lane >> 3) & 1, x = lane & 7;
-#pragma unroll 2
-  for (int k = k0; k < k1; k += 16) {
-    uint32_t a[I][4], b[J / 2][4];
-    const uint32_t ao = (((k >> 3) + ap) ^ x) << 4, bo = (((k >> 3) + bp) ^ x) << 4;
-#pragma unroll
-    for (int i = 0; i < I; ++i) ldm4(a0 + 32 * i * stride + ao, a[i]);
-#pragma unroll
-    for (int j = 0; j < J / 2; ++j) ldm4(b0 + 32 * j * stride + bo, b[j]);
-#pragma unroll
-    for (int i = 0; i < I; ++i)
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        mma_f16(acc[i][j], a[i], b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
-  }
-}
-
-// D (into d) and beta of the block at (i0, j0) of E.
-template <int I, int J>
-__device__ __forceinline__ void poly_block(const __half* e, __half* d, const float* diag,
-                                           float* beta, int np, int ns, int i0, int j0, int lane,
-                                           float pa, float pb, float pc) {
-  float acc[I][J][4];
-  block_product<I, J>(acc, smem_u32(e), ns, i0, j0, 0, np, lane);
-  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int col = j0 + 8 * j + t2;
-    const int at0 = (((col >> 3) ^ g8) << 3) + t2;
-    const float d0 = diag[col], d1 = diag[col + 1];
-#pragma unroll
-    for (int i = 0; i < I; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = i0 + 16 * i + 8 * h + g8;
-        const int at = row * ns + at0;
-        const float dm = diag[row];
-        const float2 e2 = __half22float2(*reinterpret_cast<const __half2*>(e + at));
-        const float ee0 = acc[i][j][2 * h], ee1 = acc[i][j][2 * h + 1];
-        float v0 = fmaf(fmaf(pc, dm + d0, pb) * (kXInv * kDScale), e2.x,
-                        (pc * (kEEInv * kDScale)) * ee0);
-        float v1 = fmaf(fmaf(pc, dm + d1, pb) * (kXInv * kDScale), e2.y,
-                        (pc * (kEEInv * kDScale)) * ee1);
-        if (row == col || row == col + 1) {
-          const float ee = row == col ? ee0 : ee1;
-          beta[row] = pa + dm * fmaf(pc, dm, pb) + pc * (ee * kEEInv);
-          if (row == col) v0 = 0.0f;
-          else v1 = 0.0f;
-        }
-        *reinterpret_cast<uint32_t*>(d + at) = half2_bits(v0, v1);
-      }
-  }
 }
 
 // This CTA's elements of a matrix, in runs of consecutive ones.
@@ -229,18 +192,21 @@ __device__ __forceinline__ void for_groups(const SmallRuns& r, int tall, int n, 
 
 template <typename T>
 __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const SmallParams p) {
-  extern __shared__ __align__(1024) uint8_t small_smem[];
+  extern __shared__ __align__(1024) uint8_t small_raw[];
   const SmallShape sh = p.shape;
-  const int np = sh.np, ns = sh.ns, slab = sh.slab;
-  __half* xh = reinterpret_cast<__half*>(small_smem);
-  __half* xl = reinterpret_cast<__half*>(small_smem + sh.x_bytes());
-  __half* e = reinterpret_cast<__half*>(small_smem + 2 * sh.x_bytes());
-  float* part = reinterpret_cast<float*>(small_smem + 2 * sh.x_bytes() + sh.e_bytes());
+  const int np = sh.np, slab = sh.slab;
+  uint8_t* smem = small_raw + ((1024u - (smem_u32(small_raw) & 1023u)) & 1023u);
+  __half* xh = reinterpret_cast<__half*>(smem);
+  __half* xl = reinterpret_cast<__half*>(smem + sh.x_bytes());
+  __half* e = reinterpret_cast<__half*>(smem + 2 * sh.x_bytes());
+  float* part = reinterpret_cast<float*>(smem + 2 * sh.x_bytes() + sh.e_bytes());
   __half* d = reinterpret_cast<__half*>(part);  // once the partial sums have been read
-  float* diag = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(part) + sh.p_bytes());
+  float* diag = reinterpret_cast<float*>(smem + sh.used() + static_cast<size_t>(128 - np) * 128);
   float* beta = diag + kSmallMaxN;
   float4* squares = reinterpret_cast<float4*>(beta + kSmallMaxN);  // a warp each, then the CTA's
   float* factors = reinterpret_cast<float*>(squares + kSmallWarps + 1);
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(factors + 2);
+  uint32_t* words = reinterpret_cast<uint32_t*>(bar_mem + 1);  // tensor memory, abort flag
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -258,6 +224,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   runs.pitch = p.in.cols;
   runs.quads = (runs.run + 3) / 4;
   runs.vec = p.in.cols % 4 == 0;  // rows, slabs and matrices then begin on 16 bytes
+
+  if (tid == 0) {
+    mbar_init(smem_u32(bar_mem), 1);
+    words[1] = 0u;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(words)),
+                 "r"(kSmallTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
 
   // ------------------------------------------------------------ momentum and norm
   float4 sq = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -324,7 +303,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
             lo[c] = x[c] - __half2float(__float2half_rn(x[c]));
           }
           if (!p.tall) {  // four columns of a row, in one piece; those past the end are zeros
-            const int to = swz(row, col, slab);
+            const int to = swz(row, col, np);
             *reinterpret_cast<uint2*>(xh + to) =
                 make_uint2(half2_bits(x[0], x[1]), half2_bits(x[2], x[3]));
             *reinterpret_cast<uint2*>(xl + to) =
@@ -333,7 +312,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (c >= n) break;
-              const int to = swz(row, col, slab);
+              const int to = swz(row, col, np);
               xh[to] = __float2half_rn(x[c]);
               xl[to] = __float2half_rn(lo[c]);
               if (++row == p.n) {
@@ -346,14 +325,39 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   }
   __syncthreads();
 
+  tc_fence_after();
+  const uint32_t tmem = words[0];
   const uint32_t xh_a = smem_u32(xh), e_a = smem_u32(e), d_a = smem_u32(d);
-  const int nb = np / 32, blocks = nb * nb;
-  const int pieces = np * np / 4;  // fragments of four: rows g8 and g8 + 8, two columns of each
-  // Lanes that share a fragment in the sum over CTAs, as many as there are threads for.
+  const uint32_t bar = smem_u32(bar_mem);
+  const WaitCtx wc{words + 1, p.err, p.wait_ns};
+  uint32_t parity = 0;
+  // A chain between two barriers of the CTA: shared memory as written before it, tensor memory as
+  // it leaves it.
+  auto chain = [&](auto issue) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      issue();
+      asm volatile(
+          "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+          : "memory");
+    }
+    wait_bounded(bar, parity, wc, kSiteMmaFull);
+    parity ^= 1u;
+    __syncwarp();
+    tc_fence_after();
+  };
+  const int quarter = warp & 3, group = warp >> 2;  // a thread's row, its warp's share of columns
+  const int row = quarter * 32 + lane;
+  const uint32_t tacc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const bool rows_here = quarter * 32 < np;
+  const int pieces = np * np / 4;  // of four columns: [np / 4][np rows]
+  // Lanes that share a piece in the sum over CTAs, as many as there are threads for.
   const int per = (pieces + p.cluster - 1) / p.cluster;
   int share = 1;
   while (2 * share <= p.cluster && 2 * share * per <= kSmallThreads) share *= 2;
-  const int g8 = lane >> 2, t2 = (lane & 3) * 2;  // a fragment's row and columns
   float keep = 0.0f, rate = 0.0f;
   if (p.w != nullptr) {
     const float lr = __ldg(p.lr);
@@ -362,39 +366,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   }
   for (int step = 0; step < p.steps; ++step) {
     // ---------------------------------------------------------- 1: this slab's X X^T
-    if (warp < blocks * sh.splits) {
-      const int block = warp % blocks, split = warp / blocks;
-      const int i0 = block / nb * 32, j0 = block % nb * 32;
-      const int chunks = slab / 16;
-      float acc[2][4][4];
-      block_product(acc, xh_a, slab, i0, j0, chunks * split / sh.splits * 16,
-                    chunks * (split + 1) / sh.splits * 16, lane);
-      float4* to = reinterpret_cast<float4*>(part) + split * pieces + block * 256 + lane;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          to[(i * 4 + j) * 32] =
-              make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-    }
-    __syncthreads();
-    if (sh.splits > 1) {
-      for (int q = tid; q < pieces; q += kSmallThreads) {
-        float4 s = reinterpret_cast<float4*>(part)[q];
-#pragma unroll 4
-        for (int k = 1; k < sh.splits; ++k) {
-          const float4 o = reinterpret_cast<float4*>(part)[k * pieces + q];
-          s.x += o.x;
-          s.y += o.y;
-          s.z += o.z;
-          s.w += o.w;
-        }
-        reinterpret_cast<float4*>(part)[q] = s;
+    chain([&] { chain_square(tmem, xh_a, np, slab); });
+    if (rows_here) {
+      for (int c = group * (np / 4); c < (group + 1) * (np / 4); c += 8) {
+        float v[8];
+        tmem_ld_32x32b_x8(tacc + c, v);
+        float4* to = reinterpret_cast<float4*>(part) + (c >> 2) * np + row;
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[np] = make_float4(v[4], v[5], v[6], v[7]);
       }
-      if (p.cluster == 1) __syncthreads();
     }
     // ---------------------------------------------------------- 2: the sum over CTAs
-    if (p.cluster > 1) cluster_sync();  // all partial sums are there, and nobody reads E or d
+    // all partial sums are there, and nobody reads E or d
+    if (p.cluster > 1) cluster_sync();
+    else __syncthreads();
     {
       const uint32_t part_a = smem_u32(part), diag_a = smem_u32(diag);
       const int of = tid & (share - 1);
@@ -421,101 +406,111 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
           s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
         }
         if (on) {
-          const int block = q >> 8, frag = (q >> 5) & 7, l = q & 31;
-          const int row = block / nb * 32 + 16 * (frag >> 2) + (l >> 2);
-          const int col = block % nb * 32 + 8 * (frag & 3) + (l & 3) * 2;
+          const int r0 = q % np, col = q / np * 4;
           float v[4] = {s.x * kXInv, s.y * kXInv, s.z * kXInv, s.w * kXInv};  // A times 2^12
-          float dia[2] = {0.f, 0.f};
-          bool has[2] = {false, false};
+          float dia = 0.0f;
+          const bool has = r0 >= col && r0 < col + 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (row + 8 * (k >> 1) == col + (k & 1)) {
-              has[k >> 1] = true;
-              dia[k >> 1] = v[k] * kXInv;
+            if (r0 == col + k) {
+              dia = v[k] * kXInv;
               v[k] = 0.0f;
             }
-          const uint32_t w0 = half2_bits(v[0], v[1]), w1 = half2_bits(v[2], v[3]);
-          const uint32_t to = e_a + 2 * swz(row, col, ns), at = diag_a + 4 * row;
+          const uint2 w = make_uint2(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]));
+          const uint32_t to = e_a + 2 * swz(r0, col, np), at = diag_a + 4 * r0;
           for (int r = of; r < p.cluster; r += share) {
-            const uint32_t t = p.cluster > 1 ? mapa_shared(to, r) : to;
-            const uint32_t z = p.cluster > 1 ? mapa_shared(at, r) : at;
-            st_remote4(t, __uint_as_float(w0));
-            st_remote4(t + 16 * ns, __uint_as_float(w1));  // eight rows on: the same swizzle
-            if (has[0]) st_remote4(z, dia[0]);
-            if (has[1]) st_remote4(z + 32, dia[1]);
+            st_remote8(p.cluster > 1 ? mapa_shared(to, r) : to, w);
+            if (has) st_remote4(p.cluster > 1 ? mapa_shared(at, r) : at, dia);
           }
         }
       }
     }
     if (p.cluster > 1) cluster_sync();
-    else __syncthreads();
     // ---------------------------------------------------------- 3: D and beta
-    if (np <= 64) {  // blocks of 16 x 16: more warps than 32 x 32 have
-      const int n16 = np / 16;
-      if (warp < n16 * n16)
-        poly_block<1, 2>(e, d, diag, beta, np, ns, warp / n16 * 16, warp % n16 * 16, lane, p.a, p.b,
-                         p.c);
-    } else if (warp < blocks) {
-      poly_block<2, 4>(e, d, diag, beta, np, ns, warp / nb * 32, warp % nb * 32, lane, p.a, p.b,
-                       p.c);
+    chain([&] { chain_square(tmem, e_a, np, np); });
+    if (rows_here) {
+      const float dm = diag[row];
+      for (int c = group * (np / 4); c < (group + 1) * (np / 4); c += 8) {
+        float v[8];
+        tmem_ld_32x32b_x8(tacc + c, v);
+        const int at = swz(row, c, np);
+        const uint4 w = *reinterpret_cast<const uint4*>(e + at);
+        const uint32_t ew[4] = {w.x, w.y, w.z, w.w};
+        const float4 d0 = *reinterpret_cast<const float4*>(diag + c);
+        const float4 d1 = *reinterpret_cast<const float4*>(diag + c + 4);
+        const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 e2 = __half22float2(*reinterpret_cast<const __half2*>(&ew[k >> 1]));
+          const float ee = v[k];
+          v[k] = fmaf(fmaf(p.c, dm + dj[k], p.b) * (kXInv * kDScale), k & 1 ? e2.y : e2.x,
+                      (p.c * (kEEInv * kDScale)) * ee);
+          if (c + k == row) {
+            beta[row] = p.a + dm * fmaf(p.c, dm, p.b) + p.c * (ee * kEEInv);
+            v[k] = 0.0f;
+          }
+        }
+        *reinterpret_cast<uint4*>(d + at) =
+            make_uint4(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]), half2_bits(v[4], v[5]),
+                       half2_bits(v[6], v[7]));
+      }
     }
-    __syncthreads();
     // ---------------------------------------------------------- 4: X <- beta X + D X
     const bool last = step == p.steps - 1;
-    const int ksteps = np / 16;
-    for (int c0 = warp * 16; c0 < width; c0 += kSmallWarps * 16) {
-      uint32_t x[kSmallMaxN / 16][4];  // all rows of 16 columns, as the second operand
+    for (int c0 = 0; c0 < slab; c0 += 2 * kSmallBlock) {
+      const int cols = min(2 * kSmallBlock, slab - c0);  // a multiple of 64
+      chain([&] {
+        for (int c = 0; c < cols; c += kSmallBlock)
+          chain_apply(tmem + c, d_a, xh_a, np, c0 + c, min(kSmallBlock, cols - c));
+      });
+      if (rows_here) {
+        const float bm = beta[row];
+        for (int c = group * 8; c < cols; c += 32) {  // the groups' pieces in turn
+          float v[8];
+          tmem_ld_32x32b_x8(tacc + c, v);
+          const int at = swz(row, c0 + c, np);
+          const uint4 hw = *reinterpret_cast<const uint4*>(xh + at);
+          const uint32_t h[4] = {hw.x, hw.y, hw.z, hw.w};
+          float x[8];
 #pragma unroll
-      for (int k = 0; k < kSmallMaxN / 16; ++k)
-        if (k < ksteps)
-          ldm4_t(xh_a + 2 * swz(16 * k + (lane & 15), c0 + (lane >> 4) * 8, slab), x[k]);
-      __syncwarp();
-      const int x8 = lane & 7;
-      const uint32_t da = d_a + 2 * (lane & 15) * ns;
-      // of the fragment's pairs of columns: the row's and the swizzle's part
-      const int p0 = g8 * slab + (((c0 >> 3) ^ g8) << 3) + t2;
-      const int p1 = g8 * slab + ((((c0 >> 3) + 1) ^ g8) << 3) + t2;
-      for (int r0 = 0; r0 < np; r0 += 16) {
-        float acc[2][4] = {};
-#pragma unroll
-        for (int k = 0; k < kSmallMaxN / 16; ++k)
-          if (k < ksteps) {
-            uint32_t a[4];
-            ldm4(da + 2 * r0 * ns + (((2 * k + (lane >> 4)) ^ x8) << 4), a);
-            mma_f16(acc[0], a, x[k][0], x[k][1]);
-            mma_f16(acc[1], a, x[k][2], x[k][3]);
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+            x[2 * k] = f.x;
+            x[2 * k + 1] = f.y;
           }
+          if (!last) {
+            const uint4 lw = *reinterpret_cast<const uint4*>(xl + at);
+            const uint32_t l[4] = {lw.x, lw.y, lw.z, lw.w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float bm = beta[r0 + 8 * h + g8];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int at = (r0 + 8 * h) * slab + (j == 0 ? p0 : p1);
-            const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(xh + at));
-            float v0 = hi.x, v1 = hi.y;
-            if (!last) {
-              const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(xl + at));
-              v0 += lo.x;
-              v1 += lo.y;
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&l[k]));
+              x[2 * k] += f.x;
+              x[2 * k + 1] += f.y;
             }
-            v0 = fmaf(bm, v0, acc[j][2 * h] * (1.0f / kDScale));
-            v1 = fmaf(bm, v1, acc[j][2 * h + 1] * (1.0f / kDScale));
+          }
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float v0 = fmaf(bm, x[2 * k], v[2 * k] * (1.0f / kDScale));
+            const float v1 = fmaf(bm, x[2 * k + 1], v[2 * k + 1] * (1.0f / kDScale));
             if (!last) {
-              const uint32_t hb = half2_bits(v0, v1);
-              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-              *reinterpret_cast<uint32_t*>(xh + at) = hb;
-              *reinterpret_cast<uint32_t*>(xl + at) = half2_bits(v0 - back.x, v1 - back.y);
+              hi[k] = half2_bits(v0, v1);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+              lo[k] = half2_bits(v0 - back.x, v1 - back.y);
             } else {  // fp32, its two halves in the places of the parts
               const uint32_t b0 = __float_as_uint(v0 * kXInv), b1 = __float_as_uint(v1 * kXInv);
-              *reinterpret_cast<uint32_t*>(xh + at) = __byte_perm(b0, b1, 0x7632);
-              *reinterpret_cast<uint32_t*>(xl + at) = __byte_perm(b0, b1, 0x5410);
+              hi[k] = __byte_perm(b0, b1, 0x7632);
+              lo[k] = __byte_perm(b0, b1, 0x5410);
             }
           }
+          *reinterpret_cast<uint4*>(xh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(xl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
     }
-    __syncthreads();
   }
+  tc_fence_before();
+  __syncthreads();
   // ------------------------------------------------------------ the result
   {
     float4 w4[4];
@@ -529,7 +524,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
           float v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int from = swz(row, col, slab);
+            const int from = swz(row, col, np);
             v[c] = __uint_as_float(
                 (static_cast<uint32_t>(__half_as_ushort(xh[from])) << 16) |
                 static_cast<uint32_t>(__half_as_ushort(xl[from])));
@@ -568,6 +563,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
             }
           }
         });
+  }
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kSmallTmem)
+                 : "memory");
   }
   if (p.cluster > 1) cluster_sync();  // nobody reads this CTA's shared memory any more
 }
@@ -641,6 +642,8 @@ cudaError_t launch_muon_small(const MuonInput& in, const OrthoParams& o, int ste
   p.lr = o.lr;
   p.decay = o.decay;
   p.scale = o.scale;
+  p.err = o.err;
+  p.wait_ns = kDefaultWaitNs;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   small_config(cfg, attr, in.batch, cluster, p.shape.bytes(), s);
