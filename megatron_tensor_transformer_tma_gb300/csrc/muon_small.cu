@@ -137,8 +137,9 @@ __device__ __forceinline__ float4 ld_remote4(uint32_t cluster_addr) {
   return v;
 }
 
-__device__ __forceinline__ void st_remote8(uint32_t cluster_addr, uint2 v) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y)
+__device__ __forceinline__ void st_remote16(uint32_t cluster_addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
 
@@ -151,6 +152,16 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// i / d for i, d below 2^16, by the reciprocal ceil(2^32 / d) (d > 1).
+struct Divisor {
+  uint32_t d, m;
+  __device__ __forceinline__ explicit Divisor(int by)
+      : d(static_cast<uint32_t>(by)), m(by > 1 ? 0xffffffffu / static_cast<uint32_t>(by) + 1u : 0u) {}
+  __device__ __forceinline__ int div(int i) const {
+    return d > 1u ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), m)) : i;
+  }
+};
+
 // This CTA's elements of a matrix, in runs of consecutive ones.
 struct SmallRuns {
   int runs, run, quads;  // quads: groups of four of a run, the last one shorter
@@ -158,33 +169,37 @@ struct SmallRuns {
   bool vec;  // whole groups on 16 bytes
 };
 
-// Calls f(address, elements, row, column) for groups of four elements: four addresses a thread
-// before their first use, so that the loads of four groups are in flight together.
-template <int kBatch, typename Load, typename Use>
+constexpr int kSmallBatch = 8;  // groups of a thread whose loads are in flight together
+
+// Calls load(k, address, elements) for a thread's groups of four elements, a batch at a time, then
+// use(k, address, elements, row, column).
+template <typename Load, typename Use>
 __device__ __forceinline__ void for_groups(const SmallRuns& r, int tall, int n, Load load, Use use) {
   const int total = r.runs * r.quads;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * kSmallThreads) {
+  const Divisor by(tall ? n : r.quads);
+  for (int i0 = threadIdx.x; i0 < total; i0 += kSmallBatch * kSmallThreads) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < kSmallBatch; ++k) {
       const int i = i0 + k * kSmallThreads;
       if (i < total) {
-        const int row = tall ? 0 : i / r.quads;
+        const int row = tall ? 0 : by.div(i);
         const int o = (i - row * r.quads) * 4;
         load(k, r.start + row * r.pitch + o, min(4, r.run - o));
       }
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < kSmallBatch; ++k) {
       const int i = i0 + k * kSmallThreads;
       if (i < total) {
-        int row = tall ? 0 : i / r.quads;
+        int row = tall ? 0 : by.div(i);
         const int o = (i - row * r.quads) * 4;
+        const int64_t at = r.start + (tall ? 0 : row * r.pitch) + o;
         int col = o;
         if (tall) {
-          col = o / n;
+          col = by.div(o);
           row = o - col * n;
         }
-        use(k, r.start + (tall ? 0 : row * r.pitch) + o, min(4, r.run - o), row, col);
+        use(k, at, min(4, r.run - o), row, col);
       }
     }
   }
@@ -240,16 +255,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
 
   // ------------------------------------------------------------ momentum and norm
   float4 sq = make_float4(0.f, 0.f, 0.f, 0.f);
-  {
-    float u[4][4];
-    for_groups<4>(
-        runs, p.tall, p.n,
-        [&](int k, int64_t at, int n) {
-          update4<true>(g + at, m == nullptr ? nullptr : m + at, n, runs.vec, p.in.momentum,
-                        p.in.nesterov, u[k]);
-        },
-        [&](int k, int64_t, int, int, int) { add_squares4(u[k], sq); });
-  }
+  float u[kSmallBatch][4];  // of a thread that has one batch: the second pass uses them again
+  const bool kept = runs.runs * runs.quads <= kSmallBatch * kSmallThreads;
+  for_groups(
+      runs, p.tall, p.n,
+      [&](int k, int64_t at, int n) {
+        update4<true>(g + at, m == nullptr ? nullptr : m + at, n, runs.vec, p.in.momentum,
+                      p.in.nesterov, u[k]);
+      },
+      [&](int k, int64_t, int, int, int) { add_squares4(u[k], sq); });
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
     sq.x += __shfl_xor_sync(0xffffffffu, sq.x, o);
@@ -288,12 +302,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   // ------------------------------------------------------------ X in two parts
   {
     const float s1 = factors[0], s2 = factors[1] * kXScale;
-    float u[4][4];
-    for_groups<4>(
+    for_groups(
         runs, p.tall, p.n,
         [&](int k, int64_t at, int n) {
-          update4<false>(g + at, m == nullptr ? nullptr : m + at, n, runs.vec, p.in.momentum,
-                         p.in.nesterov, u[k]);
+          if (!kept)
+            update4<false>(g + at, m == nullptr ? nullptr : m + at, n, runs.vec, p.in.momentum,
+                           p.in.nesterov, u[k]);
         },
         [&](int k, int64_t, int n, int row, int col) {
           float x[4], lo[4];
@@ -353,9 +367,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   const int row = quarter * 32 + lane;
   const uint32_t tacc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const bool rows_here = quarter * 32 < np;
-  const int pieces = np * np / 4;  // of four columns: [np / 4][np rows]
-  // Lanes that share a piece in the sum over CTAs, as many as there are threads for.
-  const int per = (pieces + p.cluster - 1) / p.cluster;
+  // The sum over CTAs: a CTA's rows, in pieces of four columns; lanes that share a piece, as many
+  // as there are threads for.
+  const int slice = np / p.cluster, per = slice * (np / 4);
+  const Divisor by_row(np / 4);
   int share = 1;
   while (2 * share <= p.cluster && 2 * share * per <= kSmallThreads) share *= 2;
   float keep = 0.0f, rate = 0.0f;
@@ -371,9 +386,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       for (int c = group * (np / 4); c < (group + 1) * (np / 4); c += 8) {
         float v[8];
         tmem_ld_32x32b_x8(tacc + c, v);
-        float4* to = reinterpret_cast<float4*>(part) + (c >> 2) * np + row;
-        to[0] = make_float4(v[0], v[1], v[2], v[3]);
-        to[np] = make_float4(v[4], v[5], v[6], v[7]);
+        // rows of np sums, pieces of four in an order that no bank meets twice
+        float4* to = reinterpret_cast<float4*>(part) + row * (np / 4);
+        to[(c >> 2) ^ (row & 7)] = make_float4(v[0], v[1], v[2], v[3]);
+        to[((c >> 2) + 1) ^ (row & 7)] = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
     // ---------------------------------------------------------- 2: the sum over CTAs
@@ -386,10 +402,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       // every lane of a group takes as many rounds: the exchange below needs them all
       for (int q0 = 0; q0 < per; q0 += kSmallThreads / share) {
         const int mine = q0 + tid / share, q = rank * per + mine;
-        const bool on = mine < per && q < pieces;
+        const bool on = mine < per;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         if (on) {
-#pragma unroll 4
+#pragma unroll 8
           for (int r = of; r < p.cluster; r += share) {
             const float4 o =
                 ld_remote4(p.cluster > 1 ? mapa_shared(part_a + 16 * q, r) : part_a + 16 * q);
@@ -405,23 +421,35 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
           s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
           s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
         }
-        if (on) {
-          const int r0 = q % np, col = q / np * 4;
+        if (on && of == 0) {
+          const int r0 = by_row.div(q), col = ((q - r0 * (np / 4)) ^ (r0 & 7)) * 4;
           float v[4] = {s.x * kXInv, s.y * kXInv, s.z * kXInv, s.w * kXInv};  // A times 2^12
-          float dia = 0.0f;
-          const bool has = r0 >= col && r0 < col + 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (r0 == col + k) {
-              dia = v[k] * kXInv;
+              diag[r0] = v[k] * kXInv;
               v[k] = 0.0f;
             }
-          const uint2 w = make_uint2(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]));
-          const uint32_t to = e_a + 2 * swz(r0, col, np), at = diag_a + 4 * r0;
-          for (int r = of; r < p.cluster; r += share) {
-            st_remote8(p.cluster > 1 ? mapa_shared(to, r) : to, w);
-            if (has) st_remote4(p.cluster > 1 ? mapa_shared(at, r) : at, dia);
-          }
+          *reinterpret_cast<uint2*>(e + swz(r0, col, np)) =
+              make_uint2(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]));
+        }
+      }
+      if (p.cluster > 1) {  // this CTA's rows of E, 16 bytes a lane, and of d, to the others
+        __syncthreads();
+        const int chunks = (np + 63) / 64, pieces = slice * 8 * chunks;
+        const Divisor by_piece(pieces), by_chunk(slice * 8);
+        for (int i = tid; i < pieces * p.cluster; i += kSmallThreads) {
+          const int to = by_piece.div(i), piece = i - to * pieces;
+          const int chunk = by_chunk.div(piece);
+          const uint32_t off = static_cast<uint32_t>((chunk * np + rank * slice) * 128 +
+                                                     (piece - chunk * slice * 8) * 16);
+          if (to != rank)
+            st_remote16(mapa_shared(e_a + off, to),
+                        *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(e) + off));
+        }
+        if (tid < slice * p.cluster) {
+          const int to = tid / slice, r0 = rank * slice + tid % slice;
+          if (to != rank) st_remote4(mapa_shared(diag_a + 4 * r0, to), diag[r0]);
         }
       }
     }
@@ -465,46 +493,38 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       });
       if (rows_here) {
         const float bm = beta[row];
-        for (int c = group * 8; c < cols; c += 32) {  // the groups' pieces in turn
-          float v[8];
-          tmem_ld_32x32b_x8(tacc + c, v);
-          const int at = swz(row, c0 + c, np);
-          const uint4 hw = *reinterpret_cast<const uint4*>(xh + at);
-          const uint32_t h[4] = {hw.x, hw.y, hw.z, hw.w};
-          float x[8];
+        for (int c0g = group * 32; c0g < cols; c0g += 128) {  // the groups' columns in turn
+          uint32_t acc[32];
+          tmem_ld_32x32b_x32(tacc + c0g, acc);
+          tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-            x[2 * k] = f.x;
-            x[2 * k + 1] = f.y;
-          }
-          if (!last) {
-            const uint4 lw = *reinterpret_cast<const uint4*>(xl + at);
-            const uint32_t l[4] = {lw.x, lw.y, lw.z, lw.w};
+          for (int j = 0; j < 4; ++j) {
+            const int at = swz(row, c0 + c0g + 8 * j, np);
+            const uint4 hw = *reinterpret_cast<const uint4*>(xh + at);
+            const uint4 lw = last ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(xl + at);
+            const uint32_t h[4] = {hw.x, hw.y, hw.z, hw.w}, l[4] = {lw.x, lw.y, lw.z, lw.w};
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&l[k]));
-              x[2 * k] += f.x;
-              x[2 * k + 1] += f.y;
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+              const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&l[k]));
+              const float v0 = fmaf(bm, f.x + f2.x,
+                                    __uint_as_float(acc[8 * j + 2 * k]) * (1.0f / kDScale));
+              const float v1 = fmaf(bm, f.y + f2.y,
+                                    __uint_as_float(acc[8 * j + 2 * k + 1]) * (1.0f / kDScale));
+              if (!last) {
+                hi[k] = half2_bits(v0, v1);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+                lo[k] = half2_bits(v0 - back.x, v1 - back.y);
+              } else {  // fp32, its two halves in the places of the parts
+                const uint32_t b0 = __float_as_uint(v0 * kXInv), b1 = __float_as_uint(v1 * kXInv);
+                hi[k] = __byte_perm(b0, b1, 0x7632);
+                lo[k] = __byte_perm(b0, b1, 0x5410);
+              }
             }
+            *reinterpret_cast<uint4*>(xh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(xl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float v0 = fmaf(bm, x[2 * k], v[2 * k] * (1.0f / kDScale));
-            const float v1 = fmaf(bm, x[2 * k + 1], v[2 * k + 1] * (1.0f / kDScale));
-            if (!last) {
-              hi[k] = half2_bits(v0, v1);
-              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-              lo[k] = half2_bits(v0 - back.x, v1 - back.y);
-            } else {  // fp32, its two halves in the places of the parts
-              const uint32_t b0 = __float_as_uint(v0 * kXInv), b1 = __float_as_uint(v1 * kXInv);
-              hi[k] = __byte_perm(b0, b1, 0x7632);
-              lo[k] = __byte_perm(b0, b1, 0x5410);
-            }
-          }
-          *reinterpret_cast<uint4*>(xh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(xl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
     }
@@ -513,25 +533,31 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   __syncthreads();
   // ------------------------------------------------------------ the result
   {
-    float4 w4[4];
+    float4 w4[kSmallBatch];
     const int64_t base = matrix * elems;
-    for_groups<4>(
+    for_groups(
         runs, p.tall, p.n,
         [&](int k, int64_t at, int) {
           if (p.w != nullptr && runs.vec) w4[k] = *reinterpret_cast<const float4*>(p.w + base + at);
         },
         [&](int k, int64_t at, int n, int row, int col) {
           float v[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          if (!p.tall) {  // four columns of a row, in one piece
             const int from = swz(row, col, np);
-            v[c] = __uint_as_float(
-                (static_cast<uint32_t>(__half_as_ushort(xh[from])) << 16) |
-                static_cast<uint32_t>(__half_as_ushort(xl[from])));
-            if (c + 1 < n) {
-              if (!p.tall) {
-                ++col;
-              } else if (++row == p.n) {
+            const uint2 hi = *reinterpret_cast<const uint2*>(xh + from);
+            const uint2 lo = *reinterpret_cast<const uint2*>(xl + from);
+            v[0] = __uint_as_float(__byte_perm(lo.x, hi.x, 0x5410));
+            v[1] = __uint_as_float(__byte_perm(lo.x, hi.x, 0x7632));
+            v[2] = __uint_as_float(__byte_perm(lo.y, hi.y, 0x5410));
+            v[3] = __uint_as_float(__byte_perm(lo.y, hi.y, 0x7632));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int from = swz(row, col, np);
+              v[c] = __uint_as_float(
+                  (static_cast<uint32_t>(__half_as_ushort(xh[from])) << 16) |
+                  static_cast<uint32_t>(__half_as_ushort(xl[from])));
+              if (c + 1 < n && ++row == p.n) {
                 row = 0;
                 ++col;
               }
