@@ -307,9 +307,8 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
   h->ldn = static_cast<int>(cdiv(h->n, kOrthoLd)) * kOrthoLd;
   h->fault_pending = (c.flags & MLPB_MUON_FAULT_INJECT) != 0;
   h->err = nullptr;
-  int major = 0, minor = 0, sms = 0;
+  int major = 0, minor = 0;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, h->device) != cudaSuccess) {
     delete h;
@@ -328,15 +327,9 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
     return MLPB_ECUDA;
   }
   h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  const int64_t length = std::max(c.rows, c.cols);
-  h->small = muon_small_cluster(h->n, length, c.batch, sms);
-  if (h->small > 0) {
-    bool fits = false;
-    if (muon_small_set_attrs(h->n, length, h->small, &fits) != cudaSuccess) {
-      delete h;
-      return MLPB_ECUDA;
-    }
-    if (!fits) h->small = 0;
+  if (muon_small_cluster(h->n, std::max(c.rows, c.cols), c.batch, &h->small) != cudaSuccess) {
+    delete h;
+    return MLPB_ECUDA;
   }
   if (ortho_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
       cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||

@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "muon_update.cuh"
+#include "pointwise.cuh"
 #include "ptx.cuh"
 
 namespace mlpb {
@@ -367,6 +368,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   const int row = quarter * 32 + lane;
   const uint32_t tacc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const bool rows_here = quarter * 32 < np;
+  // of step 4: parts of the columns, and the lane's part and row
+  const int spread_log = np == 32 ? 2 : np == 64 ? 1 : 0, spread = 1 << spread_log;
+  const int part_of = quarter * 32 / np, mrow = row - part_of * np;
   // The sum over CTAs: a CTA's rows, in pieces of four columns; lanes that share a piece, as many
   // as there are threads for.
   const int slice = np / p.cluster, per = slice * (np / 4);
@@ -484,22 +488,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       }
     }
     // ---------------------------------------------------------- 4: X <- beta X + D X
+    // A chain fills 128 lanes, D np of them: with np = 32 or 64 each part of the columns has a chain
+    // of its own whose D lies np rows lower, so that all warps have lanes to take.
     const bool last = step == p.steps - 1;
     for (int c0 = 0; c0 < slab; c0 += 2 * kSmallBlock) {
-      const int cols = min(2 * kSmallBlock, slab - c0);  // a multiple of 64
+      const int cols = min(2 * kSmallBlock, slab - c0), blocks = cols / 64;
       chain([&] {
-        for (int c = 0; c < cols; c += kSmallBlock)
-          chain_apply(tmem + c, d_a, xh_a, np, c0 + c, min(kSmallBlock, cols - c));
+        for (int j = 0; j < spread; ++j) {
+          const int end = (blocks * (j + 1) >> spread_log) * 64;
+          for (int c = (blocks * j >> spread_log) * 64; c < end; c += kSmallBlock)
+            chain_apply(tmem + c, d_a - j * np * 128, xh_a, np, c0 + c, min(kSmallBlock, end - c));
+        }
       });
-      if (rows_here) {
-        const float bm = beta[row];
-        for (int c0g = group * 32; c0g < cols; c0g += 128) {  // the groups' columns in turn
-          uint32_t acc[32];
-          tmem_ld_32x32b_x32(tacc + c0g, acc);
+      if (part_of < spread) {
+        const uint64_t bm = f2_pack(beta[mrow], beta[mrow]);
+        const uint64_t scale = f2_pack(1.0f / kDScale, 1.0f / kDScale);
+        const int end = (blocks * (part_of + 1) >> spread_log) * 64;
+        for (int c = (blocks * part_of >> spread_log) * 64 + group * 16; c < end; c += 64) {
+          uint32_t acc[16];
+          tmem_ld_32x32b_x16(tacc + c, acc);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int at = swz(row, c0 + c0g + 8 * j, np);
+          for (int j = 0; j < 2; ++j) {
+            const int at = swz(mrow, c0 + c + 8 * j, np);
             const uint4 hw = *reinterpret_cast<const uint4*>(xh + at);
             const uint4 lw = last ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(xl + at);
             const uint32_t h[4] = {hw.x, hw.y, hw.z, hw.w}, l[4] = {lw.x, lw.y, lw.z, lw.w};
@@ -507,11 +518,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-              const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&l[k]));
-              const float v0 = fmaf(bm, f.x + f2.x,
-                                    __uint_as_float(acc[8 * j + 2 * k]) * (1.0f / kDScale));
-              const float v1 = fmaf(bm, f.y + f2.y,
-                                    __uint_as_float(acc[8 * j + 2 * k + 1]) * (1.0f / kDScale));
+              const float2 g2 = __half22float2(*reinterpret_cast<const __half2*>(&l[k]));
+              const uint64_t x = f2_add(f2_pack(f.x, f.y), f2_pack(g2.x, g2.y));
+              const uint64_t a2 = f2_mul(f2_pack(__uint_as_float(acc[8 * j + 2 * k]),
+                                                 __uint_as_float(acc[8 * j + 2 * k + 1])),
+                                         scale);
+              float v0, v1;
+              f2_unpack(f2_fma(bm, x, a2), v0, v1);
               if (!last) {
                 hi[k] = half2_bits(v0, v1);
                 const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
@@ -599,17 +612,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   if (p.cluster > 1) cluster_sync();  // nobody reads this CTA's shared memory any more
 }
 
-// CTAs of a cluster for one matrix, or 0 where the matrix does not fit: the fewest that hold it,
-// more while there are SMs for them and at least 64 columns for each.
-int muon_small_cluster(int n, int64_t length, int64_t batch, int num_sms) {
-  if (n > kSmallMaxN) return 0;
-  int c = 1;
-  while (c <= kSmallMaxCluster && small_shape(n, length, c).bytes() > kSmallMaxSmem) c *= 2;
-  if (c > kSmallMaxCluster) return 0;
-  while (2 * c <= kSmallMaxCluster && batch * 2 * c <= num_sms && length > 64 * c) c *= 2;
-  return c;
-}
-
 template <typename T>
 static cudaError_t small_attrs() {
   cudaError_t e = cudaFuncSetAttribute(muon_small_kernel<T>,
@@ -635,18 +637,28 @@ static void small_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int
   cfg.numAttrs = 1;
 }
 
-cudaError_t muon_small_set_attrs(int n, int64_t length, int cluster, bool* fits) {
-  *fits = false;
+// CTAs of a cluster for one matrix, or 0 where no cluster holds it: the most (at least 64 columns
+// for each) with which all matrices are resident at once, or the fewest that hold a matrix.  (A
+// cluster has to find its SMs in one part of the GPU: of 16 CTAs only a few are resident together.)
+cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, int* cluster) {
+  *cluster = 0;
+  if (n > kSmallMaxN) return cudaSuccess;
   cudaError_t e = small_attrs<float>();
   if (e == cudaSuccess) e = small_attrs<__nv_bfloat16>();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  small_config(cfg, attr, 1, cluster, small_shape(n, length, cluster).bytes(), nullptr);
-  int clusters = 0;
-  e = cudaOccupancyMaxActiveClusters(&clusters, muon_small_kernel<float>, &cfg);
-  *fits = e == cudaSuccess && clusters > 0;
-  return e;
+  for (int c = 1; c <= kSmallMaxCluster; c *= 2) {
+    const size_t smem = small_shape(n, length, c).bytes();
+    if (smem > kSmallMaxSmem) continue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    small_config(cfg, attr, 1, c, smem, nullptr);
+    int resident = 0;
+    e = cudaOccupancyMaxActiveClusters(&resident, muon_small_kernel<float>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (resident < 1) continue;
+    if (*cluster == 0 || (batch <= resident && length > 64 * (c / 2))) *cluster = c;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_muon_small(const MuonInput& in, const OrthoParams& o, int steps, int cluster,
