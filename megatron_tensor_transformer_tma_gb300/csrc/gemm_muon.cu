@@ -251,6 +251,7 @@ __device__ __forceinline__ void symmetric_box(float (&v)[32], int j0, uint32_t s
     }
     __syncwarp();
   }
+  const float lin = fmaf(p.c, dm, p.b) * (kXInv * kDScale);  // and by the row
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int j = j0 + q;
@@ -261,8 +262,7 @@ __device__ __forceinline__ void symmetric_box(float (&v)[32], int j0, uint32_t s
       unpack_half8(lds16(at), e16);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float lin = fmaf(p.c, dm + dj.at(j0, 8 * q + i), p.b) * (kXInv * kDScale);
-        r[i] = fmaf(lin, e16[i], (p.c * (kEEInv * kDScale)) * v[8 * q + i]);
+        r[i] = fmaf(lin + dj.at(j0, 8 * q + i), e16[i], (p.c * (kEEInv * kDScale)) * v[8 * q + i]);
       }
     } else {
 #pragma unroll
@@ -411,6 +411,22 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
     float dm = 0.0f;  // the row's d or beta
     if (Op == OrthoOp::Poly && m < p.n) dm = __ldcg(p.diag + vec + m);
     if (!kSymmetric<Op> && !kTall && m < p.rows) dm = __ldcg(p.beta + vec + m);
+    // d or beta along a box's columns, read a box ahead
+    auto columns_of = [&](int col) {
+      ColumnPair c{0.0f, 0.0f};
+      if (Op == OrthoOp::Poly || (!kSymmetric<Op> && kTall)) {
+        const float* at = (Op == OrthoOp::Poly ? p.diag : p.beta) + vec;
+        const int width = kSymmetric<Op> ? p.n : p.cols;
+        if (col + lane < width) c.lo = __ldcg(at + col + lane);
+        if (col + 32 + lane < width) c.hi = __ldcg(at + col + 32 + lane);
+        if (Op == OrthoOp::Poly) {  // what of E's factor goes by the column
+          c.lo *= p.c * (kXInv * kDScale);
+          c.hi *= p.c * (kXInv * kDScale);
+        }
+      }
+      return c;
+    };
+    ColumnPair next_cj = columns_of(t.nt * BN + half * kEpiCols);
     int ok = 1;
     if (lane == 0)
       ok = wait_bounded(tfull0 + 8 * buf, (it >> 1) & 1, wc, kSiteEpiAccFull) ? 1 : 0;
@@ -447,13 +463,8 @@ __device__ __forceinline__ void ortho_epilogue(uint32_t tmem_base, uint32_t tful
 #pragma unroll 1
     for (int sub = half; sub < subs; sub += 2) {
       const int col = t.nt * BN + sub * kEpiCols;
-      ColumnPair cj{0.0f, 0.0f};
-      if (Op == OrthoOp::Poly || (!kSymmetric<Op> && kTall)) {
-        const float* c = (Op == OrthoOp::Poly ? p.diag : p.beta) + vec + col;
-        const int width = kSymmetric<Op> ? p.n : p.cols;
-        if (col + lane < width) cj.lo = __ldcg(c + lane);
-        if (col + 32 + lane < width) cj.hi = __ldcg(c + 32 + lane);
-      }
+      const ColumnPair cj = next_cj;
+      if (sub + 2 < subs) next_cj = columns_of(col + 2 * kEpiCols);
       if constexpr (Sm::loads) {
         if (lane == 0) ok = wait_bounded(box_bar, box_parity, wc, kSiteEpiAccFull) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
