@@ -19,8 +19,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libmlpb.so")
 SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_bwd.cu", "reduce.cu", "layernorm.cu",
            "reduce_noalloc.cu", "fp8.cu", "gemm_fp8.cu", "gemm_ckpt8.cu", "act8.cu",
            "join.cu", "join_bf16.cu", "join_y32.cu", "join_x32.cu", "join_f32.cu",
-           "moe.cu", "b128.cu", "gemm_b128.cu", "gemm_b128_few.cu",
-           "linear8.cu",
+           "moe.cu", "b128.cu", "gemm_b128.cu", "gemm_b128_few.cu", "linear8.cu",
            "muon.cu", "muon_prepare.cu", "gemm_muon.cu", "muon_small.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -36,6 +36,7 @@ def round_e4m3(x):
 
 def scale_exponent(amax):
     """k of a block with this finite largest magnitude."""
+    amax = float(amax)
     if amax == 0:
         return 0
     k = 126
