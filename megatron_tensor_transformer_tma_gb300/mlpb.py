@@ -694,6 +694,8 @@ def b128_values(q, rows, cols):
     """What a (codes, scales) pair stands for, as fp64 [rows][cols] (torch operations: for tests
     and inspection; fp32's largest values are rounded to 2^128)."""
     codes, scales = q
+    if rows == 0 or cols == 0:
+        return torch.empty((rows, cols), dtype=torch.float64, device=codes.device)
     n = -(-cols // 128)
     tiles = -(-rows // 128)
     e = scales.view(-1, tiles, 32, 4, 4).permute(1, 3, 2, 0, 4).reshape(tiles * 128, -1)[:rows, :n]
@@ -1136,7 +1138,7 @@ class Linear8:
                                      device=self.device)
         self.Wq = b128_empty(outputs, inputs, self.device)
         self.Wt = b128_empty(inputs, outputs, self.device) if training else None
-        self._saved = None
+        self._saved, self._tokens = None, None  # X^T of the last forward, its tokens
         if training:  # one buffer for any number of tokens
             ld, n = mlpb_b128_sizes(inputs, max_tokens)
             self._saved = torch.empty(inputs * ld + n, dtype=torch.uint8, device=self.device)
@@ -1184,6 +1186,8 @@ class Linear8:
                 *(self._saved_args(T, Xt) if Xt is not None or self.training else (None, None)),
                 self.workspace.data_ptr()]
         _call_on(dev, "mlpb_linear8_forward", args, stream)
+        if Xt is None:
+            self._tokens = T
         return Y
 
     def backward(self, dY, dX=None, dW=None, Xt=None, accumulate=False, input_grad=True,
@@ -1196,6 +1200,8 @@ class Linear8:
             raise ValueError("dW: nothing given to add into")
         h, c, dev = self.handle, self.cfg, self.device.index
         T = _linear8_rows(h, dY, c.outputs, "dY")[1]
+        if Xt is None and T > 0 and T != self._tokens:
+            raise ValueError(f"dY: {T} tokens, the last forward had {self._tokens}")
         with _on(stream, self.device):
             if dX is None and input_grad:
                 dX = torch.empty((T, c.inputs), dtype=self.out_dtype, device=self.device)

@@ -192,6 +192,11 @@ def test_zero_tokens_and_refusals():
         plan.backward(dY, accumulate=True)
     with pytest.raises(ValueError, match="training"):
         mlpb.Linear8(4, K, N, training=False).backward(dY)
+    with pytest.raises(ValueError, match="last forward"):  # none yet
+        plan.backward(dY)
+    plan.forward(X[:3])
+    with pytest.raises(ValueError, match="4 tokens, the last forward had 3"):
+        plan.backward(dY)
     h, Y = plan.handle, torch.empty(4, N, dtype=BF, device="cuda")
     with pytest.raises(ValueError, match="are needed"):
         mlpb.mlpb_linear8_forward(h, X, plan.Wq, Y, None, plan.workspace[:16])

@@ -138,3 +138,9 @@ def test_header_flag_values_match_binding():
     for name in ("MLPB_LINEAR8_OUT_F32", "MLPB_LINEAR8_FAULT_INJECT"):
         m = re.search(rf"#define\s+{name}\s+(0x[0-9a-fA-F]+)u", src)
         assert m and int(m.group(1), 16) == getattr(mlpb, name), name
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 64), (64, 0), (0, 0)])
+def test_values_of_nothing(lib, rows, cols):
+    v = mlpb.b128_values(mlpb.b128_empty(rows, cols, "cpu"), rows, cols)
+    assert tuple(v.shape) == (rows, cols) and v.dtype == torch.float64
