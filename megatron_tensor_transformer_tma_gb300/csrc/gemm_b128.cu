@@ -5,7 +5,7 @@
 // A CTA pair computes a 256 x 256 tile, as in gemm.cuh.  Each CTA (320 threads) has:
 //   warp 0      TMA producer: a 6-stage ring of 128 x 128-byte A and B-half tiles, and with every
 //               fourth k-block the 512 bytes of scales of the CTA's 128 A rows and the 1024 bytes
-//               of all 256 B rows (each SM multiplies its A rows with all of B's), beside the stage;
+//               of all 256 B rows (an SM multiplies its A rows with all of B's), beside the stage;
 //   warp 1      in the even CTA: copies scales from both CTAs' shared memory to their tensor
 //               memory (tcgen05.cp, in issue order with the MMAs that read them) and issues the
 //               MMAs; the scale byte of a k-block is chosen by the instruction descriptor;

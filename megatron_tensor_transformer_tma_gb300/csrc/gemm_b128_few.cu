@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kFewThreads)
       int stage = 0;
       uint32_t phase = 0, sbuf = 0;
       bool ok = true;
+      pdl_wait();  // the bounded waits count from where B may come
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_bounded(full0 + 8 * stage, phase, wc, kSiteMmaFull)) {
           ok = false;
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kFewThreads)
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     int ok = 1;
+    pdl_wait();
     if (lane == 0) ok = wait_bounded(tfull, 0, wc, kSiteEpiAccFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     __syncwarp();

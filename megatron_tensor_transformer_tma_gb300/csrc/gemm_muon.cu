@@ -363,7 +363,8 @@ __device__ __forceinline__ void ragged_rows(uint32_t slot, int lane, int row0, i
   }
 }
 
-// Where a 32 x 64 box of a range's sums begins: [unit][CTA][epilogue warp][box of its half][16][32].
+// Where a 32 x 64 box of a range's sums begins: [unit][CTA][epilogue warp][box of its half]
+// [16][32].
 template <int BN>
 __device__ __forceinline__ size_t partial_box(int unit, int rank, int ewarp, int i) {
   return ((static_cast<size_t>(unit) * 2 + rank) * kEpiWarps + ewarp) * (BN / 128) * 512 + i * 512;
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
+      pdl_wait();  // the bounded waits below count from where the operands may come
       for (int u = cid; u < p.units; u += nclusters, ++it) {
         const int buf = it & 1;
         const uint32_t acc_par = (it >> 1) & 1;
@@ -770,7 +772,8 @@ __global__ void __launch_bounds__(kFoldThreads) ortho_fold_kernel(const OrthoPar
   const size_t mat = static_cast<size_t>(t.b) * p.n * p.ldn;
   const float dm = Op == OrthoOp::Poly && m < p.n ? __ldcg(p.diag + vec + m) : 0.0f;
   const WaitCtx wc{&abort_word, p.err, p.wait_ns};
-  wait_bounded(bar, 0, wc, kSiteEpiAccFull);
+  // after an expired wait the copies land before shared memory is given up
+  if (!wait_bounded(bar, 0, wc, kSiteEpiAccFull)) wait_drain(bar, 0, wc);
   float4 s[4] = {};
   const float4* from = reinterpret_cast<const float4*>(fold_smem) + warp * 32 + lane;
 #pragma unroll 4
@@ -800,8 +803,8 @@ __global__ void __launch_bounds__(kFoldThreads) ortho_fold_kernel(const OrthoPar
     } else {
       float e16[4] = {0.f, 0.f, 0.f, 0.f}, dj[4] = {0.f, 0.f, 0.f, 0.f};
       if (m < p.n) {  // rows of 64 elements: inside the buffer
-        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p.e + mat +
-                                                              static_cast<size_t>(m) * p.ldn + col));
+        const __half* from_e = p.e + mat + static_cast<size_t>(m) * p.ldn + col;
+        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(from_e));
         const float2 a = unpack_half2(w.x), b = unpack_half2(w.y);
         e16[0] = a.x;
         e16[1] = a.y;

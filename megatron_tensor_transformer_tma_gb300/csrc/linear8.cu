@@ -79,10 +79,10 @@ bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
                 kB128Chunk / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Whether a product goes to the kernel for few tiles: at most 128 rows of C, or fewer tiles of
+// Whether a product goes to the kernel for few tiles: at most 128 rows of C, or no more tiles of
 // 256 x 256 than half the pairs of SMs, than all of them where K is at most 40 k-blocks (768 x
-// 5120 x 5120 21.8 against 24.2 us, but 1000 x 11008 x 4096 45.5 against 40.4); not where an fp32 sum is long enough for chunks, which
-// that kernel does not have.
+// 5120 x 5120 21.8 against 24.2 us, but 1000 x 11008 x 4096 45.5 against 40.4); not where an fp32
+// sum is long enough for chunks, which that kernel does not have.
 bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n, int64_t k, bool f32) {
   if (b128_blocks(k) > b128_chunk(f32)) return false;
   const int64_t tiles = cdiv(m, 256) * cdiv(n, 256);

@@ -127,8 +127,8 @@ Layout layout(const mlpb_muon* h, void* workspace) {
   return l;
 }
 
-bool encode(const mlpb_muon* h, CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
-            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+bool encode(const mlpb_muon* h, CUtensorMap* m, CUtensorMapDataType type, const void* base,
+            int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
             CUtensorMapSwizzle swizzle) {
   const cuuint32_t steps[4] = {1, 1, 1, 1};
   return h->encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
@@ -289,14 +289,14 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
   if (cfg == nullptr || out == nullptr) return MLPB_EINVAL;
   *out = nullptr;
   const mlpb_muon_config& c = *cfg;
-  if (c.batch < 1 || c.rows < 1 || c.cols < 1 || c.steps < 1 || (c.nesterov != 0 && c.nesterov != 1) ||
-      (c.flags & ~MLPB_MUON_FAULT_INJECT) != 0)
+  if (c.batch < 1 || c.rows < 1 || c.cols < 1 || c.steps < 1 ||
+      (c.nesterov != 0 && c.nesterov != 1) || (c.flags & ~MLPB_MUON_FAULT_INJECT) != 0)
     return MLPB_EINVAL;
   for (float f : {c.coef[0], c.coef[1], c.coef[2], c.weight_decay, c.scale})
     if (!std::isfinite(f)) return MLPB_EINVAL;
   if (!(c.momentum >= 0.0f && c.momentum < 1.0f)) return MLPB_EINVAL;
   if (c.batch > 65535 || c.rows > 65536 || c.cols > 65536 || c.steps > 64 ||
-      c.batch * cdiv(c.rows, 256) * cdiv(c.cols, 256) > (int64_t{1} << 30) || !coefficients_fit(c))
+      c.batch * cdiv(c.rows, 256) * cdiv(c.cols, 256) > (int64_t{1} << 29) || !coefficients_fit(c))
     return MLPB_EUNSUPPORTED;
   mlpb_muon* h = new (std::nothrow) mlpb_muon();
   if (h == nullptr) return MLPB_ENOMEM;

@@ -11,8 +11,8 @@
 //     is hi alone: what it loses is not amplified any more.)
 //   - The diagonal d of A is fp32 and its part E off the diagonal fp16:
 //       A A = E E + (d_i + d_j) E_ij + delta_ij d_i^2,
-//     so the identity that A comes near is not rounded.  Likewise b A + c A A + a I = D + diag(beta)
-//     and X' = beta X + D X: a X and most of (b A + c A A) X cancel (3.4 - 2.7 near the end), and
+//     so the identity that A comes near is not rounded.  Likewise b A + c A A + a I is
+//     D + diag(beta) and X' = beta X + D X: a X and most of (b A + c A A) X cancel (3.4 - 2.7 near the end), and
 //     do so in fp32.
 // Against 64 bits the result is off by 3e-4 to 7e-4 of its size (Gaussian, low-rank and decaying
 // spectra); with the diagonals in the products it is 1e-3 to 3e-3, with bf16 operands 1e-2 to

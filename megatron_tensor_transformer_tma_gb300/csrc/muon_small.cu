@@ -14,7 +14,7 @@
 // Two barriers of the cluster a step.  The products are single tcgen05 chains of M = 128 (rows past
 // n are of whatever lies behind and are not read back) that a thread issues between barriers of the
 // CTA: with mma.sync, a sixteenth of the rate here, they were two thirds of the time at n = 128
-// (128 x 4096: 102 us).  X, E and D lie in chunks of 64 columns, rows of 128 bytes with the 128-byte
+// (128 x 4096: 102 us).  X, E and D lie in chunks of 64 columns, rows of 128 bytes with that
 // swizzle: the K-major operand of 1, 3 and 4 (D) and, the same bytes, the MN-major one of 4 (X).
 #include <algorithm>
 
@@ -49,7 +49,7 @@ struct SmallShape {
     return sums > e_bytes() ? sums : e_bytes();
   }
   __host__ __device__ size_t used() const { return 2 * x_bytes() + e_bytes() + p_bytes(); }
-  // A chain reads 128 rows of its chunk, whatever np is: what lies behind the last one is there too.
+  // A chain reads 128 rows of its chunk, whatever np is: what lies behind the last is there too.
   __host__ __device__ size_t bytes() const {
     const size_t b = used() + static_cast<size_t>(128 - np) * 128 + 2 * kSmallMaxN * 4 + 512 + 1024;
     return b > kSmallMinSmem ? b : kSmallMinSmem;
@@ -157,7 +157,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 struct Divisor {
   uint32_t d, m;
   __device__ __forceinline__ explicit Divisor(int by)
-      : d(static_cast<uint32_t>(by)), m(by > 1 ? 0xffffffffu / static_cast<uint32_t>(by) + 1u : 0u) {}
+      : d(static_cast<uint32_t>(by)),
+        m(by > 1 ? 0xffffffffu / static_cast<uint32_t>(by) + 1u : 0u) {}
   __device__ __forceinline__ int div(int i) const {
     return d > 1u ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), m)) : i;
   }
@@ -175,7 +176,8 @@ constexpr int kSmallBatch = 8;  // groups of a thread whose loads are in flight 
 // Calls load(k, address, elements) for a thread's groups of four elements, a batch at a time, then
 // use(k, address, elements, row, column).
 template <typename Load, typename Use>
-__device__ __forceinline__ void for_groups(const SmallRuns& r, int tall, int n, Load load, Use use) {
+__device__ __forceinline__ void for_groups(const SmallRuns& r, int tall, int n, Load load,
+                                           Use use) {
   const int total = r.runs * r.quads;
   const Divisor by(tall ? n : r.quads);
   for (int i0 = threadIdx.x; i0 < total; i0 += kSmallBatch * kSmallThreads) {
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 && *wc.abort_flag == 0u) {  // no more products after an expired wait
       tc_fence_after();
       issue();
       asm volatile(
@@ -488,8 +490,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       }
     }
     // ---------------------------------------------------------- 4: X <- beta X + D X
-    // A chain fills 128 lanes, D np of them: with np = 32 or 64 each part of the columns has a chain
-    // of its own whose D lies np rows lower, so that all warps have lanes to take.
+    // A chain fills 128 lanes, D np of them: with np = 32 or 64 each part of the columns has a
+    // chain of its own whose D lies np rows lower, so that all warps have lanes to take.
     const bool last = step == p.steps - 1;
     for (int c0 = 0; c0 < slab; c0 += 2 * kSmallBlock) {
       const int cols = min(2 * kSmallBlock, slab - c0), blocks = cols / 64;
@@ -512,7 +514,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
           for (int j = 0; j < 2; ++j) {
             const int at = swz(mrow, c0 + c + 8 * j, np);
             const uint4 hw = *reinterpret_cast<const uint4*>(xh + at);
-            const uint4 lw = last ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(xl + at);
+            const uint4 lw =
+                last ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(xl + at);
             const uint32_t h[4] = {hw.x, hw.y, hw.z, hw.w}, l[4] = {lw.x, lw.y, lw.z, lw.w};
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -604,6 +607,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
         });
   }
   if (warp == 0) {
+    if (*wc.abort_flag != 0u) {  // the chain that a wait gave up on has long ended by then
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 20000ull) {
+      }
+      __syncwarp();
+    }
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kSmallTmem)
