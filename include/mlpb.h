@@ -472,7 +472,8 @@ mlpb_status mlpb_moe_last_device_error(mlpb_moe *h, mlpb_stream_t stream);
  * <= 448 (k = 0 for zeros), a code is e4m3(x 2^k), nearest, ties to even, and the scale byte is
  * 127 - k: a code c stands for c 2^(byte - 127), exactly.  A block that holds an infinity or a NaN
  * has the byte 255 and stands for NaN throughout.
- *   codes   [rows][ld] bytes, ld = columns rounded up to 16 (mlpb_b128_sizes); the pad holds 0
+ *   codes   [rows][ld] bytes, ld = columns rounded up to 16 (mlpb_b128_sizes); the pad holds 0 (NaN
+ *           in a block that holds one)
  *   scales  byte of (row, kb = column / 128) at
  *             ((kb / 4) * ceil(rows / 128) + row / 128) * 512
  *               + (row % 32) * 16 + (row % 128) / 32 * 4 + kb % 4,
@@ -519,6 +520,7 @@ mlpb_status mlpb_linear8_workspace_size(const mlpb_linear8 *h, size_t *bytes);
 /* Forward of `tokens` <= max_tokens rows (0 does nothing): X [tokens][inputs] bf16; Wq, Ws the
  * codes and scales of W [outputs][inputs] (mlpb_b128_quantize, square); Y [tokens][outputs].
  * Xt, Xts, NULL in serving, receive codes and scales of X^T [inputs][tokens] for the backward.
+ * Outputs overlap no input, here and in the backward.
  * The current device must be the handle's.  Calls that share a workspace must not overlap on the
  * GPU (a captured graph counts as its call, and the handle has to outlive it). */
 mlpb_status mlpb_linear8_forward(mlpb_linear8 *h, int64_t tokens, const void *X, const void *Wq,
@@ -551,7 +553,8 @@ mlpb_status mlpb_linear8_last_device_error(mlpb_linear8 *h, mlpb_stream_t stream
  * Products take fp16 operands with fixed scales, sums and both products' diagonals are fp32, X
  * keeps 22 bits between the steps: O is off by some 5e-4 of its size. */
 #define MLPB_MUON_FAULT_INJECT 0x1u /* test only, as MLPB_FLAG_FAULT_INJECT: the first product's \
-                                       first stage is never filled                              */
+                                       first stage is never filled (no effect on matrices that \
+                                       lie in shared memory, where nothing waits for a copy)    */
 
 typedef struct {
   int64_t batch;      /* matrices, 1..65535                                                     */
@@ -572,13 +575,14 @@ typedef struct mlpb_muon mlpb_muon; /* opaque; owns a device word and no tensors
 mlpb_status mlpb_muon_create(const mlpb_muon_config *cfg, mlpb_muon **out);
 void mlpb_muon_destroy(mlpb_muon *h);
 
-/* Bytes of the workspace of the calls below (three fp16 copies of X, two symmetric matrices of the
- * smaller side). */
+/* Bytes of the workspace of the calls below: three fp16 copies of X, two symmetric fp16 matrices of
+ * the smaller side, and where few tiles are cut into ranges their fp32 sums; 256 bytes where a
+ * matrix lies in shared memory (a smaller side of at most 128, a longer one of some thousands). */
 mlpb_status mlpb_muon_workspace_size(const mlpb_muon *h, size_t *bytes);
 
 /* O [batch][rows][cols] bf16 from U, bf16 or (u_f32 = 1) fp32 (O may not overlap U).  16-byte
  * aligned tensors.  The current device must be the handle's.  Calls that share a workspace must
- * not overlap on the GPU (a captured graph counts as its call, and the handle has to outlive it). */
+ * not overlap on the GPU (a captured graph counts as its call; the handle has to outlive it). */
 mlpb_status mlpb_muon_orthogonalize(mlpb_muon *h, const void *U, int32_t u_f32, void *O,
                                     void *workspace, mlpb_stream_t stream);
 

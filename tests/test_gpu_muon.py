@@ -6,8 +6,9 @@ operands rounded); the library, whose sums are fp32 besides, may be three times 
 2-norm over a matrix, and the bf16 result is off by half a step more, 2^-8 of each value.  A single
 element may be off by six times the largest error of those roundings.  (Six: 30 times an element's
 share of the norm, which is 4.7 shares at most for even matrices; where rows differ in size the
-roundings' own largest error is some 100 shares, since each is relative to its element.)  M is one fused fp32 multiplication and
-addition: one rounding of a product and a sum, 2^-23 of their magnitudes."""
+roundings' own largest error is some 100 shares, since each is relative to its element.)  M is one
+fused fp32 multiplication and addition: one rounding of a product and a sum, 2^-23 of their
+magnitudes."""
 import numpy as np
 import pytest
 import torch
@@ -191,7 +192,7 @@ def test_refusals():
 
 
 def test_an_expired_wait_is_reported_and_the_next_call_is_right():
-    U = _randn(1, 1, 300, 520)  # not a matrix that lies in shared memory: nothing waits there
+    U = _randn(1, 1, 300, 520)  # no matrix of shared memory: nothing waits for a copy there
     want = mlpb.Muon(300, 520).orthogonalize(U)
     hurt = mlpb.Muon(300, 520, flags=mlpb.MLPB_MUON_FAULT_INJECT)
     hurt.orthogonalize(U)
