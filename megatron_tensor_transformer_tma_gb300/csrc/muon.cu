@@ -53,8 +53,11 @@ struct Tiling {
 // end first, in the time of a k-block (0.26 us).  That is the same for both widths: a ring of five
 // or six stages keeps up with 256 columns and no more, so that narrow tiles pay where they are all
 // in the first wave and leave half the epilogue (a box of 64 columns for each of its warps: four
-// k-blocks) after the last product.  Ranges cost the sums' way through L2 and a launch that adds
-// them.
+// k-blocks) after the last product.  Ranges cost a launch that adds their sums (15 k-blocks) and
+// the sums' way through L2 (0.07 us for 256 KB): 1376 x 4096 280 us with ranges in the first
+// product alone, 306 with them in both, 288 with none; 2048 x 2048 260, 296 with them.  (Sums that
+// met in distributed shared memory, clusters of up to eight pairs, cost the same 4 to 5 us a
+// product as the launch and allow fewer ranges: 182 x 5158 121 us against 108.)
 Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, int64_t depth) {
   const int64_t batch = h->cfg.batch;
   Tiling best{};
@@ -81,7 +84,7 @@ Tiling tiling(const mlpb_muon* h, bool symmetric, int64_t rows, int64_t cols, in
       double cost = static_cast<double>(cdiv(t.units, h->max_clusters)) *
                         cdiv(t.num_kb, t.split) +
                     4.0 * boxes;
-      if (t.split > 1) cost += 12.0 + 0.3 * t.split;
+      if (t.split > 1) cost += 15.0 + 0.27 / (narrow ? 2 : 1) * t.units;
       if (best.split == 0 || cost < least) {
         best = t;
         least = cost;
