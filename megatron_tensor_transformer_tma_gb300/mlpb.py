@@ -263,6 +263,14 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _new(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream that the call will run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _device(device):
     """The torch.device of a plan; "cuda" is the device that is current now, for good."""
     d = torch.device(device)
@@ -1129,6 +1137,7 @@ class Linear8:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"out_dtype: bfloat16 or float32, not {out_dtype}")
         self.handle = None
+        self._inputs, self._outputs = inputs, outputs
         self.cfg = mlpb_linear8_config(max_tokens, inputs, outputs, flags | (
             MLPB_LINEAR8_OUT_F32 if out_dtype == torch.float32 else 0))
         self.device, self.training, self.out_dtype = _device(device), training, out_dtype
@@ -1168,21 +1177,20 @@ class Linear8:
     def _saved_args(self, tokens, Xt):
         """Pointers of the X^T that a call writes or reads: a given one, or this object's."""
         if Xt is not None:
-            return _b128_args(Xt, self.cfg.inputs, tokens, "Xt", self.device.index)
+            return _b128_args(Xt, self._inputs, tokens, "Xt", self.device.index)
         p = self._saved.data_ptr()  # as saved(), without its views
-        return [p, p + self.cfg.inputs * ((tokens + 15) // 16 * 16)]
+        return [p, p + self._inputs * ((tokens + 15) // 16 * 16)]
 
     def forward(self, X, Y=None, Xt=None, stream=None):
         """Y [tokens][outputs].  With `training`, Xt (or this object) receives X^T for the
         backward."""
-        h, c, dev = self.handle, self.cfg, self.device.index
-        T = _linear8_rows(h, X, c.inputs, "X")[1]
+        h, K, N = self.handle, self._inputs, self._outputs
+        dev, T = _linear8_rows(h, X, K, "X")
         if Y is None:
-            with _on(stream, self.device):
-                Y = torch.empty((T, c.outputs), dtype=self.out_dtype, device=self.device)
-        args = [h.ptr, T, _arg(X, torch.bfloat16, (T, c.inputs), "X", dev),
+            Y = _new((T, N), self.out_dtype, self.device, stream)
+        args = [h.ptr, T, _arg(X, torch.bfloat16, (T, K), "X", dev),
                 self.Wq[0].data_ptr(), self.Wq[1].data_ptr(),
-                _arg(Y, self.out_dtype, (T, c.outputs), "Y", dev),
+                _arg(Y, self.out_dtype, (T, N), "Y", dev),
                 *(self._saved_args(T, Xt) if Xt is not None or self.training else (None, None)),
                 self.workspace.data_ptr()]
         _call_on(dev, "mlpb_linear8_forward", args, stream)
@@ -1198,19 +1206,18 @@ class Linear8:
             raise ValueError("Linear8: made with training=False")
         if accumulate and dW is None:
             raise ValueError("dW: nothing given to add into")
-        h, c, dev = self.handle, self.cfg, self.device.index
-        T = _linear8_rows(h, dY, c.outputs, "dY")[1]
+        h, K, N = self.handle, self._inputs, self._outputs
+        dev, T = _linear8_rows(h, dY, N, "dY")
         if Xt is None and T > 0 and T != self._tokens:
             raise ValueError(f"dY: {T} tokens, the last forward had {self._tokens}")
-        with _on(stream, self.device):
-            if dX is None and input_grad:
-                dX = torch.empty((T, c.inputs), dtype=self.out_dtype, device=self.device)
-            if dW is None:
-                dW = torch.empty((c.outputs, c.inputs), dtype=torch.float32, device=self.device)
-        args = [h.ptr, T, _arg(dY, torch.bfloat16, (T, c.outputs), "dY", dev),
+        if dX is None and input_grad:
+            dX = _new((T, K), self.out_dtype, self.device, stream)
+        if dW is None:
+            dW = _new((N, K), torch.float32, self.device, stream)
+        args = [h.ptr, T, _arg(dY, torch.bfloat16, (T, N), "dY", dev),
                 self.Wt[0].data_ptr(), self.Wt[1].data_ptr(), *self._saved_args(T, Xt),
-                _arg(dX, self.out_dtype, (T, c.inputs), "dX", dev),
-                _arg(dW, torch.float32, (c.outputs, c.inputs), "dW", dev),
+                _arg(dX, self.out_dtype, (T, K), "dX", dev),
+                _arg(dW, torch.float32, (N, K), "dW", dev),
                 1 if accumulate else 0, self.workspace.data_ptr()]
         _call_on(dev, "mlpb_linear8_backward", args, stream)
         return dX, dW
@@ -1245,8 +1252,7 @@ class Muon:
     def orthogonalize(self, U, O=None, stream=None):
         """O, bf16 in the shape of U (bf16 or fp32)."""
         if O is None:
-            with _on(stream, self.device):
-                O = torch.empty(U.shape, dtype=torch.bfloat16, device=self.device)
+            O = _new(U.shape, torch.bfloat16, self.device, stream)
         mlpb_muon_orthogonalize(self.handle, U, O, self.workspace, stream)
         return O
 
