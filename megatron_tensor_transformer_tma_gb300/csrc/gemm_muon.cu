@@ -16,6 +16,12 @@
 // 16 bytes a lane, took 540 us for 16 matrices of 1376 x 4096, four times the product: every
 // access touches 32 lines.)  The ring has 5 stages for that, 4 where W's fp32 boxes come too.
 //
+// Measured for 16 matrices of 1376 x 4096: Gram 110 us, Poly 51, Apply 205, the last with W 245.
+// Gram runs at the rate of large products (84 % tensor-active at 4 x 2560 x 5120) but for its last
+// wave; Apply loses 30 of its 205 us to the loads and stores of X's parts: without them it takes
+// 165-170, without its arithmetic as long.  Boxes half as wide in two slots a warp took 205, in
+// three slots with a stage less 215, the next tile's X prefetched into L2 231.
+//
 // Few tiles leave pairs idle and the epilogue in the open.  Then tiles are 256 x 128 (the rule is
 // at tiling() in muon.cu), and the symmetric products' K is cut into ranges (`split`), whose fp32
 // sums go to the workspace for ortho_fold_kernel, which adds them in their order on all SMs and
