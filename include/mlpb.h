@@ -576,8 +576,9 @@ mlpb_status mlpb_muon_create(const mlpb_muon_config *cfg, mlpb_muon **out);
 void mlpb_muon_destroy(mlpb_muon *h);
 
 /* Bytes of the workspace of the calls below: three fp16 copies of X, two symmetric fp16 matrices of
- * the smaller side, and where few tiles are cut into ranges their fp32 sums; 256 bytes where a
- * matrix lies in shared memory (a smaller side of at most 128, a longer one of some thousands). */
+ * the smaller side, and where few tiles are cut into ranges their fp32 sums; 256 bytes where
+ * matrices lie in shared memory (a few with a smaller side of at most 128 and a longer one of some
+ * thousands). */
 mlpb_status mlpb_muon_workspace_size(const mlpb_muon *h, size_t *bytes);
 
 /* O [batch][rows][cols] bf16 from U, bf16 or (u_f32 = 1) fp32 (O may not overlap U).  16-byte

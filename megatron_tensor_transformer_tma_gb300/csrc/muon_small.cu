@@ -650,11 +650,27 @@ static void small_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int
   cfg.numAttrs = 1;
 }
 
-// CTAs of a cluster for one matrix, or 0 where no cluster holds it: the most (at least 64 columns
-// for each) with which all matrices are resident at once, or the fewest that hold a matrix.  (A
-// cluster has to find its SMs in one part of the GPU: of 16 CTAs only a few are resident together.)
-cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, int* cluster) {
+// Whether this kernel ends before the products of gemm_muon.cu would: us for five steps, fitted to
+// both.  A round of resident clusters takes 18.5 + 0.175 np and 0.9 ns an element of a slab (1.5 if
+// it has to be transposed), the other way 80 to 95 and 1.8 (1.3) ns for each of the longer side's
+// elements: 64 x 4096 42 against 81, 64 of them 264 against 497, but 64 of 4096 x 128 974 against
+// 453.
+static bool small_ends_first(const SmallShape& s, int64_t length, int64_t batch, int64_t resident,
+                             bool tall) {
+  const double rounds = static_cast<double>((batch + resident - 1) / resident);
+  const double here = rounds * (18.5 + 0.175 * s.np + (tall ? 0.0015 : 0.0009) * s.np * s.slab);
+  const double there =
+      (s.np <= 64 ? 80.0 : 95.0) + (tall ? 0.0013 : 0.0018) * static_cast<double>(batch * length);
+  return here <= there;
+}
+
+// CTAs of a cluster for one matrix: the most (at least 64 columns for each) with which all matrices
+// are resident at once, or the fewest that hold a matrix; 0 where no cluster holds it or many small
+// products end sooner.  (A cluster has to find its SMs in one part of the GPU: of 16 CTAs only a few
+// are resident together.)
+cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, int* cluster) {
   *cluster = 0;
+  int64_t at_once = 0;
   if (n > kSmallMaxN) return cudaSuccess;
   cudaError_t e = small_attrs<float>();
   if (e == cudaSuccess) e = small_attrs<__nv_bfloat16>();
@@ -669,8 +685,14 @@ cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, int* cluste
     e = cudaOccupancyMaxActiveClusters(&resident, muon_small_kernel<float>, &cfg);
     if (e != cudaSuccess) return e;
     if (resident < 1) continue;
-    if (*cluster == 0 || (batch <= resident && length > 64 * (c / 2))) *cluster = c;
+    if (*cluster == 0 || (batch <= resident && length > 64 * (c / 2))) {
+      *cluster = c;
+      at_once = resident;
+    }
   }
+  if (*cluster > 0 &&
+      !small_ends_first(small_shape(n, length, *cluster), length, batch, at_once, tall))
+    *cluster = 0;
   return cudaSuccess;
 }
 

@@ -36,7 +36,8 @@ def test_linear_of_the_most_tokens():
     assert mlpb.mlpb_linear8_last_device_error(plan.handle) == mlpb.MLPB_OK
 
 
-@pytest.mark.parametrize("n,r,c", [(26000, 200, 520), (26000, 520, 200), (5200, 128, 4096)])
+@pytest.mark.parametrize("n,r,c", [(26000, 200, 520), (26000, 520, 200), (5200, 128, 4096),
+                                   (65000, 32, 1304)])
 def test_update_of_the_largest_batch(n, r, c):
     m = 4  # matrices that repeat; 2.7e9 elements
     u = _randn(1, m, r, c)
