@@ -530,7 +530,8 @@ mlpb_status mlpb_linear8_forward(mlpb_linear8 *h, int64_t tokens, const void *X,
 /* Backward for dY [tokens][outputs] bf16, with as many tokens as the forward that wrote Xt and
  * Xts; Wt, Wts the codes and scales of W^T [inputs][outputs] of the same quantization.  dX
  * [tokens][inputs] or dW [outputs][inputs] fp32 may be NULL, not both (nor are their operands
- * read then).  accumulate: dW is added into.  tokens = 0 writes a zero dW, or leaves it as it is
+ * read then).  accumulate: dW is added into (by additions that take subnormal values as zeros).
+ * tokens = 0 writes a zero dW, or leaves it as it is
  * when accumulating. */
 mlpb_status mlpb_linear8_backward(mlpb_linear8 *h, int64_t tokens, const void *dY, const void *Wt,
                                   const void *Wts, const void *Xt, const void *Xts, void *dX,

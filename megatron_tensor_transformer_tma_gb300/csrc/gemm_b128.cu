@@ -15,9 +15,9 @@
 //
 // An accumulation in the tensor cores cuts off instead of rounding: sums come out too small, by
 // 6e-7 of their size after 64 k-blocks and in proportion.  So an fp32 result's sum is taken in
-// chunks of 64 k-blocks, which are added in the epilogue's registers: dW of 16384 tokens is off by
-// as much as that of 8192.  (Added in memory by TMA instead, dW of 16384 x 4096 x 11008 took 592 us,
-// so 547.)
+// chunks of 64 k-blocks: dW of 16384 tokens is off by as much as that of 8192.  Chunks are added in
+// the epilogue's registers (dW of 16384 x 4096 x 11008 547 us, 592 in memory) or, where C is added
+// to anyway, in memory, in their order, by TMA, whose additions take subnormal values as zeros.
 //
 // Measured at 8192 x 5120 x 20480: Y 498-525 us (3270-3450 TFLOP/s), 85 % of the cycles with the
 // tensor cores active; dX 537, dW (fp32, 64 k-blocks) 545.  What is left is the one accumulator's
@@ -42,8 +42,9 @@ constexpr int kMxScaleCols = 16;               // 4 of A, 8 of B, twice
 // How a tile's results leave.
 enum class MxOut {
   Direct,   // from the threads of their rows; behind the next tile's products where K is long
-  Staged,   // through shared memory by TMA: two slots of 4 KB a warp, and two stages fewer
-  Chunked,  // as Direct, of sums longer than a chunk
+  Staged,   // through shared memory by TMA: two slots of 4 KB a warp, and two stages fewer; the
+            // chunks of a long sum one by one, added in memory
+  Chunked,  // as Direct, of sums longer than a chunk, which are added in registers
 };
 
 template <MxOut O>
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_b128_kernel(const __grid_constant__ B128Maps maps, const B128Params p) {
   using Sm = MxSmem<O>;
   constexpr int S = Sm::stages;
+  constexpr bool kTurns = O != MxOut::Direct;  // sums in chunks
   constexpr bool kChunked = O == MxOut::Chunked;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const WaitCtx wc{abort_flag, p.err, p.wait_ns};
   const int num_units = p.num_pm * p.num_n;
   // a pair's turns: its tiles, each in chunks of K
-  const int chunks = kChunked ? (p.num_kb + p.chunk - 1) / p.chunk : 1;
+  const int chunks = kTurns && p.num_kb > p.chunk ? (p.num_kb + p.chunk - 1) / p.chunk : 1;
   const int turns = (num_units - cid + nclusters - 1) / nclusters * chunks;
 
   if (warp == 0) {
@@ -225,8 +227,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int stage = 0;
       uint32_t phase = 0, sbuf = 0;
       for (int it = 0; it < turns; ++it) {
-        const int kb0 = kChunked ? it % chunks * p.chunk : 0;
-        const int kb1 = kChunked ? min(p.num_kb, kb0 + p.chunk) : p.num_kb;
+        const int kb0 = kTurns ? it % chunks * p.chunk : 0;
+        const int kb1 = kTurns && chunks > 1 ? min(p.num_kb, kb0 + p.chunk) : p.num_kb;
         if (!wait_bounded(tempty, (it & 1) ^ 1u, wc, kSiteMmaAccEmpty)) break;
         tc_fence_after();
         bool ok = true;
@@ -273,8 +275,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128u * half;
     uint32_t v[4][32];  // the tile's sums
     for (int it = 0; it < turns; ++it) {
-      const int chunk = kChunked ? it % chunks : 0;
-      const int u = cid + (kChunked ? it / chunks : it) * nclusters;
+      const int chunk = kTurns ? it % chunks : 0;
+      const int u = cid + (kTurns ? it / chunks : it) * nclusters;
       int ok = 1;
       if (lane == 0) ok = wait_bounded(tfull, it & 1, wc, kSiteEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -313,6 +315,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (m0 >= p.M) continue;  // the warp's rows, all of them
         const int width = p.out_f32 ? 32 : 64;  // columns of a box
         const int boxes = min(128 / width, (p.N - n0 + width - 1) / width);
+        if (chunk > 0 && lane == 0) bulk_wait<0>();  // the chunk before is in C
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (q >= boxes) break;
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (p.accumulate) tma_add_2d(&maps.c, box, n0 + q * width, m0);
+            if (p.accumulate || chunk > 0) tma_add_2d(&maps.c, box, n0 + q * width, m0);
             else tma_store_2d(&maps.c, box, n0 + q * width, m0);
             bulk_commit();
           }
@@ -357,7 +360,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[c][e]);
         if (p.out_f32) {
           float* C = static_cast<float*>(p.C) + o + 32 * c;
-          if (p.accumulate) add_f32x32(C, nv, f);
           store_f32x32(C, nv, f);
         } else {
           store_bf16x32(static_cast<__nv_bfloat16*>(p.C) + o + 32 * c, nv, f);
@@ -422,14 +424,16 @@ cudaError_t b128_gemm_set_attrs(int* max_clusters) {
   return cudaOccupancyMaxActiveClusters(max_clusters, gemm_b128_kernel<MxOut::Chunked>, &cfg);
 }
 
-// Staged where the products of a tile (0.13 us a k-block) no longer hide its stores by threads.
-bool b128_staged(int num_kb) { return num_kb < kMxStagedBelow; }
+// Staged where the products of a tile (0.13 us a k-block) no longer hide its stores by threads, and
+// where C is added to, which the TMA does in memory: loads by threads, of 32 lines
+// each, doubled the time (dW 5120 x 5120 of 4096 tokens 237 us, now 114).
+bool b128_staged(int num_kb, bool accumulate) { return num_kb < kMxStagedBelow || accumulate; }
 
 cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters,
                              cudaStream_t s) {
-  if (p.num_kb > p.chunk) return launch_out<MxOut::Chunked>(m, p, clusters, s);
-  return b128_staged(p.num_kb) ? launch_out<MxOut::Staged>(m, p, clusters, s)
-                               : launch_out<MxOut::Direct>(m, p, clusters, s);
+  if (b128_staged(p.num_kb, p.accumulate != 0)) return launch_out<MxOut::Staged>(m, p, clusters, s);
+  return p.num_kb > p.chunk ? launch_out<MxOut::Chunked>(m, p, clusters, s)
+                            : launch_out<MxOut::Direct>(m, p, clusters, s);
 }
 
 }  // namespace mlpb

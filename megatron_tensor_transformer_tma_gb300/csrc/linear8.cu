@@ -79,26 +79,32 @@ bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
                 kB128Chunk / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Whether a product goes to the kernel for few tiles: at most 128 rows of C, or no more tiles of
-// 256 x 256 than half the pairs of SMs, than all of them where K is at most 40 k-blocks (768 x
-// 5120 x 5120 21.8 against 24.2 us, but 1000 x 11008 x 4096 45.5 against 40.4); not where an fp32
-// sum is long enough for chunks, which that kernel does not have.
-bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n, int64_t k, bool f32) {
-  if (b128_blocks(k) > b128_chunk(f32)) return false;
+// Whether a product goes to the kernel for few tiles: at most 128 rows of C; up to as many tiles of
+// 256 x 256 as pairs of SMs where K is at most 4 k-blocks, all of them epilogue (2048 x 2048 at 4
+// 10.1 against 12.0 us, but 5120 x 5120 42.9 against 30.4), or 24 to 40, long enough to be cut into
+// ranges (512 x 5120 x 5120 21.6 against 23.0, but 1000 x 5120 x 5120 38.8 against 36.3); up to a
+// quarter of that at other lengths (256 x 2048 x 2048 10.6 against 11.0, but 1000 13.4 against
+// 12.0; 256 x 11008 x 4096 23.6 against 33.2, but 512 37.0 against 35.2).  Not where C is added to,
+// which the other kernel does in memory (2048 x 2048 at 8 19.2 against 14.9), nor where an fp32 sum
+// is long enough for chunks, which this one does not have.
+bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n, int64_t k, bool f32, bool accumulate) {
+  const int64_t blocks = b128_blocks(k);
+  if (accumulate || blocks > b128_chunk(f32)) return false;
   const int64_t tiles = cdiv(m, 256) * cdiv(n, 256);
-  return m <= 128 || tiles * (b128_blocks(k) <= 40 ? 1 : 2) <= h->max_clusters;
+  const bool most = blocks <= 4 || (blocks >= 24 && blocks <= 40);
+  return m <= 128 || tiles * (most ? 1 : 4) <= h->max_clusters;
 }
 
 // C [a.rows][b.rows] (+)= A B^T over the columns that both have.
 mlpb_status product(mlpb_linear8* h, const Quantized& a, const Quantized& b, void* C, bool f32,
                     bool accumulate, cudaStream_t s) {
   B128Maps m{};
-  const bool few = few_tiles(h, a.rows, b.rows, a.cols, f32);
+  const bool few = few_tiles(h, a.rows, b.rows, a.cols, f32, accumulate);
   if (!map_codes(h, &m.a, a, few ? b128_few_columns(a.rows) : kB128) ||
       !map_codes(h, &m.b, b, kB128) || !map_scales(h, &m.sa, a) ||
       !map_scales(h, &m.sb, b))
     return MLPB_ECUDA;
-  if (!few && b128_staged(static_cast<int>(b128_blocks(a.cols))) &&
+  if (!few && b128_staged(static_cast<int>(b128_blocks(a.cols)), accumulate) &&
       !encode(h, &m.c,
               f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C,
               static_cast<uint64_t>(b.rows), static_cast<uint64_t>(a.rows),

@@ -665,9 +665,9 @@ static bool small_ends_first(const SmallShape& s, int64_t length, int64_t batch,
 }
 
 // CTAs of a cluster for one matrix: the most (at least 64 columns for each) with which all matrices
-// are resident at once, or the fewest that hold a matrix; 0 where no cluster holds it or many small
-// products end sooner.  (A cluster has to find its SMs in one part of the GPU: of 16 CTAs only a few
-// are resident together.)
+// are resident at once, or the fewest that hold a matrix; 0 where no cluster holds it or the tiled
+// products end sooner.  (A cluster has to find its SMs in one part of the GPU: of 16 CTAs only a
+// few are resident together.)
 cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, int* cluster) {
   *cluster = 0;
   int64_t at_once = 0;

@@ -168,6 +168,26 @@ def test_large_scales_do_not_meet_in_between():
     _check(plan.forward(X.to(BF)), *o["Y"], K, False)
 
 
+@pytest.mark.parametrize("T", [8, 500, 2056, 4104, 8200, 16500])
+def test_gradients_are_added_into_what_is_there(T):
+    # tiles for all SMs: both ways take the same products in the same order
+    n = 2056
+    X, dY, W = _randn(1, T, n), _randn(2, T, n), _randn(3, n, n)
+    plan = mlpb.Linear8(T, n, n)
+    plan.load(W)
+    plan.forward(X)
+    dW = plan.backward(dY, input_grad=False)[1].double()
+    base = _randn(4, n, n, std=T ** 0.5).float()
+    acc = base.clone()
+    plan.backward(dY, dW=acc, accumulate=True, input_grad=False)
+    # one rounding for each chunk of 8192 tokens and side, of no more than twice the sum of sizes
+    # (|dW| is some T^0.5, and so is a chunk's)
+    chunks = -(-T // 8192)
+    size = base.double().abs() + dW.abs() + (0.0 if chunks == 1 else 6 * T ** 0.5)
+    assert bool(((acc.double() - (base.double() + dW)).abs() <= (2 * chunks - 1) * 2.0 ** -24
+                 * size * 1.0001).all())
+
+
 def test_zero_tokens_and_refusals():
     K, N = 64, 48
     plan = mlpb.Linear8(4, K, N)
