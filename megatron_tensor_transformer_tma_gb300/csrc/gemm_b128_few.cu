@@ -12,8 +12,8 @@
 // scales, which that does not write, are on their way by then.  A CTA (192 threads) has a TMA
 // producer, an MMA issuer and four epilogue warps; scales as in gemm_b128.cu.
 //
-// Bound by the weight's bytes: one token by 5120 x 20480 takes 18.4 us with its quantization in a
-// stream of such calls (105 MB: 5.7 TB/s), 16 tokens by 11008 x 4096 11.9.  Depth of the rings
+// Bound by the weight's bytes: one token by 5120 x 20480 takes 17.2 us with its quantization in a
+// graph of such calls (105 MB: 6.1 TB/s), 16 tokens by 11008 x 4096 11.9.  Depth of the rings
 // counts: three and four CTAs an SM, with three and two stages, took 22.8 and 28.8 us where two
 // with five took 21.8.
 #include <algorithm>
