@@ -348,24 +348,44 @@ __device__ __forceinline__ void apply_box(const float (&v)[32], int j0, uint32_t
 __device__ __forceinline__ void ragged_rows(uint32_t slot, int lane, int row0, int col,
                                             const OrthoTile& t, float keep, float step,
                                             const OrthoParams& p) {
-  for (int r = 0; r < kEpiRows && row0 + r < p.rows; ++r) {
-    const size_t o = (static_cast<size_t>(t.b) * p.rows + row0 + r) * p.cols + col;
+  // eight rows at a time: all of W's values on their way before the first is used
+  constexpr int kRows = 8;
+#pragma unroll 1
+  for (int r0 = 0; r0 < kEpiRows && row0 + r0 < p.rows; r0 += kRows) {
+    float v[kRows][2], w[kRows][2];
+    const size_t o = (static_cast<size_t>(t.b) * p.rows + row0 + r0) * p.cols + col + lane;
+    auto here = [&](int r, int h) {
+      return row0 + r0 + r < p.rows && col + lane + 32 * h < p.cols;
+    };
+    if (p.w != nullptr) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = lane + 32 * h;
-      if (col + c >= p.cols) continue;
-      float v;
-      asm volatile("ld.shared.f32 %0, [%1];"
-                   : "=f"(v)
-                   : "r"(box_piece(slot + kEpiBox * (1 + h), r, lane >> 2) + (lane & 3) * 4));
-      if (p.w == nullptr) {
-        p.out[o + c] = __float2bfloat16_rn(v);
-      } else {
-        const float w = fmaf(-step * 4096.0f, v, keep * p.w[o + c]);
-        p.w[o + c] = w;
-        if (p.wb != nullptr) p.wb[o + c] = __float2bfloat16_rn(w);
-      }
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[r][h] = here(r, h) ? p.w[o + static_cast<size_t>(r) * p.cols + 32 * h] : 0.0f;
     }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(v[r][h])
+                     : "r"(box_piece(slot + kEpiBox * (1 + h), r0 + r, lane >> 2) +
+                           (lane & 3) * 4));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!here(r, h)) continue;
+        const size_t at = o + static_cast<size_t>(r) * p.cols + 32 * h;
+        if (p.w == nullptr) {
+          p.out[at] = __float2bfloat16_rn(v[r][h]);
+        } else {
+          const float x = fmaf(-step * 4096.0f, v[r][h], keep * w[r][h]);
+          p.w[at] = x;
+          if (p.wb != nullptr) p.wb[at] = __float2bfloat16_rn(x);
+        }
+      }
   }
 }
 

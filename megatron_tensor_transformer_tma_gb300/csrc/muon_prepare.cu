@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   const int64_t elems = in.rows * in.cols;
   const int groups = ldx / 8;
   const int64_t pieces = in.rows * groups;
-  const bool vec = in.cols % 4 == 0;
+  const bool vec = in.cols % 4 == 0, pairs = in.cols % 2 == 0;
   const T* g = static_cast<const T*>(in.g) + b * elems;
   float* m = in.m == nullptr ? nullptr : in.m + b * elems;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kPrepThreads;
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kPrepThreads)
       float u[4] = {0.f, 0.f, 0.f, 0.f};
       const int64_t o = row * in.cols + c;
       if (n > 0)
-        update4<false>(g + o, m == nullptr ? nullptr : m + o, n, vec, in.momentum, in.nesterov, u);
+        update4<false>(g + o, m == nullptr ? nullptr : m + o, n, vec, in.momentum, in.nesterov, u,
+                       pairs);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = e < n ? (u[e] * s1) * s2 : 0.0f;

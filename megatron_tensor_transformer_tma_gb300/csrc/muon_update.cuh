@@ -10,26 +10,49 @@
 
 namespace mlpb {
 
+// Four consecutive elements, n of them valid: in pairs where these lie on 8 bytes (bf16: 4).
+template <typename T>
+__device__ __forceinline__ void load_some(const T* x, int n, bool pairs, float (&u)[4]) {
+  if (pairs) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      u[e] = u[e + 1] = 0.0f;
+      if (e < n) {  // n is even
+        if constexpr (sizeof(T) == 2) {
+          const float2 f = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(x + e));
+          u[e] = f.x;
+          u[e + 1] = f.y;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(x + e);
+          u[e] = f.x;
+          u[e + 1] = f.y;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = e < n ? static_cast<float>(x[e]) : 0.0f;
+  }
+}
+
 // U of four consecutive elements (n of them valid), M written back by the first pass.
 template <bool kFirst, typename T>
 __device__ __forceinline__ void update4(const T* g, float* m, int n, bool vec, float mu,
-                                        int nesterov, float (&u)[4]) {
+                                        int nesterov, float (&u)[4], bool pairs = false) {
   if constexpr (sizeof(T) == 2) {
     if (vec) {
       const uint2 w = __ldg(reinterpret_cast<const uint2*>(g));
       const float2 x = unpack_bf16x2(w.x), y = unpack_bf16x2(w.y);
       u[0] = x.x; u[1] = x.y; u[2] = y.x; u[3] = y.y;
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = e < n ? __bfloat162float(g[e]) : 0.0f;
+      load_some(g, n, pairs, u);
     }
   } else {
     if (vec) {
       const float4 x = __ldg(reinterpret_cast<const float4*>(g));
       u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = e < n ? g[e] : 0.0f;
+      load_some(g, n, pairs, u);
     }
     if (m != nullptr) {
       float v[4];
@@ -37,8 +60,7 @@ __device__ __forceinline__ void update4(const T* g, float* m, int n, bool vec, f
         const float4 x = *reinterpret_cast<const float4*>(m);
         v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = e < n ? m[e] : 0.0f;
+        load_some(m, n, pairs, v);
       }
       if constexpr (kFirst) {
 #pragma unroll
