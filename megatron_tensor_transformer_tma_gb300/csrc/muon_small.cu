@@ -264,13 +264,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
   float4 sq = make_float4(0.f, 0.f, 0.f, 0.f);
   float u[kSmallBatch][4];  // of a thread that has one batch: the second pass uses them again
   const bool kept = runs.runs * runs.quads <= kSmallBatch * kSmallThreads;
+  float v[kSmallBatch][4];  // M: all loads of a batch come before its first store
   for_groups(
       runs, p.tall, p.n,
       [&](int k, int64_t at, int n) {
-        update4<true>(g + at, m == nullptr ? nullptr : m + at, n, runs.vec, p.in.momentum,
-                      p.in.nesterov, u[k]);
+        load4(g + at, m == nullptr ? nullptr : m + at, n, runs.vec, false, u[k], v[k]);
       },
-      [&](int k, int64_t, int, int, int) { add_squares4(u[k], sq); });
+      [&](int k, int64_t at, int n, int, int) {
+        finish4<true, T>(m == nullptr ? nullptr : m + at, n, runs.vec, p.in.momentum,
+                         p.in.nesterov, u[k], v[k]);
+        add_squares4(u[k], sq);
+      });
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
     sq.x += __shfl_xor_sync(0xffffffffu, sq.x, o);
@@ -557,8 +561,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
     const int64_t base = matrix * elems;
     for_groups(
         runs, p.tall, p.n,
-        [&](int k, int64_t at, int) {
-          if (p.w != nullptr && runs.vec) w4[k] = *reinterpret_cast<const float4*>(p.w + base + at);
+        [&](int k, int64_t at, int n) {
+          if (p.w == nullptr) return;
+          const float* from = p.w + base + at;
+          if (runs.vec)
+            w4[k] = *reinterpret_cast<const float4*>(from);
+          else
+            w4[k] = make_float4(from[0], n > 1 ? from[1] : 0.0f, n > 2 ? from[2] : 0.0f,
+                                n > 3 ? from[3] : 0.0f);
         },
         [&](int k, int64_t at, int n, int row, int col) {
           float v[4];
@@ -584,11 +594,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
             }
           }
           const int64_t o = base + at;
+          if (p.w != nullptr) {
+            const float w[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = fmaf(-rate, v[c], keep * w[c]);
+          }
           if (runs.vec) {
             if (p.w != nullptr) {
-              const float w[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
-#pragma unroll
-              for (int c = 0; c < 4; ++c) v[c] = fmaf(-rate, v[c], keep * w[c]);
               *reinterpret_cast<float4*>(p.w + o) = make_float4(v[0], v[1], v[2], v[3]);
             }
             __nv_bfloat16* half = p.w != nullptr ? p.wb : p.out;
@@ -602,9 +614,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
               if (p.w == nullptr) {
                 p.out[o + c] = __float2bfloat16_rn(v[c]);
               } else {
-                const float w = fmaf(-rate, v[c], keep * p.w[o + c]);
-                p.w[o + c] = w;
-                if (p.wb != nullptr) p.wb[o + c] = __float2bfloat16_rn(w);
+                p.w[o + c] = v[c];
+                if (p.wb != nullptr) p.wb[o + c] = __float2bfloat16_rn(v[c]);
               }
             }
           }

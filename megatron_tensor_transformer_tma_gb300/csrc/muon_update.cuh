@@ -35,48 +35,60 @@ __device__ __forceinline__ void load_some(const T* x, int n, bool pairs, float (
   }
 }
 
-// U of four consecutive elements (n of them valid), M written back by the first pass.
+// G and, unless m is NULL, M of four consecutive elements (n of them valid; `vec`: on 16 bytes).
+template <typename T>
+__device__ __forceinline__ void load4(const T* g, const float* m, int n, bool vec, bool pairs,
+                                      float (&u)[4], float (&v)[4]) {
+  if (!vec) {
+    load_some(g, n, pairs, u);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(g));
+    const float2 x = unpack_bf16x2(w.x), y = unpack_bf16x2(w.y);
+    u[0] = x.x; u[1] = x.y; u[2] = y.x; u[3] = y.y;
+  } else {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(g));
+    u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+  }
+  if constexpr (sizeof(T) == 4) {
+    if (m == nullptr) return;
+    if (!vec) {
+      load_some(m, n, pairs, v);
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(m);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    }
+  }
+}
+
+// Their U in u, M written back by the first pass.
+template <bool kFirst, typename T>
+__device__ __forceinline__ void finish4(float* m, int n, bool vec, float mu, int nesterov,
+                                        float (&u)[4], float (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    if (m == nullptr) return;
+    if constexpr (kFirst) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(mu, v[e], u[e]);
+      if (vec) {
+        *reinterpret_cast<float4*>(m) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < n) m[e] = v[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = nesterov ? fmaf(mu, v[e], u[e]) : v[e];
+  }
+}
+
+// U of four consecutive elements at once.
 template <bool kFirst, typename T>
 __device__ __forceinline__ void update4(const T* g, float* m, int n, bool vec, float mu,
                                         int nesterov, float (&u)[4], bool pairs = false) {
-  if constexpr (sizeof(T) == 2) {
-    if (vec) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(g));
-      const float2 x = unpack_bf16x2(w.x), y = unpack_bf16x2(w.y);
-      u[0] = x.x; u[1] = x.y; u[2] = y.x; u[3] = y.y;
-    } else {
-      load_some(g, n, pairs, u);
-    }
-  } else {
-    if (vec) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(g));
-      u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
-    } else {
-      load_some(g, n, pairs, u);
-    }
-    if (m != nullptr) {
-      float v[4];
-      if (vec) {
-        const float4 x = *reinterpret_cast<const float4*>(m);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        load_some(m, n, pairs, v);
-      }
-      if constexpr (kFirst) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(mu, v[e], u[e]);
-        if (vec) {
-          *reinterpret_cast<float4*>(m) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < n) m[e] = v[e];
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = nesterov ? fmaf(mu, v[e], u[e]) : v[e];
-    }
-  }
+  float v[4];
+  load4(g, m, n, vec, pairs, u, v);
+  finish4<kFirst, T>(m, n, vec, mu, nesterov, u, v);
 }
 
 // Sums of squares in three ranges (after Blue, 1978), so that neither large nor small values
