@@ -1128,8 +1128,8 @@ class MoEDecode:
 
 class Linear8:
     """A linear layer y = x W^T on E4M3 operands with a scale for each block of 128, for up to
-    max_tokens rows.  load() lays the weight out (again after each update); forward() and
-    backward() as in include/mlpb.h.  Owns the weight's codes (with `training`, its transpose's
+    max_tokens rows.  load() lays the weight out (before anything else, and again after each
+    update); forward() and backward() as in include/mlpb.h.  Owns the weight's codes (with `training`, its transpose's
     too), what a forward keeps of X for the backward, and the workspace."""
 
     def __init__(self, max_tokens, inputs, outputs, training=True, out_dtype=torch.bfloat16,
@@ -1147,6 +1147,7 @@ class Linear8:
                                      device=self.device)
         self.Wq = b128_empty(outputs, inputs, self.device)
         self.Wt = b128_empty(inputs, outputs, self.device) if training else None
+        self._loaded = False  # Wq and Wt hold a weight
         self._saved, self._tokens = None, None  # X^T of the last forward, its tokens
         if training:  # one buffer for any number of tokens
             ld, n = mlpb_b128_sizes(inputs, max_tokens)
@@ -1167,6 +1168,11 @@ class Linear8:
             raise ValueError(f"W: expected shape {(self.cfg.outputs, self.cfg.inputs)}, "
                              f"got {tuple(W.shape)}")
         mlpb_b128_quantize(W, self.Wq, self.Wt, True, stream)
+        self._loaded = True
+
+    def _check_loaded(self):
+        if not self._loaded:
+            raise ValueError("Linear8: no weight yet, load() comes first")
 
     def saved(self, tokens):
         """The (codes, scales) of X^T that forward() writes for this many tokens."""
@@ -1186,6 +1192,7 @@ class Linear8:
         backward."""
         h, K, N = self.handle, self._inputs, self._outputs
         dev, T = _linear8_rows(h, X, K, "X")
+        self._check_loaded()
         if Y is None:
             Y = _new((T, N), self.out_dtype, self.device, stream)
         args = [h.ptr, T, _arg(X, torch.bfloat16, (T, K), "X", dev),
@@ -1208,6 +1215,7 @@ class Linear8:
             raise ValueError("dW: nothing given to add into")
         h, K, N = self.handle, self._inputs, self._outputs
         dev, T = _linear8_rows(h, dY, N, "dY")
+        self._check_loaded()
         if Xt is None and T > 0 and T != self._tokens:
             raise ValueError(f"dY: {T} tokens, the last forward had {self._tokens}")
         if dX is None and input_grad:

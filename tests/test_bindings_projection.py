@@ -125,3 +125,26 @@ def test_tensors_of_another_device_are_refused(fake, name):
         with pytest.raises(ValueError, match="the handle on cuda:1"):
             plan.orthogonalize(_Tensor((2, 24, 40), torch.float32, dev, None))
     plan.handle.ptr = 0
+
+
+def test_a_layer_without_a_weight_is_refused(fake):
+    dev = torch.device("cuda", 1)
+    X, dY = (_Tensor((8, n), torch.bfloat16, dev, None) for n in (64, 32))
+    plan = mlpb.Linear8(8, 64, 32)
+    serving = mlpb.Linear8(8, 64, 32, training=False)
+    fake["calls"].clear()
+    for call in (lambda: plan.forward(X), lambda: serving.forward(X), lambda: plan.backward(dY),
+                 lambda: plan.backward(dY, Xt=plan.saved(8))):
+        with pytest.raises(ValueError, match="no weight yet"):
+            call()
+    with pytest.raises(ValueError, match="shape"):  # a refused weight is none
+        plan.load(_Tensor((64, 32), torch.bfloat16, dev, None))
+    with pytest.raises(ValueError, match="no weight yet"):
+        plan.forward(X)
+    assert not fake["calls"]
+    plan.load(_Tensor((32, 64), torch.bfloat16, dev, None))
+    plan.forward(X)
+    plan.backward(dY)
+    assert [c[0] for c in fake["calls"]] == ["mlpb_b128_quantize", "mlpb_linear8_forward",
+                                             "mlpb_linear8_backward"]
+    plan.handle.ptr = serving.handle.ptr = 0
