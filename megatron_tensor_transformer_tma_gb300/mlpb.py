@@ -1148,7 +1148,8 @@ class Linear8:
         self.Wq = b128_empty(outputs, inputs, self.device)
         self.Wt = b128_empty(inputs, outputs, self.device) if training else None
         self._loaded = False  # Wq and Wt hold a weight
-        self._saved, self._tokens = None, None  # X^T of the last forward, its tokens
+        self._saved = None  # X^T of the last forward that was given no Xt
+        self._tokens = None  # of the last forward; None after one whose X^T lies in a given Xt
         if training:  # one buffer for any number of tokens
             ld, n = mlpb_b128_sizes(inputs, max_tokens)
             self._saved = torch.empty(inputs * ld + n, dtype=torch.uint8, device=self.device)
@@ -1175,7 +1176,7 @@ class Linear8:
             raise ValueError("Linear8: no weight yet, load() comes first")
 
     def saved(self, tokens):
-        """The (codes, scales) of X^T that forward() writes for this many tokens."""
+        """The (codes, scales) of X^T that forward() without an Xt writes for this many tokens."""
         ld, n = mlpb_b128_sizes(self.cfg.inputs, tokens)
         m = self.cfg.inputs * ld
         return self._saved[:m].view(self.cfg.inputs, ld), self._saved[m:m + n]
@@ -1201,14 +1202,15 @@ class Linear8:
                 *(self._saved_args(T, Xt) if Xt is not None or self.training else (None, None)),
                 self.workspace.data_ptr()]
         _call_on(dev, "mlpb_linear8_forward", args, stream)
-        if Xt is None:
-            self._tokens = T
+        self._tokens = T if Xt is None else None
         return Y
 
     def backward(self, dY, dX=None, dW=None, Xt=None, accumulate=False, input_grad=True,
                  stream=None):
-        """(dX, dW) for the rows of the last forward, or for an Xt that a forward wrote; with
-        `accumulate` dW is added into; without `input_grad` dX is not computed."""
+        """(dX, dW) for the rows of the last forward, or for an Xt that a forward wrote (after a
+        forward with an Xt it has to be named; saved() is what the one before left here); with
+        `accumulate` dW is added into; without `input_grad` dX is not computed.  A captured
+        forward counts as it is captured, not as it is replayed."""
         if not self.training:
             raise ValueError("Linear8: made with training=False")
         if accumulate and dW is None:
@@ -1217,6 +1219,8 @@ class Linear8:
         dev, T = _linear8_rows(h, dY, N, "dY")
         self._check_loaded()
         if Xt is None and T > 0 and T != self._tokens:
+            if self._tokens is None:
+                raise ValueError("Xt: not given, and the last forward kept no rows here")
             raise ValueError(f"dY: {T} tokens, the last forward had {self._tokens}")
         if dX is None and input_grad:
             dX = _new((T, K), self.out_dtype, self.device, stream)

@@ -148,3 +148,26 @@ def test_a_layer_without_a_weight_is_refused(fake):
     assert [c[0] for c in fake["calls"]] == ["mlpb_b128_quantize", "mlpb_linear8_forward",
                                              "mlpb_linear8_backward"]
     plan.handle.ptr = serving.handle.ptr = 0
+
+
+def test_a_backward_takes_the_rows_of_the_last_forward(fake):
+    """After a forward into an Xt of the caller's, the X^T of an earlier forward is not taken for
+    its rows; it can be named."""
+    dev = torch.device("cuda", 1)
+    X, dY = (_Tensor((8, n), torch.bfloat16, dev, None) for n in (64, 32))
+    plan = mlpb.Linear8(8, 64, 32)
+    plan.load(_Tensor((32, 64), torch.bfloat16, dev, None))
+    with pytest.raises(ValueError, match="the last forward kept no rows here"):
+        plan.backward(dY)
+    plan.forward(X)
+    kept = mlpb.b128_empty(64, 8, dev)
+    plan.forward(X, Xt=kept)
+    fake["calls"].clear()
+    with pytest.raises(ValueError, match="the last forward kept no rows here"):
+        plan.backward(dY)
+    assert not fake["calls"]
+    plan.backward(dY, Xt=kept)
+    plan.backward(dY, Xt=plan.saved(8))
+    plan.forward(X)
+    plan.backward(dY)
+    plan.handle.ptr = 0

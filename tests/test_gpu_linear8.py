@@ -298,3 +298,23 @@ def test_an_expired_wait_is_reported_and_the_next_call_is_right():
     assert mlpb.mlpb_linear8_last_device_error(hurt.handle) == mlpb.MLPB_ETIMEOUT
     assert torch.equal(hurt.forward(X), want)
     assert mlpb.mlpb_linear8_last_device_error(hurt.handle) == mlpb.MLPB_OK
+
+
+def test_the_rows_of_an_earlier_forward_are_named():
+    """Forward into the plan, forward into an Xt, and both backwards after them."""
+    T, K, N = 40, 136, 72
+    plan = mlpb.Linear8(T, K, N)
+    plan.load(_randn(1, N, K))
+    a, b, da, db = _randn(2, T, K), _randn(3, T, K), _randn(4, T, N), _randn(5, T, N)
+    plan.forward(a)
+    want_a = plan.backward(da)
+    plan.forward(b)
+    want_b = plan.backward(db)
+    plan.forward(a)
+    kept = mlpb.b128_empty(K, T, "cuda")
+    plan.forward(b, Xt=kept)
+    with pytest.raises(ValueError, match="kept no rows here"):
+        plan.backward(db)
+    got_b = plan.backward(db, Xt=kept)
+    got_a = plan.backward(da, Xt=plan.saved(T))
+    assert all(torch.equal(p, q) for p, q in zip((*got_a, *got_b), (*want_a, *want_b)))
