@@ -26,7 +26,7 @@ struct Piece;
 template <>
 struct Piece<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld_global_nc_v4(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld_global_v4(p); }
   __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void keep(__nv_bfloat16* p) const {
     *reinterpret_cast<uint4*>(p) = u;
@@ -39,8 +39,8 @@ template <>
 struct Piece<float> {
   uint4 u, v;
   __device__ __forceinline__ void load(const float* p) {
-    u = ld_global_nc_v4(p);
-    v = ld_global_nc_v4(p + 4);
+    u = ld_global_v4(p);
+    v = ld_global_v4(p + 4);
   }
   __device__ __forceinline__ void clear() { u = v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void keep(float* p) const {
@@ -159,7 +159,7 @@ __device__ __forceinline__ void put_scale(uint8_t* s, int64_t tiles, int64_t row
 
 template <typename T>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
-    b128_quantize_kernel(const T* __restrict__ x, int64_t R, int64_t C, int square,
+    b128_quantize_kernel(const T* x, int64_t R, int64_t C, int square,
                          uint8_t* __restrict__ q, uint8_t* __restrict__ qs,
                          uint8_t* __restrict__ qt, uint8_t* __restrict__ qts) {
   extern __shared__ __align__(16) uint8_t q_smem[];

@@ -83,4 +83,14 @@ __device__ __forceinline__ uint4 ld_global_nc_v4(const void* p) {
   return __ldg(static_cast<const uint4*>(p));
 }
 
+// 16-byte load of what another kernel may have written while this one had begun (a dependent
+// launch): ld.global.nc is for memory that nobody writes as long as the kernel lives.
+__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 }  // namespace mlpb

@@ -88,3 +88,42 @@ def test_gradients_with_tiles_at_the_edge(edge, T):
     plan.backward(dY, dW=acc, accumulate=True, input_grad=False)
     _check(acc, a, b, base)
     assert mlpb.mlpb_linear8_last_device_error(plan.handle) == mlpb.MLPB_OK
+
+
+@pytest.mark.parametrize("T", [1, 16, 300])
+def test_layers_in_a_row_read_what_the_one_before_wrote(T):
+    """Each launch begins while the one that writes its input ends: a chain of layers, captured and
+    replayed, has the bits of one that waits for every call."""
+    widths = [264, 1032, 520, 264]
+    layers = []
+    for i, (k, n) in enumerate(zip(widths, widths[1:])):
+        layers.append(mlpb.Linear8(T, k, n))
+        layers[-1].load(_randn(i, n, k, std=k ** -0.5))
+    outs = [torch.empty(T, n, dtype=BF, device="cuda") for n in widths[1:]]
+    x = torch.zeros(T, widths[0], dtype=BF, device="cuda")
+    grads = [torch.zeros(n, k, device="cuda") for k, n in zip(widths, widths[1:])]
+    dxs = [torch.empty(T, k, dtype=BF, device="cuda") for k in widths[:-1]]
+
+    def chain(wait):
+        at = x
+        for layer, y in zip(layers, outs):
+            at = layer.forward(at, Y=y)
+            wait()
+        for layer, d, g in zip(layers[::-1], dxs[::-1], grads[::-1]):
+            at = layer.backward(at, dX=d, dW=g)[0]
+            wait()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for seed in range(20):
+        x.copy_(_randn(100 + seed, T, widths[0]))
+        chain(torch.cuda.synchronize)
+        want = [t.clone() for t in (*outs, *dxs, *grads)]
+        for t in (*outs, *dxs, *grads):
+            t.fill_(7)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip((*outs, *dxs, *grads), want)), seed
+        for t in (*outs, *dxs, *grads):
+            t.fill_(7)
+        chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip((*outs, *dxs, *grads), want)), seed
