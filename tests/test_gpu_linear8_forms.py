@@ -127,3 +127,46 @@ def test_layers_in_a_row_read_what_the_one_before_wrote(T):
             t.fill_(7)
         chain(lambda: None)
         assert all(torch.equal(a, b) for a, b in zip((*outs, *dxs, *grads), want)), seed
+
+
+def _layer(T, K, N, out):
+    """Forward and backward of one layer against their products."""
+    X, W, dY = _randn(1, T, K), _randn(2, N, K, std=K ** -0.5), _randn(3, T, N, std=1e-2)
+    X[:, :: max(1, K // 5)] *= 30  # uneven blocks
+    plan = mlpb.Linear8(T, K, N, out_dtype=out)
+    plan.load(W)
+    w = _values(W, True)
+    _check(plan.forward(X), _values(X), w)
+    dX, dW = plan.backward(dY)
+    _check(dX, _values(dY), w.t())
+    _check(dW, _transposed(dY), _transposed(X))
+    assert mlpb.mlpb_linear8_last_device_error(plan.handle) == mlpb.MLPB_OK
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("T,K,N", [
+    (2057, 4104, 2312),   # results from registers, in all three products or in two
+    (4100, 5120, 1096),
+    (4999, 2312, 5128),
+    (2100, 8328, 2056),   # more k-blocks than an fp32 sum takes at once
+    (8300, 1288, 2312)])  # the same in dW
+def test_long_sums_from_registers(T, K, N, out):
+    _layer(T, K, N, out)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("K,N", [(5120, 344), (3592, 1032), (11008, 264), (7816, 4096),
+                                 (20480, 136)])
+@pytest.mark.parametrize("T", [1, 16, 77, 128])
+def test_ranges_of_a_long_sum(T, K, N, out):
+    """Few tokens: K (and, for dX with the sides exchanged, N) in up to eight ranges, of as many or
+    of uneven numbers of blocks, longer than a CTA's ring."""
+    _layer(T, K, N, out)
+    _layer(T, N, K, out)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("T,K,N", [(500, 5120, 5000), (300, 3080, 4104), (1000, 4616, 2312),
+                                   (3100, 1000, 1096), (700, 512, 3080), (250, 6152, 2056)])
+def test_few_tiles(T, K, N, out):
+    _layer(T, K, N, out)
