@@ -347,9 +347,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             bulk_commit();
           }
         }
-        // Boxes take the two slots in turns from the first one on, so that a slot's last box is read
-        // when at most one later box is not.  A tile at C's right edge that ends with the first slot
-        // would break the turns: its boxes are read before the next tile begins.
+        // Boxes take the two slots in turns from the first one on, so that a slot's last box is
+        // read when at most one later box is not.  A tile at C's right edge that ends with the
+        // first slot would break the turns: its boxes are read before the next tile begins.
         if ((boxes & 1) != 0 && lane == 0) bulk_wait_read<0>();
         continue;
       }

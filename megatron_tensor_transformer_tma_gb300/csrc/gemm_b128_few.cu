@@ -369,7 +369,8 @@ cudaError_t launch_b128_few(const B128Maps& m, const B128Params& b, const int* s
   p.err = b.err;
   p.wait_ns = b.wait_ns;
   p.fault_inject = b.fault_inject;
-  // Ranges of K while every cluster is resident at once and has a group of k-blocks for each.  Two
+  // Ranges of K while every cluster is resident at once with a CTA an SM (what the occupancy call
+  // counts for a kernel with tensor memory; two are) and has a group of k-blocks for each.  Two
   // ranges of few k-blocks do not pay for the sums of many columns (128 x 1024 x 1024 9.5 us, 8.5
   // without).
   const int tiles = p.a_tiles * p.b_tiles, groups = (p.num_kb + 3) / 4;

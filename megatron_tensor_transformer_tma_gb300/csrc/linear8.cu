@@ -79,20 +79,26 @@ bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
                 kB128Chunk / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Whether a product goes to the kernel for few tiles: at most 128 rows of C; up to as many tiles of
-// 256 x 256 as pairs of SMs where K is at most 4 k-blocks, all of them epilogue (2048 x 2048 at 4
-// 10.1 against 12.0 us, but 5120 x 5120 42.9 against 30.4), or 24 to 40, long enough to be cut into
-// ranges (512 x 5120 x 5120 21.6 against 23.0, but 1000 x 5120 x 5120 38.8 against 36.3); up to a
-// quarter of that at other lengths (256 x 2048 x 2048 10.6 against 11.0, but 1000 13.4 against
-// 12.0; 256 x 11008 x 4096 23.6 against 33.2, but 512 37.0 against 35.2).  Not where C is added to,
-// which the other kernel does in memory (2048 x 2048 at 8 19.2 against 14.9), nor where an fp32 sum
-// is long enough for chunks, which this one does not have.
+// Whether a product goes to the kernel for few tiles.  It does
+//   - with at most 128 rows of C, where the bytes of B are all that counts;
+//   - where its own tiles (128 of B's rows by at most 128 of A's) are few enough for K to be cut
+//     into ranges, so that SMs work that would have no tile of a pair: the more k-blocks, the more
+//     it gains (forward of 256 x 1024 with its quantization 6.8 against 7.2 us at 4 k-blocks,
+//     10.7 / 15.2 at 24, 18.1 / 33.3 at 86; 512 x 2048 27.4 / 35.1 at 86);
+//   - with no more tiles of 256 x 256 than pairs of SMs, up to 32 k-blocks: it starts and ends
+//     sooner (a tile of 128 x 128 and one CTA, in place of a pair's), and a k-block costs it more,
+//     the bytes of both operands for a quarter of the products.  Between 12 and 40 k-blocks neither
+//     is ahead by more than 7 % (512 x 4096 7.1 / 8.0 at 4, 13.0 / 12.7 at 16, 22.2 / 21.8 at 40,
+//     41.0 / 35.8 at 86; 1024 x 4096 10.5 / 11.8 at 8, 18.9 / 18.9 at 24, 28.5 / 26.5 at 48;
+//     512 x 5120 18.4 / 18.8 at 28, 29.3 / 28.5 at 56).
+// Not where C is added to, which the other kernel does in memory (2048 x 2048 at 8 19.2 against
+// 14.9), nor where an fp32 sum is long enough for chunks, which this one does not have.
 bool few_tiles(const mlpb_linear8* h, int64_t m, int64_t n, int64_t k, bool f32, bool accumulate) {
   const int64_t blocks = b128_blocks(k);
   if (accumulate || blocks > b128_chunk(f32)) return false;
-  const int64_t tiles = cdiv(m, 256) * cdiv(n, 256);
-  const bool most = blocks <= 4 || (blocks >= 24 && blocks <= 40);
-  return m <= 128 || tiles * (most ? 1 : 4) <= h->max_clusters;
+  if (m <= 128) return true;
+  const int64_t tiles = cdiv(m, 128) * cdiv(n, 128), pairs = cdiv(m, 256) * cdiv(n, 256);
+  return tiles <= h->few_slots[1] || (pairs <= h->max_clusters && blocks <= 32);
 }
 
 // C [a.rows][b.rows] (+)= A B^T over the columns that both have.

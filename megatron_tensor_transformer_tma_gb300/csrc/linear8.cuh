@@ -35,8 +35,9 @@ bool b128_staged(int num_kb, bool accumulate);
 cudaError_t b128_gemm_set_attrs(int* max_clusters);
 cudaError_t launch_b128_gemm(const B128Maps& m, const B128Params& p, int clusters, cudaStream_t s);
 
-// gemm_b128_few.cu: the same with few tiles, C written (not added to).  `slots`: clusters of 1, 2, 4 and 8 CTAs that are
-// resident at once; the box of m.a has b128_few_columns(M) rows.
+// gemm_b128_few.cu: the same with few tiles, C written (not added to).  `slots`: clusters of 1, 2,
+// 4 and 8 CTAs that are resident at once with a CTA an SM; the box of m.a has b128_few_columns(M)
+// rows.
 constexpr int kFewSlots = 4;
 int b128_few_columns(int64_t b_rows);
 cudaError_t b128_few_set_attrs(int* slots);
