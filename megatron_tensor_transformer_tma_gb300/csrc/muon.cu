@@ -330,7 +330,7 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
     return MLPB_ECUDA;
   }
   h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  if (muon_small_cluster(h->n, std::max(c.rows, c.cols), c.batch, h->tall, &h->small) !=
+  if (muon_small_cluster(h->n, std::max(c.rows, c.cols), c.batch, h->tall, c.steps, &h->small) !=
       cudaSuccess) {
     delete h;
     return MLPB_ECUDA;

@@ -98,7 +98,8 @@ cudaError_t launch_muon_split(const MuonInput& in, const float4* part, __half* x
 
 // muon_small.cu: the whole update in one launch, for n <= 128 and lengths that a cluster's shared
 // memory holds; 0 CTAs: it does not, or takes longer.
-cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, int* cluster);
+cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, int steps,
+                               int* cluster);
 cudaError_t launch_muon_small(const MuonInput& in, const OrthoParams& o, int steps, int cluster,
                               cudaStream_t s);
 

@@ -661,17 +661,23 @@ static void small_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int
   cfg.numAttrs = 1;
 }
 
-// Whether this kernel ends before the products of gemm_muon.cu would: us for five steps, fitted to
-// both.  A round of resident clusters takes 18.5 + 0.175 np and 0.9 ns an element of a slab (1.5 if
-// it has to be transposed), the other way 80 to 95 and 1.8 (1.3) ns for each of the longer side's
-// elements: 64 x 4096 42 against 81, 64 of them 264 against 497, but 64 of 4096 x 128 974 against
-// 453.
+// Whether this kernel ends before the products of gemm_muon.cu would: us, fitted to both at 1 to
+// 24 steps of 16 x 64 to 128 x 4096 and 24 x 8300, both ways round, 1 to 300 matrices (as a rule
+// within 12 % of what they take).  A round of resident clusters takes 6.5 and 0.34 ns an element of
+// a slab (0.85 if it has to be transposed) and each step 1.15 + 0.033 np and 0.14 ns an element;
+// the other way takes 7.6 and 0.17 (0.2) ns for each element of the longer sides, and each step 12
+// (19 past 64) and 0.32 (0.21).  This one against the other: 64 x 4096 18 / 23 us at one step,
+// 43 / 81 at five; 32 of 4096 x 64 109 / 66 and 194 / 223; 16 of 128 x 2000 55 / 48 and 132 / 160;
+// 64 of 4096 x 128 564 / 154 and 969 / 451.
 static bool small_ends_first(const SmallShape& s, int64_t length, int64_t batch, int64_t resident,
-                             bool tall) {
+                             bool tall, int steps) {
   const double rounds = static_cast<double>((batch + resident - 1) / resident);
-  const double here = rounds * (18.5 + 0.175 * s.np + (tall ? 0.0015 : 0.0009) * s.np * s.slab);
-  const double there =
-      (s.np <= 64 ? 80.0 : 95.0) + (tall ? 0.0013 : 0.0018) * static_cast<double>(batch * length);
+  const double slab = static_cast<double>(s.np) * s.slab;
+  const double sides = static_cast<double>(batch * length);
+  const double here = rounds * (6.5 + (tall ? 0.00085 : 0.00034) * slab +
+                                steps * (1.15 + 0.033 * s.np + 0.00014 * slab));
+  const double there = 7.6 + (tall ? 0.0002 : 0.00017) * sides +
+                       steps * ((s.np <= 64 ? 12.0 : 19.0) + (tall ? 0.00021 : 0.00032) * sides);
   return here <= there;
 }
 
@@ -679,7 +685,8 @@ static bool small_ends_first(const SmallShape& s, int64_t length, int64_t batch,
 // are resident at once, or the fewest that hold a matrix; 0 where no cluster holds it or the tiled
 // products end sooner.  (A cluster has to find its SMs in one part of the GPU: of 16 CTAs only a
 // few are resident together.)
-cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, int* cluster) {
+cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, int steps,
+                               int* cluster) {
   *cluster = 0;
   int64_t at_once = 0;
   if (n > kSmallMaxN) return cudaSuccess;
@@ -702,7 +709,7 @@ cudaError_t muon_small_cluster(int n, int64_t length, int64_t batch, bool tall, 
     }
   }
   if (*cluster > 0 &&
-      !small_ends_first(small_shape(n, length, *cluster), length, batch, at_once, tall))
+      !small_ends_first(small_shape(n, length, *cluster), length, batch, at_once, tall, steps))
     *cluster = 0;
   return cudaSuccess;
 }

@@ -199,3 +199,19 @@ def test_an_expired_wait_is_reported_and_the_next_call_is_right():
     assert mlpb.mlpb_muon_last_device_error(hurt.handle) == mlpb.MLPB_ETIMEOUT
     assert torch.equal(hurt.orthogonalize(U), want)
     assert mlpb.mlpb_muon_last_device_error(hurt.handle) == mlpb.MLPB_OK
+
+
+@pytest.mark.parametrize("n,r,c", [(32, 4096, 64), (32, 64, 4096), (16, 128, 2000)])
+def test_the_form_goes_by_the_steps_too(n, r, c):
+    """Matrices that a cluster's shared memory holds, and that the tiled products finish sooner
+    where there are few steps: either form against the oracle."""
+    U = _randn(r, n, r, c)
+    small = []
+    for steps, coef in ((1, muon.COEF), (3, muon.COEF), (12, (1.5, -0.5, 0.0))):
+        plan = mlpb.Muon(r, c, n, steps=steps, coefficients=coef)
+        small.append(plan.workspace.numel() == 256)
+        O = plan.orthogonalize(U)
+        assert mlpb.mlpb_muon_last_device_error(plan.handle) == mlpb.MLPB_OK
+        _close(O[:3], _np(U[:3]), steps=steps, coef=coef)
+        _close(O[-1:], _np(U[-1:]), steps=steps, coef=coef)
+    assert small == sorted(small) and small[-1]  # once it pays, it pays with more steps
