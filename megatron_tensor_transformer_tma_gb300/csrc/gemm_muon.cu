@@ -296,12 +296,6 @@ __device__ __forceinline__ void apply_box(const float (&v)[32], int j0, uint32_t
     const uint32_t at = box_piece(slot, lane, j);
     float x[8], b[8], r[8];
     unpack_half8(lds16(at), x);
-    if constexpr (Op == OrthoOp::Apply) {
-      float lo[8];
-      unpack_half8(lds16(at + kEpiBox), lo);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] += lo[i];
-    }
     if constexpr (kTall) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[i] = bj.at(j0, 8 * q + i);
@@ -310,7 +304,15 @@ __device__ __forceinline__ void apply_box(const float (&v)[32], int j0, uint32_t
       for (int i = 0; i < 8; ++i) b[i] = bm;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = fmaf(b[i], x[i], v[8 * q + i] * (1.0f / kDScale));
+    for (int i = 0; i < 8; ++i) r[i] = v[8 * q + i] * (1.0f / kDScale);
+    if constexpr (Op == OrthoOp::Apply) {
+      float lo[8];
+      unpack_half8(lds16(at + kEpiBox), lo);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = fmaf(p.low_beta ? b[i] : p.a, lo[i], r[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = fmaf(b[i], x[i], r[i]);
     if constexpr (Op == OrthoOp::Apply) {  // X' times 2^12, in two parts
       sts16(at, pack_half8(r));
       if (p.low_out) {

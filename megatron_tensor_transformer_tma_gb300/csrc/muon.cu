@@ -258,6 +258,7 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   };
   for (int i = 0; i < c.steps; ++i) {
     p.low_out = i < c.steps - 2 ? 1 : 0;
+    p.low_beta = i >= c.steps - 3 ? 1 : 0;
     if (!run(OrthoOp::Gram, tg, gram[i & 1]) || !run(OrthoOp::Poly, tp, poly) ||
         !(i == c.steps - 1 ? run(OrthoOp::Last, ta, last) : run(OrthoOp::Apply, ta, apply[i & 1])))
       return MLPB_ECUDA;

@@ -12,11 +12,20 @@
 //   - The diagonal d of A is fp32 and its part E off the diagonal fp16:
 //       A A = E E + (d_i + d_j) E_ij + delta_ij d_i^2,
 //     so the identity that A comes near is not rounded.  Likewise b A + c A A + a I is
-//     D + diag(beta) and X' = beta X + D X: a X and most of (b A + c A A) X cancel (3.4 - 2.7 near the end), and
-//     do so in fp32.
-// Against 64 bits the result is off by 3e-4 to 7e-4 of its size (Gaussian, low-rank and decaying
-// spectra); with the diagonals in the products it is 1e-3 to 3e-3, with bf16 operands 1e-2 to
-// 2e-2.
+//     D + diag(beta) and X' = beta hi + D hi + a lo: a X and most of (b A + c A A) X cancel
+//     (3.4 - 2.7 near the end), and do so in fp32.
+//   - What the product does not see of lo, (b A + c A A) lo, lies along the large singular values,
+//     which stay as they are.  beta lo in place of a lo would leave out D lo alone, less where A is
+//     near the identity; but where few directions dominate, D + diag(beta) - a I has a low rank,
+//     which D has not, and what it leaves out falls into all the others, which later steps amplify
+//     a times each: 4 % of O for rank one at 2 x 40, more than O in 12 steps.  So lo goes with beta
+//     in the last two steps that have one, and with a before.
+// Against 64 bits the result of five steps is off by 3e-4 to 1.4e-3 of its size, and by up to 4e-3
+// below n = 32 or where one singular value dominates (Gaussian matrices, gradients, low ranks and
+// singular values that fall to 1e-4 of the largest, from n = 64 on: 3e-4 to 1.2e-3).  12 steps:
+// 1e-3 to 1e-2, but what lies below 2^-22 of |U| grows a times a step, to 0.1 of O for rank one.
+// With the diagonals in the products even spectra are off by 1e-3 to 3e-3, with bf16 operands by
+// 1e-2 to 2e-2.
 #pragma once
 
 #include <cuda.h>
@@ -30,7 +39,6 @@ constexpr float kXScale = 4096.0f;    // X, E are stored times 2^12
 constexpr float kXInv = 1.0f / 4096.0f;
 constexpr float kDScale = 1024.0f;    // D times 2^10
 constexpr float kEEInv = kXInv * kXInv;            // a product's scale: 2^-24
-constexpr float kDXInv = kXInv / kDScale;          // 2^-22
 constexpr int kOrthoMaxSplit = 16;  // ranges of K
 constexpr int kOrthoLd = 64;  // rows of X, E and D are padded to multiples of 64 (X's with zeros)
 
@@ -56,6 +64,7 @@ struct OrthoParams {
   float* diag;  // d [batch][ldn]
   float* beta;  // [batch][ldn]
   int low_out;  // Apply: X' has a low part (the last step's X is the high part alone)
+  int low_beta;  // Apply: the low part of X goes with beta, not with a
   // Last: O bf16, or the weight's update W <- (1 - lr wd) W - lr scale O
   __nv_bfloat16* out;
   float* w;

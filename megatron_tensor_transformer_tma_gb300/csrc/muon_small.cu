@@ -10,7 +10,7 @@
 //   2. the sum over CTAs, in rank order: each CTA adds one slice through distributed shared memory
 //      and writes E and d to all;
 //   3. E E, D and beta, by every CTA for itself;
-//   4. X <- beta X + D X in place, 512 columns at a time.
+//   4. X <- beta X + D X in place, 512 columns at a time (muon.cuh has what X's parts go with).
 // Two barriers of the cluster a step.  The products are single tcgen05 chains of M = 128 (rows past
 // n are of whatever lies behind and are not read back) that a thread issues between barriers of the
 // CTA: with mma.sync, a sixteenth of the rate here, they were two thirds of the time at n = 128
@@ -512,6 +512,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       });
       if (part_of < spread) {
         const uint64_t bm = f2_pack(beta[mrow], beta[mrow]);
+        const uint64_t gm = step >= p.steps - 3 ? bm : f2_pack(p.a, p.a);  // of X's low part
         const uint64_t scale = f2_pack(1.0f / kDScale, 1.0f / kDScale);
         const int end = (blocks * (part_of + 1) >> spread_log) * 64;
         for (int c = (blocks * part_of >> spread_log) * 64 + group * 16; c < end; c += 64) {
@@ -530,12 +531,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
             for (int k = 0; k < 4; ++k) {
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
               const float2 g2 = __half22float2(*reinterpret_cast<const __half2*>(&l[k]));
-              const uint64_t x = f2_add(f2_pack(f.x, f.y), f2_pack(g2.x, g2.y));
               const uint64_t a2 = f2_mul(f2_pack(__uint_as_float(acc[8 * j + 2 * k]),
                                                  __uint_as_float(acc[8 * j + 2 * k + 1])),
                                          scale);
               float v0, v1;
-              f2_unpack(f2_fma(bm, x, a2), v0, v1);
+              f2_unpack(f2_fma(bm, f2_pack(f.x, f.y), f2_fma(gm, f2_pack(g2.x, g2.y), a2)), v0,
+                        v1);
               if (!last) {
                 hi[k] = half2_bits(v0, v1);
                 const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));

@@ -46,8 +46,8 @@ def _half(x, scale):
 
 def rounded(U, steps=5, coef=COEF):
     """With X, the part of A off its diagonal and that of b A + c A A + a I as fp16 operands, scaled
-    by 2^12, 2^12 and 2^10, diagonals apart, and X in two fp16 parts between the steps (one before the
-    last)."""
+    by 2^12, 2^12 and 2^10, diagonals apart, and X in two fp16 parts between the steps (one before
+    the last), the low one of which goes with the diagonal beta in the last steps and with a before."""
     a, b, c = coef
     X = normalized(U)
     tall = X.shape[0] > X.shape[1]
@@ -55,7 +55,7 @@ def rounded(U, steps=5, coef=COEF):
         X = X.T
     for i in range(steps):
         hi = _half(X, 4096.0)
-        X = hi + (_half(X - hi, 4096.0) if i < steps - 1 else 0.0)
+        lo = _half(X - hi, 4096.0) if i < steps - 1 else 0.0
         A = hi @ hi.T
         d = np.diag(A).copy()
         E = _half(A - np.diag(d), 4096.0)
@@ -63,7 +63,8 @@ def rounded(U, steps=5, coef=COEF):
         beta = a + b * d + c * d * d + c * np.diag(EE)
         D = (b + c * (d[:, None] + d)) * E + c * EE
         D = _half(D - np.diag(np.diag(D)), 1024.0)
-        X = beta[:, None] * X + D @ hi
+        low = beta[:, None] if i >= steps - 3 else a
+        X = beta[:, None] * hi + low * lo + D @ hi
     return X.T if tall else X
 
 
