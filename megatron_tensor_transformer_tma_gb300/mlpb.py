@@ -1206,28 +1206,33 @@ class Linear8:
         return Y
 
     def backward(self, dY, dX=None, dW=None, Xt=None, accumulate=False, input_grad=True,
-                 stream=None):
+                 weight_grad=True, stream=None):
         """(dX, dW) for the rows of the last forward, or for an Xt that a forward wrote (after a
         forward with an Xt it has to be named; saved() is what the one before left here); with
-        `accumulate` dW is added into; without `input_grad` dX is not computed.  A captured
-        forward counts as it is captured, not as it is replayed."""
+        `accumulate` dW is added into; without `input_grad` or `weight_grad` dX or dW, unless it is
+        given, is None and not computed (dX alone takes no rows of a forward).  A captured forward
+        counts as it is captured, not as it is replayed."""
         if not self.training:
             raise ValueError("Linear8: made with training=False")
+        weight_grad = weight_grad or dW is not None
+        if not (input_grad or weight_grad or dX is not None):
+            raise ValueError("input_grad, weight_grad: neither gradient is asked for")
         if accumulate and dW is None:
             raise ValueError("dW: nothing given to add into")
         h, K, N = self.handle, self._inputs, self._outputs
         dev, T = _linear8_rows(h, dY, N, "dY")
         self._check_loaded()
-        if Xt is None and T > 0 and T != self._tokens:
+        if Xt is None and weight_grad and T > 0 and T != self._tokens:
             if self._tokens is None:
                 raise ValueError("Xt: not given, and the last forward kept no rows here")
             raise ValueError(f"dY: {T} tokens, the last forward had {self._tokens}")
         if dX is None and input_grad:
             dX = _new((T, K), self.out_dtype, self.device, stream)
-        if dW is None:
+        if dW is None and weight_grad:
             dW = _new((N, K), torch.float32, self.device, stream)
         args = [h.ptr, T, _arg(dY, torch.bfloat16, (T, N), "dY", dev),
-                self.Wt[0].data_ptr(), self.Wt[1].data_ptr(), *self._saved_args(T, Xt),
+                self.Wt[0].data_ptr(), self.Wt[1].data_ptr(),
+                *(self._saved_args(T, Xt) if weight_grad else (None, None)),
                 _arg(dX, self.out_dtype, (T, K), "dX", dev),
                 _arg(dW, torch.float32, (N, K), "dW", dev),
                 1 if accumulate else 0, self.workspace.data_ptr()]

@@ -318,3 +318,27 @@ def test_the_rows_of_an_earlier_forward_are_named():
     got_b = plan.backward(db, Xt=kept)
     got_a = plan.backward(da, Xt=plan.saved(T))
     assert all(torch.equal(p, q) for p, q in zip((*got_a, *got_b), (*want_a, *want_b)))
+
+
+def test_one_gradient_alone():
+    T, K, N = 50, 264, 136
+    plan = mlpb.Linear8(T, K, N)
+    plan.load(_randn(1, N, K))
+    X, dY = _randn(2, T, K), _randn(3, T, N)
+    plan.forward(X)
+    dX, dW = plan.backward(dY)
+    a, none = plan.backward(dY, weight_grad=False)
+    assert none is None and torch.equal(a, dX)
+    none, b = plan.backward(dY, input_grad=False)
+    assert none is None and torch.equal(b, dW)
+    # dX needs no rows of a forward: none of this plan, and of another number of tokens
+    fresh = mlpb.Linear8(T, K, N)
+    fresh.load(_randn(1, N, K))
+    assert torch.equal(fresh.backward(dY[:17], weight_grad=False)[0], dX[:17])
+    with pytest.raises(ValueError, match="neither gradient"):
+        plan.backward(dY, input_grad=False, weight_grad=False)
+    a, b = torch.zeros_like(dX), torch.zeros_like(dW)  # given ones are computed all the same
+    got = plan.backward(dY, dX=a, dW=b, input_grad=False, weight_grad=False)
+    assert got[0] is a and got[1] is b and torch.equal(a, dX) and torch.equal(b, dW)
+    with pytest.raises(ValueError, match="nothing given"):
+        plan.backward(dY, accumulate=True, weight_grad=False)
