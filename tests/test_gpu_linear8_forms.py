@@ -170,3 +170,10 @@ def test_ranges_of_a_long_sum(T, K, N, out):
                                    (3100, 1000, 1096), (700, 512, 3080), (250, 6152, 2056)])
 def test_few_tiles(T, K, N, out):
     _layer(T, K, N, out)
+
+
+@pytest.mark.parametrize("T,K,N", [(8, 2 ** 20, 8), (5, 8, 2 ** 20), (300, 2 ** 20, 16),
+                                   (300, 16, 2 ** 20), (1, 2 ** 20, 264)])
+def test_the_longest_sides(T, K, N):
+    _layer(T, K, N, F32)
+    _layer(T, K, N, BF)

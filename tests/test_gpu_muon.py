@@ -267,3 +267,16 @@ def test_errors_of_many_steps(r, c, kind):
     plan.step(W, M, torch.from_numpy(U).cuda(), torch.ones(1, device="cuda"))
     want = muon.orthogonalize(U, 12)
     assert np.linalg.norm(_np(W) - want) <= 5e-3 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("n,r,c", [(1, 1, 65536), (1, 65536, 1), (65535, 1, 3), (65535, 2, 1),
+                                   (1, 16, 65536), (1, 65536, 40), (1, 65535, 129)])
+def test_longest_sides_and_most_matrices(n, r, c):
+    U = _randn(r + c, n, r, c)
+    plan = mlpb.Muon(r, c, n)
+    plan.workspace.fill_(0xff)
+    O = plan.orthogonalize(U)
+    assert mlpb.mlpb_muon_last_device_error(plan.handle) == mlpb.MLPB_OK
+    pick = sorted({0, n // 2, n - 1})
+    _close(O[pick], _np(U[pick]))
+    assert bool(O.isfinite().all()) and bool((O != 0).flatten(1).any(1).all())
