@@ -11,9 +11,9 @@
 // 6.8 that a copy reaches).
 #include <algorithm>
 
-#include "../../include/mlpb.h"
 #include "b128.cuh"
 #include "common.cuh"
+#include "plan.h"
 
 namespace mlpb {
 
@@ -304,8 +304,6 @@ cudaError_t launch_b128_quantize(const void* x, bool f32, int64_t rows, int64_t 
   return f32 ? launch_as<float>(x, rows, cols, square, q, qs, qt, qts, s)
              : launch_as<__nv_bfloat16>(x, rows, cols, square, q, qs, qt, qts, s);
 }
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 static bool b128_in_range(int64_t rows, int64_t cols) {
   return rows <= (int64_t{1} << 20) && cols <= (int64_t{1} << 20) && cols % 8 == 0;

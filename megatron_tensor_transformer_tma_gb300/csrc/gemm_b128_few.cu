@@ -46,18 +46,6 @@ static FewShape few_shape(int64_t b_rows) {
   return s;
 }
 
-__device__ __forceinline__ void tmem_alloc_one(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-               "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc_one(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-               : "memory");
-}
-
 __device__ __forceinline__ void umma_mx_one(uint32_t d, uint64_t adesc, uint64_t bdesc,
                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                             uint32_t accumulate) {
@@ -75,12 +63,6 @@ __device__ __forceinline__ void tmem_copy_scales_one(uint32_t taddr, uint64_t de
                : "memory");
 }
 
-__device__ __forceinline__ void umma_commit_one(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
 struct FewParams {
   int a_rows, b_rows, num_kb;
   int a_tiles, b_tiles;      // tiles of C: 128 rows of A, `columns` rows of B
@@ -94,15 +76,6 @@ struct FewParams {
   uint64_t wait_ns;
   int fault_inject;
 };
-
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 __global__ void __launch_bounds__(kFewThreads)
     gemm_b128_few_kernel(const __grid_constant__ B128Maps maps, const FewParams p) {

@@ -1,33 +1,22 @@
 // A linear layer on block-scaled E4M3 operands: handle, workspace, tensor maps, launches.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <new>
 
-#include "../../include/mlpb.h"
 #include "common.cuh"
 #include "linear8.cuh"
+#include "plan.h"
 
 using namespace mlpb;
 
 struct mlpb_linear8 {
   mlpb_linear8_config cfg;
-  int device, max_clusters;
+  PlanDevice on;
+  int max_clusters;
   int few_slots[kFewSlots];
   bool fault_pending;
-  uint32_t* err;
-  PFN_cuTensorMapEncodeTiled_v12000 encode;
 };
 
 namespace {
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t code_bytes(int64_t rows, int64_t cols) {
   return align256(static_cast<size_t>(rows * b128_ld(cols)));
@@ -59,10 +48,8 @@ bool encode(const mlpb_linear8* h, CUtensorMap* m, CUtensorMapDataType type, con
             uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
             uint32_t box_outer, CUtensorMapSwizzle swizzle) {
   const cuuint64_t dims[2] = {inner, outer}, strides[1] = {stride};
-  const cuuint32_t box[2] = {box_inner, box_outer}, steps[2] = {1, 1};
-  return h->encode(m, type, 2, const_cast<void*>(base), dims, strides, box, steps,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  return h->on.map(m, type, base, 2, dims, strides, box, swizzle);
 }
 
 // Codes in tiles of `rows` (128) rows by 128 bytes; what is past the edges reads zero.
@@ -132,7 +119,7 @@ mlpb_status product(mlpb_linear8* h, const Quantized& a, const Quantized& b, voi
   // k-blocks; none or a loss from 64 on)
   p.raster_group = p.num_kb <= 48 ? 16 : 8;
   p.C = C;
-  p.err = h->err;
+  p.err = h->on.err;
   p.wait_ns = kDefaultWaitNs;
   p.fault_inject = h->fault_pending ? 1 : 0;
   h->fault_pending = false;
@@ -149,13 +136,6 @@ mlpb_status quantize(const void* x, bool f32, int64_t rows, int64_t cols, const 
                               qt ? qt->scales : nullptr, s) == cudaSuccess
              ? MLPB_OK
              : MLPB_ECUDA;
-}
-
-// The current device is the handle's.
-mlpb_status on_device(const mlpb_linear8* h) {
-  int device = -1;
-  if (cudaGetDevice(&device) != cudaSuccess) return MLPB_ECUDA;
-  return device == h->device ? MLPB_OK : MLPB_EINVAL;
 }
 
 }  // namespace
@@ -175,35 +155,15 @@ extern "C" mlpb_status mlpb_linear8_create(const mlpb_linear8_config* cfg, mlpb_
   if (h == nullptr) return MLPB_ENOMEM;
   h->cfg = c;
   h->fault_pending = (c.flags & MLPB_LINEAR8_FAULT_INJECT) != 0;
-  h->err = nullptr;
-  int major = 0, minor = 0;
-  if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, h->device) != cudaSuccess) {
+  mlpb_status st = h->on.find();
+  if (st == MLPB_OK && (b128_gemm_set_attrs(&h->max_clusters) != cudaSuccess ||
+                        h->max_clusters < 1 || b128_few_set_attrs(h->few_slots) != cudaSuccess ||
+                        h->few_slots[0] < 1))
+    st = MLPB_ECUDA;
+  if (st == MLPB_OK) st = h->on.allocate();
+  if (st != MLPB_OK) {
     delete h;
-    return MLPB_ECUDA;
-  }
-  if (major != 10 || minor != 3) {
-    delete h;
-    return MLPB_EUNSUPPORTED;
-  }
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult found{};
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                       &found) != cudaSuccess ||
-      found != cudaDriverEntryPointSuccess || fn == nullptr) {
-    delete h;
-    return MLPB_ECUDA;
-  }
-  h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  if (b128_gemm_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
-      b128_few_set_attrs(h->few_slots) != cudaSuccess || h->few_slots[0] < 1 ||
-      cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||
-      cudaMemset(h->err, 0, sizeof(uint32_t)) != cudaSuccess ||
-      cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come
-    if (h->err) cudaFree(h->err);
-    delete h;
-    return MLPB_ECUDA;
+    return st;
   }
   *out = h;
   return MLPB_OK;
@@ -211,7 +171,7 @@ extern "C" mlpb_status mlpb_linear8_create(const mlpb_linear8_config* cfg, mlpb_
 
 extern "C" void mlpb_linear8_destroy(mlpb_linear8* h) {
   if (h == nullptr) return;
-  if (h->err) cudaFree(h->err);
+  h->on.release();
   delete h;
 }
 
@@ -236,7 +196,7 @@ extern "C" mlpb_status mlpb_linear8_forward(mlpb_linear8* h, int64_t tokens, con
   for (const void* q : {X, Wq, Ws, static_cast<const void*>(Y), static_cast<const void*>(Xt),
                         static_cast<const void*>(Xts), static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MLPB_EINVAL;
-  mlpb_status st = on_device(h);
+  mlpb_status st = h->on.current();
   if (st != MLPB_OK || tokens == 0) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* at = static_cast<uint8_t*>(workspace);
@@ -263,7 +223,7 @@ extern "C" mlpb_status mlpb_linear8_backward(mlpb_linear8* h, int64_t tokens, co
        {dY, Wt, Wts, Xt, Xts, static_cast<const void*>(dX), static_cast<const void*>(dW),
         static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MLPB_EINVAL;
-  mlpb_status st = on_device(h);
+  mlpb_status st = h->on.current();
   if (st != MLPB_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (tokens == 0) {
@@ -285,16 +245,5 @@ extern "C" mlpb_status mlpb_linear8_backward(mlpb_linear8* h, int64_t tokens, co
 
 extern "C" mlpb_status mlpb_linear8_last_device_error(mlpb_linear8* h, mlpb_stream_t stream) {
   if (h == nullptr) return MLPB_EINVAL;
-  const mlpb_status st = on_device(h);  // `stream` would not be one of the handle's
-  if (st != MLPB_OK) return st;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint32_t v = 0;
-  if (cudaMemcpyAsync(&v, h->err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return MLPB_ECUDA;
-  if (v == 0) return MLPB_OK;
-  if (cudaMemsetAsync(h->err, 0, sizeof(uint32_t), s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return MLPB_ECUDA;
-  return MLPB_ETIMEOUT;
+  return h->on.last_error(reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,37 +1,27 @@
 // Orthogonalised updates of weights: handle, workspace, tensor maps, the launches of a call.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
-#include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <new>
 
-#include "../../include/mlpb.h"
 #include "common.cuh"
 #include "gemm_params.h"
 #include "muon.cuh"
+#include "plan.h"
 
 using namespace mlpb;
 
 struct mlpb_muon {
   mlpb_muon_config cfg;
-  int device, max_clusters;
+  PlanDevice on;
+  int max_clusters;
   bool tall, fault_pending;
   int n, ldx, ldn;
   int small;  // CTAs of a cluster that keeps a matrix in shared memory; 0: tiles of tensor cores
-  uint32_t* err;
-  PFN_cuTensorMapEncodeTiled_v12000 encode;
 };
 
 namespace {
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Layout {
   float4* part;
@@ -130,16 +120,6 @@ Layout layout(const mlpb_muon* h, void* workspace) {
   return l;
 }
 
-bool encode(const mlpb_muon* h, CUtensorMap* m, CUtensorMapDataType type, const void* base,
-            int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-            CUtensorMapSwizzle swizzle) {
-  const cuuint32_t steps[4] = {1, 1, 1, 1};
-  return h->encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
-                   box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 // Matrices [batch][rows][ld] in boxes of some rows by some columns.
 struct Matrices {
   const void* base;
@@ -152,8 +132,8 @@ bool map_box(const mlpb_muon* h, CUtensorMap* m, const Matrices& x, CUtensorMapD
                               static_cast<cuuint64_t>(h->cfg.batch)};
   const cuuint64_t strides[2] = {x.ld * size, static_cast<cuuint64_t>(x.rows) * x.ld * size};
   const cuuint32_t box[3] = {box_cols, box_rows, 1};
-  return encode(h, m, type, x.base, 3, dims, strides, box,
-                swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+  return h->on.map(m, type, x.base, 3, dims, strides, box,
+                   swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // As operands whose K runs along a row: `size` (128 or 64) rows by 64 columns.
@@ -170,8 +150,8 @@ bool map_mn(const mlpb_muon* h, CUtensorMap* m, const Matrices& x, int size) {
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.ld) * 2, 128,
                                  static_cast<cuuint64_t>(x.rows) * x.ld * 2};
   const cuuint32_t box[4] = {64, kBK, static_cast<cuuint32_t>(size / 64), 1};
-  return encode(h, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x.base, 4, dims, strides, box,
-                CU_TENSOR_MAP_SWIZZLE_128B);
+  return h->on.map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x.base, 4, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The epilogue's boxes of 32 rows by 64 columns, and mirrored.
@@ -189,7 +169,7 @@ mlpb_status iterate(mlpb_muon* h, const MuonInput& in, OrthoParams p, void* work
   p.a = c.coef[0];
   p.b = c.coef[1];
   p.c = c.coef[2];
-  p.err = h->err;
+  p.err = h->on.err;
   if (h->small > 0)
     return launch_muon_small(in, p, c.steps, h->small, s) == cudaSuccess ? MLPB_OK : MLPB_ECUDA;
   const Layout l = layout(h, workspace);
@@ -281,12 +261,6 @@ bool coefficients_fit(const mlpb_muon_config& c) {
   return true;
 }
 
-mlpb_status on_device(const mlpb_muon* h) {
-  int device = -1;
-  if (cudaGetDevice(&device) != cudaSuccess) return MLPB_ECUDA;
-  return device == h->device ? MLPB_OK : MLPB_EINVAL;
-}
-
 }  // namespace
 
 extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon** out) {
@@ -310,39 +284,16 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
   h->ldx = static_cast<int>(cdiv(c.cols, kOrthoLd)) * kOrthoLd;
   h->ldn = static_cast<int>(cdiv(h->n, kOrthoLd)) * kOrthoLd;
   h->fault_pending = (c.flags & MLPB_MUON_FAULT_INJECT) != 0;
-  h->err = nullptr;
-  int major = 0, minor = 0;
-  if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, h->device) != cudaSuccess) {
+  mlpb_status st = h->on.find();
+  if (st == MLPB_OK &&
+      (muon_small_cluster(h->n, std::max(c.rows, c.cols), c.batch, h->tall, c.steps, &h->small) !=
+           cudaSuccess ||
+       ortho_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1))
+    st = MLPB_ECUDA;
+  if (st == MLPB_OK) st = h->on.allocate();
+  if (st != MLPB_OK) {
     delete h;
-    return MLPB_ECUDA;
-  }
-  if (major != 10 || minor != 3) {
-    delete h;
-    return MLPB_EUNSUPPORTED;
-  }
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult found{};
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                       &found) != cudaSuccess ||
-      found != cudaDriverEntryPointSuccess || fn == nullptr) {
-    delete h;
-    return MLPB_ECUDA;
-  }
-  h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  if (muon_small_cluster(h->n, std::max(c.rows, c.cols), c.batch, h->tall, c.steps, &h->small) !=
-      cudaSuccess) {
-    delete h;
-    return MLPB_ECUDA;
-  }
-  if (ortho_set_attrs(&h->max_clusters) != cudaSuccess || h->max_clusters < 1 ||
-      cudaMalloc(reinterpret_cast<void**>(&h->err), sizeof(uint32_t)) != cudaSuccess ||
-      cudaMemset(h->err, 0, sizeof(uint32_t)) != cudaSuccess ||
-      cudaStreamSynchronize(nullptr) != cudaSuccess) {  // streams that do not wait for it may come
-    if (h->err) cudaFree(h->err);
-    delete h;
-    return MLPB_ECUDA;
+    return st;
   }
   *out = h;
   return MLPB_OK;
@@ -350,7 +301,7 @@ extern "C" mlpb_status mlpb_muon_create(const mlpb_muon_config* cfg, mlpb_muon**
 
 extern "C" void mlpb_muon_destroy(mlpb_muon* h) {
   if (h == nullptr) return;
-  if (h->err) cudaFree(h->err);
+  h->on.release();
   delete h;
 }
 
@@ -365,7 +316,7 @@ extern "C" mlpb_status mlpb_muon_orthogonalize(mlpb_muon* h, const void* U, int3
   if (h == nullptr || !U || !O || !workspace || (u_f32 != 0 && u_f32 != 1)) return MLPB_EINVAL;
   for (const void* q : {U, static_cast<const void*>(O), static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MLPB_EINVAL;
-  const mlpb_status st = on_device(h);
+  const mlpb_status st = h->on.current();
   if (st != MLPB_OK) return st;
   MuonInput in{};
   in.g = U;
@@ -386,7 +337,7 @@ extern "C" mlpb_status mlpb_muon_step(mlpb_muon* h, const float* G, float* M, fl
                         static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MLPB_EINVAL;
   if ((reinterpret_cast<uintptr_t>(lr) & 3u) != 0) return MLPB_EINVAL;
-  const mlpb_status st = on_device(h);
+  const mlpb_status st = h->on.current();
   if (st != MLPB_OK) return st;
   const mlpb_muon_config& c = h->cfg;
   MuonInput in{};
@@ -409,16 +360,5 @@ extern "C" mlpb_status mlpb_muon_step(mlpb_muon* h, const float* G, float* M, fl
 
 extern "C" mlpb_status mlpb_muon_last_device_error(mlpb_muon* h, mlpb_stream_t stream) {
   if (h == nullptr) return MLPB_EINVAL;
-  const mlpb_status st = on_device(h);  // `stream` would not be one of the handle's
-  if (st != MLPB_OK) return st;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint32_t v = 0;
-  if (cudaMemcpyAsync(&v, h->err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return MLPB_ECUDA;
-  if (v == 0) return MLPB_OK;
-  if (cudaMemsetAsync(h->err, 0, sizeof(uint32_t), s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return MLPB_ECUDA;
-  return MLPB_ETIMEOUT;
+  return h->on.last_error(reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,8 +1,8 @@
 // What stands before the Newton-Schulz products: the momentum, the Frobenius norm of the update
 // and its two fp16 parts.  Bound by memory: the norm's pass reads G and M and writes M (12 bytes
 // an element), the second reads both again and writes two parts (12 bytes); keeping U instead
-// would write and read four bytes more than it saves.  16 matrices of 1376 x 4096: 154 us (7.0 TB/s)
-// and 180 us (6.0 TB/s).
+// would write and read four bytes more than it saves.  16 matrices of 1376 x 4096: 154 us
+// (7.0 TB/s) and 180 us (6.0 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -7,8 +7,8 @@
 // (muon.cuh has the number formats); a tall matrix is transposed as it is read and written, since
 // the polynomial of X^T is that of X transposed.  A step is
 //   1. each CTA's share of X X^T over its slab;
-//   2. the sum over CTAs, in rank order: each CTA adds one slice through distributed shared memory
-//      and writes E and d to all;
+//   2. the sum over CTAs: each CTA adds one slice through distributed shared memory, in an order
+//      that is the same every run (lanes share a sum), and writes E and d to all;
 //   3. E E, D and beta, by every CTA for itself;
 //   4. X <- beta X + D X in place, 512 columns at a time (muon.cuh has what X's parts go with).
 // Two barriers of the cluster a step.  The products are single tcgen05 chains of M = 128 (rows past
@@ -133,15 +133,6 @@ __device__ __forceinline__ void chain_apply(uint32_t d, uint32_t dm, uint32_t x,
                  bdesc + static_cast<uint32_t>((k * 128) >> 4), idesc, k > 0 ? 1u : 0u);
 }
 
-__device__ __forceinline__ float4 ld_remote4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void st_remote16(uint32_t cluster_addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w)
@@ -252,13 +243,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
     words[1] = 0u;
     mbar_fence_init();
   }
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(words)),
-                 "r"(kSmallTmem)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc_one(smem_u32(words), kSmallTmem);
 
   // ------------------------------------------------------------ momentum and norm
   float4 sq = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -303,7 +288,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
     const uint32_t mine = smem_u32(squares + kSmallWarps);
     double t = 0.0;
     if (lane < p.cluster)
-      t = whole_square(ld_remote4(p.cluster > 1 ? mapa_shared(mine, lane) : mine));
+      t = whole_square(ld_cluster4(p.cluster > 1 ? mapa_shared(mine, lane) : mine));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0) norm_factors(t, factors[0], factors[1]);
@@ -365,9 +350,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
     if (tid == 0 && *wc.abort_flag == 0u) {  // no more products after an expired wait
       tc_fence_after();
       issue();
-      asm volatile(
-          "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-          : "memory");
+      umma_commit_one(bar);
     }
     wait_bounded(bar, parity, wc, kSiteMmaFull);
     parity ^= 1u;
@@ -422,7 +405,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
 #pragma unroll 8
           for (int r = of; r < p.cluster; r += share) {
             const float4 o =
-                ld_remote4(p.cluster > 1 ? mapa_shared(part_a + 16 * q, r) : part_a + 16 * q);
+                ld_cluster4(p.cluster > 1 ? mapa_shared(part_a + 16 * q, r) : part_a + 16 * q);
             s.x += o.x;
             s.y += o.y;
             s.z += o.z;
@@ -630,9 +613,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Smal
       __syncwarp();
     }
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(kSmallTmem)
-                 : "memory");
+    tmem_dealloc_one(tmem, kSmallTmem);
   }
   if (p.cluster > 1) cluster_sync();  // nobody reads this CTA's shared memory any more
 }
