@@ -495,7 +495,9 @@ mlpb_status mlpb_b128_quantize(const void *x, int32_t x_f32, int64_t rows, int64
  * MLPB_FLAG_FP8, at the same rate: the tensor cores apply the scales):
  *     Y = Xq Wq^T,   dX = dYq Wq,   dW = (dY^T)q ((X^T)q)^T
  * where (.)q rounds blocks of 128 along the axis that is summed over, and W blocks of 128 x 128.
- * Products of codes are exact, sums fp32. */
+ * Products of codes are exact, sums fp32, which the tensor cores cut off instead of rounding: by
+ * 6e-7 of a sum of 8192 products, in chunks of which an fp32 result is summed, and in proportion in
+ * a longer sum of a bf16 result. */
 #define MLPB_LINEAR8_OUT_F32 0x1u      /* Y and dX are fp32 (else bf16)                       */
 #define MLPB_LINEAR8_FAULT_INJECT 0x2u /* test only, as MLPB_FLAG_FAULT_INJECT: the first     \
                                           product's first stage is never filled               */
@@ -543,14 +545,17 @@ mlpb_status mlpb_linear8_last_device_error(mlpb_linear8 *h, mlpb_stream_t stream
 
 /* Orthogonalised updates of weights, by Newton-Schulz products ("From Install to Your First
  * Model" and the sharded optimizer's section of the source tour name the optimizer's step, which
- * this library's weight gradients feed): for `batch` matrices [rows][cols] -- a weight's shards, as
- * dW1, dW2 lie --
+ * this library's weight gradients feed): for `batch` matrices [rows][cols], each by itself,
  *     X_0 = U / |U|_F,  X <- a X + (b A + c A A) X, A = X X^T   (`steps` times),  O = X
  * (X <- a X + X (b A + c A A), A = X^T X, with more rows than columns), and, in
  * mlpb_muon_step,
  *     M <- momentum M + G,   U = G + momentum M (nesterov) or M
  *     W <- (1 - lr weight_decay) W - lr scale O
  * A zero matrix stays zero; one with an infinity or a NaN becomes NaN, alone.
+ * The shards of dW1 and dW2 can be taken as they lie, as a batch: that is the blockwise update, in
+ * which every shard is orthogonalised by itself, not the update of the whole weight.  For that one
+ * the matrices are whole: dW1 [t][Fs][H] is [F][H] as it lies, and so is dW2 with t = 1; else
+ * dW2's shards are put side by side first, and a gated dW1's apart into gate and up.
  * Products take fp16 operands with fixed scales, sums and both products' diagonals are fp32, X
  * keeps 22 bits between the steps.  With five steps of the usual coefficients O is off by 3e-4 to
  * 1.4e-3 of its size, by up to 4e-3 where the smaller side is below 32 or one singular value

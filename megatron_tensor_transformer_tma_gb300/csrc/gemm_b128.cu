@@ -16,12 +16,16 @@
 // An accumulation in the tensor cores cuts off instead of rounding: sums come out too small, by
 // 6e-7 of their size after 64 k-blocks and in proportion.  So an fp32 result's sum is taken in
 // chunks of 64 k-blocks: dW of 16384 tokens is off by as much as that of 8192.  Chunks are added in
-// the epilogue's registers (dW of 16384 x 4096 x 11008 547 us, 592 in memory) or, where C is added
-// to anyway, in memory, in their order, by TMA, whose additions take subnormal values as zeros.
+// the epilogue's registers or, where C is added to anyway, in memory, in their order, by TMA, whose
+// additions take subnormal values as zeros (16384 x 4096 x 11008 592 us, in registers 547).  128
+// sums and the next chunk's are more than 168 registers: 404 bytes a thread are spilled.  That costs
+// 3 % (the product alone 485 us without chunks, 499 so compiled and still without), the drain after
+// each chunk, which nothing overlaps, 5 % more (523).  A bf16 result's sum is taken at once, however
+// long: what is cut off is far below its own rounding.
 //
-// Measured at 8192 x 5120 x 20480: Y 498-525 us (3270-3450 TFLOP/s), 85 % of the cycles with the
-// tensor cores active; dX 537, dW (fp32, 64 k-blocks) 545.  What is left is the one accumulator's
-// drain between tiles, and the power limit.
+// Measured at 8192 x 5120 x 20480: Y 498-525 us (3270-3450 TFLOP/s), 80-85 % of the cycles with
+// the tensor cores active; dX 537, dW (fp32, 64 k-blocks) 545.  What is left is the one
+// accumulator's drain between tiles, and the power limit.
 #include <algorithm>
 
 #include "../../include/mlpb.h"

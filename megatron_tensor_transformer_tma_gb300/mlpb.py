@@ -1241,9 +1241,10 @@ class Linear8:
 
 
 class Muon:
-    """The orthogonalised update of `batch` matrices [rows][cols], such as the shards of a weight
-    (dW1 [t][2][Fs][H] is 2 t matrices): orthogonalize() alone, or step() with momentum, decay and
-    the weight's update.  Owns a handle and its workspace."""
+    """The orthogonalised update of `batch` matrices [rows][cols], each by itself: orthogonalize()
+    alone, or step() with momentum, decay and the weight's update.  The shards of a weight as a
+    batch (dW1 [t][2][Fs][H] is 2 t matrices) are the blockwise update; that of the whole weight
+    takes whole matrices (include/mlpb.h).  Owns a handle and its workspace."""
 
     def __init__(self, rows, cols, batch=1, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
                  momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0, device="cuda",
