@@ -74,8 +74,8 @@ bool map_scales(const mlpb_linear8* h, CUtensorMap* m, const Quantized& q) {
 //     10.7 / 15.2 at 24, 18.1 / 33.3 at 86; 512 x 2048 27.4 / 35.1 at 86);
 //   - with no more tiles of 256 x 256 than pairs of SMs, up to 32 k-blocks: it starts and ends
 //     sooner (a tile of 128 x 128 and one CTA, in place of a pair's), and a k-block costs it more,
-//     the bytes of both operands for a quarter of the products.  Between 12 and 40 k-blocks neither
-//     is ahead by more than 7 % (512 x 4096 7.1 / 8.0 at 4, 13.0 / 12.7 at 16, 22.2 / 21.8 at 40,
+//     half the bytes for a quarter of the products.  Between 12 and 40 k-blocks it is 11 % ahead to
+//     7 % behind, mostly within 5 (512 x 4096 7.1 / 8.0 at 4, 13.0 / 12.7 at 16, 22.2 / 21.8 at 40,
 //     41.0 / 35.8 at 86; 1024 x 4096 10.5 / 11.8 at 8, 18.9 / 18.9 at 24, 28.5 / 26.5 at 48;
 //     512 x 5120 18.4 / 18.8 at 28, 29.3 / 28.5 at 56).
 // Not where C is added to, which the other kernel does in memory (2048 x 2048 at 8 19.2 against
